@@ -329,7 +329,7 @@ def _plain_route_backward(s):
     picked = score.gather(1, chosen)
     if s["renorm"]:
         total = picked.sum(1, keepdim=True)
-        g = (g - (g * picked / total).sum(1, keepdim=True)) / total
+        g = (g - (g * (picked / total)).sum(1, keepdim=True)) / total
     ds = torch.zeros_like(x).scatter_(1, chosen, g)
     if s["score"] == "sigmoid":
         return ds.mul_(score).mul_(1.0 - score).to(s["x"].dtype)
@@ -543,7 +543,7 @@ def exact(case, seed):
         d = jac(1.0)
         if case["renorm"]:
             total = picked.sum(1)[:, None, None]
-            d = d / total - picked[:, :, None] * d.sum(1, keepdims=True) / total ** 2
+            d = d / total - (picked[:, :, None] / total) * (d.sum(1, keepdims=True) / total)
         return case["scale"] * np.einsum("tk,tke->te", host(s["dw"]), d)
     if op == "combine":
         at, y = s["position"].long(), s["y"].double()
