@@ -79,6 +79,9 @@ typedef enum {
 
 typedef enum { WST_F32 = 0, WST_BF16 = 1 } wst_dtype;
 
+/* 8-bit floating point: e4m3 (largest 448, no infinity) and e5m2 (largest 57344). */
+typedef enum { WST_E4M3 = 0, WST_E5M2 = 1 } wst_fp8;
+
 typedef enum {
   WST_EPI_NONE = 0,      /* C = A.B^T                                   */
   WST_EPI_BIAS = 1,      /* C = A.B^T + bias[n]                         */
@@ -333,6 +336,145 @@ wst_status wst_ep_receive_plan(int world_size, int experts_per_rank, const int* 
 wst_status wst_permute_rows(int n_rows, size_t row_bytes, const void* src, size_t src_stride,
                             const int* d_src_index, int n_src_rows, void* dst, size_t dst_stride,
                             const int* d_dst_index, int n_dst_rows, void* workspace, void* stream);
+
+/*
+ * Mixture-of-experts routing on the GPU: the router in front of the grouped
+ * GEMM, the plan of its rows, and the sum of its results per token.  One layer:
+ *   wst_moe_route -> wst_moe_plan -> wst_permute_rows by row_token (or
+ *   wst_quantize_fp8_dispatch by position) -> wst_grouped_gemm_bf16 (or
+ *   wst_grouped_gemm_fp8) -> wst_moe_combine,
+ * all on device arrays, without a copy to the host, so the whole layer can be
+ * captured in a CUDA graph.  The gradients: wst_moe_combine_backward,
+ * wst_grouped_gemm_wgrad_bf16 for the weights, wst_grouped_gemm_bf16 with the
+ * transposed weights for the rows, wst_moe_combine without weights to add the
+ * rows' gradients per token, wst_moe_route_backward.
+ *
+ * These entry points (and the 8-bit ones below) also require their operands on
+ * the calling thread's current device (else WST_ERR_INVALID_ARG).
+ *
+ * wst_moe_route: for each of T tokens, with x its E logits (logits_type, rows
+ * `ld` elements apart, aligned to their elements only):
+ *   x <= -3e38 (-inf, or a mask of the type's lowest value): the expert is off
+ *   s_e = exp(x_e) / sum over the live experts of exp(x)   (WST_SCORE_SOFTMAX)
+ *         or 1 / (1 + exp(-x_e))                           (WST_SCORE_SIGMOID)
+ *   v_e = s_e + bias[e]      (bias fp32 [E] or NULL; it takes part in the
+ *                            choice, not in the weights; -inf: expert off)
+ *   groups > 1: the experts form `groups` equal consecutive groups; a group's
+ *         score is the sum of its group_best (1 or 2) largest v; the
+ *         top_groups groups with the largest scores stay
+ *   experts[t][i], i < top_k: the experts with the largest v, in descending
+ *         order of v; ties (of experts and of groups) go to the lower index
+ *   weights[t][i] = scale * s_i / (renorm ? sum of the chosen s : 1)
+ * Slots for which no live expert is left get expert -1 and weight 0 (a row
+ * with every expert off gets nothing else).  A NaN ranks above every number,
+ * as in torch.topk, and shows in the weights.  Without a bias the experts are
+ * ranked by their logits (and groups by their largest, for group_best 1);
+ * otherwise as if the scores were computed in 64 bits.
+ * Limits: E <= 1024, top_k <= 16, groups <= 32, else WST_ERR_UNSUPPORTED.
+ */
+typedef enum { WST_SCORE_SOFTMAX = 0, WST_SCORE_SIGMOID = 1 } wst_score;
+
+wst_status wst_moe_route(int T, int E, int top_k, const void* logits, long ld, wst_dtype logits_type,
+                         wst_score score, const float* bias, int groups, int top_groups,
+                         int group_best, int renorm, float scale, int* experts, float* weights,
+                         void* stream);
+
+/* Gradient of wst_moe_route's weights with respect to the logits:
+ *   dlogits[t][e] = sum_i dweights[t][i] d weights[t][i] / d logits[t][e],
+ * the choice of the experts held fixed.  `experts` as wst_moe_route left it
+ * (other ids outside [0, E) count as -1: no gradient; an expert in two slots
+ * gets the sum of both).  dlogits: logits_type, rows `ldd` apart, every one of
+ * its T x E elements is written; it may be the logits array itself. */
+wst_status wst_moe_route_backward(int T, int E, int top_k, const void* logits, long ld,
+                                  wst_dtype logits_type, wst_score score, int renorm, float scale,
+                                  const int* experts, const float* dweights, void* dlogits, long ldd,
+                                  void* stream);
+
+/* The rows of the grouped product: a stable sort of the pairs p = t * top_k + i
+ * by experts[p].  All arrays DEVICE int32.
+ *   offsets    out [num_experts + 1]: rows of expert e are [offsets[e], offsets[e+1])
+ *   row_pair   out [num_tokens * top_k]: the pair of each row, pair ids
+ *              ascending inside an expert; -1 behind the last row
+ *   row_token  out, same shape: the pair's token (row_pair / top_k); -1 behind
+ *   position   out [num_tokens][top_k]: the row of each pair; -1 without one
+ * A pair with expert -1 gets no row; so does one with another id outside
+ * [0, num_experts), which also latches WST_ERR_INVALID_ARG in the workspace.
+ * workspace: zero-filled once, wst_moe_plan_workspace_size(...) bytes.
+ * num_experts <= 1024, else WST_ERR_UNSUPPORTED. */
+wst_status wst_moe_plan(int num_tokens, int top_k, const int* experts, int num_experts, int* offsets,
+                        int* row_pair, int* row_token, int* position, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Workspace bytes wst_moe_plan needs for num_pairs = num_tokens * top_k pairs
+ * (0 for invalid sizes). */
+size_t wst_moe_plan_workspace_size(int num_pairs, int num_experts);
+
+/* The weighted sum of each token's rows:
+ *   out[t][n] = sum_i w[t][i] * y[position[t][i]][n]      (i ascending, in fp32)
+ *   y         y_type [n_rows][N], rows ldy elements apart
+ *   position  DEVICE int32 [T][top_k]; a negative entry adds nothing; one of
+ *             n_rows or more adds nothing and latches WST_ERR_INVALID_ARG
+ *   weights   fp32 [T][top_k], or NULL: all 1
+ *   out       out_type [T][N], rows ldo apart; every token is written (0 where
+ *             it has no row); it must not overlap y
+ * Rows are 16-byte aligned; N is arbitrary.  top_k <= 32. */
+wst_status wst_moe_combine(int T, int top_k, int N, const void* y, long ldy, wst_dtype y_type,
+                           int n_rows, const int* position, const float* weights, void* out, long ldo,
+                           wst_dtype out_type, void* workspace, void* stream);
+
+/* Gradients of wst_moe_combine for dout (out_type [T][N]):
+ *   dy[position[t][i]][n] = w[t][i] * dout[t][n]     (y_type; NULL: not wanted)
+ *   dweights[t][i] = sum_n dout[t][n] * y[position[t][i]][n]   (fp32; NULL: not
+ *                    wanted, y is then not read and may be NULL; 0 for a pair
+ *                    without a row)
+ * Rows of dy that no pair names are left as they were; a row that two pairs
+ * name gets one of the two values (wst_moe_plan names each row once).  dy must
+ * not overlap dout or y. */
+wst_status wst_moe_combine_backward(int T, int top_k, int N, const void* dout, long ldo,
+                                    wst_dtype out_type, const void* y, long ldy, wst_dtype y_type,
+                                    int n_rows, const int* position, const float* weights, void* dy,
+                                    long lddy, float* dweights, void* workspace, void* stream);
+
+/*
+ * Quantisation to 8 bits with one fp32 scale for each block of 128 values:
+ *   amax  = max |x| over the block, at least 2^-100
+ *   scale = amax * (1/largest), or with pow2 the smallest power of two with
+ *           amax <= largest * scale
+ *   q     = round to nearest even of x * (1/scale)         (x ~ q * scale)
+ * all in fp32.  A block with a NaN or an infinity gets it as its scale.
+ * x: x_type [M][K] per batch entry.  Modes (element (i,j) of q at q + i*ldq + j,
+ * of the scales at scales + i*lds + j):
+ *   WST_FP8_ROWS      blocks 1 x 128: q [M][K], scales [ceil(K/128)][M]
+ *                     (block-major: the scales of one K block are consecutive)
+ *   WST_FP8_COLS      blocks 128 x 1, transposed: q [K][M], scales [ceil(M/128)][K]
+ *                     (the ROWS form of x transposed)
+ *   WST_FP8_BLOCKS    blocks 128 x 128: q [M][K], scales [ceil(M/128)][ceil(K/128)]
+ *   WST_FP8_BLOCKS_T  the same blocks transposed: q [K][M], scales
+ *                     [ceil(K/128)][ceil(M/128)]
+ * A last block is what is left of its row or column.  x and q are 16-byte
+ * aligned with leading dimensions and batch strides of whole 16 bytes.
+ */
+typedef enum {
+  WST_FP8_ROWS = 0,
+  WST_FP8_COLS = 1,
+  WST_FP8_BLOCKS = 2,
+  WST_FP8_BLOCKS_T = 3
+} wst_fp8_mode;
+
+wst_status wst_quantize_fp8(wst_fp8_mode mode, int batch, int M, int K, const void* x, long ldx,
+                            long strideX, wst_dtype x_type, void* q, long ldq, long strideQ,
+                            wst_fp8 q_type, float* scales, long lds, long strideS, int pow2,
+                            void* stream);
+
+/* WST_FP8_ROWS of each row m of x, stored to the rows position[m][c], c <
+ * copies, of q [n_rows][K] and the scales [ceil(K/128)][n_rows]: the tokens'
+ * rows of a grouped product (position as wst_moe_plan leaves it).  A negative
+ * entry is skipped, one of n_rows or more is skipped and latches
+ * WST_ERR_INVALID_ARG.  Rows that no entry names are left as they were. */
+wst_status wst_quantize_fp8_dispatch(int M, int K, int copies, const void* x, long ldx,
+                                     wst_dtype x_type, const int* position, int n_rows, void* q,
+                                     long ldq, wst_fp8 q_type, float* scales, long lds, int pow2,
+                                     void* workspace, void* stream);
 
 /*
  * IKBO linear compression.  Candidates of user u are [off[u], off[u+1]) of

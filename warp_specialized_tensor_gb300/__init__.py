@@ -116,6 +116,7 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.wst_last_error.restype = ctypes.c_char_p
         lib.wst_version.argtypes = []
         lib.wst_version.restype = ctypes.c_char_p
+        moe.declare(lib)
         _lib = lib
         return lib
 
@@ -561,3 +562,12 @@ def wst_permute_rows(src, dst, src_index=None, dst_index=None, n_rows=None, work
         src.shape[0], dst.data_ptr(), dst.stride(0) * dst.element_size(), _ptr(dst_index),
         dst.shape[0], workspace.data_ptr(), _stream_handle(stream))
     _check(st, "wst_permute_rows")
+
+
+# ----------------------------------------------------------------------------
+# mixture-of-experts routing, combine, 8-bit products and gradients
+# ----------------------------------------------------------------------------
+from . import moe  # noqa: E402  (uses the definitions above)
+from .moe import *  # noqa: E402,F401,F403
+
+__all__ += moe.__all__

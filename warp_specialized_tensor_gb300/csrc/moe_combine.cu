@@ -1,0 +1,333 @@
+// moe_combine.cu -- the weighted sum of the experts' rows of each token, and
+// its gradients.
+//
+//   out[t]      = sum_i w[t][i] y[pos[t][i]]          (pos -1: no row; w NULL: 1)
+//   dy[pos]     = w[t][i] dout[t]
+//   dw[t][i]    = <dout[t], y[pos[t][i]]>             (0 where there is no row)
+//
+// Both are bound by HBM: every row of y and of out moves once.  A thread holds
+// eight neighbouring columns and adds a token's rows in slot order in fp32
+// (one rounding, at the store); up to four rows' loads are in flight per
+// thread.  The gradient's block holds one or more whole tokens, so dout is
+// read once for all of a token's rows and the dot products are summed inside
+// the block, in a fixed order.
+#include "wst.h"
+#include "wst_common.cuh"
+#include "wst_host.h"
+
+namespace wst {
+
+namespace {
+
+constexpr int kCombThreads = 256;
+constexpr int kCombMaxTopK = 32;
+
+struct CombineArgs {
+  int T, top_k, N, n_rows;
+  const void* y;
+  long long ldy;
+  const int* position;
+  const float* weights;
+  void* out;  // forward: out; backward: dout
+  long long ldo;
+  void* dy;
+  long long lddy;
+  float* dweights;
+  WsHeader* ws;
+};
+
+// Eight columns from c on; columns from n on read as 0 and are not stored.
+__device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
+  if (n >= 8) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? __ldg(p + i) : 0.0f;
+  }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, int n, float (&v)[8]) {
+  if (n >= 8) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? __bfloat162float(__ldg(p + i)) : 0.0f;
+  }
+}
+__device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = __float2bfloat16_rn(v[i]);
+  }
+}
+
+// Row of slot i of token t, -1 for none; a row past the end counts as none.
+__device__ __forceinline__ int combine_row(const CombineArgs& a, int t, int i, bool latch) {
+  const int p = __ldg(a.position + (long long)t * a.top_k + i);
+  if (p < a.n_rows) return p;
+  if (latch) latch_error(a.ws, 1u /*WST_ERR_INVALID_ARG*/, 0x70000u);
+  return -1;
+}
+
+// tpt threads per token (a power of two up to kCombThreads), blockIdx.y the
+// stretch of 8 * tpt columns.
+template <typename Y, typename O>
+__global__ void __launch_bounds__(kCombThreads) k_combine(const CombineArgs a, int tpt) {
+  const int t = blockIdx.x * (kCombThreads / tpt) + (int)threadIdx.x / tpt;
+  const int v = (int)blockIdx.y * tpt + (int)threadIdx.x % tpt;
+  const int n = a.N - v * 8;
+  if (t >= a.T || n <= 0) return;
+  const Y* y = static_cast<const Y*>(a.y) + (long long)v * 8;
+  float acc[8] = {};
+  for (int i0 = 0; i0 < a.top_k; i0 += 4) {
+    float x[4][8], w[4];
+    int row[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      row[i] = i0 + i < a.top_k ? combine_row(a, t, i0 + i, v == 0) : -1;
+      if (row[i] >= 0) {
+        load8(y + (long long)row[i] * a.ldy, n, x[i]);
+        w[i] = a.weights ? __ldg(a.weights + (long long)t * a.top_k + i0 + i) : 1.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (row[i] >= 0) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = fmaf(w[i], x[i][c], acc[c]);
+      }
+  }
+  store8(static_cast<O*>(a.out) + (long long)t * a.ldo + (long long)v * 8, n, acc);
+}
+
+// KC slots at a time (more slots take further passes over dout).
+template <typename Y, typename O, int KC>
+__global__ void __launch_bounds__(kCombThreads) k_combine_backward(const CombineArgs a, int tpt) {
+  __shared__ float part[kCombThreads / 32][KC];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * (kCombThreads / tpt) + (int)threadIdx.x / tpt;
+  const int me = (int)threadIdx.x % tpt;
+  const bool there = t < a.T;
+  const O* dout = static_cast<const O*>(a.out) + (long long)(there ? t : 0) * a.ldo;
+  for (int i0 = 0; i0 < a.top_k; i0 += KC) {
+    int row[KC];
+    float w[KC], dot[KC];
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+      row[i] = there && i0 + i < a.top_k ? combine_row(a, t, i0 + i, me == 0) : -1;
+      w[i] = row[i] >= 0 && a.weights ? __ldg(a.weights + (long long)t * a.top_k + i0 + i) : 1.0f;
+      dot[i] = 0.0f;
+    }
+    for (int c = me * 8; there && c < a.N; c += tpt * 8) {
+      const int n = a.N - c;
+      float d[8];
+      load8(dout + c, n, d);
+#pragma unroll
+      for (int i = 0; i < KC; ++i) {
+        if (row[i] < 0) continue;
+        if (a.dweights) {
+          float x[8];
+          load8(static_cast<const Y*>(a.y) + (long long)row[i] * a.ldy + c, n, x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dot[i] = fmaf(d[j], x[j], dot[i]);
+        }
+        if (a.dy) {
+          float g[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] = w[i] * d[j];
+          store8(static_cast<Y*>(a.dy) + (long long)row[i] * a.lddy + c, n, g);
+        }
+      }
+    }
+    if (a.dweights) {
+#pragma unroll
+      for (int i = 0; i < KC; ++i) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], o);
+        if (lane == 0) part[warp][i] = dot[i];
+      }
+      __syncthreads();
+      if (there && me < KC && i0 + me < a.top_k) {
+        float sum = 0.0f;
+        for (int k = 0; k < tpt / 32; ++k) sum += part[warp + k][me];
+        a.dweights[(long long)t * a.top_k + i0 + me] = sum;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+int threads_per_token(int N) {
+  int tpt = 32;
+  while (tpt < kCombThreads && tpt * 8 < N) tpt *= 2;
+  return tpt;
+}
+
+template <typename Y, typename O>
+void launch_combine(const CombineArgs& a, cudaStream_t s) {
+  const int tpt = threads_per_token(a.N), per = kCombThreads / tpt;
+  const dim3 grid((unsigned)((a.T + per - 1) / per), (unsigned)((a.N + 8 * tpt - 1) / (8 * tpt)));
+  k_combine<Y, O><<<grid, kCombThreads, 0, s>>>(a, tpt);
+}
+
+template <typename Y, typename O>
+void launch_combine_backward(const CombineArgs& a, cudaStream_t s) {
+  const int tpt = threads_per_token(a.N), per = kCombThreads / tpt;
+  const unsigned grid = (unsigned)((a.T + per - 1) / per);
+  if (a.top_k == 1) k_combine_backward<Y, O, 1><<<grid, kCombThreads, 0, s>>>(a, tpt);
+  else if (a.top_k == 2) k_combine_backward<Y, O, 2><<<grid, kCombThreads, 0, s>>>(a, tpt);
+  else if (a.top_k <= 4) k_combine_backward<Y, O, 4><<<grid, kCombThreads, 0, s>>>(a, tpt);
+  else k_combine_backward<Y, O, 8><<<grid, kCombThreads, 0, s>>>(a, tpt);
+}
+
+int check_combine(const char* what, int T, int top_k, int N, int y_type, int n_rows, int out_type) {
+  if (T < 0 || top_k < 1 || N < 1 || n_rows < 0)
+    return reject(ST_INVALID_ARG, "%s: sizes out of range (T=%d top_k=%d N=%d n_rows=%d)", what, T, top_k, N, n_rows);
+  if (top_k > kCombMaxTopK)
+    return reject(ST_UNSUPPORTED, "%s: top_k=%d: this build supports up to %d", what, top_k, kCombMaxTopK);
+  if (N > 65535 * 8 * kCombThreads)
+    return reject(ST_UNSUPPORTED, "%s: N=%d is too wide", what, N);
+  if ((y_type != WST_F32 && y_type != WST_BF16) || (out_type != WST_F32 && out_type != WST_BF16))
+    return reject(ST_INVALID_ARG, "%s: unknown type", what);
+  return ST_OK;
+}
+
+int check_rows(const char* what, const char* name, const void* p, long ld, int type, int N) {
+  const long es = type == WST_F32 ? 4 : 2;
+  if (ld < N) return reject(ST_INVALID_ARG, "%s: leading dimension %ld of %s < N", what, ld, name);
+  if (!aligned_to(p, 16) || ld * es % 16)
+    return reject(ST_ALIGNMENT, "%s: %s must be 16-byte aligned, its leading dimension a multiple of 16 bytes", what, name);
+  return ST_OK;
+}
+
+}  // namespace
+}  // namespace wst
+
+using namespace wst;
+
+#define WST_TRY(expr)                  \
+  do {                                 \
+    int st__ = (expr);                 \
+    if (st__) return (wst_status)st__; \
+  } while (0)
+
+extern "C" {
+
+wst_status wst_moe_combine(int T, int top_k, int N, const void* y, long ldy, wst_dtype y_type, int n_rows,
+                           const int* position, const float* weights, void* out, long ldo, wst_dtype out_type,
+                           void* workspace, void* stream) {
+  set_error("%s", "");
+  WST_TRY(check_combine("combine", T, top_k, N, y_type, n_rows, out_type));
+  if ((n_rows && T && !y) || (T && (!position || !out)) || !workspace)
+    return (wst_status)reject(ST_INVALID_ARG, "combine: NULL array");
+  WST_TRY(check_rows("combine", "y", y, ldy, y_type, N));
+  WST_TRY(check_rows("combine", "out", out, ldo, out_type, N));
+  if (!aligned_to(position, 4) || !aligned_to(weights, 4) || !aligned_to(workspace, 16))
+    return (wst_status)reject(ST_ALIGNMENT, "combine: position and weights must be 4-byte, the workspace 16-byte aligned");
+  if (T == 0) return WST_OK;
+  if (n_rows) WST_TRY(check_operand(y, "y"));
+  WST_TRY(check_operand(position, "position"));
+  if (weights) WST_TRY(check_operand(weights, "weights"));
+  WST_TRY(check_operand(out, "out"));
+  WST_TRY(check_operand(workspace, "workspace"));
+  DeviceInfo dev;
+  WST_TRY(current_device_info(&dev));
+  CombineArgs a{};
+  a.T = T;
+  a.top_k = top_k;
+  a.N = N;
+  a.n_rows = n_rows;
+  a.y = y;
+  a.ldy = ldy;
+  a.position = position;
+  a.weights = weights;
+  a.out = out;
+  a.ldo = ldo;
+  a.ws = static_cast<WsHeader*>(workspace);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (y_type == WST_F32) {
+    if (out_type == WST_F32) launch_combine<float, float>(a, s);
+    else launch_combine<float, __nv_bfloat16>(a, s);
+  } else {
+    if (out_type == WST_F32) launch_combine<__nv_bfloat16, float>(a, s);
+    else launch_combine<__nv_bfloat16, __nv_bfloat16>(a, s);
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? WST_OK : (wst_status)cuda_fail(e, "launch k_combine");
+}
+
+wst_status wst_moe_combine_backward(int T, int top_k, int N, const void* dout, long ldo, wst_dtype out_type,
+                                    const void* y, long ldy, wst_dtype y_type, int n_rows, const int* position,
+                                    const float* weights, void* dy, long lddy, float* dweights, void* workspace,
+                                    void* stream) {
+  set_error("%s", "");
+  WST_TRY(check_combine("combine backward", T, top_k, N, y_type, n_rows, out_type));
+  if ((T && (!dout || !position)) || !workspace) return (wst_status)reject(ST_INVALID_ARG, "combine backward: NULL array");
+  if (!dy && !dweights)
+    return (wst_status)reject(ST_INVALID_ARG, "combine backward: neither dy nor dweights is asked for");
+  if (T && dweights && n_rows && !y) return (wst_status)reject(ST_INVALID_ARG, "combine backward: dweights needs y");
+  WST_TRY(check_rows("combine backward", "dout", dout, ldo, out_type, N));
+  if (dweights && n_rows) WST_TRY(check_rows("combine backward", "y", y, ldy, y_type, N));
+  if (dy) WST_TRY(check_rows("combine backward", "dy", dy, lddy, y_type, N));
+  if (!aligned_to(position, 4) || !aligned_to(weights, 4) || !aligned_to(dweights, 4) || !aligned_to(workspace, 16))
+    return (wst_status)reject(ST_ALIGNMENT,
+                              "combine backward: position and weights must be 4-byte, the workspace 16-byte aligned");
+  if (T == 0) return WST_OK;
+  WST_TRY(check_operand(dout, "dout"));
+  WST_TRY(check_operand(position, "position"));
+  if (dweights && n_rows) WST_TRY(check_operand(y, "y"));
+  if (weights) WST_TRY(check_operand(weights, "weights"));
+  if (dy) WST_TRY(check_operand(dy, "dy"));
+  if (dweights) WST_TRY(check_operand(dweights, "dweights"));
+  WST_TRY(check_operand(workspace, "workspace"));
+  DeviceInfo dev;
+  WST_TRY(current_device_info(&dev));
+  CombineArgs a{};
+  a.T = T;
+  a.top_k = top_k;
+  a.N = N;
+  a.n_rows = n_rows;
+  a.y = y;
+  a.ldy = ldy;
+  a.position = position;
+  a.weights = weights;
+  a.out = const_cast<void*>(dout);
+  a.ldo = ldo;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.dweights = dweights;
+  a.ws = static_cast<WsHeader*>(workspace);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (y_type == WST_F32) {
+    if (out_type == WST_F32) launch_combine_backward<float, float>(a, s);
+    else launch_combine_backward<float, __nv_bfloat16>(a, s);
+  } else {
+    if (out_type == WST_F32) launch_combine_backward<__nv_bfloat16, float>(a, s);
+    else launch_combine_backward<__nv_bfloat16, __nv_bfloat16>(a, s);
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? WST_OK : (wst_status)cuda_fail(e, "launch k_combine_backward");
+}
+
+}  // extern "C"

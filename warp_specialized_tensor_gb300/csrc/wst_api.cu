@@ -157,21 +157,13 @@ int encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ptr
   return ST_OK;
 }
 
-}  // namespace wst
-
-using namespace wst;
-
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // The pointer must be memory the GPU addresses as device memory.
-int check_device_ptr(const void* p, const char* name) {
+int device_attributes(const void* p, const char* name, cudaPointerAttributes& at) {
   if (!p) {
     set_error("%s is NULL", name);
     return ST_INVALID_ARG;
   }
-  cudaPointerAttributes at{};
   cudaError_t e = cudaPointerGetAttributes(&at, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -184,6 +176,42 @@ int check_device_ptr(const void* p, const char* name) {
   }
   return ST_OK;
 }
+}  // namespace
+
+int check_device_ptr(const void* p, const char* name) {
+  cudaPointerAttributes at{};
+  return device_attributes(p, name, at);
+}
+
+int check_operand(const void* p, const char* name) {
+  cudaPointerAttributes at{};
+  int st = device_attributes(p, name, at);
+  if (st) return st;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (at.type == cudaMemoryTypeDevice && at.device != dev) {
+    set_error("%s is on device %d, the current device is %d", name, at.device, dev);
+    return ST_INVALID_ARG;
+  }
+  return ST_OK;
+}
+
+int reject(int status, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return status;
+}
+
+}  // namespace wst
+
+using namespace wst;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 #define WST_TRY(expr)            \
   do {                           \

@@ -5,6 +5,7 @@
 // validating ABI layer to the per-kernel launchers.
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -23,6 +24,12 @@ enum Status : int {
 };
 
 void set_error(const char* fmt, ...);
+int reject(int status, const char* fmt, ...);  // records the message, returns `status`
+// `p` must be memory the GPU addresses as device memory (Status).
+int check_device_ptr(const void* p, const char* name);
+// The same, and on the calling thread's current device.
+int check_operand(const void* p, const char* name);
+inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 int cuda_fail(cudaError_t e, const char* what);  // records the message, returns ST_CUDA
 
 struct DeviceInfo {

@@ -1,0 +1,293 @@
+"""Binding of the mixture-of-experts operators around the grouped GEMM: routing,
+the plan of the rows, the sum of the experts' rows, 8-bit products with block
+scales, and the gradients (``include/wst.h`` has the definitions).
+
+The functions are exported by the package.  They follow its conventions: the
+C ABI's names, outputs passed in, sizes and leading dimensions read from the
+tensors, the current stream unless one is given.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+import warp_specialized_tensor_gb300 as _w
+
+__all__ = [
+    "SCORE_SOFTMAX", "SCORE_SIGMOID", "E4M3", "E5M2", "FP8_ROWS", "FP8_COLS", "FP8_BLOCKS", "FP8_BLOCKS_T",
+    "wst_moe_route", "wst_moe_route_backward", "wst_moe_plan", "wst_moe_plan_workspace_size", "moe_plan_workspace",
+    "wst_moe_combine", "wst_moe_combine_backward", "wst_quantize_fp8", "wst_quantize_fp8_dispatch",
+]
+
+# enums of include/wst.h
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+E4M3, E5M2 = 0, 1
+FP8_ROWS, FP8_COLS, FP8_BLOCKS, FP8_BLOCKS_T = 0, 1, 2, 3
+_SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+_MODES = {"rows": FP8_ROWS, "cols": FP8_COLS, "blocks": FP8_BLOCKS, "blocks_t": FP8_BLOCKS_T}
+_FP8 = {torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2}
+
+
+def declare(lib) -> None:
+    """Argument types of the functions bound here."""
+    P, I, L, Z, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_long, ctypes.c_size_t, ctypes.c_float
+    for name, res, args in (
+            ("wst_moe_route", I, [I, I, I, P, L, I, I, P, I, I, I, I, F, P, P, P]),
+            ("wst_moe_route_backward", I, [I, I, I, P, L, I, I, I, F, P, P, P, L, P]),
+            ("wst_moe_plan", I, [I, I, P, I, P, P, P, P, P, Z, P]),
+            ("wst_moe_plan_workspace_size", Z, [I, I]),
+            ("wst_moe_combine", I, [I, I, I, P, L, I, I, P, P, P, L, I, P, P]),
+            ("wst_moe_combine_backward", I, [I, I, I, P, L, I, P, L, I, I, P, P, P, L, P, P, P]),
+            ("wst_quantize_fp8", I, [I, I, I, I, P, L, L, I, P, L, L, I, P, L, L, I, P]),
+            ("wst_quantize_fp8_dispatch", I, [I, I, I, P, L, I, P, I, P, L, I, P, L, I, P, P])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = res, args
+
+
+def _fp8(t, name) -> int:
+    if t.dtype not in _FP8:
+        raise TypeError("%s must be float8_e4m3fn or float8_e5m2" % name)
+    return _FP8[t.dtype]
+
+
+def _type(t, name) -> int:
+    if t.dtype == torch.float32:
+        return _w.F32
+    if t.dtype == torch.bfloat16:
+        return _w.BF16
+    raise TypeError("%s must be float32 or bfloat16" % name)
+
+
+def _need(t, name, dtype=None, dims=None):
+    """The package's check, for tensors whose last stride means nothing (one column, or no element) too."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() and (t.shape[-1] == 1 or t.numel() == 0):
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError("%s must be %s" % (name, dtype))
+        if dims is not None and t.dim() not in dims:
+            raise ValueError("%s must have %s dimensions" % (name, dims))
+        return
+    _w._need(t, name, dtype, dims)
+
+
+def _ids(t, name, shape=None):
+    """A contiguous int32 CUDA tensor."""
+    _need(t, name, torch.int32)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _floats(t, name, shape):
+    _need(t, name, torch.float32)
+    if not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be a contiguous %s tensor" % (name, tuple(shape)))
+
+
+def _rows(t, name, dims=(2,)):
+    """A tensor of rows; returns the leading dimension (a lone row has none of its own)."""
+    _need(t, name, None, dims)
+    if t.shape[-2] > 1:
+        return t.stride(-2)
+    per = 16 // t.element_size()
+    return -(-max(t.shape[-1], 1) // per) * per
+
+
+def _ws(workspace):
+    if workspace is None:
+        raise ValueError("workspace is required (see workspace())")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _score(score) -> int:
+    return _SCORES[score] if isinstance(score, str) else int(score)
+
+
+# ----------------------------------------------------------------------------
+# routing
+# ----------------------------------------------------------------------------
+def wst_moe_route(logits, experts, weights, score="softmax", bias=None, groups=1, top_groups=None, group_best=1,
+                  renorm=True, scale=1.0, stream=None) -> None:
+    """The top_k experts of each token and their weights.
+
+    logits: bf16/fp32 [T, E]; experts: int32 [T, top_k] and weights: fp32
+    [T, top_k], written; bias: fp32 [E] added to the scores for the choice
+    only; groups / top_groups / group_best: keep the top_groups of `groups`
+    groups of experts by the sum of their group_best best scores; renorm: the
+    weights sum to `scale`.  Experts whose logit is -inf (or the type's lowest
+    value) are off; a slot without an expert holds -1 and weight 0."""
+    _need(logits, "logits", None, (2,))
+    T, E = logits.shape
+    if experts.dim() != 2 or experts.shape[0] != T:
+        raise ValueError("experts must be [T, top_k]")
+    k = experts.shape[1]
+    _ids(experts, "experts", (T, k))
+    _floats(weights, "weights", (T, k))
+    if bias is not None:
+        _floats(bias, "bias", (E,))
+    st = _w.load_library().wst_moe_route(
+        T, E, k, logits.data_ptr(), max(logits.stride(0), E) if T <= 1 else logits.stride(0), _type(logits, "logits"), _score(score),
+        _w._ptr(bias), int(groups), int(groups if top_groups is None else top_groups), int(group_best), int(bool(renorm)),
+        float(scale), experts.data_ptr(), weights.data_ptr(), _w._stream_handle(stream))
+    _w._check(st, "wst_moe_route")
+
+
+def wst_moe_route_backward(logits, experts, dweights, dlogits, score="softmax", renorm=True, scale=1.0, stream=None) -> None:
+    """dlogits = the gradient of wst_moe_route's weights for dweights (fp32
+    [T, top_k]), the experts held fixed.  dlogits: like logits; the other
+    arguments as in wst_moe_route."""
+    _need(logits, "logits", None, (2,))
+    T, E = logits.shape
+    _need(dlogits, "dlogits", logits.dtype, (2,))
+    if dlogits.shape != logits.shape or experts.dim() != 2 or experts.shape[0] != T:
+        raise ValueError("shape mismatch")
+    k = experts.shape[1]
+    _ids(experts, "experts", (T, k))
+    _floats(dweights, "dweights", (T, k))
+    lead = (lambda t: max(t.stride(0), E) if T <= 1 else t.stride(0))
+    st = _w.load_library().wst_moe_route_backward(
+        T, E, k, logits.data_ptr(), lead(logits), _type(logits, "logits"), _score(score), int(bool(renorm)), float(scale),
+        experts.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(), lead(dlogits), _w._stream_handle(stream))
+    _w._check(st, "wst_moe_route_backward")
+
+
+def wst_moe_plan_workspace_size(num_pairs: int, num_experts: int) -> int:
+    return int(_w.load_library().wst_moe_plan_workspace_size(num_pairs, num_experts))
+
+
+def moe_plan_workspace(num_pairs: int, num_experts: int, device=None, stream=None) -> torch.Tensor:
+    """A zero-filled workspace for wst_moe_plan with up to num_pairs pairs."""
+    n = max(wst_moe_plan_workspace_size(num_pairs, num_experts), _w.wst_workspace_size())
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    _w.wst_workspace_init(ws, stream)
+    return ws
+
+
+def wst_moe_plan(experts, num_experts, offsets, row_pair, row_token, position, workspace=None, stream=None) -> None:
+    """The rows of the grouped product of a routing table: a stable sort of the
+    pairs (token, slot) by expert.
+
+    experts: int32 [T, top_k], -1 for no expert; offsets: int32
+    [num_experts + 1], the grouped GEMM's offsets; row_pair, row_token: int32
+    [T * top_k], the pair and the token of each row (-1 behind the last row);
+    position: int32 [T, top_k], the row of each pair (-1: none)."""
+    if experts.dim() != 2:
+        raise ValueError("experts must be [T, top_k]")
+    T, k = experts.shape
+    _ids(experts, "experts")
+    _ids(offsets, "offsets", (num_experts + 1,))
+    _ids(row_pair, "row_pair", (T * k,))
+    _ids(row_token, "row_token", (T * k,))
+    _ids(position, "position", (T, k))
+    ws, n = _ws(workspace)
+    st = _w.load_library().wst_moe_plan(T, k, experts.data_ptr(), int(num_experts), offsets.data_ptr(), row_pair.data_ptr(),
+                                        row_token.data_ptr(), position.data_ptr(), ws, n, _w._stream_handle(stream))
+    _w._check(st, "wst_moe_plan")
+
+
+# ----------------------------------------------------------------------------
+# combine
+# ----------------------------------------------------------------------------
+def wst_moe_combine(y, position, out, weights=None, workspace=None, stream=None) -> None:
+    """out[t] = sum_i weights[t, i] * y[position[t, i]].
+
+    y: bf16/fp32 [rows, N]; position: int32 [T, top_k], negative entries add
+    nothing; weights: fp32 [T, top_k] or None (all 1); out: bf16/fp32 [T, N]."""
+    ldy, ldo = _rows(y, "y"), _rows(out, "out")
+    T, N = out.shape
+    if y.shape[1] != N or position.dim() != 2 or position.shape[0] != T:
+        raise ValueError("shape mismatch: y %s position %s out %s" % (tuple(y.shape), tuple(position.shape), tuple(out.shape)))
+    k = position.shape[1]
+    _ids(position, "position", (T, k))
+    if weights is not None:
+        _floats(weights, "weights", (T, k))
+    ws, _ = _ws(workspace)
+    st = _w.load_library().wst_moe_combine(
+        T, k, N, y.data_ptr(), ldy, _type(y, "y"), y.shape[0], position.data_ptr(), _w._ptr(weights), out.data_ptr(), ldo,
+        _type(out, "out"), ws, _w._stream_handle(stream))
+    _w._check(st, "wst_moe_combine")
+
+
+def wst_moe_combine_backward(dout, position, y=None, weights=None, dy=None, dweights=None, workspace=None, stream=None) -> None:
+    """Gradients of wst_moe_combine: dy[position[t, i]] = weights[t, i] * dout[t]
+    and dweights[t, i] = <dout[t], y[position[t, i]]>; either may be None
+    (y is needed for dweights only).  Rows of dy that no pair names are left
+    as they were."""
+    ldo = _rows(dout, "dout")
+    T, N = dout.shape
+    if position.dim() != 2 or position.shape[0] != T:
+        raise ValueError("position must be [T, top_k]")
+    k = position.shape[1]
+    _ids(position, "position", (T, k))
+    if weights is not None:
+        _floats(weights, "weights", (T, k))
+    if dweights is not None:
+        _floats(dweights, "dweights", (T, k))
+        if y is None:
+            raise ValueError("dweights needs y")
+    rows = y if y is not None else dy
+    if rows is None:
+        raise ValueError("neither dy nor dweights is asked for")
+    ldy = _rows(y, "y") if y is not None else 0
+    lddy = _rows(dy, "dy") if dy is not None else 0
+    if rows.shape[1] != N or (y is not None and dy is not None and (y.shape != dy.shape or y.dtype != dy.dtype)):
+        raise ValueError("y and dy must be alike, with rows of N values")
+    ws, _ = _ws(workspace)
+    st = _w.load_library().wst_moe_combine_backward(
+        T, k, N, dout.data_ptr(), ldo, _type(dout, "dout"), _w._ptr(y), ldy, _type(rows, "y"), rows.shape[0],
+        position.data_ptr(), _w._ptr(weights), _w._ptr(dy), lddy, _w._ptr(dweights), ws, _w._stream_handle(stream))
+    _w._check(st, "wst_moe_combine_backward")
+
+
+# ----------------------------------------------------------------------------
+# 8-bit quantisation
+# ----------------------------------------------------------------------------
+def wst_quantize_fp8(x, q, scales, mode="rows", pow2=False, stream=None) -> None:
+    """x ~ q * scale in 8 bits with one scale for each block of 128.
+
+    x: bf16/fp32 [M, K] or [batch, M, K]; mode "rows": q [M, K], scales
+    [ceil(K/128), M]; "cols": q [K, M] (x transposed), scales [ceil(M/128), K];
+    "blocks": q [M, K], scales [ceil(M/128), ceil(K/128)]; "blocks_t": both
+    transposed.  q: float8_e4m3fn or float8_e5m2; scales: fp32; both with x's
+    batch dimension.  pow2: scales are powers of two."""
+    m = _MODES[mode] if isinstance(mode, str) else int(mode)
+    ldx, ldq, lds = _rows(x, "x", (2, 3)), _rows(q, "q", (2, 3)), _rows(scales, "scales", (2, 3))
+    if q.dim() != x.dim() or scales.dim() != x.dim() or scales.dtype != torch.float32:
+        raise ValueError("q and scales (float32) must have x's dimensions")
+    M, K = x.shape[-2:]
+    mb, kb = -(-M // 128), -(-K // 128)
+    want_q = (M, K) if m in (FP8_ROWS, FP8_BLOCKS) else (K, M)
+    want_s = {FP8_ROWS: (kb, M), FP8_COLS: (mb, K), FP8_BLOCKS: (mb, kb), FP8_BLOCKS_T: (kb, mb)}[m]
+    lead = tuple(x.shape[:-2])
+    if tuple(q.shape) != lead + want_q or tuple(scales.shape) != lead + want_s:
+        raise ValueError("mode %r: q must be %s and scales %s" % (mode, lead + want_q, lead + want_s))
+    batch = lead[0] if lead else 1
+    if batch == 0:
+        return
+    s = (lambda t: t.stride(0) if t.dim() == 3 else 0)
+    st = _w.load_library().wst_quantize_fp8(
+        m, batch, M, K, x.data_ptr(), ldx, s(x), _type(x, "x"), q.data_ptr(), ldq, s(q), _fp8(q, "q"), scales.data_ptr(), lds,
+        s(scales), int(bool(pow2)), _w._stream_handle(stream))
+    _w._check(st, "wst_quantize_fp8")
+
+
+def wst_quantize_fp8_dispatch(x, position, q, scales, pow2=False, workspace=None, stream=None) -> None:
+    """Quantises each token's row (mode "rows") and stores it to the rows
+    position[t, i] of q [rows, K] and of the scales [ceil(K/128), rows].
+
+    x: bf16/fp32 [T, K]; position: int32 [T, copies], negative entries are
+    skipped; rows that no entry names are left as they were."""
+    ldx, ldq, lds = _rows(x, "x"), _rows(q, "q"), _rows(scales, "scales")
+    T, K = x.shape
+    rows = q.shape[0]
+    if q.shape[1] != K or tuple(scales.shape) != (-(-K // 128), rows) or scales.dtype != torch.float32:
+        raise ValueError("q must be [rows, K] and scales float32 [ceil(K/128), rows]")
+    if position.dim() != 2:
+        raise ValueError("position must be [T, copies]")
+    _ids(position, "position", (T, position.shape[1]))
+    ws, _ = _ws(workspace)
+    st = _w.load_library().wst_quantize_fp8_dispatch(
+        T, K, position.shape[1], x.data_ptr(), ldx, _type(x, "x"), position.data_ptr(), rows, q.data_ptr(), ldq, _fp8(q, "q"),
+        scales.data_ptr(), lds, int(bool(pow2)), ws, _w._stream_handle(stream))
+    _w._check(st, "wst_quantize_fp8_dispatch")
