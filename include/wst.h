@@ -477,6 +477,49 @@ wst_status wst_quantize_fp8_dispatch(int M, int K, int copies, const void* x, lo
                                      void* workspace, void* stream);
 
 /*
+ * Product of 8-bit matrices with block scales.  For m < M, n < N:
+ *   C[m][n] = epi( sum_b sA(m,b) sB(n,b) sum_{k in block b} A[m][k] B[n][k] (+ bias[n]) ),
+ * blocks of 128 along K (the last one what is left).
+ *   A       a_type [M][K], leading dimension lda
+ *   scaleA  fp32, sA(m,b) at scaleA + b*ldsa + m      (WST_FP8_ROWS of the rows)
+ *   B       b_type [N][K], leading dimension ldb
+ *   scaleB  fp32; b_scaling WST_FP8_ROWS: sB(n,b) at scaleB + b*ldsb + n;
+ *           WST_FP8_BLOCKS: sB(n,b) at scaleB + (n/128)*ldsb + b
+ *   bias    bf16 [N], NULL unless epi > 0
+ *   C       c_type [M][N], leading dimension ldc; M may be 0
+ * The products of a block accumulate in the tensor core; the blocks are scaled
+ * and added in fp32.  A training step's other products are the same call:
+ * dA = dC . B with B quantised as WST_FP8_BLOCKS_T, dB = dC^T . A with both
+ * quantised as WST_FP8_COLS (b_scaling WST_FP8_ROWS).
+ * a_type and b_type may differ.  A, B, C are 16-byte aligned with leading
+ * dimensions of whole 16 bytes.
+ * workspace: at least the 256-byte header, zero-filled once.  With
+ * wst_gemm_fp8_workspace_size() bytes the K loops of a product with few tiles
+ * (a step of a few tokens) are split over the idle SMs and their fp32 sums
+ * added in a fixed order; smaller ones run whole tiles.  After
+ * WST_ERR_TIMEOUT call wst_sync_status before using the workspace again.
+ */
+wst_status wst_gemm_fp8(int M, int N, int K, const void* A, long lda, wst_fp8 a_type,
+                        const float* scaleA, long ldsa, const void* B, long ldb, wst_fp8 b_type,
+                        const float* scaleB, long ldsb, wst_fp8_mode b_scaling, const void* bias, void* C,
+                        long ldc, wst_dtype c_type, wst_epilogue epi, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* The same for G groups of rows: rows [d_offsets[g], d_offsets[g+1]) of A and C
+ * with B + g*strideB_group, scaleB + g*strideSB_group and bias + g*strideBias
+ * (offsets as in wst_grouped_gemm_bf16, except that d_offsets[G] may be less
+ * than M_total: rows behind the last group are left as they were). */
+wst_status wst_grouped_gemm_fp8(int G, int M_total, int N, int K, const void* A, long lda, wst_fp8 a_type,
+                                const float* scaleA, long ldsa, const void* B, long ldb,
+                                long strideB_group, wst_fp8 b_type, const float* scaleB, long ldsb,
+                                long strideSB_group, wst_fp8_mode b_scaling, const int* d_offsets,
+                                const void* bias, long strideBias, void* C, long ldc, wst_dtype c_type,
+                                wst_epilogue epi, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes with which the 8-bit products split their K loops. */
+size_t wst_gemm_fp8_workspace_size(void);
+
+/*
  * IKBO linear compression.  Candidates of user u are [off[u], off[u+1]) of
  * the DEVICE int32 array d_user_offsets (num_users+1 entries, non-decreasing,
  * from 0 to num_cand).  For every candidate c of user u:

@@ -1,0 +1,234 @@
+"""GPU: 8-bit products with block scales, dense and grouped, against the 64-bit
+product of the numbers that the 8-bit values and their scales stand for."""
+import numpy as np
+import pytest
+import torch
+
+import moe_ref as ref
+
+pytestmark = pytest.mark.gpu
+E4, E5 = torch.float8_e4m3fn, torch.float8_e5m2
+
+
+@pytest.fixture(scope="module")
+def wst():
+    import warp_specialized_tensor_gb300 as w
+    w.load_library()
+    return w
+
+
+@pytest.fixture(scope="module")
+def big_ws(wst):
+    return wst.gemm_fp8_workspace()
+
+
+def rows16(t):
+    """t on the GPU in rows that begin on 16 bytes, the bits 0x7f (a NaN in 8 bits) behind them."""
+    per = 16 // t.element_size()
+    buf = torch.full((*t.shape[:-1], (-(-t.shape[-1] // per) + 1) * per * t.element_size()), 0x7f, dtype=torch.uint8, device="cuda")
+    out = buf.view(t.dtype)[..., :t.shape[-1]]
+    out.copy_(t)
+    return out
+
+
+def operand(M, K, mode, dtype, seed, lead=()):
+    """Random 8-bit values and scales of very different sizes."""
+    g = torch.Generator().manual_seed(seed)
+    q = (torch.randn(*lead, M, K, generator=g) * 40).clamp(-440, 440).to(dtype)
+    shape = (-(-K // 128), M) if mode == "rows" else (-(-M // 128), -(-K // 128))
+    s = torch.exp2(torch.randn(*lead, *shape, generator=g) * 2) * 0.01
+    return q, s
+
+
+def product(qa, sa, qb, sb, scaling):
+    a, b = ref.values(qa, sa, "rows"), ref.values(qb, sb, scaling)
+    return a @ b.T, abs(a) @ abs(b).T
+
+
+def bound(want, size, K, out_dtype):
+    # 128 sums of a block in the tensor core, each cut off at one unit of the
+    # sum (2u), three roundings for the scales and the sum of the blocks
+    err = (128 * 2 + -(-K // 128) + 3) * ref.U * size
+    return err + ref.half(out_dtype) * (abs(want) + err)
+
+
+def out_buffer(M, N, dtype):
+    per = 16 // torch.empty(0, dtype=dtype).element_size()
+    return torch.full((M + 2, (-(-N // per) + 1) * per), float("nan"), dtype=dtype, device="cuda")
+
+
+SIZES = [(1, 1, 1), (1, 128, 128), (3, 256, 130), (16, 300, 1024), (17, 64, 4096), (33, 4096, 512), (128, 128, 16), (129, 129, 129),
+         (256, 256, 256), (257, 500, 1000), (300, 700, 2100), (1030, 513, 640)]
+
+
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("scaling", ["blocks", "rows"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_dense(wst, big_ws, M, N, K, scaling, split):
+    qa, sa = operand(M, K, "rows", E4, 1)
+    qb, sb = operand(N, K, scaling, E4, 2)
+    ws = big_ws if split else wst.workspace()
+    want, size = product(qa, sa, qb, sb, scaling)
+    for dtype in (torch.float32, torch.bfloat16):
+        buf = out_buffer(M, N, dtype)
+        wst.wst_gemm_fp8(rows16(qa), sa.cuda(), rows16(qb), sb.cuda(), buf[:M, :N], scaling=scaling, workspace=ws)
+        assert wst.wst_sync_status(ws) == 0
+        assert (abs(ref.f64(buf[:M, :N]) - want) <= bound(want, size, K, dtype)).all()
+        assert torch.isnan(buf[M:].float()).all() and torch.isnan(buf[:, N:].float()).all()
+
+
+@pytest.mark.parametrize("ta,tb", [(E4, E5), (E5, E4), (E5, E5)])
+def test_types(wst, big_ws, ta, tb):
+    qa, sa = operand(70, 500, "rows", ta, 3)
+    qb, sb = operand(200, 500, "blocks", tb, 4)
+    want, size = product(qa, sa, qb, sb, "blocks")
+    C = torch.empty(70, 200, device="cuda")
+    wst.wst_gemm_fp8(rows16(qa), sa.cuda(), rows16(qb), sb.cuda(), C, workspace=big_ws)
+    assert (abs(ref.f64(C) - want) <= bound(want, size, 500, torch.float32)).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 300, 2048), (200, 260, 384)])
+def test_whole_numbers_are_exact(wst, big_ws, M, N, K):
+    # small whole numbers and scales that are powers of two: every partial sum is exact
+    g = torch.Generator().manual_seed(M)
+    qa, qb = torch.randint(-8, 9, (M, K), generator=g).to(E4), torch.randint(-8, 9, (N, K), generator=g).to(E4)
+    sa = torch.exp2(torch.randint(0, 3, (-(-K // 128), M), generator=g).float())
+    sb = torch.exp2(torch.randint(0, 3, (-(-N // 128), -(-K // 128)), generator=g).float())
+    C = torch.empty(M, N, device="cuda")
+    wst.wst_gemm_fp8(rows16(qa), sa.cuda(), rows16(qb), sb.cuda(), C, workspace=big_ws)
+    assert np.array_equal(ref.f64(C), product(qa, sa, qb, sb, "blocks")[0])
+
+
+@pytest.mark.parametrize("epi", ["bias", "bias_silu", "bias_gelu"])
+def test_epilogues(wst, big_ws, epi):
+    M, N, K = 37, 200, 384
+    qa, sa = operand(M, K, "rows", E4, 5)
+    qb, sb = operand(N, K, "blocks", E4, 6)
+    sa, sb = sa * 0.1, sb * 0.1
+    bias = torch.randn(N, generator=torch.Generator().manual_seed(1)).bfloat16()
+    want, size = product(qa, sa, qb, sb, "blocks")
+    x = want + ref.f64(bias)
+    t = torch.from_numpy(x)
+    y = {"bias": t, "bias_silu": t * torch.sigmoid(t), "bias_gelu": t * torch.special.ndtr(t)}[epi].numpy()
+    C = torch.empty(M, N, device="cuda")
+    wst.wst_gemm_fp8(rows16(qa), sa.cuda(), rows16(qb), sb.cuda(), C, bias=bias.cuda(), epi=epi, workspace=big_ws)
+    # slopes are below 1.13; the approximate tanh behind SiLU is off by 2^-11, its half by 2^-12 of |x|
+    tol = 1.13 * (bound(want, size, K, torch.float32) + ref.U * abs(x)) + abs(x) * (2.0 ** -12 if epi == "bias_silu" else 2.0 ** -21)
+    assert (abs(ref.f64(C) - y) <= tol).all()
+
+
+GROUPS = [[5], [0, 200, 0, 0, 77, 0], [513, 0], [1, 1, 1, 1, 127, 129, 128, 256], [0, 0, 0, 130], [16, 16, 300, 15, 17]]
+
+
+@pytest.mark.parametrize("scaling", ["blocks", "rows"])
+@pytest.mark.parametrize("sizes", GROUPS)
+def test_grouped(wst, big_ws, sizes, scaling):
+    N, K, G = 300, 400, len(sizes)
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    M = int(off[-1]) + 7                                   # rows behind the last group
+    qa, sa = operand(M, K, "rows", E4, 7)
+    qb, sb = operand(N, K, scaling, E4, 8, (G,))
+    bias = torch.randn(G, N).bfloat16()
+    for dtype, ws, epi in ((torch.float32, big_ws, "none"), (torch.bfloat16, wst.workspace(), "bias")):
+        buf = out_buffer(M, N, dtype)
+        wst.wst_grouped_gemm_fp8(rows16(qa), sa.cuda(), rows16(qb), sb.cuda(), torch.from_numpy(off).int().cuda(), buf[:M, :N],
+                                 scaling=scaling, bias=bias.cuda(), epi=epi, workspace=ws)
+        assert wst.wst_sync_status(ws) == 0
+        for g in range(G):
+            r = slice(off[g], off[g + 1])
+            want, size = product(qa[r], sa[:, r], qb[g], sb[g], scaling)
+            err = bound(want, size, K, dtype)
+            if epi == "bias":
+                want = want + ref.f64(bias[g])
+                err = err + ref.half(dtype) * abs(ref.f64(bias[g])) + ref.U * abs(want)
+            assert (abs(ref.f64(buf[r, :N]) - want) <= err).all()
+        assert torch.isnan(buf[off[-1]:].float()).all() and torch.isnan(buf[:, N:].float()).all()
+
+
+def test_grouped_many_groups(wst, big_ws):
+    rng = np.random.default_rng(1)
+    sizes = rng.integers(0, 30, 300)
+    sizes[rng.choice(300, 100, replace=False)] = 0
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    M, N, K = int(off[-1]), 128, 256
+    qa, sa = operand(M, K, "rows", E4, 9)
+    qb, sb = operand(N, K, "blocks", E4, 10, (300,))
+    C = torch.full((M, N), float("nan"), device="cuda")
+    wst.wst_grouped_gemm_fp8(qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), torch.from_numpy(off).int().cuda(), C, workspace=big_ws)
+    assert wst.wst_sync_status(big_ws) == 0
+    for g in range(300):
+        r = slice(off[g], off[g + 1])
+        want, size = product(qa[r], sa[:, r], qb[g], sb[g], "blocks")
+        assert (abs(ref.f64(C[r]) - want) <= bound(want, size, K, torch.float32)).all()
+
+
+def test_grouped_bad_offsets_latched(wst, big_ws):
+    qa, sa = operand(300, 128, "rows", E4, 11)
+    qb, sb = operand(256, 128, "blocks", E4, 12, (3,))
+    buf = out_buffer(300, 256, torch.bfloat16)
+    off = torch.tensor([0, 250, 120, 300], dtype=torch.int32, device="cuda")
+    wst.wst_grouped_gemm_fp8(qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), off, buf[:300, :256], workspace=big_ws)
+    assert wst.wst_sync_status(big_ws) == wst.WST_ERR_BAD_OFFSETS
+    assert torch.isnan(buf[300:].float()).all()
+
+
+def test_nan_rows_stay_their_own(wst, big_ws):
+    # a NaN scale or value shows in its row only, also inside a shared token tile
+    qa, sa = operand(20, 256, "rows", E4, 13)
+    qb, sb = operand(128, 256, "blocks", E4, 14)
+    sa[1, 3] = torch.nan
+    u = qa.view(torch.uint8)
+    u[7, 9] = 0x7f
+    C = torch.empty(20, 128, device="cuda")
+    wst.wst_gemm_fp8(qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), C, workspace=big_ws)
+    nan = torch.isnan(C).all(1).cpu()
+    assert nan.nonzero().ravel().tolist() == [3, 7] and not torch.isnan(C[~nan]).any()
+
+
+def test_replayed_graphs_share_a_workspace(wst, big_ws):
+    # two captured split products with one workspace, replayed in turn, and the same bits every time
+    cases = []
+    for seed, (M, N, K) in enumerate([(16, 512, 4096), (7, 1024, 2048)]):
+        qa, sa = operand(M, K, "rows", E4, 20 + seed)
+        qb, sb = operand(N, K, "blocks", E4, 30 + seed)
+        args = (qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), torch.empty(M, N, device="cuda"))
+        wst.wst_gemm_fp8(*args, workspace=big_ws)
+        first = args[4].clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            wst.wst_gemm_fp8(*args, workspace=big_ws)
+        cases.append((graph, args, first))  # (the graph reads the inputs where they are)
+    for _ in range(20):
+        for graph, (*_, out), first in cases:
+            out.fill_(float("nan"))
+            graph.replay()
+            assert torch.equal(out, first)
+    assert wst.wst_sync_status(big_ws) == 0
+
+
+def test_training_products(wst, big_ws):
+    # forward, gradient of the inputs and of the weights, each by quantise and product
+    g = torch.Generator().manual_seed(3)
+    X, W, dY = (torch.randn(s, generator=g).bfloat16().cuda() for s in ((200, 320), (256, 320), (200, 256)))
+
+    def quant(x, mode, dtype=E4):
+        r, c = x.shape if mode in ("rows", "blocks") else x.shape[::-1]
+        q = torch.empty(r, -(-c // 16) * 16, dtype=dtype, device="cuda")[:, :c]
+        kb, rb = -(-c // 128), -(-r // 128)
+        s = torch.empty(*((kb, r) if mode in ("rows", "cols") else (rb, kb)), device="cuda")
+        wst.wst_quantize_fp8(x, q, s, mode=mode)
+        return q, s
+
+    for (a, ma), (b, mb), scaling in (((X, "rows"), (W, "blocks"), "blocks"), ((dY, "rows"), (W, "blocks_t"), "blocks"),
+                                      ((dY, "cols"), (X, "cols"), "rows")):
+        (qa, sa), (qb, sb) = quant(a, ma, E5 if a is dY else E4), quant(b, mb)
+        C = torch.empty(qa.shape[0], qb.shape[0], device="cuda")
+        wst.wst_gemm_fp8(qa, sa, qb, sb, C, scaling=scaling, workspace=big_ws)
+        want, size = product(qa, sa.cpu(), qb, sb.cpu(), scaling)
+        assert (abs(ref.f64(C) - want) <= bound(want, size, qa.shape[1], torch.float32)).all()
+        # against the unquantised product: half a step of each operand's 8 bits, value by value
+        va = ref.f64(a) if ma == "rows" else ref.f64(a).T
+        vb = ref.f64(b) if mb in ("rows", "blocks") else ref.f64(b).T
+        half = ref.half(qa.dtype) + ref.half(E4)
+        full = abs(va) @ abs(vb).T
+        assert (abs(ref.f64(C) - va @ vb.T) <= half * 1.1 * full + 2.0 ** -8 * full).all()

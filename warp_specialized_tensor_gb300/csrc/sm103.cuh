@@ -65,6 +65,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
                : "memory");
 }
 
+// The same without a cluster-scope release of memory (which costs a memory
+// barrier): for handing back tensor memory, whose reads are complete
+// (tcgen05.wait::ld) and ordered by tcgen05.fence::before_thread_sync.
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // One non-blocking-ish probe: true once the phase with parity `parity` has
 // completed.  (The hardware may suspend the thread for a short, bounded,
 // implementation-defined time before returning false.)
@@ -314,6 +321,20 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t adesc, uint6
         : "memory");
 }
 
+// The same for 8-bit floating-point operands (kind::f8f6f4, K = 32 per
+// instruction); their formats are in the instruction descriptor.
+template <int CG>
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  static_assert(CG == 2, "CTA pairs only");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive (once) on a CTA-local mbarrier when all previously issued tcgen05
 // operations of this thread have completed.
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
@@ -374,6 +395,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, b
          | ((b_mn ? 1u : 0u) << 16)      // B major-ness
          | ((uint32_t)(N >> 3) << 17)    // N / 8
          | ((uint32_t)(M >> 4) << 24);   // M / 16
+}
+
+// The same for kind::f8f6f4 with K-major operands of format 0 (e4m3) or 1
+// (e5m2), without the N field.
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int a_format, int b_format) {
+  return (1u << 4) | ((uint32_t)a_format << 7) | ((uint32_t)b_format << 10) | ((uint32_t)(M >> 4) << 24);
 }
 
 // ---------------------------------------------------------------------------

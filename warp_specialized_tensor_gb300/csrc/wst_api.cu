@@ -712,7 +712,8 @@ wst_status wst_sync_status(void* workspace, void* stream) {
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return (wst_status)cuda_fail(e, "reading the workspace error word");
   if (hdr[0] == 0) return WST_OK;
-  e = cudaMemsetAsync(workspace, 0, sizeof hdr, st);
+  // (the whole header: a call that gave up may have left its counters behind)
+  e = cudaMemsetAsync(workspace, 0, kWsHeaderBytes, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return (wst_status)cuda_fail(e, "clearing the workspace error word");
   set_error("device error %u (info 0x%08x)", hdr[0], hdr[1]);

@@ -18,6 +18,7 @@ __all__ = [
     "SCORE_SOFTMAX", "SCORE_SIGMOID", "E4M3", "E5M2", "FP8_ROWS", "FP8_COLS", "FP8_BLOCKS", "FP8_BLOCKS_T",
     "wst_moe_route", "wst_moe_route_backward", "wst_moe_plan", "wst_moe_plan_workspace_size", "moe_plan_workspace",
     "wst_moe_combine", "wst_moe_combine_backward", "wst_quantize_fp8", "wst_quantize_fp8_dispatch",
+    "wst_gemm_fp8", "wst_grouped_gemm_fp8", "wst_gemm_fp8_workspace_size", "gemm_fp8_workspace",
 ]
 
 # enums of include/wst.h
@@ -40,7 +41,10 @@ def declare(lib) -> None:
             ("wst_moe_combine", I, [I, I, I, P, L, I, I, P, P, P, L, I, P, P]),
             ("wst_moe_combine_backward", I, [I, I, I, P, L, I, P, L, I, I, P, P, P, L, P, P, P]),
             ("wst_quantize_fp8", I, [I, I, I, I, P, L, L, I, P, L, L, I, P, L, L, I, P]),
-            ("wst_quantize_fp8_dispatch", I, [I, I, I, P, L, I, P, I, P, L, I, P, L, I, P, P])):
+            ("wst_quantize_fp8_dispatch", I, [I, I, I, P, L, I, P, I, P, L, I, P, L, I, P, P]),
+            ("wst_gemm_fp8", I, [I, I, I, P, L, I, P, L, P, L, I, P, L, I, P, P, L, I, I, P, Z, P]),
+            ("wst_grouped_gemm_fp8", I, [I, I, I, I, P, L, I, P, L, P, L, L, I, P, L, L, I, P, P, L, P, L, I, I, P, Z, P]),
+            ("wst_gemm_fp8_workspace_size", Z, [])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
 
@@ -291,3 +295,86 @@ def wst_quantize_fp8_dispatch(x, position, q, scales, pow2=False, workspace=None
         T, K, position.shape[1], x.data_ptr(), ldx, _type(x, "x"), position.data_ptr(), rows, q.data_ptr(), ldq, _fp8(q, "q"),
         scales.data_ptr(), lds, int(bool(pow2)), ws, _w._stream_handle(stream))
     _w._check(st, "wst_quantize_fp8_dispatch")
+
+
+# ----------------------------------------------------------------------------
+# 8-bit products
+# ----------------------------------------------------------------------------
+def wst_gemm_fp8_workspace_size() -> int:
+    return int(_w.load_library().wst_gemm_fp8_workspace_size())
+
+
+def gemm_fp8_workspace(device=None, stream=None) -> torch.Tensor:
+    """A zero-filled workspace with which the 8-bit products can split their K
+    loops (products of few tiles); any workspace() works."""
+    ws = torch.empty(wst_gemm_fp8_workspace_size(), dtype=torch.uint8, device=device or "cuda")
+    _w.wst_workspace_init(ws, stream)
+    return ws
+
+
+def _fp8_operand(q, scale, name, scaling, dims):
+    """Checks an 8-bit operand and its scales; returns (ld, type, ld of the scales)."""
+    ld, ty, lds = _rows(q, name, dims), _fp8(q, name), _rows(scale, "the scales of " + name, dims)
+    if scale.dtype != torch.float32:
+        raise TypeError("the scales of %s must be float32" % name)
+    R, K = q.shape[-2:]
+    kb = -(-K // 128)
+    want = tuple(q.shape[:-2]) + ((kb, R) if scaling == FP8_ROWS else (-(-R // 128), kb))
+    if tuple(scale.shape) != want:
+        raise ValueError("the scales of %s must be %s, not %s" % (name, want, tuple(scale.shape)))
+    return ld, ty, lds
+
+
+def wst_gemm_fp8(A, scaleA, B, scaleB, C, scaling="blocks", bias=None, epi="none", workspace=None, stream=None) -> None:
+    """C = epi((A * scaleA) . (B * scaleB)^T (+ bias)) for 8-bit A and B.
+
+    A: float8_e4m3fn/e5m2 [M, K] with scaleA fp32 [ceil(K/128), M]; B: [N, K]
+    with scaleB [ceil(N/128), ceil(K/128)] (scaling "blocks") or
+    [ceil(K/128), N] ("rows"); C: bf16/fp32 [M, N]; bias: bf16 [N].  workspace:
+    gemm_fp8_workspace() lets products of few tiles use all SMs."""
+    mode = _MODES[scaling] if isinstance(scaling, str) else int(scaling)
+    lda, ta, ldsa = _fp8_operand(A, scaleA, "A", FP8_ROWS, (2,))
+    ldb, tb, ldsb = _fp8_operand(B, scaleB, "B", mode, (2,))
+    ldc = _rows(C, "C")
+    (M, K), N = A.shape, B.shape[0]
+    if B.shape[1] != K or tuple(C.shape) != (M, N):
+        raise ValueError("shape mismatch: A %s B %s C %s" % (tuple(A.shape), tuple(B.shape), tuple(C.shape)))
+    e = _w._epi(epi)
+    if e != _w.EPI_NONE:
+        _need(bias, "bias", torch.bfloat16, (1,))
+        if bias.numel() != N:
+            raise ValueError("bias must be [N]")
+    ws, n = _ws(workspace)
+    st = _w.load_library().wst_gemm_fp8(
+        M, N, K, A.data_ptr(), lda, ta, scaleA.data_ptr(), ldsa, B.data_ptr(), ldb, tb, scaleB.data_ptr(), ldsb, mode,
+        _w._ptr(bias) if e else None, C.data_ptr(), ldc, _type(C, "C"), e, ws, n, _w._stream_handle(stream))
+    _w._check(st, "wst_gemm_fp8")
+
+
+def wst_grouped_gemm_fp8(A, scaleA, B, scaleB, offsets, C, scaling="blocks", bias=None, epi="none", workspace=None,
+                         stream=None) -> None:
+    """Rows [off[g], off[g+1]) of C = epi(rows of A . B[g]^T (+ bias[g])) for 8-bit
+    A [M_total, K] and B [G, N, K]; scales as in wst_gemm_fp8, scaleB with a
+    group dimension; offsets: device int32 [G+1]; bias: bf16 [G, N].  Rows
+    behind offsets[G] are left as they were."""
+    mode = _MODES[scaling] if isinstance(scaling, str) else int(scaling)
+    lda, ta, ldsa = _fp8_operand(A, scaleA, "A", FP8_ROWS, (2,))
+    ldb, tb, ldsb = _fp8_operand(B, scaleB, "B", mode, (3,))
+    ldc = _rows(C, "C")
+    (M, K), (G, N, K2) = A.shape, B.shape
+    if K2 != K or tuple(C.shape) != (M, N):
+        raise ValueError("shape mismatch: A %s B %s C %s" % (tuple(A.shape), tuple(B.shape), tuple(C.shape)))
+    _ids(offsets, "offsets", (G + 1,))
+    e = _w._epi(epi)
+    sbias = 0
+    if e != _w.EPI_NONE:
+        _need(bias, "bias", torch.bfloat16, (2,))
+        if tuple(bias.shape) != (G, N):
+            raise ValueError("bias must be [G, N]")
+        sbias = bias.stride(0)
+    ws, n = _ws(workspace)
+    st = _w.load_library().wst_grouped_gemm_fp8(
+        G, M, N, K, A.data_ptr(), lda, ta, scaleA.data_ptr(), ldsa, B.data_ptr(), ldb, B.stride(0), tb, scaleB.data_ptr(), ldsb,
+        scaleB.stride(0), mode, offsets.data_ptr(), _w._ptr(bias) if e else None, sbias, C.data_ptr(), ldc, _type(C, "C"), e, ws,
+        n, _w._stream_handle(stream))
+    _w._check(st, "wst_grouped_gemm_fp8")
