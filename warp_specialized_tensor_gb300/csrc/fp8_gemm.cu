@@ -51,7 +51,7 @@ int launch_fp8(const F8Problem& pr, F8Args& a, const DeviceInfo& dev, cudaStream
     uint64_t str[1] = {(uint64_t)pr.ldc * es};
     uint32_t box[2] = {32, OUT_F32 ? 16u : 32u};
     if ((st = encode_map(&tmC, OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pr.C,
-                         dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE)))
+                         dims, str, box, OUT_F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)))
       return st;
   }
   if ((st = ensure_smem_attr((const void*)kern, kF8SmemBytes))) return st;

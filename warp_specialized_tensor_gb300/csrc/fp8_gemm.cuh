@@ -12,11 +12,25 @@
 // grouped GEMM: a ragged group wastes at most 15 token columns).  A K block of
 // 128 is one 128-byte swizzled row per operand and four MMAs; its unscaled
 // product goes to one of two tensor-memory accumulators, from where the epilogue
-// warps add it, scaled, to fp32 sums in registers while the tensor core fills
-// the other one.  Per K block a pair tile of 256 x 256 costs the tensor core
-// about 512 cycles, and each of the four sub-cores of an SM 256 tensor-memory
-// columns, 256 fused multiply-adds and 64 shared
-// loads of the token scales.
+// warps add it, scaled, to fp32 sums in registers while the tensor core fills the
+// other one.
+//
+// A thread of the epilogue holds 4 features x 32 token columns (the 16x256b form
+// of tcgen05.ld): a token scale is loaded from shared memory once for four
+// products, two columns are one packed multiply-add, and bf16 results leave
+// through transposing matrix stores.  (With one feature and 128 columns a thread,
+// the scales alone took 32 16-byte shared loads per warp and K block, 1024 cycles
+// of an SM's load path.)
+//
+// What bounds it: without the scaled sums the copies and products of 8192^3 take
+// 307 us (3586 TFLOP/s); with them 617 us, about 1350 cycles per K block of a
+// 256 x 256 tile, of which the epilogue's instruction stream (about 230 per warp
+// at two warps per sub-core, few of them independent) takes nearly all: a
+// barrier test takes about 200 cycles while products run even on a phase long
+// complete, so the issuer and the epilogue test their next barrier ahead of its
+// use.  Measured and dropped: two accumulators of 128 columns each per K block
+// (749 us; N = 128 products take the tensor core nearly as long as N = 256), four
+// epilogue warps per sub-core with 96 registers each (840 us, sums spilled).
 //
 // Roles per CTA (persistent, one CTA per SM, pairs in clusters of 2):
 //   warp 0     TMA producer: this CTA's 128 rows of B[g] and its half of the
@@ -24,10 +38,10 @@
 //              the leader's full[s].
 //   warp 1     MMA issuer (leader CTA only), kind::f8f6f4, M = 256.
 //   warp 2     tensor-memory allocation, offset check.
-//   warp 3     scales of each K block to shared memory: those of the tokens
-//              (4-byte loads: a group may start at any row), with 128 x 128
-//              weight scales already times the CTA's one weight scale.
-//   warps 4-11 epilogue: two warps per 32 features, each half of the tokens.
+//   warp 3     scales to shared memory, four K blocks at a time, in 4-byte
+//              asynchronous copies (a group may start at any row; loads through
+//              registers could not run far enough ahead).
+//   warps 4-11 epilogue: two warps per 32 features, one for each half of the tokens.
 //
 // Few tiles (short token tiles of a decoding step): when the tiles fill less
 // than half of the pairs, each tile's K blocks are split over several pairs;
@@ -51,12 +65,15 @@ constexpr int kF8WBytes = 128 * kF8BK;
 constexpr int kF8XBytes = 128 * kF8BK;
 constexpr int kF8StageBytes = kF8WBytes + kF8XBytes;
 constexpr int kF8ThinRows = 16;   // token rows per TMA box of a tile of at most 128 tokens
-constexpr int kF8ScaleStages = 8;
-constexpr int kF8StgBytes = 2048;  // 32 features x 32 tokens (bf16) or 16 tokens (fp32)
+constexpr int kF8ScaleBlocks = 4;  // K blocks per slot of scales
+constexpr int kF8ScaleStages = 3;
+constexpr int kF8ScaleFloats = kF8Tile + 128;  // of one K block: the tokens', the CTA's features'
+constexpr int kF8StgBytes = 2048;  // 32 features x 32 tokens (bf16) or 16 tokens (fp32), two per warp
+constexpr int kF8StgBufs = 2;
 constexpr int kF8TabMax = 256;
 constexpr int kF8WalkBytes = 128;  // an epilogue warp's place in the walk over the tiles
-constexpr size_t kF8SmemBytes = (size_t)kF8Stages * kF8StageBytes + kF8ScaleStages * kF8Tile * 4 +
-                                kF8EpiWarps * kF8StgBytes + 512 + kF8TabMax * 4 + kF8EpiWarps * kF8WalkBytes + 1024;
+constexpr size_t kF8SmemBytes = (size_t)kF8Stages * kF8StageBytes + kF8ScaleStages * kF8ScaleBlocks * kF8ScaleFloats * 4 +
+                                kF8EpiWarps * kF8StgBufs * kF8StgBytes + 512 + kF8TabMax * 4 + kF8EpiWarps * kF8WalkBytes + 1024;
 static_assert(kF8SmemBytes <= 232448, "shared memory per CTA");
 // Workspace: header (its padding holds one counter per split tile, 0 between
 // calls, one half of it for each CTA of the pair) | one slot of fp32 sums per
@@ -88,18 +105,31 @@ struct F8Args {
   unsigned long long timeout_ns;
 };
 
-// Splits of each tile's K loop: as many as keep every unit on a pair of its own.
-__host__ __device__ inline int f8_splits(long long tiles, int pairs, int k_blocks, int max_units) {
+// Splits of each tile's K loop: no more than keep every unit on a pair of its
+// own, and no more than pay.  A K block costs a pair about 0.3 us, adding up one
+// split's sums about 0.3 us and 1.1 us more for 256 token columns, so s splits
+// of k blocks take about 0.3 (k / s + s (1 + width / 64)) us, least at
+// s = sqrt(k / (1 + width / 64)).
+__host__ __device__ inline int f8_splits(long long tiles, int pairs, int k_blocks, int max_units, int M) {
   const int room = pairs < max_units ? pairs : max_units;
   if (tiles <= 0 || tiles > room) return 1;
-  int s = room / (int)tiles;
-  if (s > k_blocks / 4) s = k_blocks / 4;  // at least four K blocks each
-  return s < 2 ? 1 : s;
+  const int most = room / (int)tiles;
+  const int width = M < kF8Tile ? M : kF8Tile;
+  int s = 1;
+  while (s < most && (s + 1) * (s + 1) * (64 + width) <= 64 * k_blocks) ++s;
+  return s;
 }
 
 struct F8Tile {
   int g, t0, nt, nmma, n0;
 };
+// The epilogue's two warps per 32 features take the first f8_half0 token columns
+// and the rest.
+__device__ __forceinline__ int f8_half0(int nmma) { return ((nmma >> 4) + 1) / 2 * 16; }
+__device__ __forceinline__ int f8_token(int nmma, int half, int c) { return half ? f8_half0(nmma) + c : c; }
+// Where the scale of column c lies among its half's 128: the columns
+// 8 j + 2 q + {0, 1} and 8 (j + 1) + 2 q + {0, 1} of a thread are one 16-byte word.
+__device__ __forceinline__ int f8_scale_at(int c) { return (c & ~15) | ((c & 6) << 1) | ((c & 8) >> 2) | (c & 1); }
 
 // Walks the groups in order; offsets are clamped into [0, M_total].
 struct F8Walker {
@@ -215,10 +245,32 @@ struct F8Place {
 };
 static_assert(sizeof(F8Place) <= kF8WalkBytes, "walk bytes");
 
-// Sixteen fp32 columns of this thread's TMEM lane, valid after tmem_wait_ld.
-__device__ __forceinline__ void tmem_load16_async(uint32_t taddr, uint32_t (&r)[16]) {
+// (a0, a1) += (s0, s1) * (v0, v1) in one packed instruction.
+__device__ __forceinline__ void f8_fma2(float& a0, float& a1, float s0, float s1, uint32_t v0, uint32_t v1) {
+  asm("{\n\t.reg .b64 a, s, v;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\t"
+      "fma.rn.f32x2 a, s, v, a;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(s0), "f"(s1), "r"(v0), "r"(v1));
+}
+
+// (a0, a1) *= w.
+__device__ __forceinline__ void f8_mul2(float& a0, float& a1, float w) {
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(w));
+}
+
+// 32 fp32 columns of 16 TMEM lanes, valid after tmem_wait_ld: thread t gets, for
+// j < 4, r[4j], r[4j+1] = lane t/4, columns 8j + 2(t%4) + {0, 1} and
+// r[4j+2], r[4j+3] = lane t/4 + 8, the same columns.
+__device__ __forceinline__ void tmem_load_16x32_async(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
@@ -227,11 +279,21 @@ __device__ __forceinline__ void tmem_load16_async(uint32_t taddr, uint32_t (&r)[
 }
 // Waits for this thread's tensor-memory loads; naming the registers keeps
 // their uses behind the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&a)[16], uint32_t (&b)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
+                 "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]),
+                 "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15])
                :
+               : "memory");
+}
+// Four 8 x 8 matrices of bf16 in the layout of tmem_load_16x32_async (a register
+// holds two columns of one row), stored transposed: lane i gives the address of
+// 16-byte row i % 8 of matrix i / 8.
+__device__ __forceinline__ void st_matrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
                : "memory");
 }
 
@@ -274,8 +336,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   uint8_t* smW = smem;
   uint8_t* smX = smW + kF8Stages * kF8WBytes;
   float* smS = reinterpret_cast<float*>(smX + kF8Stages * kF8XBytes);
-  uint8_t* smStg = reinterpret_cast<uint8_t*>(smS + kF8ScaleStages * kF8Tile);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smStg + kF8EpiWarps * kF8StgBytes);
+  uint8_t* smStg = reinterpret_cast<uint8_t*>(smS + kF8ScaleStages * kF8ScaleBlocks * kF8ScaleFloats);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smStg + kF8EpiWarps * kF8StgBufs * kF8StgBytes);
   // bars: full[S] | empty[S] | acc_full[2] | acc_empty[2] | scale_full[SS] | scale_empty[SS]
   constexpr int kNumBars = 2 * kF8Stages + 4 + 2 * kF8ScaleStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
@@ -308,7 +370,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       mbar_init(acce_bar(a), 2 * kF8EpiWarps);
     }
     for (int s = 0; s < kF8ScaleStages; ++s) {
-      mbar_init(scf_bar(s), 1);
+      mbar_init(scf_bar(s), 32);
       mbar_init(sce_bar(s), kF8EpiWarps);
     }
     *abort_flag = 0u;
@@ -326,7 +388,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     for (int i = (int)lane; i <= p.G; i += 32) off_tab[i] = __ldg(p.offsets + i);
   }
   const long long total = f8_total_tiles(p);  // every warp counts for itself
-  const int splits = f8_splits(total, p.pairs, p.k_blocks, p.max_units);
+  const int splits = f8_splits(total, p.pairs, p.k_blocks, p.max_units, p.M_total);
   tc_fence_before_sync();
   __syncthreads();
   cluster_sync();
@@ -340,131 +402,141 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   // 384 threads of 168 registers: the four role warps give some of theirs to the
   // eight epilogue warps (128 * 72 + 256 * 216 = 64512 = 384 * 168).
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp == 0) {
-    // ------------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      // ------------------------------------------------------------------ producer
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (long long u = pair_id; ok && units.get(p, u, un); u += num_pairs) {
+          const F8Tile& tl = un.tile;
+          const int w_row = tl.n0 + (int)rank * 128;
+          const int x_rows = tl.nmma >> 1;  // token rows this CTA holds
+          const int x_row = tl.t0 + (int)rank * x_rows;
+          const bool thin = x_rows <= 64;
+          const int boxes = thin ? (x_rows + kF8ThinRows - 1) / kF8ThinRows : 1;
+          const uint32_t tx = 2u * (uint32_t)(kF8WBytes + (thin ? boxes * kF8ThinRows * kF8BK : kF8XBytes));
+          for (int kb = un.k0; kb < un.k1; ++kb) {
+            if (!f8_wait<true>(guard, empty_bar(stage), phase ^ 1u, (kRoleProducer << 16) | stage)) {
+              ok = false;
+              break;
+            }
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), tx);
+            const uint32_t fb = map_to_cta(full_bar(stage), 0);
+            const int kx = kb * kF8BK;
+            tma_load_3d_pair(smem_addr(smW + stage * kF8WBytes), &tmW, fb, kx, w_row, p.w_shared ? 0 : tl.g);
+            const uint32_t xdst = smem_addr(smX + stage * kF8XBytes);
+            if (thin) {
+              for (int i = 0; i < boxes; ++i)
+                tma_load_2d_pair(xdst + i * kF8ThinRows * kF8BK, &tmXt, fb, kx, x_row + i * kF8ThinRows);
+            } else {
+              tma_load_2d_pair(xdst, &tmX, fb, kx, x_row);
+            }
+            if (++stage == kF8Stages) { stage = 0; phase ^= 1u; }
+          }
+        }
+        for (int i = 0; i < kF8Stages && ok; ++i) {
+          ok = f8_wait<true>(guard, empty_bar(stage), phase ^ 1u, (kRoleProducer << 16) | 0x100 | stage);
+          if (++stage == kF8Stages) { stage = 0; phase ^= 1u; }
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------ MMA issuer (leader)
+      if (lane == 0 && rank == 0) {
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool full_ok = false, acc_ok = false;  // the next barriers have been seen complete
+        bool ok = true;
+        for (long long u = pair_id; ok && units.get(p, u, un); u += num_pairs) {
+          const uint32_t idesc = p.idesc | ((uint32_t)(un.tile.nmma >> 3) << 17);
+          for (int kb = un.k0; kb < un.k1; ++kb) {
+            ok = (full_ok || f8_wait<false>(guard, full_bar(stage), phase, (kRoleMma << 16) | stage)) &&
+                 (acc_ok || f8_wait<false>(guard, acce_bar(acc), acc_phase ^ 1u, (kRoleMma << 16) | 0x100 | acc));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t wBase = smem_addr(smW + stage * kF8WBytes);
+            const uint32_t xBase = smem_addr(smX + stage * kF8XBytes);
+            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kF8Tile);
+            const uint32_t this_empty = empty_bar(stage), this_acc = accf_bar(acc);
+            if (++stage == kF8Stages) { stage = 0; phase ^= 1u; }
+            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+            // (a failed test costs nothing: the wait above repeats it)
+            full_ok = mbar_test_wait(full_bar(stage), phase);
+            acc_ok = mbar_test_wait(acce_bar(acc), acc_phase ^ 1u);
+  #pragma unroll
+            for (int k = 0; k < kF8BK / 32; ++k)
+              umma_f8<2>(d_tmem, sdesc_sw128(wBase + k * 32, 16, 1024), sdesc_sw128(xBase + k * 32, 16, 1024), idesc,
+                         k != 0 ? 1u : 0u);
+            umma_commit_pair(this_acc, 0x3);
+            umma_commit_pair(this_empty, 0x3);
+          }
+        }
+      }
+    } else if (warp == 2) {
+      if (lane == 0 && blockIdx.x == 0 && p.offsets) f8_check_offsets(p.offsets, p.G, p.M_total, p.ws);
+    } else if (warp == 3) {
+      // ------------------------------------------------------------------ scales
+      auto copy4 = [](uint32_t dst, const float* src, bool in) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+      };
+      int slot = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (long long u = pair_id; ok && units.get(p, u, un); u += num_pairs) {
         const F8Tile& tl = un.tile;
-        const int w_row = tl.n0 + (int)rank * 128;
-        const int x_rows = tl.nmma >> 1;  // token rows this CTA holds
-        const int x_row = tl.t0 + (int)rank * x_rows;
-        const bool thin = x_rows <= 64;
-        const int boxes = thin ? (x_rows + kF8ThinRows - 1) / kF8ThinRows : 1;
-        const uint32_t tx = 2u * (uint32_t)(kF8WBytes + (thin ? boxes * kF8ThinRows * kF8BK : kF8XBytes));
-        for (int kb = un.k0; kb < un.k1; ++kb) {
-          if (!f8_wait<true>(guard, empty_bar(stage), phase ^ 1u, (kRoleProducer << 16) | stage)) {
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), tx);
-          const uint32_t fb = map_to_cta(full_bar(stage), 0);
-          const int kx = kb * kF8BK;
-          tma_load_3d_pair(smem_addr(smW + stage * kF8WBytes), &tmW, fb, kx, w_row, p.w_shared ? 0 : tl.g);
-          const uint32_t xdst = smem_addr(smX + stage * kF8XBytes);
-          if (thin) {
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d_pair(xdst + i * kF8ThinRows * kF8BK, &tmXt, fb, kx, x_row + i * kF8ThinRows);
-          } else {
-            tma_load_2d_pair(xdst, &tmX, fb, kx, x_row);
-          }
-          if (++stage == kF8Stages) { stage = 0; phase ^= 1u; }
+        // 128 x 128 scales: this CTA's features share one per K block.
+        const int f0 = tl.n0 + (int)rank * 128;
+        const float* sb = p.sb + (long long)tl.g * p.strideSB +
+                          (SB_ROWS ? 0 : (long long)(min(f0, p.N - 1) >> 7) * p.ldsb);
+        const float* sa = p.sa + tl.t0;
+        int tok[8];
+  #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = (i & 3) * 32 + (int)lane, n0 = f8_half0(tl.nmma);
+          tok[i] = c < (i < 4 ? n0 : tl.nmma - n0) ? f8_token(tl.nmma, i >> 2, c) : kF8Tile;
         }
-      }
-      for (int i = 0; i < kF8Stages && ok; ++i) {
-        ok = f8_wait<true>(guard, empty_bar(stage), phase ^ 1u, (kRoleProducer << 16) | 0x100 | stage);
-        if (++stage == kF8Stages) { stage = 0; phase ^= 1u; }
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer (leader)
-    if (lane == 0 && rank == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      bool ok = true;
-      for (long long u = pair_id; ok && units.get(p, u, un); u += num_pairs) {
-        const uint32_t idesc = p.idesc | ((uint32_t)(un.tile.nmma >> 3) << 17);
-        for (int kb = un.k0; kb < un.k1; ++kb) {
-          ok = f8_wait<true>(guard, acce_bar(acc), acc_phase ^ 1u, (kRoleMma << 16) | 0x100 | acc) &&
-               f8_wait<false>(guard, full_bar(stage), phase, (kRoleMma << 16) | stage);
+        for (int kb = un.k0; ok && kb < un.k1; kb += kF8ScaleBlocks) {
+          ok = f8_wait<false>(guard, sce_bar(slot), phase ^ 1u, (kRoleProducer << 16) | 0x200 | slot);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          tc_fence_after_sync();
-          const uint32_t wBase = smem_addr(smW + stage * kF8WBytes);
-          const uint32_t xBase = smem_addr(smX + stage * kF8XBytes);
-          const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kF8Tile);
-#pragma unroll
-          for (int k = 0; k < kF8BK / 32; ++k)
-            umma_f8<2>(d_tmem, sdesc_sw128(wBase + k * 32, 16, 1024), sdesc_sw128(xBase + k * 32, 16, 1024), idesc,
-                       k != 0 ? 1u : 0u);
-          umma_commit_pair(empty_bar(stage), 0x3);
-          umma_commit_pair(accf_bar(acc), 0x3);
-          if (++stage == kF8Stages) { stage = 0; phase ^= 1u; }
-          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
-        }
-      }
-    }
-  } else if (warp == 2) {
-    if (lane == 0 && blockIdx.x == 0 && p.offsets) f8_check_offsets(p.offsets, p.G, p.M_total, p.ws);
-  } else if (warp == 3) {
-    // ------------------------------------------------------------------ scales
-    int slot = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (long long u = pair_id; ok && units.get(p, u, un); u += num_pairs) {
-      const F8Tile& tl = un.tile;
-      // 128 x 128 scales: this CTA's features share one per K block.
-      const int block = min(tl.n0 + (int)rank * 128, p.N - 1) >> 7;
-      const float* sb = p.sb + (long long)tl.g * p.strideSB + (long long)block * p.ldsb;
-      const float* sa = p.sa + tl.t0 + lane;
-      // The loads run kAhead blocks ahead of the stores.
-      constexpr int kAhead = 4;
-      float v[kAhead][8], w[kAhead];
-      auto load = [&](int kb, float (&x)[8], float& y) {
-        const bool in = kb < un.k1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          // columns past the group's rows get 0
-          x[i] = in && i * 32 + (int)lane < tl.nt ? __ldg(sa + (long long)kb * p.ldsa + i * 32) : 0.0f;
-        y = !SB_ROWS && in ? __ldg(sb + kb) : 1.0f;
-      };
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) load(un.k0 + i, v[i], w[i]);
-      for (int kb0 = un.k0; ok && kb0 < un.k1; kb0 += kAhead) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          if (kb0 + i < un.k1 && ok) {
-            ok = f8_wait<false>(guard, sce_bar(slot), phase ^ 1u, (kRoleProducer << 16) | 0x200 | slot);
-            if (ok) {
-              float* dst = smS + slot * kF8Tile + lane;
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (j * 32 < tl.nmma) dst[j * 32] = v[i][j] * w[i];
+  #pragma unroll
+          for (int k = 0; k < kF8ScaleBlocks; ++k) {
+            if (kb + k >= un.k1) continue;
+            const uint32_t dst = smem_addr(smS + (slot * kF8ScaleBlocks + k) * kF8ScaleFloats);
+            const float* src = sa + (long long)(kb + k) * p.ldsa;
+            // (columns past the group's rows get 0)
+  #pragma unroll
+            for (int i = 0; i < 8; ++i)
+              copy4(dst + 4u * (i * 32 + f8_scale_at((int)lane)), src + (tok[i] < tl.nt ? tok[i] : 0), tok[i] < tl.nt);
+            if constexpr (SB_ROWS) {
+  #pragma unroll
+              for (int i = 0; i < 4; ++i)
+                copy4(dst + 4u * (kF8Tile + i * 32 + lane),
+                      sb + (long long)(kb + k) * p.ldsb + min(f0 + i * 32 + (int)lane, p.N - 1), true);
+            } else {
+              if (lane == 0) copy4(dst + 4u * kF8Tile, sb + kb + k, true);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(scf_bar(slot));
-            if (++slot == kF8ScaleStages) { slot = 0; phase ^= 1u; }
-            load(kb0 + i + kAhead, v[i], w[i]);
           }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(scf_bar(slot)) : "memory");
+          if (++slot == kF8ScaleStages) { slot = 0; phase ^= 1u; }
         }
-        ok = __all_sync(0xffffffffu, ok);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
-  }
   } else {
     // ------------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int q = warp & 3, part = (warp - 4) >> 2;
-    const uint32_t stg = smem_addr(smStg + (warp - 4) * kF8StgBytes);
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t stg0 = smem_addr(smStg + (warp - 4) * kF8StgBufs * kF8StgBytes);
+    const int row = (int)lane >> 2, cq = (int)lane & 3;  // this thread's features row + 8 i and columns 8 j + 2 cq + {0, 1}
     int acc = 0;
     uint32_t acc_phase = 0;
     int slot = 0;
     uint32_t sc_phase = 0;
+    int sbuf = 0;
     bool ok = true;
+    bool acc_ok = false, sc_ok = false;  // the next accumulator, scales have been seen complete
     F8Place* place = reinterpret_cast<F8Place*>(reinterpret_cast<uint8_t*>(off_tab + kF8TabMax) + (warp - 4) * kF8WalkBytes);
     if (lane == 0) place->units.init(p, tab, total, splits);
     for (long long u = pair_id; ok; u += num_pairs) {
@@ -472,89 +544,155 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       if (lane == 0) place->more = place->units.get(p, u, place->unit) ? 1 : 0;
       __syncwarp();
       if (!place->more) break;
-      const F8Unit un = place->unit;
-      const F8Tile tl = un.tile;
-      // This warp's 32 features and its share of the token columns.
-      const int n_base = tl.n0 + (int)rank * 128 + q * 32;
-      const int n_lane = min(n_base + (int)lane, p.N - 1);
-      const int share = ((tl.nmma >> 4) + kF8Parts - 1) / kF8Parts * 16;
-      const int c_lo = part * share;
-      const int c_n = max(0, min(share, tl.nmma - c_lo));
-      const float* sb = p.sb + (long long)tl.g * p.strideSB + n_lane;
-      float sb_next = SB_ROWS ? __ldg(sb + un.k0 * p.ldsb) : 1.0f;
-      float sum[kF8PartCols];
+      // (Read again where they are needed: the loop below has no registers left.)
+      const volatile F8Unit& un = place->unit;
+      const volatile F8Tile& tl = un.tile;
+      // This warp's half of the token columns.
+      const int c_n = half ? tl.nmma - f8_half0(tl.nmma) : f8_half0(tl.nmma);
+      const uint32_t t_warp = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(half ? f8_half0(tl.nmma) : 0);
+      int left = un.k1 - un.k0, kk = 0;
+      // sum[h][j][i]: features row + 16 h + 8 (i / 2), columns 8 j + 2 cq + i % 2
+      float sum[2][16][4];
 #pragma unroll
-      for (int i = 0; i < kF8PartCols; ++i) sum[i] = 0.0f;
-      for (int kb = un.k0; kb < un.k1; ++kb) {
-        const float w = sb_next;
-        if (SB_ROWS && kb + 1 < un.k1) sb_next = __ldg(sb + (kb + 1) * p.ldsb);
-        ok = f8_wait<false>(guard, scf_bar(slot), sc_phase, (kRoleEpilogue << 16) | 0x200 | slot) &&
-             f8_wait<false>(guard, accf_bar(acc), acc_phase, (kRoleEpilogue << 16) | acc);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after_sync();
-        const uint32_t xs = smem_addr(smS + slot * kF8Tile + c_lo);
-        const uint32_t t_lane = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kF8Tile + c_lo);
-        auto add = [&](int c, const uint32_t (&r)[16]) {
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float4 s;
+        for (int j = 0; j < 16; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[h][j][i] = 0.0f;
+#pragma unroll 1
+      for (; left > 0; --left) {
+        if (kk == 0 && !__all_sync(0xffffffffu, sc_ok)) {
+          ok = f8_wait<false>(guard, scf_bar(slot), sc_phase, (kRoleEpilogue << 16) | 0x200 | slot);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        const uint32_t sc = smem_addr(smS + (slot * kF8ScaleBlocks + kk) * kF8ScaleFloats);
+        float w[SB_ROWS ? 4 : 1];
+#pragma unroll
+        for (int i = 0; i < (SB_ROWS ? 4 : 1); ++i)
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(sc + (kF8Tile + (SB_ROWS ? q * 32 + row + 8 * i : 0)) * 4u));
+        // This thread's scales of 64 columns.
+        float s[4][4];
+        auto load_scales = [&](int c64) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
             asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(s.x), "=f"(s.y), "=f"(s.z), "=f"(s.w)
-                         : "r"(xs + c * 64 + i * 16));
-            if constexpr (SB_ROWS) {
-              s.x *= w;
-              s.y *= w;
-              s.z *= w;
-              s.w *= w;
+                         : "=f"(s[i][0]), "=f"(s[i][1]), "=f"(s[i][2]), "=f"(s[i][3])
+                         : "r"(sc + (half * kF8PartCols + c64 * 64 + i * 16 + cq * 4) * 4u));
+        };
+        auto mul_scales = [&]() {
+          if constexpr (!SB_ROWS) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f8_mul2(s[i][0], s[i][1], w[0]);
+              f8_mul2(s[i][2], s[i][3], w[0]);
             }
-            float* a = sum + c * 16 + i * 4;
-            a[0] = fmaf(s.x, __uint_as_float(r[4 * i]), a[0]);
-            a[1] = fmaf(s.y, __uint_as_float(r[4 * i + 1]), a[1]);
-            a[2] = fmaf(s.z, __uint_as_float(r[4 * i + 2]), a[2]);
-            a[3] = fmaf(s.w, __uint_as_float(r[4 * i + 3]), a[3]);
           }
         };
-        // Sixteen columns are added while the next sixteen load.
-        uint32_t r0[16], r1[16];
-        if (c_n == kF8PartCols) {
-          tmem_load16_async(t_lane, r0);
+        load_scales(0);
+        uint32_t r0[16], r1[16] = {};
+        const uint32_t t_lane = t_warp + (uint32_t)(acc * kF8Tile);
+        // Step k: columns 32 (k / 2) .., features 16 (k % 2) ..
+        auto fetch = [&](int k, uint32_t (&r)[16]) {
+          tmem_load_16x32_async(t_lane + ((uint32_t)(k & 1) << 20) + (k >> 1) * 32, r);
+        };
+        if (!__all_sync(0xffffffffu, acc_ok)) {
+          ok = f8_wait<false>(guard, accf_bar(acc), acc_phase, (kRoleEpilogue << 16) | acc);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        tc_fence_after_sync();
+        if (c_n > 0) fetch(0, r0);
+        if (c_n == kF8PartCols) fetch(1, r1);
+        mul_scales();
+        auto add = [&](int k, const uint32_t (&r)[16]) {
+          const int c = k >> 1, h = k & 1;
 #pragma unroll
-          for (int c = 0; c < kF8PartCols / 16; c += 2) {
-            tmem_wait_ld(r0);
-            tmem_load16_async(t_lane + c * 16 + 16, r1);
-            add(c, r0);
-            tmem_wait_ld(r1);
-            if (c + 2 < kF8PartCols / 16) tmem_load16_async(t_lane + c * 16 + 32, r0);
-            add(c + 1, r1);
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              float* a = sum[h][c * 4 + j] + i;
+              float s0 = s[(c & 1) * 2 + j / 2][2 * (j & 1)], s1 = s[(c & 1) * 2 + j / 2][2 * (j & 1) + 1];
+              if constexpr (SB_ROWS) {
+                s0 *= w[2 * h + i / 2];
+                s1 *= w[2 * h + i / 2];
+              }
+              f8_fma2(a[0], a[1], s0, s1, r[4 * j + i], r[4 * j + i + 1]);
+            }
+        };
+        // One step is added while the next one loads.  The next accumulator's
+        // barrier is tested (which takes long) ahead of its use.
+        const int next_acc = acc ^ 1;
+        auto test_next = [&]() {
+          acc_ok = mbar_test_wait(accf_bar(next_acc), acc_phase ^ (next_acc == 0 ? 1u : 0u));
+          if (kk == kF8ScaleBlocks - 1 || left == 1) {
+            const int n = slot + 1 == kF8ScaleStages ? 0 : slot + 1;
+            sc_ok = mbar_test_wait(scf_bar(n), sc_phase ^ (n == 0 ? 1u : 0u));
+          }
+        };
+        // Hands the accumulator back: every lane's loads are complete.
+        auto release = [&]() {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_tmem(map_to_cta(acce_bar(acc), 0));
+        };
+        if (c_n == kF8PartCols) {
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            tmem_wait_ld(r0, r1);
+            add(k, r0);
+            if (k + 2 < 8) fetch(k + 2, r0);
+            else release();
+            add(k + 1, r1);
+            if (k + 2 < 8) fetch(k + 3, r1);
+            if (k == 2) {
+              load_scales(1);
+              mul_scales();
+            }
+            if (k == 4) test_next();
           }
         } else {
+          // (columns behind c_n, up to 16 of them, are loaded and added too; they
+          // lie inside the accumulators and are not stored)
 #pragma unroll
-          for (int c = 0; c < kF8PartCols / 16; ++c)
-            if (c * 16 < c_n) {
-              tmem_load16_async(t_lane + c * 16, r0);
-              tmem_wait_ld(r0);
-              add(c, r0);
+          for (int k = 0; k < 8; ++k)
+            if ((k >> 1) * 32 < c_n) {
+              if (k == 4) {
+                load_scales(1);
+                mul_scales();
+              }
+              if (k > 0) fetch(k, r0);
+              tmem_wait_ld(r0, r1);
+              add(k, r0);
             }
+          test_next();
+          release();
         }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_tmem(map_to_cta(acce_bar(acc), 0));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sce_bar(slot));
+        if (++kk == kF8ScaleBlocks || left == 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sce_bar(slot));
+          kk = 0;
+          if (++slot == kF8ScaleStages) { slot = 0; sc_phase ^= 1u; }
+        }
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
-        if (++slot == kF8ScaleStages) { slot = 0; sc_phase ^= 1u; }
       }
+
+      const int n_base = tl.n0 + (int)rank * 128 + q * 32;
       if (un.split >= 0) {
-        // Store the sums, [token column][128 features], and count in.  (A pair
-        // has one split unit at most; a warp that gave up waiting still takes
-        // part in the barriers, and nothing is counted then.)
-        float* slots = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.ws) + kWsHeaderBytes);
+        // Store the sums, 128 of each of the epilogue's threads, and count in.
+        // (A warp that gave up waiting still takes part in the barriers, and
+        // nothing is counted then.)
+        float* slots = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.ws) + kWsHeaderBytes) + (threadIdx.x - 128);
         const long long first = un.index * splits;
-        float* mine = slots + ((first + un.split) * 2 + rank) * kF8SlotFloats + q * 32 + lane;
+        float* mine = slots + ((first + un.split) * 2 + rank) * kF8SlotFloats;
 #pragma unroll
-        for (int i = 0; i < kF8PartCols; ++i)
-          if (i < c_n) __stcg(mine + (long long)(c_lo + i) * 128, sum[i]);
+        for (int j = 0; j < 16; ++j)
+          if (j * 8 < c_n) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) __stcg(mine + ((j * 2 + h) * 4 + i) * (32 * kF8EpiWarps), sum[h][j][i]);
+          }
         __threadfence();
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kF8EpiWarps) : "memory");
         if (warp == 4 && lane == 0) {
@@ -571,79 +709,121 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         if (!ok) break;
         if (!*last_flag) continue;
         __threadfence();
-        const float* parts = slots + (first * 2 + rank) * kF8SlotFloats + q * 32 + lane;
+        const float* parts = slots + (first * 2 + rank) * kF8SlotFloats;
 #pragma unroll
-        for (int i = 0; i < kF8PartCols; ++i) sum[i] = 0.0f;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[h][j][i] = 0.0f;
 #pragma unroll 1
         for (int s = 0; s < splits; ++s, parts += 2 * kF8SlotFloats) {
-          // (sixteen loads in flight)
+          // (thirty-two loads in flight)
 #pragma unroll
-          for (int c = 0; c < kF8PartCols / 16; ++c) {
-            if (c * 16 < c_n) {
-              float v[16];
+          for (int j0 = 0; j0 < 16; j0 += 4)
+            if (j0 * 8 < c_n) {
+              float v[4][2][4];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = __ldcg(parts + (c_lo + c * 16 + i) * 128);
+              for (int j = 0; j < 4; ++j)
+                if ((j0 + j) * 8 < c_n) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) sum[c * 16 + i] += v[i];
+                  for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                      v[j][h][i] = __ldcg(parts + (((j0 + j) * 2 + h) * 4 + i) * (32 * kF8EpiWarps));
+                }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if ((j0 + j) * 8 < c_n) {
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[h][j0 + j][i] += v[j][h][i];
+                }
             }
-          }
         }
       }
       if (!ok) break;
-      float bias_v = 0.0f;
-      if (EPI && n_base + (int)lane < p.N) bias_v = __bfloat162float(p.bias[(long long)tl.g * p.bias_stride + n_lane]);
-      constexpr int kTok = OUT_F32 ? 16 : 32;  // tokens per staged block
+
+      if constexpr (EPI) {
+        float bias[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = n_base + row + 8 * i;
+          bias[i] = n < p.N ? __bfloat162float(p.bias[(long long)tl.g * p.bias_stride + n]) : 0.0f;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[h][j][i] = f8_act(p.epi, sum[h][j][i] + bias[2 * h + i / 2]);
+      }
+      constexpr int kTok = OUT_F32 ? 16 : 32;  // tokens per staged block of [token][32 features]
+      const bool whole = tl.nt == kF8Tile && n_base + 32 <= p.N;
 #pragma unroll
       for (int c = 0; c < kF8PartCols / kTok; ++c) {
         if (c * kTok < c_n) {
-          const int width = min(kTok, c_n - c * kTok);
-          const int col = c_lo + c * kTok;
-          if (lane == 0) bulk_wait_group_read<0>();
+          const uint32_t stg = stg0 + sbuf * kF8StgBytes;
+          // The stores that read this buffer (all but the newest) are done with it.
+          if (lane == 0) bulk_wait_group_read<kF8StgBufs - 1>();
           __syncwarp();
-          // Transpose: lane (feature) writes column `lane` of the [token][feature] block.
+          // 16-byte words of a row are swizzled as the tensor map says, which
+          // also keeps these stores free of bank conflicts.
+          if constexpr (OUT_F32) {
 #pragma unroll
-          for (int j = 0; j < kTok; ++j) {
-            if (j < width) {
-              float v = sum[c * kTok + j];
-              if constexpr (EPI) v = f8_act(p.epi, v + bias_v);
-              if constexpr (OUT_F32) {
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(stg + j * 128u + lane * 4u), "f"(v) : "memory");
-              } else {
-                const __nv_bfloat16 h = __float2bfloat16_rn(v);
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(stg + j * 64u + lane * 2u),
-                             "h"(*reinterpret_cast<const unsigned short*>(&h)) : "memory");
-              }
+            for (int j = 0; j < kTok / 8; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int tok = j * 8 + 2 * cq + (i & 1), f = row + 16 * h + 8 * (i >> 1);
+                  asm volatile("st.shared.f32 [%0], %1;" ::"r"(stg + tok * 128u + (((f >> 2) ^ (tok & 7)) * 16u) + (f & 3) * 4u),
+                               "f"(sum[h][c * 2 + j][i])
+                               : "memory");
+                }
+          } else {
+            const int tok = (int)lane & 7, m = (int)lane >> 3;  // the row this lane addresses
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float(&s0)[4] = sum[0][c * 4 + j];
+              const float(&s1)[4] = sum[1][c * 4 + j];
+              st_matrix4_trans(stg + (j * 8 + tok) * 64u + ((m ^ ((tok >> 1) & 3)) * 16u), pack_bf16x2(s0[0], s0[1]),
+                               pack_bf16x2(s0[2], s0[3]), pack_bf16x2(s1[0], s1[1]), pack_bf16x2(s1[2], s1[3]));
             }
           }
-          if (col + kTok <= tl.nt && width == kTok && n_base + 32 <= p.N) {
+          if (whole) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&tmC, stg, n_base, tl.t0 + col);
+              tma_store_2d(&tmC, stg, n_base, tl.t0 + f8_token(kF8Tile, half, c * kTok));
               bulk_commit_group();
             }
+            sbuf = sbuf + 1 == kF8StgBufs ? 0 : sbuf + 1;
             continue;
           }
           __syncwarp();
-          // The group's last tokens or the last features: masked stores of row segments.
+          // A group's last tokens or the last features: masked stores of row segments.
           constexpr int kSegs = OUT_F32 ? 8 : 4;
           constexpr int kElems = OUT_F32 ? 4 : 8;
           const int seg = (int)lane % kSegs;
           const int ncol = n_base + seg * kElems;
 #pragma unroll
           for (int pass = 0; pass < kTok * kSegs / 32; ++pass) {
-            const int row = (int)lane / kSegs + pass * (32 / kSegs);
-            uint4 w;
+            const int r = (int)lane / kSegs + pass * (32 / kSegs);  // column of the block
+            uint4 v;
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                         : "r"(stg + row * (OUT_F32 ? 128u : 64u) + seg * 16u));
-            if (row < width && col + row < tl.nt && ncol < p.N) {
-              const long long off = (long long)(tl.t0 + col + row) * p.ldc + ncol;
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(OUT_F32 ? stg + r * 128u + ((seg ^ (r & 7)) * 16u)
+                                       : stg + r * 64u + ((seg ^ ((r >> 1) & 3)) * 16u)));
+            const int tok = f8_token(tl.nmma, half, c * kTok + r);
+            if (c * kTok + r < c_n && tok < tl.nt && ncol < p.N) {
+              const long long off = (long long)(tl.t0 + tok) * p.ldc + ncol;
               if (ncol + kElems <= p.N) {
-                if constexpr (OUT_F32) *reinterpret_cast<uint4*>(static_cast<float*>(p.C) + off) = w;
-                else *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.C) + off) = w;
+                if constexpr (OUT_F32) *reinterpret_cast<uint4*>(static_cast<float*>(p.C) + off) = v;
+                else *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.C) + off) = v;
               } else {
-                const uint32_t parts[4] = {w.x, w.y, w.z, w.w};
+                const uint32_t parts[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < kElems; ++e) {
                   if (ncol + e >= p.N) continue;
