@@ -520,6 +520,26 @@ wst_status wst_grouped_gemm_fp8(int G, int M_total, int N, int K, const void* A,
 size_t wst_gemm_fp8_workspace_size(void);
 
 /*
+ * Weight gradient of the grouped GEMM: for every group g, n < N, k < K
+ *   dB[g][n][k] = sum_{m in group g} dC[m][n] * A[m][k]        (fp32 accumulation)
+ * or, with accumulate != 0, that added to what dB holds (rounded once to
+ * db_type each time).  An empty group's gradient is 0 (or adds nothing).
+ *   dC  bf16 [M_total][N], leading dimension lddc
+ *   A   bf16 [M_total][K], leading dimension lda
+ *   dB  db_type, element (g,n,k) at dB + g*stride_dB + n*lddb + k; it must not
+ *       overlap dC or A
+ * d_offsets as in wst_grouped_gemm_bf16, except that d_offsets[G] may be less
+ * than M_total: rows behind the last group belong to no gradient (whatever they
+ * hold).  Pointers 16-byte aligned, leading dimensions and strides multiples of
+ * 16 bytes.  (The gradient of the rows is wst_grouped_gemm_bf16 of dC with the
+ * weights transposed.)
+ */
+wst_status wst_grouped_gemm_wgrad_bf16(int G, int M_total, int N, int K, const void* dC, long lddc,
+                                       const void* A, long lda, const int* d_offsets, void* dB,
+                                       long lddb, long stride_dB, wst_dtype db_type, int accumulate,
+                                       void* workspace, void* stream);
+
+/*
  * IKBO linear compression.  Candidates of user u are [off[u], off[u+1]) of
  * the DEVICE int32 array d_user_offsets (num_users+1 entries, non-decreasing,
  * from 0 to num_cand).  For every candidate c of user u:

@@ -22,9 +22,9 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwst.so")
 
 SOURCES = ["gemm_dense.cu", "grouped_ws.cu", "ikbo_ws.cu", "ikbo_attn.cu", "wst_api.cu", "expert_parallel.cu",
-           "moe_route.cu", "moe_plan.cu", "moe_combine.cu", "fp8_quant.cu", "fp8_gemm.cu"]
+           "moe_route.cu", "moe_plan.cu", "moe_combine.cu", "fp8_quant.cu", "fp8_gemm.cu", "wgrad_ws.cu"]
 HEADERS = ["sm103.cuh", "wst_common.cuh", "gemm_ws.cuh", "grouped_ws.cuh", "ikbo_ws.cuh", "ikbo_attn_ws.cuh",
-           "fp8_gemm.cuh", "wst_host.h"]
+           "fp8_gemm.cuh", "wgrad_ws.cuh", "wst_host.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

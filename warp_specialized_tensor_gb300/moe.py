@@ -19,6 +19,7 @@ __all__ = [
     "wst_moe_route", "wst_moe_route_backward", "wst_moe_plan", "wst_moe_plan_workspace_size", "moe_plan_workspace",
     "wst_moe_combine", "wst_moe_combine_backward", "wst_quantize_fp8", "wst_quantize_fp8_dispatch",
     "wst_gemm_fp8", "wst_grouped_gemm_fp8", "wst_gemm_fp8_workspace_size", "gemm_fp8_workspace",
+    "wst_grouped_gemm_wgrad_bf16",
 ]
 
 # enums of include/wst.h
@@ -44,7 +45,8 @@ def declare(lib) -> None:
             ("wst_quantize_fp8_dispatch", I, [I, I, I, P, L, I, P, I, P, L, I, P, L, I, P, P]),
             ("wst_gemm_fp8", I, [I, I, I, P, L, I, P, L, P, L, I, P, L, I, P, P, L, I, I, P, Z, P]),
             ("wst_grouped_gemm_fp8", I, [I, I, I, I, P, L, I, P, L, P, L, L, I, P, L, L, I, P, P, L, P, L, I, I, P, Z, P]),
-            ("wst_gemm_fp8_workspace_size", Z, [])):
+            ("wst_gemm_fp8_workspace_size", Z, []),
+            ("wst_grouped_gemm_wgrad_bf16", I, [I, I, I, I, P, L, P, L, P, P, L, L, I, I, P, P])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
 
@@ -378,3 +380,25 @@ def wst_grouped_gemm_fp8(A, scaleA, B, scaleB, offsets, C, scaling="blocks", bia
         scaleB.stride(0), mode, offsets.data_ptr(), _w._ptr(bias) if e else None, sbias, C.data_ptr(), ldc, _type(C, "C"), e, ws,
         n, _w._stream_handle(stream))
     _w._check(st, "wst_grouped_gemm_fp8")
+
+
+# ----------------------------------------------------------------------------
+# weight gradient of the grouped GEMM
+# ----------------------------------------------------------------------------
+def wst_grouped_gemm_wgrad_bf16(dC, A, offsets, dB, accumulate=False, workspace=None, stream=None) -> None:
+    """dB[g] = dC[rows of g]^T . A[rows of g] (added to dB with accumulate).
+
+    dC: bf16 [M_total, N]; A: bf16 [M_total, K]; offsets: device int32 [G+1];
+    dB: bf16/fp32 [G, N, K].  Rows behind offsets[G] belong to no group."""
+    _need(dC, "dC", torch.bfloat16, (2,))
+    _need(A, "A", torch.bfloat16, (2,))
+    lddc, lda, lddb = _rows(dC, "dC"), _rows(A, "A"), _rows(dB, "dB", (3,))
+    G, N, K = dB.shape
+    if A.shape[0] != dC.shape[0] or dC.shape[1] != N or A.shape[1] != K:
+        raise ValueError("shape mismatch: dC %s A %s dB %s" % (tuple(dC.shape), tuple(A.shape), tuple(dB.shape)))
+    _ids(offsets, "offsets", (G + 1,))
+    ws, _ = _ws(workspace)
+    st = _w.load_library().wst_grouped_gemm_wgrad_bf16(
+        G, dC.shape[0], N, K, dC.data_ptr(), lddc, A.data_ptr(), lda, offsets.data_ptr(), dB.data_ptr(), lddb, dB.stride(0),
+        _type(dB, "dB"), int(bool(accumulate)), ws, _w._stream_handle(stream))
+    _w._check(st, "wst_grouped_gemm_wgrad_bf16")
