@@ -51,6 +51,11 @@ def declare(lib) -> None:
         fn.restype, fn.argtypes = res, args
 
 
+# The checks below first ask everything in one expression, which is all a good
+# call pays for, and look for what is wrong only when it fails.
+_I32, _F32 = torch.int32, torch.float32
+
+
 def _fp8(t, name) -> int:
     if t.dtype not in _FP8:
         raise TypeError("%s must be float8_e4m3fn or float8_e5m2" % name)
@@ -58,9 +63,9 @@ def _fp8(t, name) -> int:
 
 
 def _type(t, name) -> int:
-    if t.dtype == torch.float32:
+    if t.dtype is _F32:
         return _w.F32
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return _w.BF16
     raise TypeError("%s must be float32 or bfloat16" % name)
 
@@ -76,24 +81,18 @@ def _need(t, name, dtype=None, dims=None):
     _w._need(t, name, dtype, dims)
 
 
-def _ids(t, name, shape=None):
-    """A contiguous int32 CUDA tensor."""
-    _need(t, name, torch.int32)
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+def _dense(t, name, dtype, shape):
+    """A contiguous CUDA tensor of this type and shape; returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype)
+        raise ValueError("%s must be a contiguous %s tensor, not %s" % (name, tuple(shape), tuple(t.shape)))
+    return t.data_ptr()
 
 
-def _floats(t, name, shape):
-    _need(t, name, torch.float32)
-    if not t.is_contiguous() or tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be a contiguous %s tensor" % (name, tuple(shape)))
-
-
-def _rows(t, name, dims=(2,)):
-    """A tensor of rows; returns the leading dimension (a lone row has none of its own)."""
-    _need(t, name, None, dims)
+def _rows(t, name, dims=2):
+    """A CUDA tensor of rows; returns the leading dimension (a lone row has none of its own)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == dims and t.stride(-1) == 1):
+        _need(t, name, None, (dims,))
     if t.shape[-2] > 1:
         return t.stride(-2)
     per = 16 // t.element_size()
@@ -110,9 +109,30 @@ def _score(score) -> int:
     return _SCORES[score] if isinstance(score, str) else int(score)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, t) -> int:
+    """The handle of `stream`, or of the current stream of t's device."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _w._stream_handle(stream)
+
+
+def _lib():
+    return _w._lib or _w.load_library()
+
+
 # ----------------------------------------------------------------------------
 # routing
 # ----------------------------------------------------------------------------
+def _logits(t, name):
+    """Logits [T, E]; returns the leading dimension (rows need no alignment of their own)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2 and t.stride(1) == 1):
+        _need(t, name, None, (2,))
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 def wst_moe_route(logits, experts, weights, score="softmax", bias=None, groups=1, top_groups=None, group_best=1,
                   renorm=True, scale=1.0, stream=None) -> None:
     """The top_k experts of each token and their weights.
@@ -123,19 +143,16 @@ def wst_moe_route(logits, experts, weights, score="softmax", bias=None, groups=1
     groups of experts by the sum of their group_best best scores; renorm: the
     weights sum to `scale`.  Experts whose logit is -inf (or the type's lowest
     value) are off; a slot without an expert holds -1 and weight 0."""
-    _need(logits, "logits", None, (2,))
+    ld = _logits(logits, "logits")
     T, E = logits.shape
     if experts.dim() != 2 or experts.shape[0] != T:
         raise ValueError("experts must be [T, top_k]")
     k = experts.shape[1]
-    _ids(experts, "experts", (T, k))
-    _floats(weights, "weights", (T, k))
-    if bias is not None:
-        _floats(bias, "bias", (E,))
-    st = _w.load_library().wst_moe_route(
-        T, E, k, logits.data_ptr(), max(logits.stride(0), E) if T <= 1 else logits.stride(0), _type(logits, "logits"), _score(score),
-        _w._ptr(bias), int(groups), int(groups if top_groups is None else top_groups), int(group_best), int(bool(renorm)),
-        float(scale), experts.data_ptr(), weights.data_ptr(), _w._stream_handle(stream))
+    st = _lib().wst_moe_route(
+        T, E, k, logits.data_ptr(), ld, _type(logits, "logits"), _score(score),
+        None if bias is None else _dense(bias, "bias", _F32, (E,)), groups, groups if top_groups is None else top_groups,
+        group_best, 1 if renorm else 0, scale, _dense(experts, "experts", _I32, (T, k)), _dense(weights, "weights", _F32, (T, k)),
+        _stream(stream, logits))
     _w._check(st, "wst_moe_route")
 
 
@@ -143,23 +160,20 @@ def wst_moe_route_backward(logits, experts, dweights, dlogits, score="softmax", 
     """dlogits = the gradient of wst_moe_route's weights for dweights (fp32
     [T, top_k]), the experts held fixed.  dlogits: like logits; the other
     arguments as in wst_moe_route."""
-    _need(logits, "logits", None, (2,))
+    ld, ldd = _logits(logits, "logits"), _logits(dlogits, "dlogits")
     T, E = logits.shape
-    _need(dlogits, "dlogits", logits.dtype, (2,))
-    if dlogits.shape != logits.shape or experts.dim() != 2 or experts.shape[0] != T:
-        raise ValueError("shape mismatch")
+    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or experts.dim() != 2 or experts.shape[0] != T:
+        raise ValueError("dlogits must be like logits, experts [T, top_k]")
     k = experts.shape[1]
-    _ids(experts, "experts", (T, k))
-    _floats(dweights, "dweights", (T, k))
-    lead = (lambda t: max(t.stride(0), E) if T <= 1 else t.stride(0))
-    st = _w.load_library().wst_moe_route_backward(
-        T, E, k, logits.data_ptr(), lead(logits), _type(logits, "logits"), _score(score), int(bool(renorm)), float(scale),
-        experts.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(), lead(dlogits), _w._stream_handle(stream))
+    st = _lib().wst_moe_route_backward(
+        T, E, k, logits.data_ptr(), ld, _type(logits, "logits"), _score(score), 1 if renorm else 0, scale,
+        _dense(experts, "experts", _I32, (T, k)), _dense(dweights, "dweights", _F32, (T, k)), dlogits.data_ptr(), ldd,
+        _stream(stream, logits))
     _w._check(st, "wst_moe_route_backward")
 
 
 def wst_moe_plan_workspace_size(num_pairs: int, num_experts: int) -> int:
-    return int(_w.load_library().wst_moe_plan_workspace_size(num_pairs, num_experts))
+    return int(_lib().wst_moe_plan_workspace_size(num_pairs, num_experts))
 
 
 def moe_plan_workspace(num_pairs: int, num_experts: int, device=None, stream=None) -> torch.Tensor:
@@ -181,14 +195,11 @@ def wst_moe_plan(experts, num_experts, offsets, row_pair, row_token, position, w
     if experts.dim() != 2:
         raise ValueError("experts must be [T, top_k]")
     T, k = experts.shape
-    _ids(experts, "experts")
-    _ids(offsets, "offsets", (num_experts + 1,))
-    _ids(row_pair, "row_pair", (T * k,))
-    _ids(row_token, "row_token", (T * k,))
-    _ids(position, "position", (T, k))
     ws, n = _ws(workspace)
-    st = _w.load_library().wst_moe_plan(T, k, experts.data_ptr(), int(num_experts), offsets.data_ptr(), row_pair.data_ptr(),
-                                        row_token.data_ptr(), position.data_ptr(), ws, n, _w._stream_handle(stream))
+    st = _lib().wst_moe_plan(
+        T, k, _dense(experts, "experts", _I32, (T, k)), num_experts, _dense(offsets, "offsets", _I32, (num_experts + 1,)),
+        _dense(row_pair, "row_pair", _I32, (T * k,)), _dense(row_token, "row_token", _I32, (T * k,)),
+        _dense(position, "position", _I32, (T, k)), ws, n, _stream(stream, experts))
     _w._check(st, "wst_moe_plan")
 
 
@@ -205,13 +216,12 @@ def wst_moe_combine(y, position, out, weights=None, workspace=None, stream=None)
     if y.shape[1] != N or position.dim() != 2 or position.shape[0] != T:
         raise ValueError("shape mismatch: y %s position %s out %s" % (tuple(y.shape), tuple(position.shape), tuple(out.shape)))
     k = position.shape[1]
-    _ids(position, "position", (T, k))
-    if weights is not None:
-        _floats(weights, "weights", (T, k))
+    at = _dense(position, "position", _I32, (T, k))
+    w = None if weights is None else _dense(weights, "weights", _F32, (T, k))
     ws, _ = _ws(workspace)
-    st = _w.load_library().wst_moe_combine(
-        T, k, N, y.data_ptr(), ldy, _type(y, "y"), y.shape[0], position.data_ptr(), _w._ptr(weights), out.data_ptr(), ldo,
-        _type(out, "out"), ws, _w._stream_handle(stream))
+    st = _lib().wst_moe_combine(
+        T, k, N, y.data_ptr(), ldy, _type(y, "y"), y.shape[0], at, w, out.data_ptr(), ldo,
+        _type(out, "out"), ws, _stream(stream, out))
     _w._check(st, "wst_moe_combine")
 
 
@@ -225,13 +235,11 @@ def wst_moe_combine_backward(dout, position, y=None, weights=None, dy=None, dwei
     if position.dim() != 2 or position.shape[0] != T:
         raise ValueError("position must be [T, top_k]")
     k = position.shape[1]
-    _ids(position, "position", (T, k))
-    if weights is not None:
-        _floats(weights, "weights", (T, k))
-    if dweights is not None:
-        _floats(dweights, "dweights", (T, k))
-        if y is None:
-            raise ValueError("dweights needs y")
+    at = _dense(position, "position", _I32, (T, k))
+    w = None if weights is None else _dense(weights, "weights", _F32, (T, k))
+    dw = None if dweights is None else _dense(dweights, "dweights", _F32, (T, k))
+    if dw is not None and y is None:
+        raise ValueError("dweights needs y")
     rows = y if y is not None else dy
     if rows is None:
         raise ValueError("neither dy nor dweights is asked for")
@@ -240,9 +248,9 @@ def wst_moe_combine_backward(dout, position, y=None, weights=None, dy=None, dwei
     if rows.shape[1] != N or (y is not None and dy is not None and (y.shape != dy.shape or y.dtype != dy.dtype)):
         raise ValueError("y and dy must be alike, with rows of N values")
     ws, _ = _ws(workspace)
-    st = _w.load_library().wst_moe_combine_backward(
+    st = _lib().wst_moe_combine_backward(
         T, k, N, dout.data_ptr(), ldo, _type(dout, "dout"), _w._ptr(y), ldy, _type(rows, "y"), rows.shape[0],
-        position.data_ptr(), _w._ptr(weights), _w._ptr(dy), lddy, _w._ptr(dweights), ws, _w._stream_handle(stream))
+        at, w, _w._ptr(dy), lddy, dw, ws, _stream(stream, dout))
     _w._check(st, "wst_moe_combine_backward")
 
 
@@ -258,9 +266,10 @@ def wst_quantize_fp8(x, q, scales, mode="rows", pow2=False, stream=None) -> None
     transposed.  q: float8_e4m3fn or float8_e5m2; scales: fp32; both with x's
     batch dimension.  pow2: scales are powers of two."""
     m = _MODES[mode] if isinstance(mode, str) else int(mode)
-    ldx, ldq, lds = _rows(x, "x", (2, 3)), _rows(q, "q", (2, 3)), _rows(scales, "scales", (2, 3))
-    if q.dim() != x.dim() or scales.dim() != x.dim() or scales.dtype != torch.float32:
-        raise ValueError("q and scales (float32) must have x's dimensions")
+    dims = 3 if x.dim() == 3 else 2
+    ldx, ldq, lds = _rows(x, "x", dims), _rows(q, "q", dims), _rows(scales, "scales", dims)
+    if scales.dtype is not _F32:
+        raise TypeError("scales must be float32")
     M, K = x.shape[-2:]
     mb, kb = -(-M // 128), -(-K // 128)
     want_q = (M, K) if m in (FP8_ROWS, FP8_BLOCKS) else (K, M)
@@ -272,9 +281,9 @@ def wst_quantize_fp8(x, q, scales, mode="rows", pow2=False, stream=None) -> None
     if batch == 0:
         return
     s = (lambda t: t.stride(0) if t.dim() == 3 else 0)
-    st = _w.load_library().wst_quantize_fp8(
+    st = _lib().wst_quantize_fp8(
         m, batch, M, K, x.data_ptr(), ldx, s(x), _type(x, "x"), q.data_ptr(), ldq, s(q), _fp8(q, "q"), scales.data_ptr(), lds,
-        s(scales), int(bool(pow2)), _w._stream_handle(stream))
+        s(scales), 1 if pow2 else 0, _stream(stream, x))
     _w._check(st, "wst_quantize_fp8")
 
 
@@ -291,11 +300,11 @@ def wst_quantize_fp8_dispatch(x, position, q, scales, pow2=False, workspace=None
         raise ValueError("q must be [rows, K] and scales float32 [ceil(K/128), rows]")
     if position.dim() != 2:
         raise ValueError("position must be [T, copies]")
-    _ids(position, "position", (T, position.shape[1]))
+    at = _dense(position, "position", _I32, (T, position.shape[1]))
     ws, _ = _ws(workspace)
-    st = _w.load_library().wst_quantize_fp8_dispatch(
-        T, K, position.shape[1], x.data_ptr(), ldx, _type(x, "x"), position.data_ptr(), rows, q.data_ptr(), ldq, _fp8(q, "q"),
-        scales.data_ptr(), lds, int(bool(pow2)), ws, _w._stream_handle(stream))
+    st = _lib().wst_quantize_fp8_dispatch(
+        T, K, position.shape[1], x.data_ptr(), ldx, _type(x, "x"), at, rows, q.data_ptr(), ldq, _fp8(q, "q"),
+        scales.data_ptr(), lds, 1 if pow2 else 0, ws, _stream(stream, x))
     _w._check(st, "wst_quantize_fp8_dispatch")
 
 
@@ -303,7 +312,7 @@ def wst_quantize_fp8_dispatch(x, position, q, scales, pow2=False, workspace=None
 # 8-bit products
 # ----------------------------------------------------------------------------
 def wst_gemm_fp8_workspace_size() -> int:
-    return int(_w.load_library().wst_gemm_fp8_workspace_size())
+    return int(_lib().wst_gemm_fp8_workspace_size())
 
 
 def gemm_fp8_workspace(device=None, stream=None) -> torch.Tensor:
@@ -321,8 +330,8 @@ def _fp8_operand(q, scale, name, scaling, dims):
         raise TypeError("the scales of %s must be float32" % name)
     R, K = q.shape[-2:]
     kb = -(-K // 128)
-    want = tuple(q.shape[:-2]) + ((kb, R) if scaling == FP8_ROWS else (-(-R // 128), kb))
-    if tuple(scale.shape) != want:
+    want = (*q.shape[:-2], kb, R) if scaling == FP8_ROWS else (*q.shape[:-2], -(-R // 128), kb)
+    if scale.shape != want:
         raise ValueError("the scales of %s must be %s, not %s" % (name, want, tuple(scale.shape)))
     return ld, ty, lds
 
@@ -335,8 +344,8 @@ def wst_gemm_fp8(A, scaleA, B, scaleB, C, scaling="blocks", bias=None, epi="none
     [ceil(K/128), N] ("rows"); C: bf16/fp32 [M, N]; bias: bf16 [N].  workspace:
     gemm_fp8_workspace() lets products of few tiles use all SMs."""
     mode = _MODES[scaling] if isinstance(scaling, str) else int(scaling)
-    lda, ta, ldsa = _fp8_operand(A, scaleA, "A", FP8_ROWS, (2,))
-    ldb, tb, ldsb = _fp8_operand(B, scaleB, "B", mode, (2,))
+    lda, ta, ldsa = _fp8_operand(A, scaleA, "A", FP8_ROWS, 2)
+    ldb, tb, ldsb = _fp8_operand(B, scaleB, "B", mode, 2)
     ldc = _rows(C, "C")
     (M, K), N = A.shape, B.shape[0]
     if B.shape[1] != K or tuple(C.shape) != (M, N):
@@ -347,9 +356,9 @@ def wst_gemm_fp8(A, scaleA, B, scaleB, C, scaling="blocks", bias=None, epi="none
         if bias.numel() != N:
             raise ValueError("bias must be [N]")
     ws, n = _ws(workspace)
-    st = _w.load_library().wst_gemm_fp8(
+    st = _lib().wst_gemm_fp8(
         M, N, K, A.data_ptr(), lda, ta, scaleA.data_ptr(), ldsa, B.data_ptr(), ldb, tb, scaleB.data_ptr(), ldsb, mode,
-        _w._ptr(bias) if e else None, C.data_ptr(), ldc, _type(C, "C"), e, ws, n, _w._stream_handle(stream))
+        _w._ptr(bias) if e else None, C.data_ptr(), ldc, _type(C, "C"), e, ws, n, _stream(stream, C))
     _w._check(st, "wst_gemm_fp8")
 
 
@@ -360,13 +369,13 @@ def wst_grouped_gemm_fp8(A, scaleA, B, scaleB, offsets, C, scaling="blocks", bia
     group dimension; offsets: device int32 [G+1]; bias: bf16 [G, N].  Rows
     behind offsets[G] are left as they were."""
     mode = _MODES[scaling] if isinstance(scaling, str) else int(scaling)
-    lda, ta, ldsa = _fp8_operand(A, scaleA, "A", FP8_ROWS, (2,))
-    ldb, tb, ldsb = _fp8_operand(B, scaleB, "B", mode, (3,))
+    lda, ta, ldsa = _fp8_operand(A, scaleA, "A", FP8_ROWS, 2)
+    ldb, tb, ldsb = _fp8_operand(B, scaleB, "B", mode, 3)
     ldc = _rows(C, "C")
     (M, K), (G, N, K2) = A.shape, B.shape
     if K2 != K or tuple(C.shape) != (M, N):
         raise ValueError("shape mismatch: A %s B %s C %s" % (tuple(A.shape), tuple(B.shape), tuple(C.shape)))
-    _ids(offsets, "offsets", (G + 1,))
+    off = _dense(offsets, "offsets", _I32, (G + 1,))
     e = _w._epi(epi)
     sbias = 0
     if e != _w.EPI_NONE:
@@ -375,10 +384,10 @@ def wst_grouped_gemm_fp8(A, scaleA, B, scaleB, offsets, C, scaling="blocks", bia
             raise ValueError("bias must be [G, N]")
         sbias = bias.stride(0)
     ws, n = _ws(workspace)
-    st = _w.load_library().wst_grouped_gemm_fp8(
+    st = _lib().wst_grouped_gemm_fp8(
         G, M, N, K, A.data_ptr(), lda, ta, scaleA.data_ptr(), ldsa, B.data_ptr(), ldb, B.stride(0), tb, scaleB.data_ptr(), ldsb,
-        scaleB.stride(0), mode, offsets.data_ptr(), _w._ptr(bias) if e else None, sbias, C.data_ptr(), ldc, _type(C, "C"), e, ws,
-        n, _w._stream_handle(stream))
+        scaleB.stride(0), mode, off, _w._ptr(bias) if e else None, sbias, C.data_ptr(), ldc, _type(C, "C"), e, ws,
+        n, _stream(stream, C))
     _w._check(st, "wst_grouped_gemm_fp8")
 
 
@@ -390,15 +399,15 @@ def wst_grouped_gemm_wgrad_bf16(dC, A, offsets, dB, accumulate=False, workspace=
 
     dC: bf16 [M_total, N]; A: bf16 [M_total, K]; offsets: device int32 [G+1];
     dB: bf16/fp32 [G, N, K].  Rows behind offsets[G] belong to no group."""
-    _need(dC, "dC", torch.bfloat16, (2,))
-    _need(A, "A", torch.bfloat16, (2,))
-    lddc, lda, lddb = _rows(dC, "dC"), _rows(A, "A"), _rows(dB, "dB", (3,))
+    if dC.dtype is not torch.bfloat16 or A.dtype is not torch.bfloat16:
+        raise TypeError("dC and A must be bfloat16")
+    lddc, lda, lddb = _rows(dC, "dC"), _rows(A, "A"), _rows(dB, "dB", 3)
     G, N, K = dB.shape
     if A.shape[0] != dC.shape[0] or dC.shape[1] != N or A.shape[1] != K:
         raise ValueError("shape mismatch: dC %s A %s dB %s" % (tuple(dC.shape), tuple(A.shape), tuple(dB.shape)))
-    _ids(offsets, "offsets", (G + 1,))
+    off = _dense(offsets, "offsets", _I32, (G + 1,))
     ws, _ = _ws(workspace)
-    st = _w.load_library().wst_grouped_gemm_wgrad_bf16(
-        G, dC.shape[0], N, K, dC.data_ptr(), lddc, A.data_ptr(), lda, offsets.data_ptr(), dB.data_ptr(), lddb, dB.stride(0),
-        _type(dB, "dB"), int(bool(accumulate)), ws, _w._stream_handle(stream))
+    st = _lib().wst_grouped_gemm_wgrad_bf16(
+        G, dC.shape[0], N, K, dC.data_ptr(), lddc, A.data_ptr(), lda, off, dB.data_ptr(), lddb, dB.stride(0),
+        _type(dB, "dB"), 1 if accumulate else 0, ws, _stream(stream, dB))
     _w._check(st, "wst_grouped_gemm_wgrad_bf16")
