@@ -13,8 +13,8 @@
 // transposed; BLOCKS 128 x 128; BLOCKS_T 128 x 128, values and scales
 // transposed.
 //
-// All forms are bound by HBM (2 or 4 bytes in, 1 byte out).  ROWS: 16 lanes
-// hold one block, eight values each, and find its largest by shuffles; with a
+// All forms are bound by HBM (2 or 4 bytes in, 1 byte out).  ROWS: eight
+// lanes hold one block, 16 values each, and find its largest by shuffles; with a
 // row index each block is quantised once and stored to every row that wants
 // it.  The others: one 128 x 128 tile per block of threads, an 8 x 8 patch in
 // each thread's registers, so a transposed patch leaves as eight 8-byte words
@@ -76,85 +76,105 @@ struct QuantArgs {
   WsHeader* ws;
 };
 
-__device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
+// Values held per 16-byte load of X.
+template <typename X>
+constexpr int vec_of() { return 16 / (int)sizeof(X); }
 
-__device__ __forceinline__ void load_vec(const float* p, float* v) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+// The largest |x| of 16 raw bytes of X as fp32 bits (NaN above infinity).
+__device__ __forceinline__ uint32_t vec_amax(uint4 r, uint32_t so_far, float) {
+  return max(max(so_far, max(r.x & 0x7fffffffu, r.y & 0x7fffffffu)), max(r.z & 0x7fffffffu, r.w & 0x7fffffffu));
 }
-__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float* v) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ uint32_t vec_amax(uint4 r, uint32_t so_far, __nv_bfloat16) {
+  // two at a time: |x| of bf16 is ordered like 16-bit integers, too
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t a = __vmaxu2(__vmaxu2(r.x & m, r.y & m), __vmaxu2(r.z & m, r.w & m));
+  return max(so_far, max(a & 0xffff0000u, a << 16));
+}
+__device__ __forceinline__ void unpack(uint4 r, float (&v)[4]) {
+  v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y); v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void unpack(uint4 r, float (&v)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-
-// Values held per 16-byte load of X.
+// 16 bytes of a row from element k on; what lies behind the row's K is 0.
 template <typename X>
-constexpr int vec_of() { return 16 / (int)sizeof(X); }
+__device__ __forceinline__ uint4 load_raw(const X* x, int k, int K) {
+  constexpr int V = vec_of<X>();
+  if (k + V <= K) return __ldg(reinterpret_cast<const uint4*>(x + k));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (k + i < K) {
+      if constexpr (V == 4) w[i] = __float_as_uint(__ldg(x + k + i));
+      else w[i >> 1] |= (uint32_t)__bfloat16_as_ushort(__ldg(x + k + i)) << (16 * (i & 1));
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
-// One warp per 256 columns (two blocks) of a row.
+// One warp per four blocks of a row, eight lanes and 16 values a lane each; bf16
+// as two 16-byte loads of eight, fp32 as four of four.
 template <typename X, bool E5, bool POW2>
-__global__ void __launch_bounds__(kQThreads) k_quant_rows(const QuantArgs a, int strips) {
-  constexpr int V = vec_of<X>(), P = 8 / V;  // values per load, loads per lane
-  const int lane = threadIdx.x & 31, l16 = lane & 15;
-  const long long w = (long long)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
-  const int m = (int)(w / strips), strip = (int)(w % strips);
+__global__ void __launch_bounds__(kQThreads) k_quant_rows(const QuantArgs a) {
+  constexpr int V = vec_of<X>(), P = 16 / V;  // values per load, loads per lane
+  const int lane = threadIdx.x & 31, l8 = lane & 7;
+  const int m = (int)blockIdx.x * (kQThreads / 32) + (int)(threadIdx.x >> 5);
   if (m >= a.M) return;
-  const int kb = strip * 2 + (lane >> 4);
-  const X* x = static_cast<const X*>(a.x) + blockIdx.y * a.strideX + (long long)m * a.ldx;
-  float v[8];
-  uint32_t amax = 0;
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int k = kb * 128 + p * 16 * V + l16 * V;
-    if (k + V <= a.K) {
-      load_vec(x + k, v + p * V);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[p * V + i] = k + i < a.K ? load1(x + k + i) : 0.0f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, abs_bits(v[i]));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (kb * 128 >= a.K) return;
-  const float scale = block_scale<E5, POW2>(amax);
-  const float inv = 1.0f / scale;
-  uint32_t out[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    out[i] = Fp8<E5>::pack4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+  const X* x = static_cast<const X*>(a.x) + blockIdx.z * a.strideX + (long long)m * a.ldx;
   const int copies = a.position ? a.copies : 1;
-  for (int c = 0; c < copies; ++c) {
-    int row = m;
-    if (a.position) {
-      row = __ldg(a.position + (long long)m * copies + c);
-      if (row < 0) continue;
-      if (row >= a.n_rows) {
-        if (lane == 0) latch_error(a.ws, 1u /*WST_ERR_INVALID_ARG*/, 0x80000u);
-        continue;
-      }
-    }
-    uint8_t* q = a.q + blockIdx.y * a.strideQ + (long long)row * a.ldq;
+  const int blocks = (a.K + 127) >> 7;
+  // blockIdx.y shares a row's strips between blocks of threads (few rows)
+  for (int kb0 = (int)blockIdx.y * 4; kb0 < blocks; kb0 += (int)gridDim.y * 4) {
+    const int kb = kb0 + (lane >> 3), k0 = kb * 128 + l8 * V;
+    uint4 raw[P];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int p = 0; p < P; ++p) raw[p] = load_raw(x, k0 + p * 8 * V, a.K);
+#pragma unroll
+    for (int p = 0; p < P; ++p) amax = vec_amax(raw[p], amax, X());
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (kb >= blocks) continue;
+    const float scale = block_scale<E5, POW2>(amax);
+    const float inv = 1.0f / scale;
+    uint32_t out[P][V / 4];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int k = kb * 128 + p * 16 * V + l16 * V;
-      if (k + V <= a.K) {
-        if constexpr (V == 8) *reinterpret_cast<uint2*>(q + k) = make_uint2(out[0], out[1]);
-        else *reinterpret_cast<uint32_t*>(q + k) = out[p];
-      } else {
+      float v[V];
+      unpack(raw[p], v);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (k + i < a.K) q[k + i] = (uint8_t)(out[(p * V + i) >> 2] >> (8 * (i & 3)));
-      }
+      for (int i = 0; i < V / 4; ++i)
+        out[p][i] = Fp8<E5>::pack4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
     }
-    if (l16 == 0) a.scales[blockIdx.y * a.strideS + (long long)kb * a.lds + row] = scale;
+    for (int c = 0; c < copies; ++c) {
+      int row = m;
+      if (a.position) {
+        row = __ldg(a.position + (long long)m * copies + c);
+        if (row < 0) continue;
+        if (row >= a.n_rows) {
+          if (lane == 0) latch_error(a.ws, 1u /*WST_ERR_INVALID_ARG*/, 0x80000u);
+          continue;
+        }
+      }
+      uint8_t* q = a.q + blockIdx.z * a.strideQ + (long long)row * a.ldq;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int k = k0 + p * 8 * V;
+        if (k + V <= a.K) {
+          if constexpr (V == 8) *reinterpret_cast<uint2*>(q + k) = make_uint2(out[p][0], out[p][1]);
+          else *reinterpret_cast<uint32_t*>(q + k) = out[p][0];
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (k + i < a.K) q[k + i] = (uint8_t)(out[p][i >> 2] >> (8 * (i & 3)));
+        }
+      }
+      if (l8 == 0) a.scales[blockIdx.z * a.strideS + (long long)kb * a.lds + row] = scale;
+    }
   }
 }
 
@@ -169,37 +189,35 @@ __global__ void __launch_bounds__(kQThreads) k_quant_tile(const QuantArgs a) {
   const int t = threadIdx.x, r8 = t >> 4, c8 = t & 15;
   const int m0 = (int)blockIdx.y * 128, k0 = (int)blockIdx.x * 128;
   const X* x = static_cast<const X*>(a.x) + blockIdx.z * a.strideX;
-  float v[8][8];
+  // (held as loaded: unpacked, bf16 would take twice the registers)
+  uint4 raw[8][P];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int m = m0 + r8 * 8 + i;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int k = k0 + c8 * 8 + p * V;
-      const X* src = x + (long long)m * a.ldx + k;
-      if (m < a.M && k + V <= a.K) {
-        load_vec(src, &v[i][p * V]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[i][p * V + j] = m < a.M && k + j < a.K ? load1(src + j) : 0.0f;
-      }
-    }
+    for (int p = 0; p < P; ++p)
+      raw[i][p] = m < a.M ? load_raw(x + (long long)m * a.ldx, k0 + c8 * 8 + p * V, a.K) : make_uint4(0, 0, 0, 0);
   }
   float inv[8];
   if constexpr (COLS) {
+    uint32_t b[8] = {};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t b = 0;
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b = max(b, abs_bits(v[i][j]));
-      part[r8][c8 * 8 + j] = b;
-    }
+      for (int p = 0; p < P; ++p) {
+        float v[V];
+        unpack(raw[i][p], v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) b[p * V + j] = max(b[p * V + j], abs_bits(v[j]));
+      }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[r8][c8 * 8 + j] = b[j];
     __syncthreads();
     if (t < 128) {
-      uint32_t b = 0;
+      uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) b = max(b, part[i][t]);
-      const float s = block_scale<E5, POW2>(b);
+      for (int i = 0; i < 16; ++i) m = max(m, part[i][t]);
+      const float s = block_scale<E5, POW2>(m);
       col_scale[t] = 1.0f / s;
       if (k0 + t < a.K) a.scales[blockIdx.z * a.strideS + (long long)blockIdx.y * a.lds + k0 + t] = s;
     }
@@ -211,7 +229,7 @@ __global__ void __launch_bounds__(kQThreads) k_quant_tile(const QuantArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) b = max(b, abs_bits(v[i][j]));
+      for (int p = 0; p < P; ++p) b = vec_amax(raw[i][p], b, X());
     b = __reduce_max_sync(0xffffffffu, b);
     if ((t & 31) == 0) part[0][t >> 5] = b;
     __syncthreads();
@@ -225,14 +243,24 @@ __global__ void __launch_bounds__(kQThreads) k_quant_tile(const QuantArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) inv[j] = 1.0f / s;
   }
+  // Value (row i, column j) of the patch.
+  auto at = [&](int i, int j) {
+    const uint4& r = raw[i][j / V];
+    if constexpr (V == 4) {
+      return __uint_as_float((j & 3) == 0 ? r.x : (j & 3) == 1 ? r.y : (j & 3) == 2 ? r.z : r.w);
+    } else {
+      const uint32_t w = j < 2 ? r.x : j < 4 ? r.y : j < 6 ? r.z : r.w;
+      return __uint_as_float((j & 1) ? (w & 0xffff0000u) : (w << 16));
+    }
+  };
   uint8_t* q = a.q + blockIdx.z * a.strideQ;
   if constexpr (TRANS) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float f = inv[j];
       tile[c8 * 8 + j][r8 ^ c8] = make_uint2(
-          Fp8<E5>::pack4(v[0][j] * f, v[1][j] * f, v[2][j] * f, v[3][j] * f),
-          Fp8<E5>::pack4(v[4][j] * f, v[5][j] * f, v[6][j] * f, v[7][j] * f));
+          Fp8<E5>::pack4(at(0, j) * f, at(1, j) * f, at(2, j) * f, at(3, j) * f),
+          Fp8<E5>::pack4(at(4, j) * f, at(5, j) * f, at(6, j) * f, at(7, j) * f));
     }
     __syncthreads();
     // 16 lanes per transposed row: 128 consecutive bytes.
@@ -254,8 +282,8 @@ __global__ void __launch_bounds__(kQThreads) k_quant_tile(const QuantArgs a) {
       const int m = m0 + r8 * 8 + i, k = k0 + c8 * 8;
       if (m >= a.M || k >= a.K) continue;
       const uint2 word = make_uint2(
-          Fp8<E5>::pack4(v[i][0] * inv[0], v[i][1] * inv[1], v[i][2] * inv[2], v[i][3] * inv[3]),
-          Fp8<E5>::pack4(v[i][4] * inv[4], v[i][5] * inv[5], v[i][6] * inv[6], v[i][7] * inv[7]));
+          Fp8<E5>::pack4(at(i, 0) * inv[0], at(i, 1) * inv[1], at(i, 2) * inv[2], at(i, 3) * inv[3]),
+          Fp8<E5>::pack4(at(i, 4) * inv[4], at(i, 5) * inv[5], at(i, 6) * inv[6], at(i, 7) * inv[7]));
       uint8_t* dst = q + (long long)m * a.ldq + k;
       if (k + 8 <= a.K) {
         *reinterpret_cast<uint2*>(dst) = word;
@@ -269,9 +297,11 @@ __global__ void __launch_bounds__(kQThreads) k_quant_tile(const QuantArgs a) {
 template <typename X, bool E5, bool POW2>
 void launch_quant(int mode, const QuantArgs& a, int batch, cudaStream_t s) {
   if (mode == WST_FP8_ROWS) {
-    const int strips = (a.K + 255) / 256;
-    const long long warps = (long long)a.M * strips;
-    k_quant_rows<X, E5, POW2><<<dim3((unsigned)((warps + 7) / 8), (unsigned)batch), kQThreads, 0, s>>>(a, strips);
+    // One warp per row, or per strip of four blocks where there are few rows.
+    const unsigned strips = (unsigned)((a.K + 511) / 512);
+    const unsigned rows = (unsigned)((a.M + 7) / 8);
+    const unsigned share = rows >= 1024 ? 1 : strips < 1024 / rows + 1 ? strips : 1024 / rows + 1;
+    k_quant_rows<X, E5, POW2><<<dim3(rows, share, (unsigned)batch), kQThreads, 0, s>>>(a);
     return;
   }
   const dim3 grid((unsigned)((a.K + 127) / 128), (unsigned)((a.M + 127) / 128), (unsigned)batch);

@@ -90,44 +90,63 @@ __device__ __forceinline__ int combine_row(const CombineArgs& a, int t, int i, b
   return -1;
 }
 
-// tpt threads per token (a power of two up to kCombThreads), blockIdx.y the
-// stretch of 8 * tpt columns.
-template <typename Y, typename O>
+// tpt threads per token (a power of two from 32 to kCombThreads); each takes V
+// vectors of eight columns at a time, KC rows of each in flight.
+template <typename Y, typename O, int KC, int V>
 __global__ void __launch_bounds__(kCombThreads) k_combine(const CombineArgs a, int tpt) {
   const int t = blockIdx.x * (kCombThreads / tpt) + (int)threadIdx.x / tpt;
-  const int v = (int)blockIdx.y * tpt + (int)threadIdx.x % tpt;
-  const int n = a.N - v * 8;
-  if (t >= a.T || n <= 0) return;
-  const Y* y = static_cast<const Y*>(a.y) + (long long)v * 8;
-  float acc[8] = {};
-  for (int i0 = 0; i0 < a.top_k; i0 += 4) {
-    float x[4][8], w[4];
-    int row[4];
+  const int me = (int)threadIdx.x & (tpt - 1);
+  if (t >= a.T) return;
+  const Y* y = static_cast<const Y*>(a.y);
+  O* out = static_cast<O*>(a.out) + (long long)t * a.ldo;
+  for (int c0 = me * 8; c0 < a.N; c0 += tpt * 8 * V) {
+    float acc[V][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      row[i] = i0 + i < a.top_k ? combine_row(a, t, i0 + i, v == 0) : -1;
-      if (row[i] >= 0) {
-        load8(y + (long long)row[i] * a.ldy, n, x[i]);
-        w[i] = a.weights ? __ldg(a.weights + (long long)t * a.top_k + i0 + i) : 1.0f;
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[v][c] = 0.0f;
+    for (int i0 = 0; i0 < a.top_k; i0 += KC) {
+      long long row[KC];
+      float w[KC];
+#pragma unroll
+      for (int i = 0; i < KC; ++i) {
+        const int r = i0 + i < a.top_k ? combine_row(a, t, i0 + i, c0 == 0) : -1;
+        w[i] = r >= 0 && a.weights ? __ldg(a.weights + (long long)t * a.top_k + i0 + i) : 1.0f;
+        row[i] = r >= 0 ? (long long)r * a.ldy : -1;
       }
+      float x[V][KC][8];
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < KC; ++i) {
+          const int c = c0 + v * tpt * 8;
+          if (row[i] >= 0 && c < a.N) load8(y + row[i] + c, a.N - c, x[v][i]);
+        }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < KC; ++i)
+          if (row[i] >= 0) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[v][c] = fmaf(w[i], x[v][i][c], acc[v][c]);
+          }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (row[i] >= 0) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] = fmaf(w[i], x[i][c], acc[c]);
-      }
+    for (int v = 0; v < V; ++v) {
+      const int c = c0 + v * tpt * 8;
+      if (c < a.N) store8(out + c, a.N - c, acc[v]);
+    }
   }
-  store8(static_cast<O*>(a.out) + (long long)t * a.ldo + (long long)v * 8, n, acc);
 }
 
-// KC slots at a time (more slots take further passes over dout).
+// KC slots at a time (more slots take further passes over dout), two vectors of
+// each row in flight.
 template <typename Y, typename O, int KC>
 __global__ void __launch_bounds__(kCombThreads) k_combine_backward(const CombineArgs a, int tpt) {
   __shared__ float part[kCombThreads / 32][KC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (kCombThreads / tpt) + (int)threadIdx.x / tpt;
-  const int me = (int)threadIdx.x % tpt;
+  const int me = (int)threadIdx.x & (tpt - 1);
   const bool there = t < a.T;
   const O* dout = static_cast<const O*>(a.out) + (long long)(there ? t : 0) * a.ldo;
   for (int i0 = 0; i0 < a.top_k; i0 += KC) {
@@ -139,18 +158,23 @@ __global__ void __launch_bounds__(kCombThreads) k_combine_backward(const Combine
       w[i] = row[i] >= 0 && a.weights ? __ldg(a.weights + (long long)t * a.top_k + i0 + i) : 1.0f;
       dot[i] = 0.0f;
     }
+#pragma unroll 2
     for (int c = me * 8; there && c < a.N; c += tpt * 8) {
       const int n = a.N - c;
       float d[8];
       load8(dout + c, n, d);
+      float x[KC][8];
+      if (a.dweights) {
+#pragma unroll
+        for (int i = 0; i < KC; ++i)
+          if (row[i] >= 0) load8(static_cast<const Y*>(a.y) + (long long)row[i] * a.ldy + c, n, x[i]);
+      }
 #pragma unroll
       for (int i = 0; i < KC; ++i) {
         if (row[i] < 0) continue;
         if (a.dweights) {
-          float x[8];
-          load8(static_cast<const Y*>(a.y) + (long long)row[i] * a.ldy + c, n, x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dot[i] = fmaf(d[j], x[j], dot[i]);
+          for (int j = 0; j < 8; ++j) dot[i] = fmaf(d[j], x[i][j], dot[i]);
         }
         if (a.dy) {
           float g[8];
@@ -162,38 +186,51 @@ __global__ void __launch_bounds__(kCombThreads) k_combine_backward(const Combine
     }
     if (a.dweights) {
 #pragma unroll
-      for (int i = 0; i < KC; ++i) {
+      for (int i = 0; i < KC; ++i)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], o);
-        if (lane == 0) part[warp][i] = dot[i];
+      if (tpt > 32) {
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < KC; ++i) part[warp][i] = dot[i];
+        }
+        __syncthreads();
+        if (there && me < KC && i0 + me < a.top_k) {
+          float sum = 0.0f;
+          for (int k = 0; k < tpt / 32; ++k) sum += part[warp + k][me];
+          a.dweights[(long long)t * a.top_k + i0 + me] = sum;
+        }
+        __syncthreads();
+      } else if (there && lane == 0) {
+#pragma unroll
+        for (int i = 0; i < KC; ++i)
+          if (i0 + i < a.top_k) a.dweights[(long long)t * a.top_k + i0 + i] = dot[i];
       }
-      __syncthreads();
-      if (there && me < KC && i0 + me < a.top_k) {
-        float sum = 0.0f;
-        for (int k = 0; k < tpt / 32; ++k) sum += part[warp + k][me];
-        a.dweights[(long long)t * a.top_k + i0 + me] = sum;
-      }
-      __syncthreads();
     }
   }
 }
 
-int threads_per_token(int N) {
+// One warp per token where there are tokens enough to fill the SMs with warps
+// (each warp then has more loads in flight and needs no barrier); more threads
+// per token for few tokens.
+int threads_per_token(int T, int N, int sms) {
   int tpt = 32;
-  while (tpt < kCombThreads && tpt * 8 < N) tpt *= 2;
+  while (tpt < kCombThreads && tpt * 8 < N && (long long)T * tpt < 512LL * sms) tpt *= 2;
   return tpt;
 }
 
 template <typename Y, typename O>
-void launch_combine(const CombineArgs& a, cudaStream_t s) {
-  const int tpt = threads_per_token(a.N), per = kCombThreads / tpt;
-  const dim3 grid((unsigned)((a.T + per - 1) / per), (unsigned)((a.N + 8 * tpt - 1) / (8 * tpt)));
-  k_combine<Y, O><<<grid, kCombThreads, 0, s>>>(a, tpt);
+void launch_combine(const CombineArgs& a, int sms, cudaStream_t s) {
+  const int tpt = threads_per_token(a.T, a.N, sms), per = kCombThreads / tpt;
+  const unsigned grid = (unsigned)((a.T + per - 1) / per);
+  if (a.top_k == 1) k_combine<Y, O, 1, 4><<<grid, kCombThreads, 0, s>>>(a, tpt);
+  else if (a.top_k == 2) k_combine<Y, O, 2, 2><<<grid, kCombThreads, 0, s>>>(a, tpt);
+  else k_combine<Y, O, 4, 1><<<grid, kCombThreads, 0, s>>>(a, tpt);
 }
 
 template <typename Y, typename O>
-void launch_combine_backward(const CombineArgs& a, cudaStream_t s) {
-  const int tpt = threads_per_token(a.N), per = kCombThreads / tpt;
+void launch_combine_backward(const CombineArgs& a, int sms, cudaStream_t s) {
+  const int tpt = threads_per_token(a.T, a.N, sms), per = kCombThreads / tpt;
   const unsigned grid = (unsigned)((a.T + per - 1) / per);
   if (a.top_k == 1) k_combine_backward<Y, O, 1><<<grid, kCombThreads, 0, s>>>(a, tpt);
   else if (a.top_k == 2) k_combine_backward<Y, O, 2><<<grid, kCombThreads, 0, s>>>(a, tpt);
@@ -206,8 +243,7 @@ int check_combine(const char* what, int T, int top_k, int N, int y_type, int n_r
     return reject(ST_INVALID_ARG, "%s: sizes out of range (T=%d top_k=%d N=%d n_rows=%d)", what, T, top_k, N, n_rows);
   if (top_k > kCombMaxTopK)
     return reject(ST_UNSUPPORTED, "%s: top_k=%d: this build supports up to %d", what, top_k, kCombMaxTopK);
-  if (N > 65535 * 8 * kCombThreads)
-    return reject(ST_UNSUPPORTED, "%s: N=%d is too wide", what, N);
+  if (N > 0x7fffffff - 8 * kCombThreads * 4) return reject(ST_UNSUPPORTED, "%s: N=%d is too wide", what, N);
   if ((y_type != WST_F32 && y_type != WST_BF16) || (out_type != WST_F32 && out_type != WST_BF16))
     return reject(ST_INVALID_ARG, "%s: unknown type", what);
   return ST_OK;
@@ -267,11 +303,11 @@ wst_status wst_moe_combine(int T, int top_k, int N, const void* y, long ldy, wst
   a.ws = static_cast<WsHeader*>(workspace);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (y_type == WST_F32) {
-    if (out_type == WST_F32) launch_combine<float, float>(a, s);
-    else launch_combine<float, __nv_bfloat16>(a, s);
+    if (out_type == WST_F32) launch_combine<float, float>(a, dev.num_sms, s);
+    else launch_combine<float, __nv_bfloat16>(a, dev.num_sms, s);
   } else {
-    if (out_type == WST_F32) launch_combine<__nv_bfloat16, float>(a, s);
-    else launch_combine<__nv_bfloat16, __nv_bfloat16>(a, s);
+    if (out_type == WST_F32) launch_combine<__nv_bfloat16, float>(a, dev.num_sms, s);
+    else launch_combine<__nv_bfloat16, __nv_bfloat16>(a, dev.num_sms, s);
   }
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? WST_OK : (wst_status)cuda_fail(e, "launch k_combine");
@@ -320,11 +356,11 @@ wst_status wst_moe_combine_backward(int T, int top_k, int N, const void* dout, l
   a.ws = static_cast<WsHeader*>(workspace);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (y_type == WST_F32) {
-    if (out_type == WST_F32) launch_combine_backward<float, float>(a, s);
-    else launch_combine_backward<float, __nv_bfloat16>(a, s);
+    if (out_type == WST_F32) launch_combine_backward<float, float>(a, dev.num_sms, s);
+    else launch_combine_backward<float, __nv_bfloat16>(a, dev.num_sms, s);
   } else {
-    if (out_type == WST_F32) launch_combine_backward<__nv_bfloat16, float>(a, s);
-    else launch_combine_backward<__nv_bfloat16, __nv_bfloat16>(a, s);
+    if (out_type == WST_F32) launch_combine_backward<__nv_bfloat16, float>(a, dev.num_sms, s);
+    else launch_combine_backward<__nv_bfloat16, __nv_bfloat16>(a, dev.num_sms, s);
   }
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? WST_OK : (wst_status)cuda_fail(e, "launch k_combine_backward");

@@ -25,13 +25,14 @@ namespace {
 
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanOne = 4096;
-constexpr int kPlanChunk = 2048;
+constexpr int kPlanOne = 2048;
+constexpr int kPlanChunk = 1024;
 constexpr int kPlanChunks = 128;
 constexpr int kPlanMaxExperts = 1024;
 
 struct PlanArgs {
   int pairs, top_k, E;
+  int bits;          // of an expert id
   int chunk;         // pairs per block, a multiple of 32 * kPlanWarps
   const int* experts;
   int* offsets;
@@ -43,7 +44,7 @@ struct PlanArgs {
 };
 
 // Expert of pair p, -1 for none; a bad id counts as none.
-__device__ __forceinline__ int plan_expert(const PlanArgs& a, long long p, long long end, bool latch) {
+__device__ __forceinline__ int plan_expert(const PlanArgs& a, int p, int end, bool latch) {
   if (p >= end) return -1;
   const int e = __ldg(a.experts + p);
   if (e >= 0 && e < a.E) return e;
@@ -55,9 +56,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_count(const PlanArgs a) {
   extern __shared__ int sm[];
   for (int e = threadIdx.x; e < a.E; e += kPlanThreads) sm[e] = 0;
   __syncthreads();
-  const long long p0 = (long long)blockIdx.x * a.chunk;
-  const long long p1 = min(p0 + a.chunk, (long long)a.pairs);
-  for (long long p = p0 + threadIdx.x; p < p1; p += kPlanThreads) {
+  const int p0 = (int)blockIdx.x * a.chunk;  // (pairs + chunk fits 32 bits)
+  const int p1 = min(p0 + a.chunk, a.pairs);
+#pragma unroll 4
+  for (int p = p0 + (int)threadIdx.x; p < p1; p += kPlanThreads) {
     const int e = plan_expert(a, p, p1, false);
     if (e >= 0) atomicAdd(&sm[e], 1);  // integers: the order does not matter
   }
@@ -71,36 +73,51 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_place(const PlanArgs a) {
   __shared__ int warp_total[kPlanWarps];
   int* offs = sm + kPlanWarps * a.E;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long p0 = (long long)blockIdx.x * a.chunk;
-  const long long p1 = min(p0 + a.chunk, (long long)a.pairs);
+  const int p0 = (int)blockIdx.x * a.chunk;
+  const int p1 = min(p0 + a.chunk, a.pairs);
   const int part = a.chunk / kPlanWarps;
-  const long long w0 = p0 + (long long)warp * part;
-  const long long w1 = min(w0 + part, p1);
+  const int w0 = p0 + warp * part;
+  const int w1 = min(w0 + part, p1);
   for (int i = threadIdx.x; i < kPlanWarps * a.E; i += kPlanThreads) sm[i] = 0;
   __syncthreads();
-  for (long long p = w0 + lane; p < w1; p += 32) {
+#pragma unroll 4
+  for (int p = w0 + lane; p < w1; p += 32) {
     const int e = plan_expert(a, p, w1, true);
     if (e >= 0) atomicAdd(&sm[warp * a.E + e], 1);
   }
   __syncthreads();
-  // Total of each expert, and of the chunks before this one.
-  for (int e = threadIdx.x; e < a.E; e += kPlanThreads) {
+  // Total of each expert, and of the chunks before this one: `per` threads share
+  // an expert's chunks (all 256 threads where there are few experts).
+  int per = 1;
+  while (per < 8 && per * 2 * a.E <= kPlanThreads) per *= 2;
+  for (int i0 = warp * 32; i0 < a.E * per; i0 += kPlanThreads) {
+    // (whole warps; the threads of an expert are neighbours)
+    const int e = (i0 + lane) / per, part_of = lane & (per - 1);
     int before = 0, total = 0;
-    if (a.counts) {
+    if (e < a.E) {
+      if (a.counts) {
 #pragma unroll 8
-      for (int c = 0; c < (int)gridDim.x; ++c) {
-        const int n = __ldg(a.counts + (long long)c * a.E + e);
-        total += n;
-        if (c < (int)blockIdx.x) before += n;
+        for (int c = part_of; c < (int)gridDim.x; c += per) {
+          const int n = __ldg(a.counts + c * a.E + e);
+          total += n;
+          if (c < (int)blockIdx.x) before += n;
+        }
+      } else if (part_of == 0) {
+        for (int w = 0; w < kPlanWarps; ++w) total += sm[w * a.E + e];
       }
-    } else {
-      for (int w = 0; w < kPlanWarps; ++w) total += sm[w * a.E + e];
     }
-    offs[e] = total;
-    for (int w = 0; w < kPlanWarps; ++w) {
-      const int n = sm[w * a.E + e];
-      sm[w * a.E + e] = before;
-      before += n;
+    __syncwarp();
+    for (int o = 1; o < per; o <<= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    if (e < a.E && part_of == 0) {
+      offs[e] = total;
+      for (int w = 0; w < kPlanWarps; ++w) {
+        const int n = sm[w * a.E + e];
+        sm[w * a.E + e] = before;
+        before += n;
+      }
     }
   }
   __syncthreads();
@@ -133,11 +150,17 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_place(const PlanArgs a) {
     a.row_pair[r] = -1;
     a.row_token[r] = -1;
   }
-  // Place this warp's pairs in order.
+  // Place this warp's pairs in order, 32 at a time.  The lanes with the same
+  // expert are found bit by bit (ten ballots at most; a match instruction takes a
+  // step for each different expert).
   int* first = sm + warp * a.E;
-  for (long long p = w0 + lane; p - lane < w1; p += 32) {
+  for (int p = w0 + lane; p - lane < w1; p += 32) {
     const int e = plan_expert(a, p, w1, false);
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    uint32_t same = __ballot_sync(0xffffffffu, e >= 0);
+    for (int bit = 0; bit < a.bits; ++bit) {
+      const uint32_t ones = __ballot_sync(0xffffffffu, (e >> bit) & 1);
+      same &= (e >> bit) & 1 ? ones : ~ones;
+    }
     const int rank = __popc(same & ((1u << lane) - 1u));
     int row = -1;
     if (e >= 0) row = offs[e] + first[e] + rank;
@@ -146,15 +169,16 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_place(const PlanArgs a) {
     __syncwarp();
     if (p < w1) a.position[p] = row;
     if (row >= 0) {
-      a.row_pair[row] = (int)p;
-      a.row_token[row] = (int)(p / a.top_k);
+      a.row_pair[row] = p;
+      a.row_token[row] = (int)((unsigned)p / (unsigned)a.top_k);
     }
   }
 }
 
 int plan_blocks(long long pairs, int* chunk) {
   if (pairs <= kPlanOne) {
-    *chunk = kPlanOne;
+    *chunk = (int)((pairs + 255) / 256 * 256);
+    if (*chunk == 0) *chunk = 256;
     return 1;
   }
   constexpr long long unit = 32 * kPlanWarps;
@@ -193,7 +217,7 @@ wst_status wst_moe_plan(int num_tokens, int top_k, const int* experts, int num_e
   if (num_experts > kPlanMaxExperts)
     return (wst_status)reject(ST_UNSUPPORTED, "plan: %d experts: this build supports up to %d", num_experts, kPlanMaxExperts);
   const long long pairs = (long long)num_tokens * top_k;
-  if (pairs > 0x7fffffffLL - kPlanOne) return (wst_status)reject(ST_INVALID_ARG, "plan: too many pairs");
+  if (pairs > 0x7fffffffLL - (1 << 25)) return (wst_status)reject(ST_INVALID_ARG, "plan: too many pairs");
   if (!offsets || !workspace || (pairs && (!experts || !row_pair || !row_token || !position)))
     return (wst_status)reject(ST_INVALID_ARG, "plan: NULL array");
   const size_t need = wst_moe_plan_workspace_size((int)pairs, num_experts);
@@ -222,6 +246,7 @@ wst_status wst_moe_plan(int num_tokens, int top_k, const int* experts, int num_e
   a.row_token = row_token;
   a.position = position;
   a.ws = static_cast<WsHeader*>(workspace);
+  while ((1 << a.bits) < num_experts) ++a.bits;
   const int blocks = plan_blocks(pairs, &a.chunk);
   a.counts = blocks > 1 ? reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + kWsHeaderBytes) : nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -47,7 +47,9 @@ struct RouteArgs {
   long long ld;
   const float* bias;
   int groups, top_groups, group_best;
-  uint32_t group_magic;  // e / (E / groups) == e * group_magic >> 20 for e < 1024
+  int group_size;
+  int group_shift;       // 2^group_shift lanes share the scan of a group
+  uint32_t group_magic;  // e / group_size == e * group_magic >> 20 for e < 1024
   int renorm;
   float scale;
   int* experts;
@@ -59,10 +61,10 @@ __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __b
 
 // Order-preserving keys: larger value, larger key; NaN above +inf (as
 // torch.topk ranks it), -0 equal to +0; 0 stands for "not a candidate".
+// (The addition makes -0 +0 and any NaN the one with bits 0x7fffffff.)
 __device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0xffffffffu;
-  const uint32_t b = __float_as_uint(v + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const int32_t b = __float_as_int(v + 0.0f);
+  return (uint32_t)(b ^ ((b >> 31) | (int32_t)0x80000000));
 }
 __device__ __forceinline__ uint64_t order_key(double v) {
   if (v != v) return ~0ull;
@@ -103,17 +105,18 @@ template <bool SOFTMAX, typename R>
 __device__ __forceinline__ R route_score(float x, const RowStats<R>& st) {
   if (x <= kRouteOff) return R(0);
   if constexpr (SOFTMAX) return route_exp(R(x) - st.top) / st.sum;
+  else if constexpr (sizeof(R) == 4) return __fdividef(1.0f, 1.0f + expf(-x));  // (two units off at most)
   else return R(1) / (R(1) + route_exp(-R(x)));
 }
 
 // Bound on the error of an fp32 score s of logit x.  sigmoid: expf 2^-22, the
-// sum and the quotient 2^-24 each.  softmax: the sum of up to 1024 terms in a
+// sum 2^-24, the approximate quotient 2^-22.  softmax: the sum of up to 1024 terms in a
 // tree of at most 37 additions, expf and the quotient below 2^-18; the rounded
 // difference x - top adds |x - top| 2^-24, and s |x - top| <= max s / e.
 template <bool SOFTMAX>
 __device__ __forceinline__ float score_error(float s, float s_max_if_softmax, const RowStats<float>& st) {
   if constexpr (SOFTMAX) return 0x1p-18f * fminf(s, s_max_if_softmax / st.sum) + 0x1p-24f / st.sum;
-  else return 0x1p-21f * s;
+  else return 0x1.4p-21f * s;
 }
 
 template <typename R>
@@ -164,10 +167,8 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
     }
     __syncwarp();
     // `lpg` lanes scan each group's members for its two largest keys.
-    const int size = a.E / a.groups;
-    int lpg = 1;
-    while (lpg * 2 * a.groups <= 32) lpg *= 2;
-    const int g = lane / lpg, part = lane % lpg;
+    const int size = a.group_size, lpg = 1 << a.group_shift;
+    const int g = lane >> a.group_shift, part = lane & (lpg - 1);
     K k1 = 0, k2 = 0;
     if (g < a.groups) {
       for (int i = part; i < size; i += lpg) {
@@ -215,27 +216,42 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
       if (e < a.E && !((kept_lanes >> (ge * lpg)) & 1u)) key[j] = 0;
     }
   }
+  // Every lane keeps its two best candidates and looks through its keys again
+  // only when both are taken.
   mine = -1;
-  K best = 0;
-  int bj = 0;
+  uint32_t taken = 0;
+  K b1, b2;
+  int j1, j2, have;
+  auto look = [&]() {
+    b1 = b2 = 0;
+    j1 = j2 = 0;
 #pragma unroll
-  for (int j = 0; j < VPL; ++j)
-    if (key[j] > best) { best = key[j]; bj = j; }
+    for (int j = 0; j < VPL; ++j) {
+      const K k = (taken >> j) & 1u ? K(0) : key[j];
+      if (k > b1) {
+        b2 = b1;
+        j2 = j1;
+        b1 = k;
+        j1 = j;
+      } else if (k > b2) {
+        b2 = k;
+        j2 = j;
+      }
+    }
+    have = 2;
+  };
+  look();
   for (int r = 0; r <= a.top_k; ++r) {
-    const K top = warp_max(best);
+    const K top = warp_max(b1);
     if (top == 0) break;
-    const unsigned e = best == top ? (unsigned)(bj * 32 + lane) : 0xffffffffu;
+    const unsigned e = b1 == top ? (unsigned)(j1 * 32 + lane) : 0xffffffffu;
     const unsigned win = __reduce_min_sync(0xffffffffu, e);
     if (lane == r) mine = (int)win;
     if (e == win) {
-      best = 0;
-      int nj = 0;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        if (j == bj) key[j] = 0;
-        if (key[j] > best) { best = key[j]; nj = j; }
-      }
-      bj = nj;
+      taken |= 1u << j1;
+      b1 = b2;
+      j1 = j2;
+      if (--have == 0) look();
     }
   }
   return sure;
@@ -529,6 +545,8 @@ wst_status wst_moe_route(int T, int E, int top_k, const void* logits, long ld, w
   a.top_groups = a.groups == 1 ? 1 : top_groups;
   a.group_best = group_best;
   const int size = E / a.groups;
+  a.group_size = size;
+  while ((2 << a.group_shift) * a.groups <= 32) ++a.group_shift;
   a.group_magic = (uint32_t)(((1 << 20) + size - 1) / size);
   a.renorm = renorm != 0;
   a.scale = scale;
