@@ -36,29 +36,48 @@ struct CombineArgs {
   WsHeader* ws;
 };
 
-// Eight columns from c on; columns from n on read as 0 and are not stored.
-__device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
+// Eight columns as loaded (one 16-byte word of bf16, two of fp32); columns from n
+// on read as 0 and are not stored.
+template <typename X>
+struct Eight {
+  uint4 w[sizeof(X) / 2];
+};
+template <typename X>
+__device__ __forceinline__ Eight<X> load8(const X* p, int n) {
+  Eight<X> r;
   if (n >= 8) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? __ldg(p + i) : 0.0f;
+    for (int i = 0; i < (int)sizeof(X) / 2; ++i) r.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  } else {
+    uint32_t u[sizeof(X) * 2];
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(X) * 2; ++i) u[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        if constexpr (sizeof(X) == 4) u[i] = __float_as_uint(__ldg(reinterpret_cast<const float*>(p) + i));
+        else u[i >> 1] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + i) << (16 * (i & 1));
+      }
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(X) / 2; ++i) r.w[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+  }
+  return r;
+}
+__device__ __forceinline__ void unpack8(const Eight<float>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(r.w[i].x);
+    v[4 * i + 1] = __uint_as_float(r.w[i].y);
+    v[4 * i + 2] = __uint_as_float(r.w[i].z);
+    v[4 * i + 3] = __uint_as_float(r.w[i].w);
   }
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, int n, float (&v)[8]) {
-  if (n >= 8) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void unpack8(const Eight<__nv_bfloat16>& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? __bfloat162float(__ldg(p + i)) : 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
 __device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
@@ -114,21 +133,23 @@ __global__ void __launch_bounds__(kCombThreads) k_combine(const CombineArgs a, i
         w[i] = r >= 0 && a.weights ? __ldg(a.weights + (long long)t * a.top_k + i0 + i) : 1.0f;
         row[i] = r >= 0 ? (long long)r * a.ldy : -1;
       }
-      float x[V][KC][8];
+      Eight<Y> raw[V][KC];
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
           const int c = c0 + v * tpt * 8;
-          if (row[i] >= 0 && c < a.N) load8(y + row[i] + c, a.N - c, x[v][i]);
+          if (row[i] >= 0 && c < a.N) raw[v][i] = load8(y + row[i] + c, a.N - c);
         }
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < KC; ++i)
           if (row[i] >= 0) {
+            float x[8];
+            unpack8(raw[v][i], x);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) acc[v][c] = fmaf(w[i], x[v][i][c], acc[v][c]);
+            for (int c = 0; c < 8; ++c) acc[v][c] = fmaf(w[i], x[c], acc[v][c]);
           }
     }
 #pragma unroll
@@ -158,29 +179,41 @@ __global__ void __launch_bounds__(kCombThreads) k_combine_backward(const Combine
       w[i] = row[i] >= 0 && a.weights ? __ldg(a.weights + (long long)t * a.top_k + i0 + i) : 1.0f;
       dot[i] = 0.0f;
     }
-#pragma unroll 2
-    for (int c = me * 8; there && c < a.N; c += tpt * 8) {
-      const int n = a.N - c;
-      float d[8];
-      load8(dout + c, n, d);
-      float x[KC][8];
-      if (a.dweights) {
+    for (int c0 = me * 8; there && c0 < a.N; c0 += 2 * tpt * 8) {
+      Eight<O> draw[2];
+      Eight<Y> raw[2][KC];
 #pragma unroll
-        for (int i = 0; i < KC; ++i)
-          if (row[i] >= 0) load8(static_cast<const Y*>(a.y) + (long long)row[i] * a.ldy + c, n, x[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < KC; ++i) {
-        if (row[i] < 0) continue;
+      for (int v = 0; v < 2; ++v) {
+        const int c = c0 + v * tpt * 8;
+        if (c >= a.N) continue;
+        draw[v] = load8(dout + c, a.N - c);
         if (a.dweights) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dot[i] = fmaf(d[j], x[i][j], dot[i]);
+          for (int i = 0; i < KC; ++i)
+            if (row[i] >= 0) raw[v][i] = load8(static_cast<const Y*>(a.y) + (long long)row[i] * a.ldy + c, a.N - c);
         }
-        if (a.dy) {
-          float g[8];
+      }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = w[i] * d[j];
-          store8(static_cast<Y*>(a.dy) + (long long)row[i] * a.lddy + c, n, g);
+      for (int v = 0; v < 2; ++v) {
+        const int c = c0 + v * tpt * 8;
+        if (c >= a.N) continue;
+        float d[8];
+        unpack8(draw[v], d);
+#pragma unroll
+        for (int i = 0; i < KC; ++i) {
+          if (row[i] < 0) continue;
+          if (a.dweights) {
+            float x[8];
+            unpack8(raw[v][i], x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dot[i] = fmaf(d[j], x[j], dot[i]);
+          }
+          if (a.dy) {
+            float g[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = w[i] * d[j];
+            store8(static_cast<Y*>(a.dy) + (long long)row[i] * a.lddy + c, a.N - c, g);
+          }
         }
       }
     }
@@ -223,9 +256,9 @@ template <typename Y, typename O>
 void launch_combine(const CombineArgs& a, int sms, cudaStream_t s) {
   const int tpt = threads_per_token(a.T, a.N, sms), per = kCombThreads / tpt;
   const unsigned grid = (unsigned)((a.T + per - 1) / per);
-  if (a.top_k == 1) k_combine<Y, O, 1, 4><<<grid, kCombThreads, 0, s>>>(a, tpt);
-  else if (a.top_k == 2) k_combine<Y, O, 2, 2><<<grid, kCombThreads, 0, s>>>(a, tpt);
-  else k_combine<Y, O, 4, 1><<<grid, kCombThreads, 0, s>>>(a, tpt);
+  if (a.top_k == 1) k_combine<Y, O, 1, 8><<<grid, kCombThreads, 0, s>>>(a, tpt);
+  else if (a.top_k == 2) k_combine<Y, O, 2, 4><<<grid, kCombThreads, 0, s>>>(a, tpt);
+  else k_combine<Y, O, 4, 2><<<grid, kCombThreads, 0, s>>>(a, tpt);
 }
 
 template <typename Y, typename O>

@@ -23,7 +23,7 @@ namespace wst {
 
 namespace {
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanOne = 2048;
 constexpr int kPlanChunk = 1024;
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_place(const PlanArgs a) {
   }
   __syncthreads();
   // Total of each expert, and of the chunks before this one: `per` threads share
-  // an expert's chunks (all 256 threads where there are few experts).
+  // an expert's chunks (all threads where there are few experts).
   int per = 1;
   while (per < 8 && per * 2 * a.E <= kPlanThreads) per *= 2;
   for (int i0 = warp * 32; i0 < a.E * per; i0 += kPlanThreads) {
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_place(const PlanArgs a) {
     int before = 0, total = 0;
     if (e < a.E) {
       if (a.counts) {
-#pragma unroll 8
+#pragma unroll 16
         for (int c = part_of; c < (int)gridDim.x; c += per) {
           const int n = __ldg(a.counts + c * a.E + e);
           total += n;
@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_place(const PlanArgs a) {
 
 int plan_blocks(long long pairs, int* chunk) {
   if (pairs <= kPlanOne) {
-    *chunk = (int)((pairs + 255) / 256 * 256);
-    if (*chunk == 0) *chunk = 256;
+    constexpr long long unit = 32 * kPlanWarps;
+    *chunk = (int)std::max(unit, (pairs + unit - 1) / unit * unit);
     return 1;
   }
   constexpr long long unit = 32 * kPlanWarps;
@@ -251,6 +251,7 @@ wst_status wst_moe_plan(int num_tokens, int top_k, const int* experts, int num_e
   a.counts = blocks > 1 ? reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + kWsHeaderBytes) : nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t smem = (size_t)(kPlanWarps + 1) * num_experts * 4;
+  WST_TRY(ensure_smem_attr((const void*)k_plan_place, smem));
   if (blocks > 1) k_plan_count<<<blocks, kPlanThreads, (size_t)num_experts * 4, s>>>(a);
   k_plan_place<<<blocks, kPlanThreads, smem, s>>>(a);
   const cudaError_t e = cudaGetLastError();

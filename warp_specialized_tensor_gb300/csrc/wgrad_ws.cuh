@@ -22,8 +22,8 @@
 // the fp32 output stream take about as long as each other.
 //
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (leader), warp 2 tensor
-// memory and offset check, warp 3 row masks, warps 4-7 epilogue (32 output rows
-// each; through swizzled shared memory and TMA stores, or TMA adds when the
+// memory and offset check, warp 3 row masks, warps 4-11 epilogue (32 output rows
+// by 128 columns each; through swizzled shared memory and TMA stores, or TMA adds when the
 // gradient accumulates).
 #pragma once
 
@@ -33,15 +33,16 @@ namespace wst {
 
 constexpr int kWgTile = 256;    // n and k per pair
 constexpr int kWgBK = 64;       // tokens per block
-constexpr int kWgStages = 6;
-constexpr int kWgEpiWarps = 4;
+constexpr int kWgStages = 4;
+constexpr int kWgEpiWarps = 8;
+constexpr int kWgStgBufs = 3;     // staging buffers per epilogue warp
 constexpr int kWgThreads = 128 + 32 * kWgEpiWarps;
 constexpr int kWgChunk = 64 * kWgBK * 2;        // 64 features x 64 tokens
 constexpr int kWgOpBytes = 2 * kWgChunk;        // this CTA's 128 features of one operand
 constexpr int kWgStageBytes = 2 * kWgOpBytes;
 constexpr int kWgStgBytes = 32 * 128;           // 32 output rows of 128 bytes
 constexpr size_t kWgSmemBytes =
-    (size_t)kWgStages * kWgStageBytes + kWgEpiWarps * 2 * kWgStgBytes + 512 + 1024;
+    (size_t)kWgStages * kWgStageBytes + kWgEpiWarps * kWgStgBufs * kWgStgBytes + 512 + 1024;
 static_assert(kWgSmemBytes <= 232448, "shared memory per CTA");
 
 struct WgArgs {
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   uint8_t* smD = smem;
   uint8_t* smA = smD + kWgStages * kWgOpBytes;
   uint8_t* smStg = smA + kWgStages * kWgOpBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smStg + kWgEpiWarps * 2 * kWgStgBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smStg + kWgEpiWarps * kWgStgBufs * kWgStgBytes);
   // bars: full[S] | empty[S] | acc_full[2] | acc_empty[2] | masked[S] | go[S]
   constexpr int kNumBars = 4 * kWgStages + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
@@ -272,8 +273,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue
-    const int q = warp & 3;
-    const uint32_t stg0 = smem_addr(smStg + (warp - 4) * 2 * kWgStgBytes);
+    const int q = warp & 3, half = (warp - 4) >> 2;  // 32 rows, 128 columns of them
+    const uint32_t stg0 = smem_addr(smStg + (warp - 4) * kWgStgBufs * kWgStgBytes);
     int sbuf = 0, acc = 0;
     uint32_t acc_phase = 0;
     for (int t = pair_id; t < tiles; t += pairs) {
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       const uint32_t t_lane = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kWgTile);
       constexpr int kCols = OUT_F32 ? 32 : 64;  // columns per 128-byte row
 #pragma unroll 1
-      for (int c = 0; c < kWgTile; c += kCols) {
+      for (int c = half * (kWgTile / 2); c < (half + 1) * (kWgTile / 2); c += kCols) {
         if (n >= p.N || tl.k0 + c >= p.K) break;  // (warp-uniform; nothing of it is stored)
         uint32_t w[32];
         if constexpr (OUT_F32) {
@@ -331,8 +332,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           continue;
         }
         const uint32_t stg = stg0 + sbuf * kWgStgBytes;
-        // the store that read this buffer (not the newest one) is done with it
-        if (lane == 0) bulk_wait_group_read<1>();
+        // the store that read this buffer (not the newest ones) is done with it
+        if (lane == 0) bulk_wait_group_read<kWgStgBufs - 1>();
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < 8; ++u)
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           else tma_store_3d(&tmOut, stg, tl.k0 + c, n, tl.g);
           bulk_commit_group();
         }
-        sbuf ^= 1;
+        sbuf = sbuf + 1 == kWgStgBufs ? 0 : sbuf + 1;
       }
       if (!empty) {
         tc_fence_before_sync();
