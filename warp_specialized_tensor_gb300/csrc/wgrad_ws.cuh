@@ -14,8 +14,11 @@
 // belong to the next group (or to none) are overwritten with zeros in shared
 // memory by warp 3 of both CTAs before that block is multiplied -- in both
 // operands, since a NaN or an infinity there would survive a zero on one side.
-// The leader's barrier alone sees both CTAs' copies land, so the leader's warp 3
-// passes the word on to the other CTA's.
+// Such a block's copies complete on a barrier of each CTA's own, and the tensor
+// core waits for both masks instead of the copies.  A group's blocks run
+// backwards, so the one with masked rows is a tile's first: its copies land
+// several blocks ahead of their use (as a tile's last block it held the tensor
+// core up for about 2000 cycles a tile).
 //
 // What bounds it: per tile 2 (N + K) bytes a token in from L2, 256 x 256 outputs
 // to HBM; at about 450 tokens a group the products (512 cycles per 64 tokens) and
@@ -33,16 +36,17 @@ namespace wst {
 
 constexpr int kWgTile = 256;    // n and k per pair
 constexpr int kWgBK = 64;       // tokens per block
-constexpr int kWgStages = 4;
+constexpr int kWgStages = 6;
 constexpr int kWgEpiWarps = 8;
-constexpr int kWgStgBufs = 3;     // staging buffers per epilogue warp
+constexpr int kWgStgBufs = 1;     // staging buffers per epilogue warp
 constexpr int kWgThreads = 128 + 32 * kWgEpiWarps;
 constexpr int kWgChunk = 64 * kWgBK * 2;        // 64 features x 64 tokens
 constexpr int kWgOpBytes = 2 * kWgChunk;        // this CTA's 128 features of one operand
 constexpr int kWgStageBytes = 2 * kWgOpBytes;
 constexpr int kWgStgBytes = 32 * 128;           // 32 output rows of 128 bytes
+constexpr int kWgTabMax = 256;                  // offsets kept in shared memory (fewer groups than that)
 constexpr size_t kWgSmemBytes =
-    (size_t)kWgStages * kWgStageBytes + kWgEpiWarps * kWgStgBufs * kWgStgBytes + 512 + 1024;
+    (size_t)kWgStages * kWgStageBytes + kWgEpiWarps * kWgStgBufs * kWgStgBytes + 512 + kWgTabMax * 4 + 1024;
 static_assert(kWgSmemBytes <= 232448, "shared memory per CTA");
 
 struct WgArgs {
@@ -64,7 +68,7 @@ struct WgTile {
 };
 
 // Tile t: k fastest, so that consecutive pairs share the dC columns.
-__device__ __forceinline__ WgTile wg_tile(const WgArgs& p, int t) {
+__device__ __forceinline__ WgTile wg_tile(const WgArgs& p, const int* offsets, int t) {
   WgTile x;
   const int per = p.n_tiles * p.k_tiles;
   x.g = t / per;
@@ -72,8 +76,8 @@ __device__ __forceinline__ WgTile wg_tile(const WgArgs& p, int t) {
   const int ni = r / p.k_tiles;
   x.n0 = ni * kWgTile;
   x.k0 = (r - ni * p.k_tiles) * kWgTile;
-  const int a = min(max(__ldg(p.offsets + x.g), 0), p.M_total);
-  const int b = min(max(__ldg(p.offsets + x.g + 1), a), p.M_total);
+  const int a = min(max(offsets[x.g], 0), p.M_total);
+  const int b = min(max(offsets[x.g + 1], a), p.M_total);
   x.r0 = a;
   x.rows = b - a;
   x.blocks = (x.rows + kWgBK - 1) / kWgBK;
@@ -111,7 +115,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   uint8_t* smA = smD + kWgStages * kWgOpBytes;
   uint8_t* smStg = smA + kWgStages * kWgOpBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smStg + kWgEpiWarps * kWgStgBufs * kWgStgBytes);
-  // bars: full[S] | empty[S] | acc_full[2] | acc_empty[2] | masked[S] | go[S]
+  // bars: full[S] | empty[S] | acc_full[2] | acc_empty[2] | masked[S] | own[S]
   constexpr int kNumBars = 4 * kWgStages + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   volatile uint32_t* abort_flag = tmem_slot + 1;
@@ -126,14 +130,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   auto acce_bar = [&](int a) { return bar_base + 8u * (2 * kWgStages + 2 + a); };
   // One pair per stage: several groups may end within the ring at once.
   auto masked_bar = [&](int s) { return bar_base + 8u * (2 * kWgStages + 4 + s); };  // leader: both CTAs' rows are zeroed
-  auto go_bar = [&](int s) { return bar_base + 8u * (3 * kWgStages + 4 + s); };      // the other CTA: the copies have landed
+  auto own_bar = [&](int s) { return bar_base + 8u * (3 * kWgStages + 4 + s); };     // this CTA's copies of a block to mask
   const uint32_t rank = cluster_ctarank();
   const int pair_id = (int)(blockIdx.x / 2), pairs = (int)(gridDim.x / 2);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kWgStages; ++s) {
       mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), rank == 0 ? 2 : 1);  // the MMAs' commit; the leader's warp 3 has seen the block
+      mbar_init(empty_bar(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(accf_bar(a), 1);
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     }
     for (int s = 0; s < kWgStages; ++s) {
       mbar_init(masked_bar(s), 2);
-      mbar_init(go_bar(s), 1);
+      mbar_init(own_bar(s), 1);
     }
     *abort_flag = 0u;
     fence_mbar_init();
@@ -153,6 +157,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     tmem_alloc<2>(smem_addr(tmem_slot), 512);
     tmem_relinquish<2>();
   }
+  // (a tile's rows are looked up by every role; a load from global memory there
+  // holds up the start of each tile)
+  int* tab = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 512);
+  const int* offsets = p.G < kWgTabMax ? tab : p.offsets;
+  if (warp == 3 && p.G < kWgTabMax)
+    for (int i = (int)lane; i <= p.G; i += 32) tab[i] = __ldg(p.offsets + i);
   tc_fence_before_sync();
   __syncthreads();
   cluster_sync();
@@ -166,18 +176,28 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       WgRing ring;
       bool ok = true;
       for (int t = pair_id; ok && t < tiles; t += pairs) {
-        const WgTile tl = wg_tile(p, t);
+        const WgTile tl = wg_tile(p, offsets, t);
         const int nx = tl.n0 + (int)rank * 128, kx = tl.k0 + (int)rank * 128;
         for (int b = 0; b < tl.blocks; ++b) {
           ok = wait_phase_cluster(guard, empty_bar(ring.stage), ring.phase ^ 1u, (kRoleProducer << 16) | ring.stage);
           if (!ok) break;
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(ring.stage), 2u * kWgStageBytes);
-          const uint32_t fb = map_to_cta(full_bar(ring.stage), 0);
           const uint32_t d = smem_addr(smD + ring.stage * kWgOpBytes), a = smem_addr(smA + ring.stage * kWgOpBytes);
-          const int y = tl.r0 + b * kWgBK;
-          for (int c = 0; c < 2; ++c) {
-            tma_load_2d_pair(d + c * kWgChunk, &tmD, fb, nx + c * 64, y);
-            tma_load_2d_pair(a + c * kWgChunk, &tmA, fb, kx + c * 64, y);
+          const int y = tl.r0 + (tl.blocks - 1 - b) * kWgBK;
+          if (b == 0 && (tl.last & 15)) {
+            if (rank == 0) mbar_arrive(full_bar(ring.stage));  // (completes the phase; the masks stand for the copies)
+            const uint32_t own = own_bar(ring.stage);
+            mbar_arrive_expect_tx(own, kWgStageBytes);
+            for (int c = 0; c < 2; ++c) {
+              tma_load_2d(d + c * kWgChunk, &tmD, own, nx + c * 64, y);
+              tma_load_2d(a + c * kWgChunk, &tmA, own, kx + c * 64, y);
+            }
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(ring.stage), 2u * kWgStageBytes);
+            const uint32_t fb = map_to_cta(full_bar(ring.stage), 0);
+            for (int c = 0; c < 2; ++c) {
+              tma_load_2d_pair(d + c * kWgChunk, &tmD, fb, nx + c * 64, y);
+              tma_load_2d_pair(a + c * kWgChunk, &tmA, fb, kx + c * 64, y);
+            }
           }
           ring.next();
         }
@@ -194,18 +214,18 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       WgRing ring;
       int acc = 0;
       uint32_t acc_phase = 0, masked_phase = 0;  // (bit s: the parity of stage s)
-      bool ok = true;
+      bool ok = true, full_ok = false;
       for (int t = pair_id; ok && t < tiles; t += pairs) {
-        const WgTile tl = wg_tile(p, t);
+        const WgTile tl = wg_tile(p, offsets, t);
         if (tl.blocks == 0) continue;
         ok = wait_phase_cluster(guard, acce_bar(acc), acc_phase ^ 1u, (kRoleMma << 16) | 0x100 | acc);
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kWgTile);
         for (int b = 0; b < tl.blocks; ++b) {
-          ok = wait_phase(guard, full_bar(ring.stage), ring.phase, (kRoleMma << 16) | ring.stage);
+          ok = full_ok || wait_phase(guard, full_bar(ring.stage), ring.phase, (kRoleMma << 16) | ring.stage);
           int steps = kWgBK / 16;
-          if (ok && b + 1 == tl.blocks) {
+          if (ok && b == 0) {
             steps = (tl.last + 15) / 16;
             if (tl.last & 15) {
               ok = wait_phase_cluster(guard, masked_bar(ring.stage), (masked_phase >> ring.stage) & 1u, (kRoleMma << 16) | 0x200);
@@ -215,11 +235,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           if (!ok) break;
           tc_fence_after_sync();
           const uint32_t d = smem_addr(smD + ring.stage * kWgOpBytes), a = smem_addr(smA + ring.stage * kWgOpBytes);
+          const uint32_t this_empty = empty_bar(ring.stage);
+          ring.next();
+          // (a barrier test takes long while products run: ahead of its use)
+          full_ok = mbar_test_wait(full_bar(ring.stage), ring.phase);
           for (int k = 0; k < steps; ++k)
             umma_bf16<2>(d_tmem, sdesc_sw128(d + k * 2048, kWgChunk, 1024), sdesc_sw128(a + k * 2048, kWgChunk, 1024),
                          idesc, (b | k) != 0 ? 1u : 0u);
-          umma_commit_pair(empty_bar(ring.stage), 0x3);
-          ring.next();
+          umma_commit_pair(this_empty, 0x3);
         }
         if (!ok) break;
         umma_commit_pair(accf_bar(acc), 0x3);
@@ -231,32 +254,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   } else if (warp == 3) {
     // ------------------------------------------------------------------ row masks
     WgRing ring;
-    uint32_t go_phase = 0;  // (bit s: the parity of stage s)
+    uint32_t own_phase = 0;  // (bit s: the parity of stage s)
     bool ok = true;
     for (int t = pair_id; ok && t < tiles; t += pairs) {
-      const WgTile tl = wg_tile(p, t);
-      if (tl.blocks == 0) continue;
-      // The leader follows every block, since a barrier's parity tells two
-      // neighbouring phases apart only; its arrival on the empty barrier keeps
-      // the ring from wrapping past it.
-      for (int b = 0; b < tl.blocks; ++b) {
-        const bool mask = b + 1 == tl.blocks && (tl.last & 15);
-        if (rank == 0) {
-          ok = warp_wait_phase(guard, full_bar(ring.stage), ring.phase, (kRoleFlag << 16) | ring.stage);
-          if (!ok) break;
-          if (lane == 0) {
-            if (mask) mbar_arrive_cluster(map_to_cta(go_bar(ring.stage), 1));
-            mbar_arrive(empty_bar(ring.stage));
-          }
-        } else if (mask) {
-          ok = warp_wait_phase_cluster(guard, go_bar(ring.stage), (go_phase >> ring.stage) & 1u, (kRoleFlag << 16) | 0x100);
-          go_phase ^= 1u << ring.stage;
-          if (!ok) break;
-        }
-        if (!mask) {
-          ring.next();
-          continue;
-        }
+      const WgTile tl = wg_tile(p, offsets, t);
+      if (tl.blocks > 0 && (tl.last & 15)) {
+        ok = warp_wait_phase(guard, own_bar(ring.stage), (own_phase >> ring.stage) & 1u, (kRoleFlag << 16) | ring.stage);
+        if (!ok) break;
+        own_phase ^= 1u << ring.stage;
         // Rows last .. of the step, 128 bytes each, in the four chunks: eight
         // lanes per row (whole rows, so the swizzle does not matter).
         const int rows = 16 - (tl.last & 15);
@@ -268,8 +273,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(map_to_cta(masked_bar(ring.stage), 0));
-        ring.next();
       }
+      for (int b = 0; b < tl.blocks; ++b) ring.next();
     }
   } else {
     // ------------------------------------------------------------------ epilogue
@@ -278,7 +283,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     int sbuf = 0, acc = 0;
     uint32_t acc_phase = 0;
     for (int t = pair_id; t < tiles; t += pairs) {
-      const WgTile tl = wg_tile(p, t);
+      const WgTile tl = wg_tile(p, offsets, t);
       const bool empty = tl.blocks == 0;
       if (empty && p.accumulate) continue;
       if (!empty) {
