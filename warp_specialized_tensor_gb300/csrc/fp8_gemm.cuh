@@ -23,24 +23,28 @@
 // of an SM's load path.)
 //
 // What bounds it: without the scaled sums the copies and products of 8192^3 take
-// 307 us (3586 TFLOP/s); with them 617 us, about 1350 cycles per K block of a
-// 256 x 256 tile, of which the epilogue's instruction stream (about 230 per warp
-// at two warps per sub-core, few of them independent) takes nearly all: a
-// barrier test takes about 200 cycles while products run even on a phase long
-// complete, so the issuer and the epilogue test their next barrier ahead of its
-// use.  Measured and dropped: two accumulators of 128 columns each per K block
-// (749 us; N = 128 products take the tensor core nearly as long as N = 256), four
-// epilogue warps per sub-core with 96 registers each (840 us, sums spilled).
+// 307 us (3586 TFLOP/s); with them 527 us (2085), about 1050 cycles per K block of
+// a 256 x 256 tile, which is the epilogue's chain of a barrier wait (about 200
+// cycles while products run, even on a phase long complete), four rounds of
+// tensor-memory loads and packed multiply-adds, and the hand-back, at two warps
+// per sub-core.  Measured and dropped: testing the next barriers ahead of their
+// use (617 us: a test holds the warp up as long as a wait); the weights' scale
+// multiplied in by the epilogue (+50 us); two accumulators of 128 columns per K
+// block (749 us), tiles of 128 tokens with four accumulators (820 us), sixteen
+// epilogue warps with 96 registers each (840 us, sums spilled).
 //
 // Roles per CTA (persistent, one CTA per SM, pairs in clusters of 2):
 //   warp 0     TMA producer: this CTA's 128 rows of B[g] and its half of the
 //              token tile, 128 bytes of K each; both CTAs' copies complete on
 //              the leader's full[s].
-//   warp 1     MMA issuer (leader CTA only), kind::f8f6f4, M = 256.
-//   warp 2     tensor-memory allocation, offset check.
+//   warps 1-2  MMA issuers (leader CTA only), kind::f8f6f4, M = 256: a unit's
+//              even and odd K blocks, one accumulator each (either's two waits
+//              per block take most of the 512 cycles of its products).  Warp 2
+//              also allocates the tensor memory and checks the offsets.
 //   warp 3     scales to shared memory, four K blocks at a time, in 4-byte
 //              asynchronous copies (a group may start at any row; loads through
-//              registers could not run far enough ahead).
+//              registers could not run far enough ahead); with 128 x 128 weight
+//              scales it multiplies the token scales by the CTA's one.
 //   warps 4-11 epilogue: two warps per 32 features, one for each half of the tokens.
 //
 // Few tiles (short token tiles of a decoding step): when the tiles fill less
@@ -49,6 +53,8 @@
 // (a counter per tile and CTA, which it sets back to 0) adds them in the order
 // of the splits, so the result does not depend on which one is last.
 #pragma once
+
+#include <type_traits>
 
 #include "wst_common.cuh"
 
@@ -255,16 +261,6 @@ __device__ __forceinline__ void f8_fma2(float& a0, float& a1, float s0, float s1
       : "f"(s0), "f"(s1), "r"(v0), "r"(v1));
 }
 
-// (a0, a1) *= w.
-__device__ __forceinline__ void f8_mul2(float& a0, float& a1, float w) {
-  asm("{\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
-      "mul.rn.f32x2 a, a, b;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(w));
-}
-
 // 32 fp32 columns of 16 TMEM lanes, valid after tmem_wait_ld: thread t gets, for
 // j < 4, r[4j], r[4j+1] = lane t/4, columns 8j + 2(t%4) + {0, 1} and
 // r[4j+2], r[4j+3] = lane t/4 + 8, the same columns.
@@ -370,7 +366,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       mbar_init(acce_bar(a), 2 * kF8EpiWarps);
     }
     for (int s = 0; s < kF8ScaleStages; ++s) {
-      mbar_init(scf_bar(s), 32);
+      mbar_init(scf_bar(s), SB_ROWS ? 32 : 1);
       mbar_init(sce_bar(s), kF8EpiWarps);
     }
     *abort_flag = 0u;
@@ -441,44 +437,64 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           if (++stage == kF8Stages) { stage = 0; phase ^= 1u; }
         }
       }
-    } else if (warp == 1) {
-      // ------------------------------------------------------------------ MMA issuer (leader)
+    } else if (warp <= 2) {
+      // ------------------------------------------------------------------ MMA issuers (leader)
+      const int mine = warp - 1;
       if (lane == 0 && rank == 0) {
-        int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0;
-        bool full_ok = false, acc_ok = false;  // the next barriers have been seen complete
+        int stage = 0;
+        uint32_t phase = 0, acc_phase = 0;  // (acc_phase: this issuer's accumulator)
         bool ok = true;
         for (long long u = pair_id; ok && units.get(p, u, un); u += num_pairs) {
           const uint32_t idesc = p.idesc | ((uint32_t)(un.tile.nmma >> 3) << 17);
           for (int kb = un.k0; kb < un.k1; ++kb) {
-            ok = (full_ok || f8_wait<false>(guard, full_bar(stage), phase, (kRoleMma << 16) | stage)) &&
-                 (acc_ok || f8_wait<false>(guard, acce_bar(acc), acc_phase ^ 1u, (kRoleMma << 16) | 0x100 | acc));
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint32_t wBase = smem_addr(smW + stage * kF8WBytes);
-            const uint32_t xBase = smem_addr(smX + stage * kF8XBytes);
-            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kF8Tile);
-            const uint32_t this_empty = empty_bar(stage), this_acc = accf_bar(acc);
+            if (((kb - un.k0) & 1) == mine) {
+              ok = f8_wait<false>(guard, full_bar(stage), phase, (kRoleMma << 16) | stage) &&
+                   f8_wait<false>(guard, acce_bar(mine), acc_phase ^ 1u, (kRoleMma << 16) | 0x100 | mine);
+              if (!ok) break;
+              tc_fence_after_sync();
+              const uint32_t wBase = smem_addr(smW + stage * kF8WBytes);
+              const uint32_t xBase = smem_addr(smX + stage * kF8XBytes);
+              const uint32_t d_tmem = tmem_base + (uint32_t)(mine * kF8Tile);
+#pragma unroll
+              for (int k = 0; k < kF8BK / 32; ++k)
+                umma_f8<2>(d_tmem, sdesc_sw128(wBase + k * 32, 16, 1024), sdesc_sw128(xBase + k * 32, 16, 1024), idesc,
+                           k != 0 ? 1u : 0u);
+              umma_commit_pair(accf_bar(mine), 0x3);
+              umma_commit_pair(empty_bar(stage), 0x3);
+              acc_phase ^= 1u;
+            }
             if (++stage == kF8Stages) { stage = 0; phase ^= 1u; }
-            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
-            // (a failed test costs nothing: the wait above repeats it)
-            full_ok = mbar_test_wait(full_bar(stage), phase);
-            acc_ok = mbar_test_wait(acce_bar(acc), acc_phase ^ 1u);
-  #pragma unroll
-            for (int k = 0; k < kF8BK / 32; ++k)
-              umma_f8<2>(d_tmem, sdesc_sw128(wBase + k * 32, 16, 1024), sdesc_sw128(xBase + k * 32, 16, 1024), idesc,
-                         k != 0 ? 1u : 0u);
-            umma_commit_pair(this_acc, 0x3);
-            umma_commit_pair(this_empty, 0x3);
           }
         }
       }
-    } else if (warp == 2) {
-      if (lane == 0 && blockIdx.x == 0 && p.offsets) f8_check_offsets(p.offsets, p.G, p.M_total, p.ws);
+      if (warp == 2 && lane == 1 && blockIdx.x == 0 && p.offsets) f8_check_offsets(p.offsets, p.G, p.M_total, p.ws);
     } else if (warp == 3) {
       // ------------------------------------------------------------------ scales
       auto copy4 = [](uint32_t dst, const float* src, bool in) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+      };
+      // 128 x 128 scales: a slot's token scales times the weights' one of each K
+      // block.  (Blocks the slot does not hold are multiplied too: nothing reads them.)
+      int before = -1;
+      auto finish = [&](int filled) {
+        __syncwarp();
+        float* s = smS + filled * kF8ScaleBlocks * kF8ScaleFloats;
+#pragma unroll
+        for (int k = 0; k < kF8ScaleBlocks; ++k, s += kF8ScaleFloats) {
+          const float w = s[kF8Tile];
+          float4* v = reinterpret_cast<float4*>(s) + lane;
+#pragma unroll
+          for (int i = 0; i < kF8Tile / 128; ++i) {
+            float4 x = v[i * 32];
+            x.x *= w;
+            x.y *= w;
+            x.z *= w;
+            x.w *= w;
+            v[i * 32] = x;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(scf_bar(filled));
       };
       int slot = 0;
       uint32_t phase = 0;
@@ -518,11 +534,23 @@ __global__ void __launch_bounds__(kF8Threads, 1)
               if (lane == 0) copy4(dst + 4u * kF8Tile, sb + kb + k, true);
             }
           }
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(scf_bar(slot)) : "memory");
+          if constexpr (SB_ROWS) {
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(scf_bar(slot)) : "memory");
+          } else {
+            // The copies of the slot before are waited for and multiplied while
+            // these are under way.
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (before >= 0) {
+              asm volatile("cp.async.wait_group 1;" ::: "memory");
+              finish(before);
+            }
+            before = slot;
+          }
           if (++slot == kF8ScaleStages) { slot = 0; phase ^= 1u; }
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!SB_ROWS && before >= 0) finish(before);
     }
   } else {
     // ------------------------------------------------------------------ epilogue
@@ -530,13 +558,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t stg0 = smem_addr(smStg + (warp - 4) * kF8StgBufs * kF8StgBytes);
     const int row = (int)lane >> 2, cq = (int)lane & 3;  // this thread's features row + 8 i and columns 8 j + 2 cq + {0, 1}
-    int acc = 0;
-    uint32_t acc_phase = 0;
+    uint32_t acc_phase = 0;  // (bit a: accumulator a's parity)
     int slot = 0;
     uint32_t sc_phase = 0;
     int sbuf = 0;
     bool ok = true;
-    bool acc_ok = false, sc_ok = false;  // the next accumulator, scales have been seen complete
     F8Place* place = reinterpret_cast<F8Place*>(reinterpret_cast<uint8_t*>(off_tab + kF8TabMax) + (warp - 4) * kF8WalkBytes);
     if (lane == 0) place->units.init(p, tab, total, splits);
     for (long long u = pair_id; ok; u += num_pairs) {
@@ -550,6 +576,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       // This warp's half of the token columns.
       const int c_n = half ? tl.nmma - f8_half0(tl.nmma) : f8_half0(tl.nmma);
       const uint32_t t_warp = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(half ? f8_half0(tl.nmma) : 0);
+      // This thread's scales in a slot: its columns', and its features'.
+      const uint32_t sc_warp = smem_addr(smS) + (half * kF8PartCols + cq * 4) * 4u;
+      const uint32_t sc_rows = (uint32_t)(kF8Tile + q * 32 + row - half * kF8PartCols - cq * 4) * 4u;
+      const uint32_t acce_leader = map_to_cta(acce_bar(0), 0);
       int left = un.k1 - un.k0, kk = 0;
       // sum[h][j][i]: features row + 16 h + 8 (i / 2), columns 8 j + 2 cq + i % 2
       float sum[2][16][4];
@@ -559,18 +589,24 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         for (int j = 0; j < 16; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) sum[h][j][i] = 0.0f;
-#pragma unroll 1
-      for (; left > 0; --left) {
-        if (kk == 0 && !__all_sync(0xffffffffu, sc_ok)) {
+      // One K block, of accumulator ACC (a constant: its addresses cost no
+      // instructions).  All of this warp's 128 columns are loaded and added; in a
+      // tile of fewer tokens those behind c_n lie inside the accumulators and are
+      // not stored.
+      auto step = [&](auto acc_constant) -> bool {
+        constexpr int ACC = decltype(acc_constant)::value;
+        if (kk == 0) {
           ok = f8_wait<false>(guard, scf_bar(slot), sc_phase, (kRoleEpilogue << 16) | 0x200 | slot);
           ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          if (!ok) return false;
         }
-        const uint32_t sc = smem_addr(smS + (slot * kF8ScaleBlocks + kk) * kF8ScaleFloats);
-        float w[SB_ROWS ? 4 : 1];
+        const uint32_t sc = sc_warp + (uint32_t)((slot * kF8ScaleBlocks + kk) * kF8ScaleFloats * 4);
+        float w[4];
+        if constexpr (SB_ROWS) {
 #pragma unroll
-        for (int i = 0; i < (SB_ROWS ? 4 : 1); ++i)
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(sc + (kF8Tile + (SB_ROWS ? q * 32 + row + 8 * i : 0)) * 4u));
+          for (int i = 0; i < 4; ++i)
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(sc + sc_rows + i * 32u));
+        }
         // This thread's scales of 64 columns.
         float s[4][4];
         auto load_scales = [&](int c64) {
@@ -578,33 +614,21 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           for (int i = 0; i < 4; ++i)
             asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                          : "=f"(s[i][0]), "=f"(s[i][1]), "=f"(s[i][2]), "=f"(s[i][3])
-                         : "r"(sc + (half * kF8PartCols + c64 * 64 + i * 16 + cq * 4) * 4u));
-        };
-        auto mul_scales = [&]() {
-          if constexpr (!SB_ROWS) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              f8_mul2(s[i][0], s[i][1], w[0]);
-              f8_mul2(s[i][2], s[i][3], w[0]);
-            }
-          }
+                         : "r"(sc + (c64 * 64 + i * 16) * 4u));
         };
         load_scales(0);
-        uint32_t r0[16], r1[16] = {};
-        const uint32_t t_lane = t_warp + (uint32_t)(acc * kF8Tile);
+        uint32_t r0[16], r1[16];
         // Step k: columns 32 (k / 2) .., features 16 (k % 2) ..
         auto fetch = [&](int k, uint32_t (&r)[16]) {
-          tmem_load_16x32_async(t_lane + ((uint32_t)(k & 1) << 20) + (k >> 1) * 32, r);
+          tmem_load_16x32_async(t_warp + (uint32_t)(ACC * kF8Tile) + ((uint32_t)(k & 1) << 20) + (k >> 1) * 32, r);
         };
-        if (!__all_sync(0xffffffffu, acc_ok)) {
-          ok = f8_wait<false>(guard, accf_bar(acc), acc_phase, (kRoleEpilogue << 16) | acc);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-        }
+        ok = f8_wait<false>(guard, accf_bar(ACC), (acc_phase >> ACC) & 1u, (kRoleEpilogue << 16) | ACC);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        acc_phase ^= 1u << ACC;
         tc_fence_after_sync();
-        if (c_n > 0) fetch(0, r0);
-        if (c_n == kF8PartCols) fetch(1, r1);
-        mul_scales();
+        fetch(0, r0);
+        fetch(1, r1);
         auto add = [&](int k, const uint32_t (&r)[16]) {
           const int c = k >> 1, h = k & 1;
 #pragma unroll
@@ -620,62 +644,33 @@ __global__ void __launch_bounds__(kF8Threads, 1)
               f8_fma2(a[0], a[1], s0, s1, r[4 * j + i], r[4 * j + i + 1]);
             }
         };
-        // One step is added while the next one loads.  The next accumulator's
-        // barrier is tested (which takes long) ahead of its use.
-        const int next_acc = acc ^ 1;
-        auto test_next = [&]() {
-          acc_ok = mbar_test_wait(accf_bar(next_acc), acc_phase ^ (next_acc == 0 ? 1u : 0u));
-          if (kk == kF8ScaleBlocks - 1 || left == 1) {
-            const int n = slot + 1 == kF8ScaleStages ? 0 : slot + 1;
-            sc_ok = mbar_test_wait(scf_bar(n), sc_phase ^ (n == 0 ? 1u : 0u));
-          }
-        };
-        // Hands the accumulator back: every lane's loads are complete.
-        auto release = [&]() {
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_tmem(map_to_cta(acce_bar(acc), 0));
-        };
-        if (c_n == kF8PartCols) {
+        // 32 columns x 16 features are added while others load.
 #pragma unroll
-          for (int k = 0; k < 8; k += 2) {
-            tmem_wait_ld(r0, r1);
-            add(k, r0);
-            if (k + 2 < 8) fetch(k + 2, r0);
-            else release();
-            add(k + 1, r1);
-            if (k + 2 < 8) fetch(k + 3, r1);
-            if (k == 2) {
-              load_scales(1);
-              mul_scales();
-            }
-            if (k == 4) test_next();
+        for (int k = 0; k < 8; k += 2) {
+          tmem_wait_ld(r0, r1);
+          if (k == 6) {
+            // Every load is complete: the accumulator goes back.
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_tmem(acce_leader + 8u * ACC);
           }
-        } else {
-          // (columns behind c_n, up to 16 of them, are loaded and added too; they
-          // lie inside the accumulators and are not stored)
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if ((k >> 1) * 32 < c_n) {
-              if (k == 4) {
-                load_scales(1);
-                mul_scales();
-              }
-              if (k > 0) fetch(k, r0);
-              tmem_wait_ld(r0, r1);
-              add(k, r0);
-            }
-          test_next();
-          release();
+          add(k, r0);
+          if (k < 6) fetch(k + 2, r0);
+          add(k + 1, r1);
+          if (k < 6) fetch(k + 3, r1);
+          if (k == 2) load_scales(1);
         }
         if (++kk == kF8ScaleBlocks || left == 1) {
-          __syncwarp();
           if (lane == 0) mbar_arrive(sce_bar(slot));
           kk = 0;
           if (++slot == kF8ScaleStages) { slot = 0; sc_phase ^= 1u; }
         }
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
-      }
+        return true;
+      };
+      using I0 = std::integral_constant<int, 0>;
+      using I1 = std::integral_constant<int, 1>;
+#pragma unroll 1
+      while (step(I0()) && --left > 0 && step(I1()) && --left > 0) {}
 
       const int n_base = tl.n0 + (int)rank * 128 + q * 32;
       if (un.split >= 0) {
