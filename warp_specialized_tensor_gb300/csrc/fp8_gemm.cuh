@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           if (!ok) return false;
         }
         const uint32_t sc = sc_warp + (uint32_t)((slot * kF8ScaleBlocks + kk) * kF8ScaleFloats * 4);
-        float w[4];
+        [[maybe_unused]] float w[4];  // this thread's features' scales
         if constexpr (SB_ROWS) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -669,8 +669,64 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       };
       using I0 = std::integral_constant<int, 0>;
       using I1 = std::integral_constant<int, 1>;
+      if (c_n > 32) {
 #pragma unroll 1
-      while (step(I0()) && --left > 0 && step(I1()) && --left > 0) {}
+        while (step(I0()) && --left > 0 && step(I1()) && --left > 0) {}
+      } else {
+        // At most 32 columns (tiles of up to 64 tokens, whose products wait for
+        // the weights from HBM): one round of loads.
+#pragma unroll 1
+        for (int acc = 0; left > 0; --left, acc ^= 1) {
+          if (kk == 0) {
+            ok = f8_wait<false>(guard, scf_bar(slot), sc_phase, (kRoleEpilogue << 16) | 0x200 | slot);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          const uint32_t sc = sc_warp + (uint32_t)((slot * kF8ScaleBlocks + kk) * kF8ScaleFloats * 4);
+          float w[4], s[2][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i] = 1.0f;
+            if constexpr (SB_ROWS) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w[i]) : "r"(sc + sc_rows + i * 32u));
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(s[i][0]), "=f"(s[i][1]), "=f"(s[i][2]), "=f"(s[i][3])
+                         : "r"(sc + i * 64u));
+          ok = f8_wait<false>(guard, accf_bar(acc), (acc_phase >> acc) & 1u, (kRoleEpilogue << 16) | acc);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          acc_phase ^= 1u << acc;
+          tc_fence_after_sync();
+          uint32_t r[2][16];
+          tmem_load_16x32_async(t_warp + (uint32_t)(acc * kF8Tile), r[0]);
+          tmem_load_16x32_async(t_warp + (uint32_t)(acc * kF8Tile) + (16u << 16), r[1]);
+          tmem_wait_ld(r[0], r[1]);
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_tmem(acce_leader + 8u * acc);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; i += 2) {
+                float s0 = s[j / 2][2 * (j & 1)], s1 = s[j / 2][2 * (j & 1) + 1];
+                if constexpr (SB_ROWS) {
+                  s0 *= w[2 * h + i / 2];
+                  s1 *= w[2 * h + i / 2];
+                }
+                f8_fma2(sum[h][j][i], sum[h][j][i + 1], s0, s1, r[h][4 * j + i], r[h][4 * j + i + 1]);
+              }
+          if (++kk == kF8ScaleBlocks || left == 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sce_bar(slot));
+            kk = 0;
+            if (++slot == kF8ScaleStages) { slot = 0; sc_phase ^= 1u; }
+          }
+        }
+      }
 
       const int n_base = tl.n0 + (int)rank * 128 + q * 32;
       if (un.split >= 0) {

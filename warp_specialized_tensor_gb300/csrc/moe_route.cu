@@ -103,10 +103,11 @@ struct RowStats {
 
 template <bool SOFTMAX, typename R>
 __device__ __forceinline__ R route_score(float x, const RowStats<R>& st) {
-  if (x <= kRouteOff) return R(0);
-  if constexpr (SOFTMAX) return route_exp(R(x) - st.top) / st.sum;
-  else if constexpr (sizeof(R) == 4) return __fdividef(1.0f, 1.0f + expf(-x));  // (two units off at most)
-  else return R(1) / (R(1) + route_exp(-R(x)));
+  R s;
+  if constexpr (SOFTMAX) s = route_exp(R(x) - st.top) / st.sum;
+  else if constexpr (sizeof(R) == 4) s = __fdividef(1.0f, 1.0f + expf(-x));  // (two units off at most)
+  else s = R(1) / (R(1) + route_exp(-R(x)));
+  return x <= kRouteOff ? R(0) : s;
 }
 
 // Bound on the error of an fp32 score s of logit x.  sigmoid: expf 2^-22, the
@@ -138,23 +139,18 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
                                        void* row_mem, int lane, int& mine) {
   using K = typename KeyOf<R>::type;
   K key[VPL];
+  float bias[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) bias[j] = !BY_LOGIT && a.bias && j * 32 + lane < a.E ? __ldg(a.bias + j * 32 + lane) : 0.0f;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    const int e = j * 32 + lane;
-    K k = 0;
-    if (e < a.E && !(x[j] <= kRouteOff)) {
-      R v;
-      if constexpr (BY_LOGIT) {
-        v = R(x[j]);
-        if (SOFTMAX && row_nan) v = R(NAN);
-      } else {
-        v = route_score<SOFTMAX, R>(x[j], st);
-        if (a.bias) v += R(__ldg(a.bias + e));
-      }
-      // a bias of -inf turns an expert off too
-      k = (v == R(-INFINITY)) ? K(0) : order_key(v);
-    }
-    key[j] = k;
+    R v;
+    if constexpr (BY_LOGIT) v = SOFTMAX && row_nan ? R(NAN) : R(x[j]);
+    else v = route_score<SOFTMAX, R>(x[j], st) + R(bias[j]);
+    // (a bias of -inf turns an expert off too; x past the last expert is -inf)
+    const bool off = x[j] <= kRouteOff || v == R(-INFINITY);
+    const K k = order_key(v);
+    key[j] = off ? K(0) : k;
   }
   bool sure = true;
   if (a.groups > 1) {
@@ -222,25 +218,21 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
   uint32_t taken = 0;
   K b1, b2;
   int j1, j2, have;
-  auto look = [&]() {
+  auto look = [&](auto first) {
     b1 = b2 = 0;
     j1 = j2 = 0;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      const K k = (taken >> j) & 1u ? K(0) : key[j];
-      if (k > b1) {
-        b2 = b1;
-        j2 = j1;
-        b1 = k;
-        j1 = j;
-      } else if (k > b2) {
-        b2 = k;
-        j2 = j;
-      }
+      const K k = !decltype(first)::value && ((taken >> j) & 1u) ? K(0) : key[j];
+      const bool g1 = k > b1, g2 = k > b2;
+      b2 = g1 ? b1 : g2 ? k : b2;
+      j2 = g1 ? j1 : g2 ? j : j2;
+      b1 = g1 ? k : b1;
+      j1 = g1 ? j : j1;
     }
     have = 2;
   };
-  look();
+  look(std::true_type());
   for (int r = 0; r <= a.top_k; ++r) {
     const K top = warp_max(b1);
     if (top == 0) break;
@@ -251,7 +243,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
       taken |= 1u << j1;
       b1 = b2;
       j1 = j2;
-      if (--have == 0) look();
+      if (--have == 0) look(std::false_type());
     }
   }
   return sure;
