@@ -2,7 +2,10 @@
  * wst.h -- C ABI of libwst: persistent, warp-specialized bf16 contractions
  * for NVIDIA GB300 (sm_103a).
  *
- * Three operations, each one hand-written CUDA kernel behind one call:
+ * The first three operations, each one hand-written CUDA kernel behind one call
+ * (the declarations below hold the others: norm-fused GEMMs, IKBO attention,
+ * expert parallelism, mixture-of-experts routing and its gradients, 8-bit
+ * products with block scales):
  *
  *   wst_gemm_bf16            dense (optionally strided-batched) GEMM with an
  *                            optional fused bias / bias+SiLU epilogue.
@@ -470,7 +473,8 @@ wst_status wst_quantize_fp8(wst_fp8_mode mode, int batch, int M, int K, const vo
  * copies, of q [n_rows][K] and the scales [ceil(K/128)][n_rows]: the tokens'
  * rows of a grouped product (position as wst_moe_plan leaves it).  A negative
  * entry is skipped, one of n_rows or more is skipped and latches
- * WST_ERR_INVALID_ARG.  Rows that no entry names are left as they were. */
+ * WST_ERR_INVALID_ARG.  Rows that no entry names are left as they were; a row
+ * that two entries name gets either of the two. */
 wst_status wst_quantize_fp8_dispatch(int M, int K, int copies, const void* x, long ldx,
                                      wst_dtype x_type, const int* position, int n_rows, void* q,
                                      long ldq, wst_fp8 q_type, float* scales, long lds, int pow2,

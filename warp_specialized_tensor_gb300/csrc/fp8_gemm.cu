@@ -1,5 +1,6 @@
 // fp8_gemm.cu -- launcher and C ABI of the 8-bit products (dense and grouped).
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "fp8_gemm.cuh"
@@ -66,8 +67,8 @@ int launch_fp8(const F8Problem& pr, F8Args& a, const DeviceInfo& dev, cudaStream
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  static int max_clusters[64] = {0};
-  int& mc = max_clusters[dev.device & 63];
+  static std::atomic<int> max_clusters[64];
+  int mc = max_clusters[dev.device & 63].load(std::memory_order_relaxed);
   if (mc == 0) {
     cfg.gridDim = dim3((unsigned)(dev.num_sms & ~1), 1, 1);
     int n = 0;
@@ -77,6 +78,7 @@ int launch_fp8(const F8Problem& pr, F8Args& a, const DeviceInfo& dev, cudaStream
       n = dev.num_sms / 2;
     }
     mc = n;
+    max_clusters[dev.device & 63].store(n, std::memory_order_relaxed);
   }
   a.pairs = mc;
   // Persistent grid, no larger than the units of work (an upper bound where
@@ -95,6 +97,8 @@ int fp8_product(const char* what, bool grouped, int G, int M, int N, int K, cons
                 long ldc, int c_type, int epi, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (G < 1 || M < 0 || N < 1 || K < 1)
     return reject(ST_INVALID_ARG, "%s: sizes out of range (G=%d M=%d N=%d K=%d)", what, G, M, N, K);
+  if (M > 0x7fffffff - 1024 || N > 0x7fffffff - 1024 || K > 0x7fffffff - 1024)
+    return reject(ST_UNSUPPORTED, "%s: M=%d N=%d K=%d: too large", what, M, N, K);
   if ((a_type != WST_E4M3 && a_type != WST_E5M2) || (b_type != WST_E4M3 && b_type != WST_E5M2))
     return reject(ST_INVALID_ARG, "%s: unknown 8-bit type", what);
   if (c_type != WST_F32 && c_type != WST_BF16) return reject(ST_INVALID_ARG, "%s: unknown c_type %d", what, c_type);

@@ -332,6 +332,8 @@ int run_quant(int mode, const QuantArgs& a, int batch, int x_type, int q_type, b
 
 int check_quant(const char* what, int M, int K, const void* x, long ldx, int x_type, const void* q, long ldq, long q_cols,
                 int q_type, const void* scales) {
+  if (M > 0x7fffffff - 1024 || K > 0x7fffffff - 1024)
+    return reject(ST_UNSUPPORTED, "%s: M=%d K=%d: too large", what, M, K);
   if (M < 0 || K < 1) return reject(ST_INVALID_ARG, "%s: sizes out of range (M=%d K=%d)", what, M, K);
   if (x_type != WST_F32 && x_type != WST_BF16) return reject(ST_INVALID_ARG, "%s: unknown type %d", what, x_type);
   if (q_type != WST_E4M3 && q_type != WST_E5M2) return reject(ST_INVALID_ARG, "%s: unknown 8-bit type %d", what, q_type);

@@ -201,7 +201,8 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
       if (out) {
         const int li = __ffs(in) - 1, lo = __ffs(out) - 1;
         const K ki = __shfl_sync(0xffffffffu, gk, li), ko = __shfl_sync(0xffffffffu, gk, lo);
-        const float tol = __shfl_sync(0xffffffffu, gerr, li) + __shfl_sync(0xffffffffu, gerr, lo);
+        // (any group may lie behind the border with the largest error)
+        const float tol = 2.0f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(gerr)));
         if (ko != 0 && ko != 0xffffffffu) sure = key_value(ki) - key_value(ko) > tol;
       }
     }
@@ -292,7 +293,11 @@ __global__ void __launch_bounds__(32 * route_warps(VPL)) k_route(const RouteArgs
     const float err = score_error<SOFTMAX>(s, 1.0f, st) + 0x1p-23f * fabsf(v);
     const int next = __shfl_down_sync(0xffffffffu, mine, 1);
     const float nx = __shfl_down_sync(0xffffffffu, xe, 1), nb = __shfl_down_sync(0xffffffffu, be, 1);
-    const float nv = __shfl_down_sync(0xffffffffu, v, 1), ne = __shfl_down_sync(0xffffffffu, err, 1);
+    const float nv = __shfl_down_sync(0xffffffffu, v, 1);
+    float ne = __shfl_down_sync(0xffffffffu, err, 1);
+    // Behind the last chosen one any expert may follow: one with the largest score
+    // (and a bias that nearly cancels it) has the largest error.
+    if (lane == a.top_k - 1) ne = fmaxf(ne, score_error<SOFTMAX>(1.0f, 1.0f, st) + 0x1p-22f * fabsf(v));
     const bool decides = lane < a.top_k && next >= 0 && !(nx == xe && nb == be) && nv == nv;
     sure = sure && !__any_sync(0xffffffffu, decides && !(v - nv > err + ne) && v == v);
     if (!sure) {

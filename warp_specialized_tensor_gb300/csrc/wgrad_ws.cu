@@ -1,5 +1,6 @@
 // wgrad_ws.cu -- launcher and C ABI of the grouped GEMM's weight gradient.
 #include <algorithm>
+#include <atomic>
 
 #include "wgrad_ws.cuh"
 #include "wst.h"
@@ -48,8 +49,8 @@ int launch_wgrad(const WgArgs& a, const void* dC, long lddc, const void* A, long
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  static int max_clusters[64] = {0};
-  int& mc = max_clusters[dev.device & 63];
+  static std::atomic<int> max_clusters[64];
+  int mc = max_clusters[dev.device & 63].load(std::memory_order_relaxed);
   if (mc == 0) {
     cfg.gridDim = dim3((unsigned)(dev.num_sms & ~1), 1, 1);
     int n = 0;
@@ -59,6 +60,7 @@ int launch_wgrad(const WgArgs& a, const void* dC, long lddc, const void* A, long
       n = dev.num_sms / 2;
     }
     mc = n;
+    max_clusters[dev.device & 63].store(n, std::memory_order_relaxed);
   }
   cfg.gridDim = dim3((unsigned)(2 * std::min<long long>(mc, tiles)), 1, 1);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmD, tmA, tmOut, a, (int)tiles);
@@ -77,6 +79,8 @@ extern "C" wst_status wst_grouped_gemm_wgrad_bf16(int G, int M_total, int N, int
   set_error("%s", "");
   if (G < 1 || M_total < 0 || N < 1 || K < 1)
     return (wst_status)reject(ST_INVALID_ARG, "wgrad: sizes out of range (G=%d M_total=%d N=%d K=%d)", G, M_total, N, K);
+  if (M_total > 0x7fffffff - 1024 || N > 0x7fffffff - 1024 || K > 0x7fffffff - 1024)
+    return (wst_status)reject(ST_UNSUPPORTED, "wgrad: M_total=%d N=%d K=%d: too large", M_total, N, K);
   if (db_type != WST_F32 && db_type != WST_BF16)
     return (wst_status)reject(ST_INVALID_ARG, "wgrad: unknown db_type %d", (int)db_type);
   if (lddc < N || lda < K || lddb < K || (G > 1 && stride_dB < (long)(N - 1) * lddb + K))
