@@ -119,7 +119,7 @@ __device__ __forceinline__ uint4 load_raw(const X* x, int k, int K) {
 // One warp per four blocks of a row, eight lanes and 16 values a lane each; bf16
 // as two 16-byte loads of eight, fp32 as four of four.
 template <typename X, bool E5, bool POW2>
-__global__ void __launch_bounds__(kQThreads) k_quant_rows(const QuantArgs a) {
+__global__ void __launch_bounds__(kQThreads, 6) k_quant_rows(const QuantArgs a) {
   constexpr int V = vec_of<X>(), P = 16 / V;  // values per load, loads per lane
   const int lane = threadIdx.x & 31, l8 = lane & 7;
   const int m = (int)blockIdx.x * (kQThreads / 32) + (int)(threadIdx.x >> 5);
@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kQThreads) k_quant_rows(const QuantArgs a) {
       for (int i = 0; i < V / 4; ++i)
         out[p][i] = Fp8<E5>::pack4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
     }
+#pragma unroll 1
     for (int c = 0; c < copies; ++c) {
       int row = m;
       if (a.position) {

@@ -518,7 +518,7 @@ wst_status wst_moe_route(int T, int E, int top_k, const void* logits, long ld, w
   if ((long long)top_groups * (E / groups) < top_k)
     return (wst_status)reject(ST_INVALID_ARG, "route: %d groups of %d experts hold fewer than top_k=%d", top_groups,
                               E / groups, top_k);
-  if ((long long)T * top_k > 0x7fffffffLL) return (wst_status)reject(ST_INVALID_ARG, "route: too many pairs");
+  if ((long long)T * top_k > 0x7fffffffLL - (1 << 20)) return (wst_status)reject(ST_INVALID_ARG, "route: too many pairs");
   if (T && (!logits || !experts || !weights)) return (wst_status)reject(ST_INVALID_ARG, "route: NULL array");
   if (!aligned_to(logits, logits_type == WST_F32 ? 4 : 2) || !aligned_to(bias, 4) || !aligned_to(experts, 4) ||
       !aligned_to(weights, 4))
