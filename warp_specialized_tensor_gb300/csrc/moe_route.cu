@@ -19,9 +19,11 @@
 // in fp32 together with a bound on their error; if every gap that decides
 // something (between neighbours among the chosen and the first expert left
 // out, and at the border of the kept groups) exceeds the bound, the ranking
-// is that of the exact scores.  If one does not, the warp repeats the token in
-// fp64 (about one token in a thousand for 256 sigmoid scores with a random
-// bias).
+// is that of the exact scores.  If one does not (about one token in a thousand
+// for 256 sigmoid scores with a random bias), the candidates are ranked in fp64,
+// one per lane; a border of groups, a softmax row or a third close candidate
+// takes the whole token through fp64.  (All such tokens in fp64 throughout cost
+// 9 of 32 us at 16384 tokens of 256 experts.)
 //
 // One warp per token, E/32 logits per lane in registers; each of the top_k
 // rounds is one warp-wide integer maximum over order-preserving keys and one
@@ -131,7 +133,7 @@ constexpr int route_warps(int vpl) { return vpl <= 8 ? 8 : 4; }
 constexpr int route_row(int vpl) { return vpl * 36; }
 __device__ __forceinline__ int row_at(int e) { return e + 4 * (e >> 5); }
 
-// Chooses the top_k + 1 best experts of a row into lanes 0 .. top_k (-1: none
+// Chooses the top_k + 2 best experts of a row into lanes 0 .. top_k + 1 (-1: none
 // left).  BY_LOGIT ranks by the logits, else by v in arithmetic R.  Returns
 // whether the kept groups are certain (always, in fp64 and by logits).
 template <int VPL, bool SOFTMAX, bool BY_LOGIT, typename R>
@@ -234,7 +236,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
     have = 2;
   };
   look(std::true_type());
-  for (int r = 0; r <= a.top_k; ++r) {
+  for (int r = 0; r < a.top_k + (BY_LOGIT ? 0 : 2); ++r) {
     const K top = warp_max(b1);
     if (top == 0) break;
     const unsigned e = b1 == top ? (unsigned)(j1 * 32 + lane) : 0xffffffffu;
@@ -299,7 +301,39 @@ __global__ void __launch_bounds__(32 * route_warps(VPL)) k_route(const RouteArgs
     // (and a bias that nearly cancels it) has the largest error.
     if (lane == a.top_k - 1) ne = fmaxf(ne, score_error<SOFTMAX>(1.0f, 1.0f, st) + 0x1p-22f * fabsf(v));
     const bool decides = lane < a.top_k && next >= 0 && !(nx == xe && nb == be) && nv == nv;
+    const bool groups_sure = sure;
     sure = sure && !__any_sync(0xffffffffu, decides && !(v - nv > err + ne) && v == v);
+    if (!SOFTMAX && !sure && groups_sure) {
+      // Sigmoid scores: only the candidates are computed in fp64, one per lane.
+      // They hold the chosen ones if the second expert left out lies certainly
+      // below every chosen one.
+      const float most = score_error<SOFTMAX>(1.0f, 1.0f, st) +
+                         0x1p-22f * fmaxf(fabsf(__shfl_sync(0xffffffffu, v, 0)), fabsf(__shfl_sync(0xffffffffu, v, a.top_k + 1)));
+      const bool more = __shfl_sync(0xffffffffu, mine, a.top_k + 1) >= 0;
+      const float gap = __shfl_sync(0xffffffffu, v, a.top_k - 1) - __shfl_sync(0xffffffffu, v, a.top_k + 1);
+      if (!more || gap > 2.0f * most) {
+        const bool candidate = lane <= a.top_k && mine >= 0;
+        const RowStats<double> sd{0.0, 1.0};
+        const uint64_t key = candidate ? order_key(route_score<SOFTMAX, double>(xe, sd) + (double)be) : 0ull;
+        int rank = 0;
+        for (int i = 0; i <= a.top_k; ++i) {
+          const uint64_t other = __shfl_sync(0xffffffffu, key, i);
+          const int oe = __shfl_sync(0xffffffffu, mine, i);
+          rank += other > key || (other == key && oe < mine) ? 1 : 0;
+        }
+        int* order = reinterpret_cast<int*>(rows[warp]);
+        __syncwarp();
+        if (lane <= a.top_k) order[lane] = -1;
+        __syncwarp();
+        if (candidate) order[rank] = mine;
+        __syncwarp();
+        mine = lane <= a.top_k ? order[lane] : -1;
+        __syncwarp();
+        xe = mine >= 0 ? load_logit(src + mine) : -INFINITY;
+        s = route_score<SOFTMAX, float>(xe, st);
+        sure = true;
+      }
+    }
     if (!sure) {
       RowStats<double> sd{(double)st.top, 1.0};
       if constexpr (SOFTMAX) {
