@@ -206,6 +206,25 @@ def test_replayed_graphs_share_a_workspace(wst, big_ws):
     assert wst.wst_sync_status(big_ws) == 0
 
 
+def test_two_streams_with_their_own_workspaces(wst):
+    # split products on two streams at once, each with a workspace of its own
+    cases = []
+    for seed, (M, N, K) in enumerate([(16, 1024, 4096), (9, 768, 8192)]):
+        qa, sa = operand(M, K, "rows", E4, 40 + seed)
+        qb, sb = operand(N, K, "blocks", E4, 50 + seed)
+        ws = wst.gemm_fp8_workspace()
+        args = (qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), torch.empty(M, N, device="cuda"))
+        wst.wst_gemm_fp8(*args, workspace=ws)
+        cases.append((args, ws, args[4].clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for args, ws, _, stream in cases:
+            wst.wst_gemm_fp8(*args, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for args, ws, first, stream in cases:
+        assert wst.wst_sync_status(ws, stream) == 0 and torch.equal(args[4], first)
+
+
 def test_training_products(wst, big_ws):
     # forward, gradient of the inputs and of the weights, each by quantise and product
     g = torch.Generator().manual_seed(3)

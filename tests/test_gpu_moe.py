@@ -106,6 +106,27 @@ def test_route_scores_closer_than_fp32(wst, score):
     check_route(wst, row.repeat(3, 1), 12, score, bias=bias, groups=8, top_groups=3, group_best=2)
 
 
+@pytest.mark.parametrize("place", ["inside", "border", "group"])
+def test_route_one_close_pair(wst, place):
+    # In every row two experts' sums differ by a few 2^-26: among the chosen, at the
+    # border of the chosen ones, or in two groups of which one is kept.
+    g = torch.Generator().manual_seed(17)
+    T, E, k = 400, 64, 6
+    x = torch.randn(T, E, generator=g) * 0.5 - 2.0
+    x[:, [3, 11, 20]] = torch.randn(T, 3, generator=g) * 0.1 + 2.0     # certainly chosen
+    bias = torch.randn(E, generator=g) * 0.02
+    if place == "border":
+        x[:, [30, 31]] = 1.0                                            # chosen too: five in front of the pair
+    sum5 = 1.0 / (1.0 + np.exp(-0.2 * np.random.default_rng(1).random(T))) + float(bias[5])
+    for e in (5, 37):
+        s = sum5 - float(bias[e])
+        x[:, e] = torch.from_numpy(np.log(s / (1 - s))).float()         # rounded: the sums are no longer equal
+    kw = dict(groups=2, top_groups=1, group_best=1) if place == "group" else {}
+    if place == "group":
+        x[:, [3, 11, 20]] -= 6.0
+    check_route(wst, x, k, "sigmoid", bias=bias, **kw)
+
+
 def test_route_is_the_same_on_every_call_and_stream(wst):
     x = torch.randn(3000, 256, device="cuda")
     bias = torch.randn(256) * 0.05

@@ -67,9 +67,9 @@ def test_plan_workspace():
     big = wst.wst_moe_plan_workspace_size(1 << 20, 1024)
     assert 256 < big <= 256 + 128 * 1024 * 4
     assert wst.wst_moe_plan_workspace_size(-1, 8) == 0 and wst.wst_moe_plan_workspace_size(8, 0) == 0
-    # never less for more pairs up to a multiple of the chunks, so one workspace serves smaller calls
-    for pairs in (3000, 50000, 131072, 10 ** 6, 10 ** 8):
-        assert wst.wst_moe_plan_workspace_size(pairs, 64) <= 256 + 128 * 64 * 4
+    # never less for more pairs, so a workspace serves every smaller call
+    sizes = [wst.wst_moe_plan_workspace_size(p, 64) for p in (1, 2048, 2049, 3000, 50000, 131071, 131072, 131073, 10 ** 6, 10 ** 8)]
+    assert sizes == sorted(sizes) and sizes[-1] == 256 + 128 * 64 * 4
 
 
 COMB = dict(T=8, k=4, N=64, y=FAKE, ldy=64, yt=1, rows=32, pos=FAKE, w=None, out=FAKE, ldo=64, ot=1, ws=FAKE, st=None)

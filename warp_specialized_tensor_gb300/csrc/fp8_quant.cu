@@ -19,7 +19,9 @@
 // it.  The others: one 128 x 128 tile per block of threads, an 8 x 8 patch in
 // each thread's registers, so a transposed patch leaves as eight 8-byte words
 // through shared memory (words XOR-swizzled by the column group: no bank
-// conflicts either way).
+// conflicts either way).  On GB300: 16384 x 4096 bf16 to two rows each 51 us
+// (5.3 TB/s), 16 x 1536 x 4096 bf16 in transposed 128 x 128 blocks 50 us (6.0
+// TB/s; 98 us with the patch unpacked to fp32, at half the resident warps).
 #include <type_traits>
 
 #include <cuda_fp8.h>

