@@ -115,10 +115,15 @@ struct F8Args {
 // own, and no more than pay.  A K block costs a pair about 0.3 us, adding up one
 // split's sums about 0.3 us and 1.1 us more for 256 token columns, so s splits
 // of k blocks take about 0.3 (k / s + s (1 + width / 64)) us, least at
-// s = sqrt(k / (1 + width / 64)).
+// s = sqrt(k / (1 + width / 64)); counting in and out costs 2 us more, so short
+// loops stay whole.  Measured whole / as chosen / best of other splits, us:
+// 16 x 256 x 8192 25.7 / 14.8 (7) / 14.6 (6), 128 x 1024 x 8192 42.6 / 25.1 (4) /
+// 24.3 (5), 256 x 512 x 8192 42.6 / 28.4 (3) / 28.3, 64 x 2048 x 4096 18.5 / 16.1
+// (4) / 15.7 (3), 512 x 2048 x 2048 16.3 (whole) / 20.7 (2), 16 x 256 x 1024 8.8
+// (whole) / 10.4 (2).
 __host__ __device__ inline int f8_splits(long long tiles, int pairs, int k_blocks, int max_units, int M) {
   const int room = pairs < max_units ? pairs : max_units;
-  if (tiles <= 0 || tiles > room) return 1;
+  if (tiles <= 0 || tiles > room || k_blocks <= 12) return 1;
   const int most = room / (int)tiles;
   const int width = M < kF8Tile ? M : kF8Tile;
   int s = 1;
