@@ -23,9 +23,9 @@ struct F8Problem {
   long long ldc;
 };
 
-template <bool OUT_F32, bool SB_ROWS, bool EPI>
+template <bool OUT_F32, bool SB_ROWS, bool EPI, bool THIN>
 int launch_fp8(const F8Problem& pr, F8Args& a, const DeviceInfo& dev, cudaStream_t stream) {
-  auto kern = k_gemm_fp8<OUT_F32, SB_ROWS, EPI>;
+  auto kern = k_gemm_fp8<OUT_F32, SB_ROWS, EPI, THIN>;
   CUtensorMap tmW, tmX, tmXt, tmC;
   int st;
   a.w_shared = pr.strideB == 0 ? 1 : 0;
@@ -156,7 +156,10 @@ int fp8_product(const char* what, bool grouped, int G, int M, int N, int K, cons
   a.timeout_ns = wait_timeout_ns();
   auto go = [&](auto out_f32, auto sb_rows) {
     constexpr bool F = decltype(out_f32)::value, R = decltype(sb_rows)::value;
-    return epi ? launch_fp8<F, R, true>(pr, a, dev, stream) : launch_fp8<F, R, false>(pr, a, dev, stream);
+    // Groups of at most 64 rows on average: most tiles are thin.
+    if (M <= 64LL * G)
+      return epi ? launch_fp8<F, R, true, true>(pr, a, dev, stream) : launch_fp8<F, R, false, true>(pr, a, dev, stream);
+    return epi ? launch_fp8<F, R, true, false>(pr, a, dev, stream) : launch_fp8<F, R, false, false>(pr, a, dev, stream);
   };
   const bool rows = b_scaling == WST_FP8_ROWS;
   if (c_type == WST_F32)

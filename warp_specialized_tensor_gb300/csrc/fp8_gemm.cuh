@@ -328,7 +328,8 @@ __device__ __forceinline__ float f8_act(int epi, float v) {
 }
 
 // SB_ROWS: B has one scale per feature and K block (else one per 128 features).
-template <bool OUT_F32, bool SB_ROWS, bool EPI>
+// THIN: tiles of at most 64 tokens have a loop of their own (see there).
+template <bool OUT_F32, bool SB_ROWS, bool EPI, bool THIN>
 __global__ void __launch_bounds__(kF8Threads, 1)
     k_gemm_fp8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                const __grid_constant__ CUtensorMap tmXt, const __grid_constant__ CUtensorMap tmC, const F8Args p) {
@@ -674,12 +675,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       };
       using I0 = std::integral_constant<int, 0>;
       using I1 = std::integral_constant<int, 1>;
-      if (c_n > 32) {
+      if (!THIN || c_n > 32) {
 #pragma unroll 1
         while (step(I0()) && --left > 0 && step(I1()) && --left > 0) {}
       } else {
         // At most 32 columns (tiles of up to 64 tokens, whose products wait for
-        // the weights from HBM): one round of loads.
+        // the weights from HBM): one round of loads.  16 x 4096 x 8192 takes 17 us
+        // with it and 20 us in the loop above; its mere presence costs large
+        // products 3 % (8192^3 543 against 527 us), so they run a kernel without.
 #pragma unroll 1
         for (int acc = 0; left > 0; --left, acc ^= 1) {
           if (kk == 0) {
