@@ -127,6 +127,35 @@ def test_route_one_close_pair(wst, place):
     check_route(wst, x, k, "sigmoid", bias=bias, **kw)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("k", [1, 2, 3])
+@pytest.mark.parametrize("row", [[18.0, 18.0, 20.0, 1.0], [18.0, 18.0, 18.0, 18.0, 18.0, 19.0], [0.0, 0.0, 1e-8, -1.0],
+                                 [20.0, 18.0, 18.0, 19.0], [20.0, 19.0, 18.0, 18.0, 18.5, 18.0], [3.0, 17.0, 17.0, 17.0]])
+def test_route_equals_at_the_border_and_one_behind(wst, row, k, dtype):
+    # The last chosen expert has an exact equal just outside, and behind the two
+    # lies one that is larger by less than fp32 tells apart.
+    x = torch.tensor([row, row[::-1]]).to(dtype)
+    check_route(wst, x, k, "sigmoid", bias=torch.zeros(len(row)))
+    check_route(wst, x, k, "softmax", bias=torch.zeros(len(row)))
+    check_route(wst, x, k, "sigmoid", bias=torch.full((len(row),), 0.25), renorm=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_equals_at_the_border_in_groups(wst, score):
+    x = torch.tensor([[0.0, 0.0, 0.0, 0.0, 1e-8, 1e-8, 0.0, 0.0], [18.0, 1.0, 18.0, 1.0, 19.0, 1.0, 18.0, 1.0]])
+    check_route(wst, x, 1, score, groups=4, top_groups=3, group_best=2)
+    check_route(wst, x, 2, score, groups=4, top_groups=3, group_best=2)
+
+
+def test_route_many_equal_logits(wst):
+    # few different values, most of them where the sigmoid of fp32 is 1
+    g = torch.Generator().manual_seed(23)
+    x = torch.randint(30, 44, (300, 64), generator=g) / 2.0
+    for bias in (torch.zeros(64), torch.randint(0, 3, (64,), generator=g) * 0.001):
+        check_route(wst, x, 4, "sigmoid", bias=bias)
+        check_route(wst, x.bfloat16(), 8, "sigmoid", bias=bias, groups=8, top_groups=4, group_best=2)
+
+
 def test_route_is_the_same_on_every_call_and_stream(wst):
     x = torch.randn(3000, 256, device="cuda")
     bias = torch.randn(256) * 0.05

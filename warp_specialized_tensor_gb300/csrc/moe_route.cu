@@ -304,18 +304,27 @@ __global__ void __launch_bounds__(32 * route_warps(VPL)) k_route(const RouteArgs
     // Behind the last chosen one any expert may follow: one with the largest score
     // (and a bias that nearly cancels it) has the largest error.
     if (lane == a.top_k - 1) ne = fmaxf(ne, score_error<SOFTMAX>(1.0f, 1.0f, st) + 0x1p-22f * fabsf(v));
-    const bool decides = lane < a.top_k && next >= 0 && !(nx == xe && nb == be) && nv == nv;
+    const bool equal = nx == xe && nb == be;
+    bool decides = lane < a.top_k && next >= 0 && !equal && nv == nv;
+    float gap = v - nv;
+    // The last chosen one and an exact equal left out: their order is certain, but
+    // the expert behind the two may be larger than both.
+    const bool more = __shfl_sync(0xffffffffu, mine, a.top_k + 1) >= 0;
+    const float v_more = __shfl_sync(0xffffffffu, v, a.top_k + 1);
+    if (lane == a.top_k - 1 && next >= 0 && equal) {
+      decides = more;
+      gap = v - v_more;
+    }
     const bool groups_sure = sure;
-    sure = sure && !__any_sync(0xffffffffu, decides && !(v - nv > err + ne) && v == v);
+    sure = sure && !__any_sync(0xffffffffu, decides && !(gap > err + ne) && v == v);
     if (!SOFTMAX && !sure && groups_sure) {
       // Sigmoid scores: only the candidates are computed in fp64, one per lane.
       // They hold the chosen ones if the second expert left out lies certainly
       // below every chosen one.
       const float most = score_error<SOFTMAX>(1.0f, 1.0f, st) +
-                         0x1p-22f * fmaxf(fabsf(__shfl_sync(0xffffffffu, v, 0)), fabsf(__shfl_sync(0xffffffffu, v, a.top_k + 1)));
-      const bool more = __shfl_sync(0xffffffffu, mine, a.top_k + 1) >= 0;
-      const float gap = __shfl_sync(0xffffffffu, v, a.top_k - 1) - __shfl_sync(0xffffffffu, v, a.top_k + 1);
-      if (!more || gap > 2.0f * most) {
+                         0x1p-22f * fmaxf(fabsf(__shfl_sync(0xffffffffu, v, 0)), fabsf(v_more));
+      const float left = __shfl_sync(0xffffffffu, v, a.top_k - 1) - v_more;
+      if (!more || left > 2.0f * most) {
         const bool candidate = lane <= a.top_k && mine >= 0;
         const RowStats<double> sd{0.0, 1.0};
         const uint64_t key = candidate ? order_key(route_score<SOFTMAX, double>(xe, sd) + (double)be) : 0ull;
