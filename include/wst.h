@@ -54,7 +54,8 @@
  *    wst_workspace_size(...) bytes, zero-filled once before first use (for
  *    example with wst_workspace_init).  It carries the device error word and,
  *    for IKBO, the per-user partial products and their ready flags.  One
- *    workspace must not be used by two calls that can run at the same time.
+ *    workspace may serve different operations one after another, but must not
+ *    be used by two calls that can run at the same time.
  *  - Errors found on the host are returned before anything is enqueued.
  *    Errors found on the device (a bounded wait that ran out, inconsistent
  *    device offsets, a row index out of range in wst_permute_rows) are

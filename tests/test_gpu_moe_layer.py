@@ -207,3 +207,51 @@ def test_gradient_from_a_graph(wst):
     for got, w in zip((dy, dw, dlog, dB), want):
         assert torch.equal(got, w)
     assert layer.status() == [0, 0, 0]
+
+
+SHARED_WORKSPACE = r'''
+import sys, torch
+sys.path.insert(0, %r); sys.path.insert(0, %r)
+import synthetic
+import warp_specialized_tensor_gb300 as wst
+wst.load_library()
+ws = wst.gemm_fp8_workspace()
+# counts of 1 for experts 0 .. 63 of the first chunk, behind the header: where the
+# first IKBO call of the process keeps the flags of 64 users
+e = torch.full((4096,), 64, dtype=torch.int32)
+e[:64] = torch.arange(64)
+i32 = dict(dtype=torch.int32, device="cuda")
+wst.wst_moe_plan(e.view(1024, 4).cuda(), 65, torch.empty(66, **i32), torch.empty(4096, **i32), torch.empty(4096, **i32),
+                 torch.empty(1024, 4, **i32), workspace=ws)
+d = {k: v.cuda() for k, v in synthetic.ikbo(users=64, cand_per_user=40, seed=5).items()}
+O, D = d["W"].shape[0], d["U"].shape[2]
+assert ws.numel() >= wst.wst_workspace_size(64, O, D)
+def ikbo(ws):
+    Y = torch.full((d["C"].shape[0], O, D), float("nan"), device="cuda")
+    wst.wst_ikbo_linear_compress(d["U"], d["C"], d["W"], d["user_offsets"], Y, ws)
+    assert wst.wst_sync_status(ws) == 0
+    return Y
+first = ikbo(ws)
+want = ikbo(wst.workspace(64, O, D))
+assert torch.equal(first, want)
+# the sums of a split product in the same place
+f8 = torch.float8_e4m3fn
+q, qb = torch.ones(16, 8192, device="cuda").to(f8), torch.ones(512, 8192, device="cuda").to(f8)
+C = torch.empty(16, 512, device="cuda")
+for _ in range(3):
+    wst.wst_gemm_fp8(q, torch.ones(64, 16, device="cuda"), qb, torch.ones(4, 64, device="cuda"), C, workspace=ws)
+    assert (C == 8192).all()
+    assert torch.equal(ikbo(ws), want)
+print("ok")
+'''
+
+
+def test_other_operations_on_the_same_workspace():
+    # in a process of its own: the flags' values count its calls
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", SHARED_WORKSPACE % (root, os.path.join(root, "tests"))], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.rstrip().endswith("ok"), r.stdout + r.stderr

@@ -184,3 +184,14 @@ def test_every_function_has_its_argument_types(lib):
     for name in [n for n in wst.moe.__all__ if n.startswith("wst_")]:
         fn = getattr(lib, name)
         assert fn.argtypes is not None and fn.restype in (ctypes.c_int, ctypes.c_size_t)
+
+
+def test_flag_values_equal_no_count_and_no_sum(lib):
+    # A workspace may hold the plan's counts or fp32 sums where another operation
+    # keeps its ready flags: the flags' values are NaNs that arithmetic does not return.
+    import numpy as np
+    fresh = getattr(lib, "_ZN3wst15next_flag_epochEv")
+    fresh.restype = ctypes.c_uint32
+    v = np.array([fresh() for _ in range(100000)], dtype=np.uint32)
+    assert len(set(v.tolist())) == v.size
+    assert np.isnan(v.view(np.float32)).all() and not np.isin(v, [0x7fffffff, 0xffffffff]).any()

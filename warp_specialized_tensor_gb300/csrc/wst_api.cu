@@ -48,10 +48,13 @@ int cuda_fail(cudaError_t e, const char* what) {
 }
 
 uint32_t next_flag_epoch() {
-  static std::atomic<uint32_t> counter{0};
-  uint32_t e = counter.fetch_add(1u, std::memory_order_relaxed) + 1u;
-  if (e == 0u) e = counter.fetch_add(1u, std::memory_order_relaxed) + 1u;  // skip 0 on wrap
-  return e;
+  // NaNs other than the one that arithmetic returns (all mantissa bits set): a
+  // workspace may hold other calls' counts or fp32 sums where the flags lie, and
+  // neither ever has these bits.  The values come round again after 16.7 million calls.
+  constexpr uint64_t n = 0x7ffffeu;
+  static std::atomic<uint64_t> counter{0};
+  const uint64_t i = counter.fetch_add(1u, std::memory_order_relaxed) % (2 * n);
+  return (i >= n ? 0xff800001u : 0x7f800001u) + (uint32_t)(i % n);
 }
 
 int current_device_info(DeviceInfo* out) {

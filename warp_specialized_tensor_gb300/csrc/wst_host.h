@@ -50,9 +50,10 @@ enum Option : int {
 int option_value(int opt);
 
 unsigned long long wait_timeout_ns();
-// A fresh nonzero value for the cross-CTA ready flags of one call (IKBO
-// partials, split attention items): a process-wide counter, so flags left in
-// a workspace by earlier calls never equal it (zeroed workspaces hold 0).
+// A fresh value for the cross-CTA ready flags of one call (IKBO partials, split
+// attention items), from a process-wide counter.  Flags left in a workspace by
+// earlier calls do not equal it, nor do the zeros of a fresh workspace, counts
+// (wst_moe_plan) or fp32 sums that other operations left where the flags lie.
 uint32_t next_flag_epoch();
 
 // Test hook for the bounded-wait error path: when the environment variable
