@@ -251,3 +251,21 @@ def test_training_products(wst, big_ws):
         half = ref.half(qa.dtype) + ref.half(E4)
         full = abs(va) @ abs(vb).T
         assert (abs(ref.f64(C) - va @ vb.T) <= half * 1.1 * full + 2.0 ** -8 * full).all()
+
+
+@pytest.mark.parametrize("K", [384, 130, 640, 900])
+def test_odd_numbers_of_blocks_are_exact(wst, K):
+    # Many units a pair, each of an odd number of K blocks (three at 384): whole
+    # numbers and scales that are powers of two, so that every bit counts.
+    M, N = 4096, 4100
+    g = torch.Generator().manual_seed(K)
+    qa, qb = torch.randint(-8, 9, (M, K), generator=g), torch.randint(-8, 9, (N, K), generator=g)
+    sa = torch.exp2(torch.randint(0, 3, (-(-K // 128), M), generator=g).float())
+    sb = torch.exp2(torch.randint(0, 3, (-(-N // 128), -(-K // 128)), generator=g).float())
+    va, vb = torch.from_numpy(ref.values(qa, sa, "rows")).cuda(), torch.from_numpy(ref.values(qb, sb, "blocks")).cuda()
+    want = (va @ vb.T).float()
+    A, B, C = rows16(qa.to(E4)), rows16(qb.to(E4)), torch.empty(M, N, device="cuda")
+    for _ in range(10):
+        C.fill_(float("nan"))
+        wst.wst_gemm_fp8(A, sa.cuda(), B, sb.cuda(), C, workspace=wst.workspace())
+        assert torch.equal(C, want)

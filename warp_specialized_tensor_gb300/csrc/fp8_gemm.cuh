@@ -454,8 +454,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           const uint32_t idesc = p.idesc | ((uint32_t)(un.tile.nmma >> 3) << 17);
           for (int kb = un.k0; kb < un.k1; ++kb) {
             if (((kb - un.k0) & 1) == mine) {
-              ok = f8_wait<false>(guard, full_bar(stage), phase, (kRoleMma << 16) | stage) &&
-                   f8_wait<false>(guard, acce_bar(mine), acc_phase ^ 1u, (kRoleMma << 16) | 0x100 | mine);
+              // The accumulator first: its hand-back means that the epilogue has added
+              // this issuer's block before, hence every block up to it, so full[stage]
+              // has completed the lap before this one.  (With three K blocks a unit an
+              // issuer's blocks are three apart, and without that full[stage] could be
+              // two laps behind, whose parity reads as complete.)
+              ok = f8_wait<false>(guard, acce_bar(mine), acc_phase ^ 1u, (kRoleMma << 16) | 0x100 | mine) &&
+                   f8_wait<false>(guard, full_bar(stage), phase, (kRoleMma << 16) | stage);
               if (!ok) break;
               tc_fence_after_sync();
               const uint32_t wBase = smem_addr(smW + stage * kF8WBytes);
