@@ -127,3 +127,60 @@ def test_the_kernel_waits_in_that_order():
     issuer = text[text.index("MMA issuers (leader)"):text.index("umma_commit_pair(accf_bar(mine)")]
     waits = re.findall(r"f8_wait<false>\(guard, (\w+)\(", issuer)
     assert waits == ["acce_bar", "full_bar"]
+
+
+def leave(units, rule, rng, warps=8):
+    """The warps of the split epilogue: True if none is left waiting for another.
+
+    A warp's wait for a unit's blocks may run out (or find that another's did); the
+    rule says whether it then leaves by itself or by what warp 4 wrote down
+    between the two barriers."""
+    abort, last = False, None
+    state = [dict(unit=0, bar=0, ok=True) for _ in range(warps)]   # bar: barriers passed in this unit
+    out = [False] * warps
+    waiting = [False] * warps
+    for _ in range(5000):
+        live = [w for w in range(warps) if not out[w]]
+        if not live:
+            return True
+        ready = [w for w in live if not waiting[w]]
+        if not ready:
+            if len(live) < warps:
+                return False                                       # (a warp that left does not come to the barrier)
+            waiting = [False] * warps
+            for s in state:
+                s["bar"] += 1
+            continue
+        w = rng.choice(ready)
+        s = state[w]
+        if s["bar"] == 0:
+            if s["unit"] == units:
+                out[w] = True
+                continue
+            if s["ok"] and rng.random() < (0.5 if abort else 0.1):
+                s["ok"], abort = False, True
+            waiting[w] = True
+        elif s["bar"] == 1:
+            if w == 0:
+                last = "given up" if abort else "store"
+            waiting[w] = True
+        else:
+            if (not s["ok"]) if rule == "alone" else last == "given up":
+                out[w] = True
+                continue
+            s["unit"] += 1
+            s["bar"] = 0
+    return False
+
+
+def test_warps_that_give_up_leave_together():
+    for seed in range(500):
+        assert leave(4, "together", random.Random(seed))
+    assert not all(leave(4, "alone", random.Random(seed)) for seed in range(500))
+
+
+def test_the_kernel_leaves_by_what_was_written_down():
+    text = open(SOURCE).read()
+    split = text[text.index("if (un.split >= 0) {"):]
+    after = split[:split.index("const float* parts")].split("bar.sync 1")[2]
+    assert re.findall(r"if \(([^)]*)\) (break|continue);", after) == [("last == 2u", "break"), ("last == 0u", "continue")]

@@ -269,3 +269,22 @@ def test_odd_numbers_of_blocks_are_exact(wst, K):
         C.fill_(float("nan"))
         wst.wst_gemm_fp8(A, sa.cuda(), B, sb.cuda(), C, workspace=wst.workspace())
         assert torch.equal(C, want)
+
+
+def test_bad_offsets_of_split_products(wst, big_ws):
+    # Overlapping groups: more units of a split loop than pairs; clamped, latched,
+    # and the workspace is as good as before.
+    G, M, N, K = 60, 2, 256, 2048
+    qa, sa = operand(M, K, "rows", E4, 60)
+    qb, sb = operand(N, K, "blocks", E4, 61, (G,))
+    C = torch.zeros(M, N, device="cuda")
+    off = torch.tensor([0, 2] * 30 + [0], dtype=torch.int32, device="cuda")
+    args = (rows16(qa), sa.cuda(), rows16(qb), sb.cuda())
+    wst.wst_grouped_gemm_fp8(*args, off, C, workspace=big_ws)
+    assert wst.wst_sync_status(big_ws) == wst.WST_ERR_BAD_OFFSETS
+    off = torch.tensor([0, 1] + [1] * 58 + [2], dtype=torch.int32, device="cuda")
+    wst.wst_grouped_gemm_fp8(*args, off, C, workspace=big_ws)
+    assert wst.wst_sync_status(big_ws) == 0
+    for row, g in ((0, 0), (1, G - 1)):
+        want, size = product(qa[row:row + 1], sa[:, row:row + 1], qb[g], sb[g], "blocks")
+        assert (abs(ref.f64(C[row:row + 1]) - want) <= bound(want, size, K, torch.float32)).all()

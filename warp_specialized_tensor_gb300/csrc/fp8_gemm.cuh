@@ -744,8 +744,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       const int n_base = tl.n0 + (int)rank * 128 + q * 32;
       if (un.split >= 0) {
         // Store the sums, 128 of each of the epilogue's threads, and count in.
-        // (A warp that gave up waiting still takes part in the barriers, and
-        // nothing is counted then.)
+        // (A warp that gave up waiting still takes part in the barriers; nothing
+        // is counted then, and all warps leave together, or the others would wait
+        // for it at the next unit's barrier.)
         float* slots = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.ws) + kWsHeaderBytes) + (threadIdx.x - 128);
         const long long first = un.index * splits;
         float* mine = slots + ((first + un.split) * 2 + rank) * kF8SlotFloats;
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         __threadfence();
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kF8EpiWarps) : "memory");
         if (warp == 4 && lane == 0) {
-          uint32_t last = 0u;
+          uint32_t last = 2u;  // 2: given up
           if (!*abort_flag) {
             uint32_t* c = p.ws->pad + un.index;
             const uint32_t shift = 16u * rank;
@@ -770,8 +771,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           *last_flag = last;
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kF8EpiWarps) : "memory");
-        if (!ok) break;
-        if (!*last_flag) continue;
+        const uint32_t last = *last_flag;
+        if (last == 2u) break;
+        if (last == 0u) continue;
         __threadfence();
         const float* parts = slots + (first * 2 + rank) * kF8SlotFloats;
 #pragma unroll
