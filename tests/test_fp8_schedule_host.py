@@ -184,3 +184,39 @@ def test_the_kernel_leaves_by_what_was_written_down():
     split = text[text.index("if (un.split >= 0) {"):]
     after = split[:split.index("const float* parts")].split("bar.sync 1")[2]
     assert re.findall(r"if \(([^)]*)\) (break|continue);", after) == [("last == 2u", "break"), ("last == 0u", "continue")]
+
+
+@pytest.fixture(scope="module")
+def splits(tmp_path_factory):
+    """The kernel's own rule, compiled for the host."""
+    import ctypes
+    import subprocess
+    text = open(SOURCE).read()
+    body = re.search(r"__host__ __device__ inline (int f8_splits\(.*?\n}\n)", text, re.S).group(1)
+    tile = re.search(r"constexpr int kF8Tile = (\d+);", text).group(1)
+    units = int(re.search(r"constexpr int kF8MaxUnits = (\d+);", text).group(1))
+    d = tmp_path_factory.mktemp("splits")
+    (d / "s.cpp").write_text("constexpr int kF8Tile = %s;\nextern \"C\" %s" % (tile, body))
+    subprocess.run(["g++", "-shared", "-fPIC", "-o", str(d / "s.so"), str(d / "s.cpp")], check=True)
+    fn = ctypes.CDLL(str(d / "s.so")).f8_splits
+    fn.argtypes = [ctypes.c_longlong] + [ctypes.c_int] * 4
+    return lambda tiles, pairs, M, K: fn(tiles, pairs, -(-K // 128), units, M)
+
+
+@pytest.mark.parametrize("pairs", [70, 74, 76])
+def test_the_sizes_meant_to_split_do(splits, pairs):
+    from test_gpu_fp8 import SPLIT_DENSE, SPLIT_GROUPED
+    for M, N, K in SPLIT_DENSE:
+        tiles = -(-M // 256) * -(-N // 256)
+        assert 2 <= splits(tiles, pairs, M, K) <= pairs // tiles
+    for sizes, N, K in SPLIT_GROUPED:
+        tiles = sum(-(-s // 256) for s in sizes) * -(-N // 256)
+        assert 2 <= splits(tiles, pairs, sum(sizes) + 7, K) <= pairs // tiles
+
+
+def test_the_rule_keeps_every_unit_on_a_pair_of_its_own(splits):
+    rng = random.Random(0)
+    for _ in range(5000):
+        tiles, pairs, M, K = rng.randrange(0, 200), rng.randrange(1, 80), rng.randrange(1, 5000), rng.randrange(1, 20000)
+        s = splits(tiles, pairs, M, K)
+        assert s >= 1 and (s == 1 or (s * tiles <= min(pairs, 120) and s <= -(-K // 128)))

@@ -288,3 +288,92 @@ def test_bad_offsets_of_split_products(wst, big_ws):
     for row, g in ((0, 0), (1, G - 1)):
         want, size = product(qa[row:row + 1], sa[:, row:row + 1], qb[g], sb[g], "blocks")
         assert (abs(ref.f64(C[row:row + 1]) - want) <= bound(want, size, K, torch.float32)).all()
+
+
+# Sizes whose K loops are split (tests/test_fp8_schedule_host.py holds the rule
+# to that): one token tile and several, at most 64 tokens and more, ragged ends.
+SPLIT_DENSE = [(7, 1030, 1800), (64, 512, 4096), (65, 520, 2100), (128, 1024, 8192), (200, 300, 4096), (300, 512, 4096),
+               (520, 260, 8197)]
+SPLIT_GROUPED = [([5, 0, 130, 0, 17], 300, 4096), ([300, 0, 70], 260, 4000), ([0, 16, 0, 33, 1, 0], 700, 2560), ([257], 128, 6000)]
+
+
+def activated(x, epi):
+    t = torch.from_numpy(x)
+    return {"none": t, "bias": t, "bias_silu": t * torch.sigmoid(t), "bias_gelu": t * torch.special.ndtr(t)}[epi].numpy()
+
+
+def activated_bound(x, err, y, epi, dtype):
+    # slopes are below 1.13; the approximate tanh behind SiLU is off by 2^-11, its half by 2^-12 of |x|
+    tol = 1.13 * (err + ref.U * abs(x)) + abs(x) * {"none": 0.0, "bias": 0.0, "bias_silu": 2.0 ** -12, "bias_gelu": 2.0 ** -21}[epi]
+    return tol + ref.half(dtype) * (abs(y) + tol)
+
+
+@pytest.mark.parametrize("scaling", ["blocks", "rows"])
+@pytest.mark.parametrize("M,N,K", SPLIT_DENSE)
+def test_split_dense(wst, big_ws, M, N, K, scaling):
+    qa, sa = operand(M, K, "rows", E4, 70)
+    qb, sb = operand(N, K, scaling, E4, 71)
+    sb = sb * 0.01
+    want, size = product(qa, sa, qb, sb, scaling)
+    bias = torch.randn(N, generator=torch.Generator().manual_seed(2)).bfloat16()
+    args = (rows16(qa), sa.cuda(), rows16(qb), sb.cuda())
+    for dtype in (torch.float32, torch.bfloat16):
+        for epi in ("none", "bias", "bias_silu", "bias_gelu"):
+            x = want if epi == "none" else want + ref.f64(bias)
+            y = activated(x, epi)
+            tol = activated_bound(x, bound(want, size, K, torch.float32), y, epi, dtype)
+            buf = out_buffer(M, N, dtype)
+            outs = []
+            for _ in range(2):
+                buf[:M, :N] = float("nan")
+                wst.wst_gemm_fp8(*args, buf[:M, :N], scaling=scaling, bias=bias.cuda(), epi=epi, workspace=big_ws)
+                outs.append(buf[:M, :N].clone())
+            assert wst.wst_sync_status(big_ws) == 0
+            assert torch.equal(*outs)
+            assert (abs(ref.f64(outs[0]) - y) <= tol).all()
+            assert torch.isnan(buf[M:].float()).all() and torch.isnan(buf[:, N:].float()).all()
+
+
+@pytest.mark.parametrize("scaling", ["blocks", "rows"])
+@pytest.mark.parametrize("sizes,N,K", SPLIT_GROUPED)
+def test_split_grouped(wst, big_ws, sizes, N, K, scaling):
+    G, off = len(sizes), np.concatenate([[0], np.cumsum(sizes)])
+    M = int(off[-1]) + 7                                   # rows behind the last group
+    qa, sa = operand(M, K, "rows", E4, 72)
+    qb, sb = operand(N, K, scaling, E4, 73, (G,))
+    sb = sb * 0.01
+    bias = torch.randn(G, N, generator=torch.Generator().manual_seed(3)).bfloat16()
+    args = (rows16(qa), sa.cuda(), rows16(qb), sb.cuda(), torch.from_numpy(off).int().cuda())
+    for dtype in (torch.float32, torch.bfloat16):
+        for epi in ("none", "bias", "bias_silu", "bias_gelu"):
+            buf = out_buffer(M, N, dtype)
+            wst.wst_grouped_gemm_fp8(*args, buf[:M, :N], scaling=scaling, bias=bias.cuda(), epi=epi, workspace=big_ws)
+            assert wst.wst_sync_status(big_ws) == 0
+            for g in range(G):
+                r = slice(off[g], off[g + 1])
+                want, size = product(qa[r], sa[:, r], qb[g], sb[g], scaling)
+                x = want if epi == "none" else want + ref.f64(bias[g])
+                y = activated(x, epi)
+                tol = activated_bound(x, bound(want, size, K, torch.float32), y, epi, dtype)
+                assert (abs(ref.f64(buf[r, :N]) - y) <= tol).all()
+            assert torch.isnan(buf[off[-1]:].float()).all() and torch.isnan(buf[:, N:].float()).all()
+
+
+def test_split_exact_and_in_graphs(wst, big_ws):
+    # whole numbers, several token tiles: every bit, eagerly and replayed
+    M, N, K = 300, 512, 4096
+    g = torch.Generator().manual_seed(9)
+    qa, qb = torch.randint(-8, 9, (M, K), generator=g), torch.randint(-8, 9, (N, K), generator=g)
+    sa, sb = torch.ones(32, M), torch.full((4, 32), 0.5)
+    want = torch.from_numpy((qa.double() @ qb.double().T * 0.5).numpy()).float()
+    args = (qa.to(E4).cuda(), sa.cuda(), qb.to(E4).cuda(), sb.cuda(), torch.empty(M, N, device="cuda"))
+    wst.wst_gemm_fp8(*args, workspace=big_ws)
+    assert torch.equal(args[4].cpu(), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        wst.wst_gemm_fp8(*args, workspace=big_ws)
+    for _ in range(5):
+        args[4].fill_(float("nan"))
+        graph.replay()
+        assert torch.equal(args[4].cpu(), want)
+    assert wst.wst_sync_status(big_ws) == 0
