@@ -78,7 +78,7 @@ typedef enum {
   WST_ERR_UNSUPPORTED = 3,  /* valid request this build does not implement        */
   WST_ERR_CUDA = 4,         /* a CUDA runtime/driver call failed (see message)    */
   WST_ERR_TIMEOUT = 5,      /* a device-side bounded wait ran out                 */
-  WST_ERR_BAD_OFFSETS = 6   /* device offsets not non-decreasing from 0 to total  */
+  WST_ERR_BAD_OFFSETS = 6   /* device offsets break their operation's rule       */
 } wst_status;
 
 typedef enum { WST_F32 = 0, WST_BF16 = 1 } wst_dtype;
@@ -257,9 +257,10 @@ size_t wst_gemm_norm_workspace_size(int batch, int M, int N, long strideA, long 
 
 /*
  * Grouped GEMM over G groups sharing N and K.  d_offsets is a DEVICE int32
- * array of G+1 entries, non-decreasing, d_offsets[0] = 0, d_offsets[G] =
+ * array of G+1 entries, non-decreasing, d_offsets[0] = 0, d_offsets[G] <=
  * M_total; group g owns rows [d_offsets[g], d_offsets[g+1]) of A and C
- * (empty groups allowed):
+ * (empty groups allowed; rows behind the last group belong to none, as where
+ * wst_moe_plan had pairs without an expert):
  *   C[m][n] = epi( sum_k A[m][k] * B[g][n][k] (+ bias[g][n]) ),  m in group g
  *   A     bf16 [M_total][K] row-major, leading dimension lda
  *   B     bf16, element (g,n,k) at B + g*strideB_group + n*ldb + k
@@ -332,8 +333,9 @@ wst_status wst_ep_receive_plan(int world_size, int experts_per_rank, const int* 
  * src, dst: DEVICE pointers, rows of row_bytes bytes at src_stride /
  * dst_stride bytes apart (row_bytes and strides multiples of 16, pointers
  * 16-byte aligned); the index arrays are DEVICE int32 (or NULL), and the
- * source / destination hold n_src_rows / n_dst_rows rows.  An index outside
- * them skips the row and latches WST_ERR_INVALID_ARG in `workspace` (a
+ * source / destination hold n_src_rows / n_dst_rows rows.  An index of -1 (no
+ * row: what wst_moe_plan leaves behind the last one) skips the row; another
+ * outside them skips it and latches WST_ERR_INVALID_ARG in `workspace` (a
  * zero-filled workspace of at least wst_workspace_size(0, 0, 0) bytes) for
  * wst_sync_status.  Asynchronous on `stream`.
  */
@@ -512,8 +514,8 @@ wst_status wst_gemm_fp8(int M, int N, int K, const void* A, long lda, wst_fp8 a_
 
 /* The same for G groups of rows: rows [d_offsets[g], d_offsets[g+1]) of A and C
  * with B + g*strideB_group, scaleB + g*strideSB_group and bias + g*strideBias
- * (offsets as in wst_grouped_gemm_bf16, except that d_offsets[G] may be less
- * than M_total: rows behind the last group are left as they were). */
+ * (offsets as in wst_grouped_gemm_bf16: rows behind the last group are left as
+ * they were). */
 wst_status wst_grouped_gemm_fp8(int G, int M_total, int N, int K, const void* A, long lda, wst_fp8 a_type,
                                 const float* scaleA, long ldsa, const void* B, long ldb,
                                 long strideB_group, wst_fp8 b_type, const float* scaleB, long ldsb,
@@ -533,10 +535,9 @@ size_t wst_gemm_fp8_workspace_size(void);
  *   A   bf16 [M_total][K], leading dimension lda
  *   dB  db_type, element (g,n,k) at dB + g*stride_dB + n*lddb + k; it must not
  *       overlap dC or A
- * d_offsets as in wst_grouped_gemm_bf16, except that d_offsets[G] may be less
- * than M_total: rows behind the last group belong to no gradient (whatever they
- * hold).  Pointers 16-byte aligned, leading dimensions and strides multiples of
- * 16 bytes.  (The gradient of the rows is wst_grouped_gemm_bf16 of dC with the
+ * d_offsets as in wst_grouped_gemm_bf16; rows behind the last group belong to
+ * no gradient (whatever they hold).  Pointers 16-byte aligned, leading
+ * dimensions and strides multiples of 16 bytes.  (The gradient of the rows is wst_grouped_gemm_bf16 of dC with the
  * weights transposed.)
  */
 wst_status wst_grouped_gemm_wgrad_bf16(int G, int M_total, int N, int K, const void* dC, long lddc,

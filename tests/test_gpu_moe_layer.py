@@ -255,3 +255,70 @@ def test_other_operations_on_the_same_workspace():
     r = subprocess.run([sys.executable, "-c", SHARED_WORKSPACE % (root, os.path.join(root, "tests"))], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and r.stdout.rstrip().endswith("ok"), r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("live", [100, 1, 0])
+@pytest.mark.parametrize("schedule", ["SCHED_STATIC", "SCHED_CLC"])
+def test_layer_in_bf16_with_padding_tokens(wst, live, schedule):
+    # Padding tokens have no expert: no row, no error, a zero in the output and in
+    # the gradients; rows behind the last group stay as they were.
+    T, E, k, K, N = 120, 8, 2, 256, 264
+    logits, x, B = inputs(T, E, K, N, 11)
+    logits[live:] = -torch.inf
+    x[live:] = torch.nan
+    layer = Layer(wst, T, E, k, K, N)
+    layer.rows.fill_(float("nan"))
+    layer.y.fill_(7.0)
+    dl, dB_ = logits.cuda(), B.cuda()
+    wst.wst_set_option(wst.OPT_GROUPED_SCHEDULE, getattr(wst, schedule))
+    try:
+        layer.forward(dl, x.cuda(), dB_)
+        assert layer.status() == [0, 0, 0]
+        e, w = experts_of(layer, logits, k)
+        rows = live * k
+        assert int(layer.offsets[-1]) == rows and (layer.y[rows:] == 7.0).all() and torch.isnan(layer.rows[rows:].float()).all()
+        assert (layer.out[live:] == 0).all()
+        X, W = ref.f64(x[:live]), ref.f64(B)
+        want = np.einsum("ti,tk,tink->tn", w[:live], X, W[e[:live]])
+        size = np.einsum("ti,tk,tink->tn", abs(w[:live]), abs(X), abs(W[e[:live]]))
+        assert (abs(ref.f64(layer.out[:live]) - want) <= 2.02 * BF * size).all()
+
+        dout = torch.randn(T, N, generator=torch.Generator().manual_seed(1)).bfloat16()
+        D = ref.f64(dout[:live])
+        dy, dweights, dlogits = torch.full_like(layer.y, float("nan")), torch.empty(T, k, device="cuda"), torch.empty(T, E, device="cuda")
+        drows = torch.full((T * k, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+        dx, dB = torch.empty(T, K, device="cuda"), torch.empty(E, N, K, device="cuda")
+        wst.wst_moe_combine_backward(dout.cuda(), layer.position, y=layer.y, weights=layer.weights, dy=dy, dweights=dweights,
+                                     workspace=layer.ws)
+        wst.wst_moe_route_backward(dl, layer.experts, dweights, dlogits, score="sigmoid", renorm=True, scale=1.5)
+        wst.wst_grouped_gemm_bf16(dy, dB_.transpose(1, 2).contiguous(), layer.offsets, drows, workspace=layer.ws)
+        wst.wst_moe_combine(drows, layer.position, dx, workspace=layer.ws)
+        wst.wst_grouped_gemm_wgrad_bf16(dy, layer.rows, layer.offsets, dB, workspace=layer.ws)
+        assert layer.status() == [0, 0, 0]
+    finally:
+        wst.wst_set_option(wst.OPT_GROUPED_SCHEDULE, wst.SCHED_STATIC)
+    assert (dweights[live:] == 0).all() and (dlogits[live:] == 0).all() and (dx[live:] == 0).all()
+    assert torch.isnan(drows[rows:].float()).all()
+    want_dx = np.einsum("ti,tn,tink->tk", w[:live], D, W[e[:live]])
+    size_dx = np.einsum("ti,tn,tink->tk", abs(w[:live]), abs(D), abs(W[e[:live]]))
+    assert (abs(ref.f64(dx[:live]) - want_dx) <= 2.02 * BF * size_dx).all()                # dy's and the rows' rounding
+    want_dB, size_dB = np.zeros((E, N, K)), np.zeros((E, N, K))
+    for t in range(live):
+        for i in range(k):
+            want_dB[e[t, i]] += w[t, i] * np.outer(D[t], X[t])
+            size_dB[e[t, i]] += abs(w[t, i]) * np.outer(abs(D[t]), abs(X[t]))
+    assert (abs(ref.f64(dB) - want_dB) <= 1.01 * BF * size_dB).all()                       # dy's rounding
+
+
+def test_other_bad_rows_and_offsets_are_still_latched(wst):
+    ws = wst.workspace()
+    src, dst = torch.randn(4, 8, device="cuda").bfloat16(), torch.zeros(3, 8, device="cuda").bfloat16()
+    for bad in (-2, 4):
+        idx = torch.tensor([1, bad, -1], dtype=torch.int32, device="cuda")
+        wst.wst_permute_rows(src, dst, src_index=idx, workspace=ws)
+        assert wst.wst_sync_status(ws) == wst.WST_ERR_INVALID_ARG
+        assert torch.equal(dst[0], src[1]) and (dst[1:] == 0).all()
+    A, B, C = torch.randn(8, 64).bfloat16().cuda(), torch.randn(2, 64, 64).bfloat16().cuda(), torch.zeros(8, 64, device="cuda")
+    for off in ([1, 2, 8], [0, 5, 4], [0, 5, 9]):
+        wst.wst_grouped_gemm_bf16(A, B, torch.tensor(off, dtype=torch.int32, device="cuda"), C, workspace=ws)
+        assert wst.wst_sync_status(ws) == wst.WST_ERR_BAD_OFFSETS

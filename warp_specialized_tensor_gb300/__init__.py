@@ -355,7 +355,8 @@ def wst_grouped_gemm_bf16(A, B, offsets, C, bias=None, epi="none", workspace=Non
     """Rows [off[g], off[g+1]) of C = epi(rows of A . B[g]^T (+ bias[g])).
 
     A: bf16 [M_total,K]; B: bf16 [G,N,K]; offsets: device int32 [G+1];
-    C: bf16/fp32 [M_total,N]; bias: bf16 [G,N]."""
+    C: bf16/fp32 [M_total,N]; bias: bf16 [G,N].  Rows behind offsets[G] are
+    left as they were."""
     _need(A, "A", torch.bfloat16, (2,))
     _need(B, "B", torch.bfloat16, (3,))
     _need(C, "C", None, (2,))
@@ -542,8 +543,8 @@ def wst_permute_rows(src, dst, src_index=None, dst_index=None, n_rows=None, work
     """dst[dst_index[i] (or i)] = src[src_index[i] (or i)] for i < n_rows, on the GPU.
 
     src, dst: CUDA tensors of rows (2-D, last dimension contiguous, the same
-    bytes per row); src_index / dst_index: CUDA int32 tensors or None;
-    n_rows defaults to the index length (else the source's rows)."""
+    bytes per row); src_index / dst_index: CUDA int32 tensors or None (-1: no
+    row, skipped); n_rows defaults to the index length (else the source's rows)."""
     for t, n in ((src, "src"), (dst, "dst")):
         _need(t, n, None, (2,))
     row_bytes = src.shape[1] * src.element_size()

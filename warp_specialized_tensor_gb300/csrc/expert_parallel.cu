@@ -36,8 +36,8 @@ namespace wst {
 
 // Row permutation: dst[d ? d[i] : i] = src[s ? s[i] : i] for i < n, each row
 // `vecs` 16-byte vectors.  One warp per row, rows strided over the grid;
-// indices outside [0, n_src) / [0, n_dst) skip the row and latch
-// WST_ERR_INVALID_ARG in the workspace header.
+// an index of -1 (no row) skips the row, others outside [0, n_src) /
+// [0, n_dst) skip it and latch WST_ERR_INVALID_ARG in the workspace header.
 __global__ void __launch_bounds__(256) k_permute_rows(int n, int vecs, const uint4* __restrict__ src,
                                                       long long src_stride, const int* __restrict__ sidx,
                                                       int n_src, uint4* __restrict__ dst,
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(256) k_permute_rows(int n, int vecs, const uin
     const int si = sidx ? __ldg(sidx + i) : (int)i;
     const int di = didx ? __ldg(didx + i) : (int)i;
     if (si < 0 || si >= n_src || di < 0 || di >= n_dst) {
-      if (lane == 0) latch_error(ws, 1u /*WST_ERR_INVALID_ARG*/, 0x50000u);
+      if (lane == 0 && si != -1 && di != -1) latch_error(ws, 1u /*WST_ERR_INVALID_ARG*/, 0x50000u);
       continue;
     }
     const uint4* s = src + (long long)si * src_stride;

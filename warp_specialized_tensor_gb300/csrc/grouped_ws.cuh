@@ -181,7 +181,7 @@ __device__ __forceinline__ long long grp_total_tiles(const GroupedArgs& p) {
 }
 
 static __device__ __noinline__ void grouped_check_offsets(const GroupedArgs& p) {
-  bool bad = __ldg(p.offsets) != 0 || __ldg(p.offsets + p.G) != p.M_total;
+  bool bad = __ldg(p.offsets) != 0;  // (rows behind the last group belong to none)
   int prev = 0;
   for (int g = 0; g <= p.G && !bad; ++g) {
     const int v = __ldg(p.offsets + g);
