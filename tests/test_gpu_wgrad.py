@@ -102,3 +102,25 @@ def test_bad_offsets_latched(wst):
     assert status == wst.WST_ERR_BAD_OFFSETS
     _, status = run(wst, dC, A, [3, 100, 120, 300], torch.float32)
     assert status == wst.WST_ERR_BAD_OFFSETS
+
+
+@pytest.mark.parametrize("N,K", [(16, 24), (200, 328), (33, 70), (300, 333), (264, 520), (1, 3)])
+def test_bf16_accumulation_rounds_once(wst, N, K):
+    # dB holds the negative of the gradient in bf16, so what is left is the part that
+    # a gradient rounded to bf16 first would have lost; and an ordinary dB.
+    sizes = [40, 0, 129, 7]
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    g = torch.Generator().manual_seed(N * K)
+    dC, A = torch.randn(int(off[-1]), N, generator=g).bfloat16(), torch.randn(int(off[-1]), K, generator=g).bfloat16()
+    d, a = ref.f64(dC), ref.f64(A)
+    parts = [slice(off[i], off[i + 1]) for i in range(len(sizes))]
+    want = np.stack([d[r].T @ a[r] for r in parts])
+    size = np.stack([abs(d[r]).T @ abs(a[r]) for r in parts])
+    for before in (-torch.from_numpy(want).bfloat16(), torch.randn(len(sizes), N, K, generator=g).bfloat16() * 8):
+        out, status = run(wst, dC, A, off, torch.bfloat16, before)
+        assert status == 0
+        b = ref.f64(before)
+        # one fp32 rounding (cut off: 2u) per token, one of the sum in fp32, one to bf16
+        err = 2 * ref.U * np.array(sizes)[:, None, None] * size
+        err = err + ref.U * (abs(want + b) + err)
+        assert (abs(ref.f64(out) - (want + b)) <= err + ref.half(torch.bfloat16) * (abs(want + b) + err)).all()

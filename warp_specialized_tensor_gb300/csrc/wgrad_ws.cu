@@ -10,10 +10,10 @@ namespace wst {
 
 namespace {
 
-template <bool OUT_F32>
+template <bool OUT_F32, bool ADD_BF16>
 int launch_wgrad(const WgArgs& a, const void* dC, long lddc, const void* A, long lda, void* dB, long lddb, long stride_dB,
                  const DeviceInfo& dev, cudaStream_t stream) {
-  auto kern = k_wgrad_ws<OUT_F32>;
+  auto kern = k_wgrad_ws<OUT_F32, ADD_BF16>;
   CUtensorMap tmD, tmA, tmOut;
   int st;
   // Without a row there is nothing to load (every group is empty): the maps
@@ -116,6 +116,6 @@ extern "C" wst_status wst_grouped_gemm_wgrad_bf16(int G, int M_total, int N, int
   a.ws = static_cast<WsHeader*>(workspace);
   a.timeout_ns = wait_timeout_ns();
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return (wst_status)(db_type == WST_F32 ? launch_wgrad<true>(a, dC, lddc, A, lda, dB, lddb, stride_dB, dev, s)
-                                         : launch_wgrad<false>(a, dC, lddc, A, lda, dB, lddb, stride_dB, dev, s));
+  auto launch = db_type == WST_F32 ? launch_wgrad<true, false> : a.accumulate ? launch_wgrad<false, true> : launch_wgrad<false, false>;
+  return (wst_status)launch(a, dC, lddc, A, lda, dB, lddb, stride_dB, dev, s);
 }

@@ -31,7 +31,7 @@
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (leader), warp 2 tensor
 // memory and offset check, warp 3 row masks, warps 4-11 epilogue (32 output rows
 // by 128 columns each; through swizzled shared memory and TMA stores, or TMA adds
-// when the gradient accumulates).
+// when the gradient accumulates in fp32).
 #pragma once
 
 #include "wst_common.cuh"
@@ -109,7 +109,9 @@ struct WgRing {
   }
 };
 
-template <bool OUT_F32>
+// ADD_BF16: the gradient is added to a bf16 dB (a form of its own: the registers
+// of what dB holds slow the others down, 316 -> 320 us).
+template <bool OUT_F32, bool ADD_BF16>
 __global__ void __launch_bounds__(kWgThreads, 1)
     k_wgrad_ws(const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmA,
                const __grid_constant__ CUtensorMap tmOut, const WgArgs p, const int tiles) {
@@ -290,13 +292,48 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       const WgTile tl = wg_tile(p, offsets, t);
       const bool empty = tl.blocks == 0;
       if (empty && p.accumulate) continue;
+      constexpr int kCols = OUT_F32 ? 32 : 64;  // columns per 128-byte row
+      const int n = tl.n0 + (int)rank * 128 + q * 32;  // first of this warp's rows
+      // ADD_BF16: what dB holds is added to the fp32 sum and rounded once (a TMA add
+      // would round the sum first and the result again).  It is fetched to L2 a
+      // tile ahead, read ahead of the wait, eight lanes to a row of 128 bytes, and
+      // goes through the staging buffer to the lanes that hold the rows.  64 groups
+      // of 512 rows, 1536 x 4096: 369 us (without accumulation 316; with one
+      // row a lane, read behind the wait, 521).
+      [[maybe_unused]] uint4 held[8];
+      [[maybe_unused]] auto read_old = [&](int c) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int row = n + u * 4 + (int)(lane >> 3), col = tl.k0 + c + (int)(lane & 7) * 8;
+          const int cols = row < p.N ? p.K - col : 0;  // (rows begin on 16 bytes; this tile is no other CTA's)
+          const unsigned short* src =
+              static_cast<const unsigned short*>(p.dB) + tl.g * p.stride_dB + (long long)row * p.lddb + col;
+          held[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (cols >= 8) {
+            held[u] = *reinterpret_cast<const uint4*>(src);
+          } else if (cols > 0) {
+            uint32_t part[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e < cols) part[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+            held[u] = make_uint4(part[0], part[1], part[2], part[3]);
+          }
+        }
+      };
+      if constexpr (ADD_BF16) {
+        read_old(half * (kWgTile / 2));
+        if (lane == 0 && t + pairs < tiles) {
+          const WgTile next = wg_tile(p, offsets, t + pairs);
+          const int row = next.n0 + (int)rank * 128 + q * 32, col = next.k0 + half * (kWgTile / 2);
+          for (int c = 0; c < kWgTile / 2; c += kCols)
+            if (row < p.N && col + c < p.K) tma_prefetch_3d(&tmOut, col + c, row, next.g);
+        }
+      }
       if (!empty) {
         if (!warp_wait_phase_cluster(guard, accf_bar(acc), acc_phase, (kRoleEpilogue << 16) | acc)) break;
         tc_fence_after_sync();
       }
-      const int n = tl.n0 + (int)rank * 128 + q * 32;  // first of this warp's rows
       const uint32_t t_lane = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kWgTile);
-      constexpr int kCols = OUT_F32 ? 32 : 64;  // columns per 128-byte row
 #pragma unroll 1
       for (int c = half * (kWgTile / 2); c < (half + 1) * (kWgTile / 2); c += kCols) {
         if (n >= p.N || tl.k0 + c >= p.K) break;  // (warp-uniform; nothing of it is stored)
@@ -309,12 +346,39 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
         } else {
+          [[maybe_unused]] uint4 old[8];  // what dB holds of this lane's row
+          if constexpr (ADD_BF16) {
+            const uint32_t stg = stg0 + sbuf * kWgStgBytes;
+            if (lane == 0) bulk_wait_group_read<kWgStgBufs - 1>();
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const uint32_t r = u * 4 + (lane >> 3);
+              st_shared_v4(stg + r * 128u + (((lane ^ r) & 7) * 16u), held[u].x, held[u].y, held[u].z, held[u].w);
+            }
+            if (c + kCols < (half + 1) * (kWgTile / 2)) read_old(c + kCols);
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(old[u].x), "=r"(old[u].y), "=r"(old[u].z), "=r"(old[u].w)
+                           : "r"(stg + lane * 128u + ((u ^ (lane & 7)) * 16u)));
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float v[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.0f;
             if (!empty) tmem_load32(t_lane + c + h * 32, v);
+            if constexpr (ADD_BF16) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const uint4& word = old[h * 4 + (j >> 3)];
+                const uint32_t two = (j & 6) == 0 ? word.x : (j & 6) == 2 ? word.y : (j & 6) == 4 ? word.z : word.w;
+                v[j] += __uint_as_float(two << 16);
+                v[j + 1] += __uint_as_float(two & 0xffff0000u);
+              }
+            }
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[h * 16 + j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
           }
@@ -332,8 +396,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                   *o = p.accumulate ? *o + __uint_as_float(w[j]) : __uint_as_float(w[j]);
                 } else {
                   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.dB) + at + j;
-                  const float v = __uint_as_float((j & 1) ? (w[j >> 1] & 0xffff0000u) : (w[j >> 1] << 16));
-                  *o = __float2bfloat16_rn(p.accumulate ? __bfloat162float(*o) + v : v);
+                  *o = __float2bfloat16_rn(__uint_as_float((j & 1) ? (w[j >> 1] & 0xffff0000u) : (w[j >> 1] << 16)));
                 }
               }
             }
@@ -351,7 +414,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         __syncwarp();
         if (lane == 0) {
           // (columns and rows past K and N are not stored)
-          if (p.accumulate) tma_add_3d(&tmOut, stg, tl.k0 + c, n, tl.g);
+          if (OUT_F32 && p.accumulate) tma_add_3d(&tmOut, stg, tl.k0 + c, n, tl.g);
           else tma_store_3d(&tmOut, stg, tl.k0 + c, n, tl.g);
           bulk_commit_group();
         }
