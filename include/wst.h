@@ -423,7 +423,8 @@ size_t wst_moe_plan_workspace_size(int num_pairs, int num_experts);
  *   weights   fp32 [T][top_k], or NULL: all 1
  *   out       out_type [T][N], rows ldo apart; every token is written (0 where
  *             it has no row); it must not overlap y
- * Rows are 16-byte aligned; N is arbitrary.  top_k <= 32. */
+ * Rows are 16-byte aligned; N is arbitrary.  top_k <= 32, N < 2^31 - 8192, T <
+ * 2^31 - 1024 (also for the gradients), else WST_ERR_UNSUPPORTED. */
 wst_status wst_moe_combine(int T, int top_k, int N, const void* y, long ldy, wst_dtype y_type,
                            int n_rows, const int* position, const float* weights, void* out, long ldo,
                            wst_dtype out_type, void* workspace, void* stream);

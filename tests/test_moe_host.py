@@ -195,3 +195,16 @@ def test_flag_values_equal_no_count_and_no_sum(lib):
     v = np.array([fresh() for _ in range(100000)], dtype=np.uint32)
     assert len(set(v.tolist())) == v.size
     assert np.isnan(v.view(np.float32)).all() and not np.isin(v, [0x7fffffff, 0xffffffff]).any()
+
+
+@pytest.mark.parametrize("k", [1, 2, 4])
+def test_combine_rejects_what_32_bits_do_not_hold(lib, k):
+    # A thread's next columns are at most 128 threads x 8 vectors x 8 columns on, a
+    # block's tokens at most 4: beyond that an index would turn negative.  (INVALID:
+    # past the check of the sizes, not device memory.)
+    widest = 2 ** 31 - 1 - 8 * 128 * 8
+    ld = 2 ** 31
+    for N, T, code in ((widest, 8, INVALID), (widest + 1, 8, UNSUPPORTED), (2 ** 31 - 1 - 8 * 128 * 4, 8, UNSUPPORTED),
+                       (64, 2 ** 31 - 1, UNSUPPORTED), (64, 2 ** 31 - 1025, INVALID)):
+        assert call(lib, "wst_moe_combine", COMB, N=N, T=T, k=k, ldy=ld, ldo=ld) == code
+        assert call(lib, "wst_moe_combine_backward", CBWD, N=N, T=T, k=k, ldy=ld, ldo=ld, lddy=ld) == code

@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kCombThreads = 128;  // (256: 72 against 65 us for 16384 x 2 x 4096, a longer last wave)
 constexpr int kCombMaxTopK = 32;
+constexpr int kCombMaxVecs = 8;    // vectors of eight columns a thread takes at a time, at most
 
 struct CombineArgs {
   int T, top_k, N, n_rows;
@@ -116,6 +117,7 @@ __device__ __forceinline__ int combine_row(const CombineArgs& a, int t, int i, b
 // vectors of eight columns at a time, KC rows of each in flight.
 template <typename Y, typename O, int KC, int V>
 __global__ void __launch_bounds__(kCombThreads) k_combine(const CombineArgs a, int tpt) {
+  static_assert(V <= kCombMaxVecs, "columns fit 32 bits");
   const int t = blockIdx.x * (kCombThreads / tpt) + (int)threadIdx.x / tpt;
   const int me = (int)threadIdx.x & (tpt - 1);
   if (t >= a.T) return;
@@ -267,7 +269,9 @@ int check_combine(const char* what, int T, int top_k, int N, int y_type, int n_r
     return reject(ST_INVALID_ARG, "%s: sizes out of range (T=%d top_k=%d N=%d n_rows=%d)", what, T, top_k, N, n_rows);
   if (top_k > kCombMaxTopK)
     return reject(ST_UNSUPPORTED, "%s: top_k=%d: this build supports up to %d", what, top_k, kCombMaxTopK);
-  if (N > 0x7fffffff - 8 * kCombThreads * 4) return reject(ST_UNSUPPORTED, "%s: N=%d is too wide", what, N);
+  // (a step past the last column, and a block of tokens past the last one, fit 32 bits)
+  if (N > 0x7fffffff - 8 * kCombThreads * kCombMaxVecs) return reject(ST_UNSUPPORTED, "%s: N=%d is too wide", what, N);
+  if (T > 0x7fffffff - 1024) return reject(ST_UNSUPPORTED, "%s: T=%d: too many tokens", what, T);
   if ((y_type != WST_F32 && y_type != WST_BF16) || (out_type != WST_F32 && out_type != WST_BF16))
     return reject(ST_INVALID_ARG, "%s: unknown type", what);
   return ST_OK;
