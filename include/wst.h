@@ -376,7 +376,8 @@ wst_status wst_permute_rows(int n_rows, size_t row_bytes, const void* src, size_
  * as in torch.topk, and shows in the weights.  Without a bias the experts are
  * ranked by their logits (and groups by their largest, for group_best 1);
  * otherwise as if the scores were computed in 64 bits.
- * Limits: E <= 1024, top_k <= 16, groups <= 32, else WST_ERR_UNSUPPORTED.
+ * Limits: E <= 1024, top_k <= 16, groups <= 32, T < 2^31 - 1024 (also for the
+ * gradient), else WST_ERR_UNSUPPORTED; T * top_k is below 2^31 - 2^20.
  */
 typedef enum { WST_SCORE_SOFTMAX = 0, WST_SCORE_SIGMOID = 1 } wst_score;
 

@@ -208,3 +208,9 @@ def test_combine_rejects_what_32_bits_do_not_hold(lib, k):
                        (64, 2 ** 31 - 1, UNSUPPORTED), (64, 2 ** 31 - 1025, INVALID)):
         assert call(lib, "wst_moe_combine", COMB, N=N, T=T, k=k, ldy=ld, ldo=ld) == code
         assert call(lib, "wst_moe_combine_backward", CBWD, N=N, T=T, k=k, ldy=ld, ldo=ld, lddy=ld) == code
+
+
+def test_route_rejects_more_tokens_than_32_bits_hold(lib):
+    for T, code in ((2 ** 31 - 1, UNSUPPORTED), (2 ** 31 - 1024, UNSUPPORTED), (2 ** 31 - 1025, INVALID)):
+        assert call(lib, "wst_moe_route", ROUTE, T=T) == code                # (too many pairs, below)
+        assert call(lib, "wst_moe_route_backward", BWD, T=T, k=1) == code    # (not device memory, below)

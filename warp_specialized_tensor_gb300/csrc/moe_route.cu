@@ -531,6 +531,8 @@ int check_route_sizes(const char* what, int T, int E, int top_k, long ld, int ty
   if (E > kRouteMaxExperts || top_k > kRouteMaxTopK)
     return reject(ST_UNSUPPORTED, "%s: E=%d, top_k=%d: this build supports E <= %d, top_k <= %d", what, E, top_k,
                   kRouteMaxExperts, kRouteMaxTopK);
+  // (a block of tokens past the last one fits 32 bits)
+  if (T > 0x7fffffff - 1024) return reject(ST_UNSUPPORTED, "%s: T=%d: too many tokens", what, T);
   if (ld < E) return reject(ST_INVALID_ARG, "%s: leading dimension %ld < E", what, ld);
   if (type != WST_F32 && type != WST_BF16) return reject(ST_INVALID_ARG, "%s: unknown type %d", what, type);
   if (score != WST_SCORE_SOFTMAX && score != WST_SCORE_SIGMOID)
