@@ -400,3 +400,14 @@ def test_quantise_dispatch(wst, T, k, K):
     bad = torch.full((T, k), rows + 2, dtype=torch.int32, device="cuda")
     wst.wst_quantize_fp8_dispatch(padded(x), bad, q, s, workspace=ws)
     assert wst.wst_sync_status(ws) == wst.WST_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("K", [64, 256])
+def test_quantise_dispatch_to_no_rows(wst, K):
+    # a batch of which no token has an expert
+    x, ws = torch.randn(5, K, device="cuda"), wst.workspace()
+    q, s = torch.empty(0, K, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(-(-K // 128), 0, device="cuda")
+    wst.wst_quantize_fp8_dispatch(x, torch.full((5, 2), -1, dtype=torch.int32, device="cuda"), q, s, workspace=ws)
+    assert wst.wst_sync_status(ws) == 0
+    wst.wst_quantize_fp8_dispatch(x, torch.zeros(5, 2, dtype=torch.int32, device="cuda"), q, s, workspace=ws)
+    assert wst.wst_sync_status(ws) == wst.WST_ERR_INVALID_ARG        # a row that is not there

@@ -214,3 +214,9 @@ def test_route_rejects_more_tokens_than_32_bits_hold(lib):
     for T, code in ((2 ** 31 - 1, UNSUPPORTED), (2 ** 31 - 1024, UNSUPPORTED), (2 ** 31 - 1025, INVALID)):
         assert call(lib, "wst_moe_route", ROUTE, T=T) == code                # (too many pairs, below)
         assert call(lib, "wst_moe_route_backward", BWD, T=T, k=1) == code    # (not device memory, below)
+
+
+def test_dispatch_to_no_rows_needs_no_arrays(lib):
+    assert call(lib, "wst_quantize_fp8_dispatch", DISP, rows=128, q=None) == INVALID and b"NULL" in lib.wst_last_error()
+    assert call(lib, "wst_quantize_fp8_dispatch", DISP, rows=0, q=None, s=None) == INVALID
+    assert b"NULL" not in lib.wst_last_error()                       # (x is not device memory here)

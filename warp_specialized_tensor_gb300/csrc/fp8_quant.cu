@@ -334,13 +334,13 @@ int run_quant(int mode, const QuantArgs& a, int batch, int x_type, int q_type, b
 }
 
 int check_quant(const char* what, int M, int K, const void* x, long ldx, int x_type, const void* q, long ldq, long q_cols,
-                int q_type, const void* scales) {
+                int q_type, const void* scales, bool stores = true) {
   if (M > 0x7fffffff - 1024 || K > 0x7fffffff - 1024)
     return reject(ST_UNSUPPORTED, "%s: M=%d K=%d: too large", what, M, K);
   if (M < 0 || K < 1) return reject(ST_INVALID_ARG, "%s: sizes out of range (M=%d K=%d)", what, M, K);
   if (x_type != WST_F32 && x_type != WST_BF16) return reject(ST_INVALID_ARG, "%s: unknown type %d", what, x_type);
   if (q_type != WST_E4M3 && q_type != WST_E5M2) return reject(ST_INVALID_ARG, "%s: unknown 8-bit type %d", what, q_type);
-  if (M && (!x || !q || !scales)) return reject(ST_INVALID_ARG, "%s: NULL array", what);
+  if (M && (!x || (stores && (!q || !scales)))) return reject(ST_INVALID_ARG, "%s: NULL array", what);
   if (ldx < K || ldq < q_cols)
     return reject(ST_INVALID_ARG, "%s: leading dimensions too small (ldx=%ld ldq=%ld)", what, ldx, ldq);
   const long es = x_type == WST_F32 ? 4 : 2;
@@ -407,7 +407,8 @@ wst_status wst_quantize_fp8_dispatch(int M, int K, int copies, const void* x, lo
                                      const int* position, int n_rows, void* q, long ldq, wst_fp8 q_type, float* scales,
                                      long lds, int pow2, void* workspace, void* stream) {
   set_error("%s", "");
-  WST_TRY(check_quant("quantize dispatch", M, K, x, ldx, x_type, q, ldq, K, q_type, scales));
+  // (without a row nothing is stored, and q and the scales may be NULL)
+  WST_TRY(check_quant("quantize dispatch", M, K, x, ldx, x_type, q, ldq, K, q_type, scales, n_rows > 0));
   if (copies < 1 || n_rows < 0 || (M && !position) || !workspace)
     return (wst_status)reject(ST_INVALID_ARG, "quantize dispatch: copies=%d n_rows=%d, or a NULL array", copies, n_rows);
   if (lds < n_rows)
@@ -417,8 +418,10 @@ wst_status wst_quantize_fp8_dispatch(int M, int K, int copies, const void* x, lo
   if (M == 0) return WST_OK;
   WST_TRY(check_operand(x, "x"));
   WST_TRY(check_operand(position, "position"));
-  WST_TRY(check_operand(q, "q"));
-  WST_TRY(check_operand(scales, "scales"));
+  if (n_rows > 0) {
+    WST_TRY(check_operand(q, "q"));
+    WST_TRY(check_operand(scales, "scales"));
+  }
   WST_TRY(check_operand(workspace, "workspace"));
   QuantArgs a{};
   a.M = M;
