@@ -411,3 +411,15 @@ def test_quantise_dispatch_to_no_rows(wst, K):
     assert wst.wst_sync_status(ws) == 0
     wst.wst_quantize_fp8_dispatch(x, torch.zeros(5, 2, dtype=torch.int32, device="cuda"), q, s, workspace=ws)
     assert wst.wst_sync_status(ws) == wst.WST_ERR_INVALID_ARG        # a row that is not there
+
+
+def test_combine_backward_to_no_rows(wst):
+    # a batch of which no token has an expert
+    ws, dout, dy = wst.workspace(), torch.randn(5, 32, device="cuda"), torch.empty(0, 32, device="cuda")
+    none = torch.full((5, 2), -1, dtype=torch.int32, device="cuda")
+    wst.wst_moe_combine_backward(dout, none, dy=dy, workspace=ws)
+    dw = torch.full((5, 2), 3.0, device="cuda")
+    wst.wst_moe_combine_backward(dout, none, y=torch.empty(0, 32, device="cuda"), dy=dy, dweights=dw, workspace=ws)
+    assert wst.wst_sync_status(ws) == 0 and (dw == 0).all()
+    wst.wst_moe_combine_backward(dout, torch.zeros_like(none), dy=dy, workspace=ws)
+    assert wst.wst_sync_status(ws) == wst.WST_ERR_INVALID_ARG        # a row that is not there

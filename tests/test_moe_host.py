@@ -220,3 +220,9 @@ def test_dispatch_to_no_rows_needs_no_arrays(lib):
     assert call(lib, "wst_quantize_fp8_dispatch", DISP, rows=128, q=None) == INVALID and b"NULL" in lib.wst_last_error()
     assert call(lib, "wst_quantize_fp8_dispatch", DISP, rows=0, q=None, s=None) == INVALID
     assert b"NULL" not in lib.wst_last_error()                       # (x is not device memory here)
+
+
+def test_combine_backward_to_no_rows(lib):
+    for rows, said in ((32, True), (0, False)):
+        assert call(lib, "wst_moe_combine_backward", CBWD, rows=rows, dy=None, dw=None, y=None) == INVALID
+        assert (b"neither" in lib.wst_last_error()) == said          # (else: not device memory here)

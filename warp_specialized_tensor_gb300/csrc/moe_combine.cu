@@ -348,7 +348,8 @@ wst_status wst_moe_combine_backward(int T, int top_k, int N, const void* dout, l
   set_error("%s", "");
   WST_TRY(check_combine("combine backward", T, top_k, N, y_type, n_rows, out_type));
   if ((T && (!dout || !position)) || !workspace) return (wst_status)reject(ST_INVALID_ARG, "combine backward: NULL array");
-  if (!dy && !dweights)
+  // (a dy without a row may be NULL: only the positions are looked at)
+  if (!dy && !dweights && n_rows)
     return (wst_status)reject(ST_INVALID_ARG, "combine backward: neither dy nor dweights is asked for");
   if (T && dweights && n_rows && !y) return (wst_status)reject(ST_INVALID_ARG, "combine backward: dweights needs y");
   WST_TRY(check_rows("combine backward", "dout", dout, ldo, out_type, N));
