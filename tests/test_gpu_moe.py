@@ -423,3 +423,15 @@ def test_combine_backward_to_no_rows(wst):
     assert wst.wst_sync_status(ws) == 0 and (dw == 0).all()
     wst.wst_moe_combine_backward(dout, torch.zeros_like(none), dy=dy, workspace=ws)
     assert wst.wst_sync_status(ws) == wst.WST_ERR_INVALID_ARG        # a row that is not there
+
+
+@pytest.mark.parametrize("lead", [(), (2,)])
+@pytest.mark.parametrize("mode", ["rows", "cols", "blocks", "blocks_t"])
+def test_quantise_no_rows(wst, mode, lead):
+    q = {"rows": (0, 256), "cols": (256, 0), "blocks": (0, 256), "blocks_t": (256, 0)}[mode]
+    s = {"rows": (2, 0), "cols": (0, 256), "blocks": (0, 2), "blocks_t": (2, 0)}[mode]
+    wst.wst_quantize_fp8(torch.empty(*lead, 0, 256, device="cuda"), torch.empty(*lead, *q, dtype=torch.float8_e4m3fn, device="cuda"),
+                         torch.empty(*lead, *s, device="cuda"), mode=mode)
+    with pytest.raises(wst.WstError):
+        wst.wst_quantize_fp8(torch.empty(4, 0, device="cuda"), torch.empty(4, 0, dtype=torch.float8_e4m3fn, device="cuda"),
+                             torch.empty(0, 4, device="cuda"))       # blocks of no column

@@ -278,7 +278,7 @@ def wst_quantize_fp8(x, q, scales, mode="rows", pow2=False, stream=None) -> None
     if tuple(q.shape) != lead + want_q or tuple(scales.shape) != lead + want_s:
         raise ValueError("mode %r: q must be %s and scales %s" % (mode, lead + want_q, lead + want_s))
     batch = lead[0] if lead else 1
-    if batch == 0:
+    if batch == 0 or (M == 0 and K > 0):  # (strides of an empty tensor mean nothing)
         return
     s = (lambda t: t.stride(0) if t.dim() == 3 else 0)
     st = _lib().wst_quantize_fp8(
