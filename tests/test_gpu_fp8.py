@@ -377,3 +377,17 @@ def test_split_exact_and_in_graphs(wst, big_ws):
         graph.replay()
         assert torch.equal(args[4].cpu(), want)
     assert wst.wst_sync_status(big_ws) == 0
+
+
+@pytest.mark.parametrize("N,K", [(1, 100), (3, 200)])
+def test_one_group_whatever_its_stride(wst, big_ws, N, K):
+    qa, sa = operand(9, K, "rows", E4, 80)
+    qb, sb = operand(N, K, "blocks", E4, 81, (1,))
+    store = torch.zeros(N * 208 + 100, dtype=torch.uint8, device="cuda").view(E4)
+    B = store.as_strided((1, N, K), (100, 208, 1))           # a group stride of no multiple of 16 bytes
+    B.copy_(qb)
+    C = torch.full((9, 4), float("nan"), device="cuda")
+    off = torch.tensor([0, 9], dtype=torch.int32, device="cuda")
+    wst.wst_grouped_gemm_fp8(rows16(qa), sa.cuda(), B, sb.cuda(), off, C[:, :N], workspace=big_ws)
+    want, size = product(qa, sa, qb[0], sb[0], "blocks")
+    assert (abs(ref.f64(C[:, :N]) - want) <= bound(want, size, K, torch.float32)).all()

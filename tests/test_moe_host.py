@@ -226,3 +226,9 @@ def test_combine_backward_to_no_rows(lib):
     for rows, said in ((32, True), (0, False)):
         assert call(lib, "wst_moe_combine_backward", CBWD, rows=rows, dy=None, dw=None, y=None) == INVALID
         assert (b"neither" in lib.wst_last_error()) == said          # (else: not device memory here)
+
+
+def test_one_group_has_no_stride(lib):
+    # (what is left to refuse is that nothing here is device memory)
+    for G, code in ((4, ALIGN), (1, INVALID)):
+        assert call(lib, "wst_grouped_gemm_fp8", GROUP8, G=G, stB=100) == code

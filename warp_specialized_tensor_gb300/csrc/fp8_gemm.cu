@@ -112,7 +112,7 @@ int fp8_product(const char* what, bool grouped, int G, int M, int N, int K, cons
   if (lda < K || ldb < K || ldc < N || ldsa < M || ldsb < sb_cols)
     return reject(ST_INVALID_ARG, "%s: leading dimensions too small (lda=%ld ldb=%ld ldc=%ld ldsa=%ld ldsb=%ld)", what, lda,
                   ldb, ldc, ldsa, ldsb);
-  if (grouped && (strideB < 0 || strideBias < 0 || strideSB < 0))
+  if (G > 1 && (strideB < 0 || strideBias < 0 || strideSB < 0))  // (one group has no stride)
     return reject(ST_INVALID_ARG, "%s: negative group stride", what);
   if (M == 0) return ST_OK;  // no rows: nothing to compute or store
   if (!A || !B || !C || !scaleA || !scaleB || (grouped && !offsets) || (epi && !bias))
@@ -121,7 +121,7 @@ int fp8_product(const char* what, bool grouped, int G, int M, int N, int K, cons
   if (!aligned_to(A, 16) || !aligned_to(B, 16) || !aligned_to(C, 16) || (epi && !aligned_to(bias, 2)) ||
       !aligned_to(workspace, 16) || !aligned_to(scaleA, 4) || !aligned_to(scaleB, 4) || !aligned_to(offsets, 4))
     return reject(ST_ALIGNMENT, "%s: A, B, C and the workspace must be 16-byte aligned, scales and offsets 4-byte", what);
-  if (lda % 16 || ldb % 16 || ldc * es % 16 || (grouped && strideB % 16))
+  if (lda % 16 || ldb % 16 || ldc * es % 16 || (G > 1 && strideB % 16))
     return reject(ST_ALIGNMENT, "%s: leading dimensions and strides must be multiples of 16 bytes", what);
   int st;
   if ((st = check_operand(A, "A")) || (st = check_operand(B, "B")) || (st = check_operand(C, "C")) ||
