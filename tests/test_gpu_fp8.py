@@ -391,3 +391,45 @@ def test_one_group_whatever_its_stride(wst, big_ws, N, K):
     wst.wst_grouped_gemm_fp8(rows16(qa), sa.cuda(), B, sb.cuda(), off, C[:, :N], workspace=big_ws)
     want, size = product(qa, sa, qb[0], sb[0], "blocks")
     assert (abs(ref.f64(C[:, :N]) - want) <= bound(want, size, K, torch.float32)).all()
+
+
+@pytest.mark.parametrize("scaling", ["blocks", "rows"])
+def test_groups_that_share_their_weights(wst, big_ws, scaling):
+    # group strides of 0, and scales in rows of a larger array
+    sizes, N, K = [20, 0, 300, 5], 200, 520
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    M, G = int(off[-1]), len(sizes)
+    qa, sa = operand(M, K, "rows", E4, 82)
+    qb, sb = operand(N, K, scaling, E4, 83)
+    bias = torch.randn(N, generator=torch.Generator().manual_seed(4)).bfloat16()
+    wide = [torch.full((t.shape[0], t.shape[1] + 5), float("nan"), device="cuda") for t in (sa, sb)]
+    ka, kb = wide[0][:, :M], wide[1][:, :sb.shape[1]]
+    ka.copy_(sa), kb.copy_(sb)
+    C = torch.full((M, N), float("nan"), device="cuda")
+    wst.wst_grouped_gemm_fp8(rows16(qa), ka, rows16(qb).expand(G, N, K), kb.expand(G, *kb.shape), torch.from_numpy(off).int().cuda(), C,
+                             scaling=scaling, bias=bias.cuda().expand(G, N), epi="bias", workspace=big_ws)
+    assert wst.wst_sync_status(big_ws) == 0
+    want, size = product(qa, sa, qb, sb, scaling)
+    err = bound(want, size, K, torch.float32)
+    want = want + ref.f64(bias)
+    assert (abs(ref.f64(C) - want) <= err + 2 * ref.U * (abs(want) + err)).all()
+
+
+def test_grouped_rows_behind_32_bits(wst, big_ws):
+    # the last group's rows lie more than 2^31 elements into A and C
+    sizes, N, K = [529900, 100], 4100, 4096
+    M = sum(sizes)
+    qa, sa = operand(100, K, "rows", E4, 84)
+    qb, sb = operand(N, K, "blocks", E4, 85)
+    A = torch.zeros(M, K, dtype=torch.uint8, device="cuda")
+    A[-100:] = qa.view(torch.uint8).cuda()
+    scale = torch.ones(32, M, device="cuda")
+    scale[:, -100:] = sa.cuda()
+    buf = torch.full((M, 4104), float("nan"), dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, sizes[0], M], dtype=torch.int32, device="cuda")
+    wst.wst_grouped_gemm_fp8(A.view(E4), scale, rows16(qb).expand(2, N, K), sb.cuda().expand(2, *sb.shape), off, buf[:, :N],
+                             workspace=big_ws)
+    assert wst.wst_sync_status(big_ws) == 0
+    want, size = product(qa, sa, qb, sb, "blocks")
+    assert (abs(ref.f64(buf[-100:, :N]) - want) <= bound(want, size, K, torch.bfloat16)).all()
+    assert (buf[:-100, :N] == 0).all() and torch.isnan(buf[:, N:].float()).all()

@@ -435,3 +435,43 @@ def test_quantise_no_rows(wst, mode, lead):
     with pytest.raises(wst.WstError):
         wst.wst_quantize_fp8(torch.empty(4, 0, device="cuda"), torch.empty(4, 0, dtype=torch.float8_e4m3fn, device="cuda"),
                              torch.empty(0, 4, device="cuda"))       # blocks of no column
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_backward_into_the_logits(wst, score, renorm, dtype):
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(300, 40, generator=g).to(dtype).cuda()
+    e = torch.stack([torch.randperm(40, generator=g)[:4] for _ in range(300)]).int().cuda()
+    dw, want = torch.randn(300, 4, generator=g).cuda(), torch.empty(300, 40, dtype=dtype, device="cuda")
+    wst.wst_moe_route_backward(x, e, dw, want, score=score, renorm=renorm)
+    wst.wst_moe_route_backward(x, e, dw, x, score=score, renorm=renorm)
+    assert torch.equal(x, want)
+
+
+def test_rows_behind_32_bits(wst):
+    # y, dy and the rows of a dispatch whose last elements lie more than 2^31 elements in
+    rows, N, T = 530000, 4096, 3
+    ws = wst.workspace()
+    y = torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda")
+    y[-2:] = torch.randn(2, N, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    pos = torch.tensor([[rows - 1, 5], [-1, rows - 2], [7, 9]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[0.5, 1.0], [1.0, 2.0], [1.0, 1.0]], device="cuda")
+    out = torch.empty(T, N, device="cuda")
+    wst.wst_moe_combine(y, pos, out, weights=w, workspace=ws)
+    assert torch.equal(out, torch.stack([0.5 * y[-1].float(), 2 * y[-2].float(), torch.zeros(N, device="cuda")]))
+    dout, dw = torch.randn(T, N, generator=torch.Generator().manual_seed(3)).bfloat16().cuda(), torch.empty(T, 2, device="cuda")
+    want = (dout[0].double() * y[-1].double()).sum()
+    dy = torch.zeros(rows, N, dtype=torch.bfloat16, device="cuda")
+    wst.wst_moe_combine_backward(dout, pos, y=y, weights=w, dy=dy, dweights=dw, workspace=ws)
+    # at most 8 ceil(N / 256) products a thread, then 5 + 8 sums
+    assert abs(float(dw[0, 0]) - float(want)) <= (8 * 16 + 14) * ref.U * float((dout[0].double() * y[-1].double()).abs().sum())
+    assert torch.equal(dy[-1], (0.5 * dout[0].float()).bfloat16()) and torch.equal(dy[-2], (2 * dout[1].float()).bfloat16())
+    assert torch.equal(dy[9], dout[2]) and (dy[10:1000] == 0).all()
+    del y, dy
+    q, s = torch.zeros(rows, N, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn), torch.zeros(32, rows, device="cuda")
+    wst.wst_quantize_fp8_dispatch(dout, pos, q, s, workspace=ws)
+    want_q, want_s = ref.quantise(dout.cpu(), "rows", torch.float8_e4m3fn)
+    assert np.array_equal(ref.f64(q[-2:]), ref.f64(want_q)[[1, 0]]) and np.array_equal(s[:, -2:].cpu().numpy(), want_s[:, [1, 0]])
+    assert wst.wst_sync_status(ws) == 0

@@ -124,3 +124,24 @@ def test_bf16_accumulation_rounds_once(wst, N, K):
         err = 2 * ref.U * np.array(sizes)[:, None, None] * size
         err = err + ref.U * (abs(want + b) + err)
         assert (abs(ref.f64(out) - (want + b)) <= err + ref.half(torch.bfloat16) * (abs(want + b) + err)).all()
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_and_gradients_behind_32_bits(wst, dtype, accumulate):
+    # the last group's rows lie more than 2^31 elements into A, and so does its gradient
+    G, N, K = 130, 4096, 4104
+    M = 530000
+    off = torch.tensor([0] * (G - 1) + [M - 40, M], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(8)
+    dC, A = torch.zeros(M, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    d, a = torch.randn(40, 64, generator=g).bfloat16(), torch.randn(40, K, generator=g).bfloat16()
+    dC[-40:], A[-40:] = d.cuda(), a.cuda()
+    dB = torch.full((G, N, K), 1.0, dtype=dtype, device="cuda")[:, :64]     # (64 of every 4096 rows)
+    ws = wst.workspace()
+    wst.wst_grouped_gemm_wgrad_bf16(dC, A, off, dB, accumulate=accumulate, workspace=ws)
+    assert wst.wst_sync_status(ws) == 0
+    want, size = ref.f64(d).T @ ref.f64(a) + accumulate, abs(ref.f64(d)).T @ abs(ref.f64(a)) + accumulate
+    err = 2 * ref.U * 41 * size
+    assert (abs(ref.f64(dB[-1]) - want) <= err + ref.half(dtype) * (abs(want) + err)).all()
+    assert (dB[:-1] == (1 if accumulate else 0)).all()
