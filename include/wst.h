@@ -460,7 +460,9 @@ wst_status wst_moe_combine_backward(int T, int top_k, int N, const void* dout, l
  *   WST_FP8_BLOCKS_T  the same blocks transposed: q [K][M], scales
  *                     [ceil(K/128)][ceil(M/128)]
  * A last block is what is left of its row or column.  x and q are 16-byte
- * aligned with leading dimensions and batch strides of whole 16 bytes.
+ * aligned with leading dimensions and batch strides of whole 16 bytes.  M <=
+ * 65535 * 128 in every mode (the modes with 128-row blocks use a grid dimension
+ * per block; longer inputs go in parts), else WST_ERR_UNSUPPORTED.
  */
 typedef enum {
   WST_FP8_ROWS = 0,
@@ -497,9 +499,10 @@ wst_status wst_quantize_fp8_dispatch(int M, int K, int copies, const void* x, lo
  *   bias    bf16 [N], NULL unless epi > 0
  *   C       c_type [M][N], leading dimension ldc; M may be 0
  * The products of a block accumulate in the tensor core; the blocks are scaled
- * and added in fp32.  A training step's other products are the same call:
- * dA = dC . B with B quantised as WST_FP8_BLOCKS_T, dB = dC^T . A with both
- * quantised as WST_FP8_COLS (b_scaling WST_FP8_ROWS).
+ * (by sA sB, itself an fp32 product that has to be finite) and added in fp32.
+ * A training step's other products are the same call: dA = dC . B with B
+ * quantised as WST_FP8_BLOCKS_T, dB = dC^T . A with both quantised as
+ * WST_FP8_COLS (b_scaling WST_FP8_ROWS).
  * a_type and b_type may differ.  A, B, C are 16-byte aligned with leading
  * dimensions of whole 16 bytes.
  * workspace: at least the 256-byte header, zero-filled once.  With

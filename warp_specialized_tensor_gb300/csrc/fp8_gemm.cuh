@@ -22,13 +22,14 @@
 // the scales alone took 32 16-byte shared loads per warp and K block, 1024 cycles
 // of an SM's load path.)
 //
-// What bounds it: without the scaled sums the copies and products of 8192^3 take
-// 307 us (3586 TFLOP/s); with them 527 us (2085), about 1050 cycles per K block of
-// a 256 x 256 tile, which is the epilogue's chain of a barrier wait (about 200
-// cycles while products run, even on a phase long complete), four rounds of
-// tensor-memory loads and packed multiply-adds, and the hand-back, at two warps
-// per sub-core.  Measured and dropped: testing the next barriers ahead of their
-// use (617 us: a test holds the warp up as long as a wait); the weights' scale
+// What bounds it: 8192^3 takes 546-563 us (2.0 PFLOP/s) call after call, under the
+// power cap, and 388 us (2.8 PFLOP/s) without the scaled sums.  A K block of a
+// 256 x 256 tile costs about 1050 cycles: the epilogue's chain of a barrier wait
+// (about 200 cycles while products run, even on a phase long complete), four
+// rounds of tensor-memory loads and packed multiply-adds, and the hand-back, at
+// two warps per sub-core.  Measured and dropped (each against 527-531 us for this
+// form, in runs of a few passes): testing the next barriers ahead of their use
+// (617 us: a test holds the warp up as long as a wait); the weights' scale
 // multiplied in by the epilogue (+50 us); two accumulators of 128 columns per K
 // block (749 us), tiles of 128 tokens with four accumulators (820 us), sixteen
 // epilogue warps with 96 registers each (840 us, sums spilled).
@@ -685,9 +686,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         while (step(I0()) && --left > 0 && step(I1()) && --left > 0) {}
       } else {
         // At most 32 columns (tiles of up to 64 tokens, whose products wait for
-        // the weights from HBM): one round of loads.  16 x 4096 x 8192 takes 17 us
+        // the weights from HBM): one round of loads.  16 x 4096 x 8192 takes 18 us
         // with it and 20 us in the loop above; its mere presence costs large
-        // products 3 % (8192^3 543 against 527 us), so they run a kernel without.
+        // products 2 % (8192^3 559 against 547 us), so they run a kernel without.
 #pragma unroll 1
         for (int acc = 0; left > 0; --left, acc ^= 1) {
           if (kk == 0) {
