@@ -196,7 +196,7 @@ def prepare(case, seed):
         s["a"] = _padded(torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16))
         # two 4-bit numbers a byte, rows that begin on 16 bytes
         s["w"] = torch.randint(0, 256, (*lead, N, _up(-(-K // 2), 16)), generator=g, device="cuda", dtype=torch.uint8)[..., :-(-K // 2)]
-        s["scales"] = ((torch.rand(*lead, -(-K // group), N, generator=g, device="cuda") + 0.5) * 0.02).to(torch.bfloat16)
+        s["scales"] = _padded(((torch.rand(*lead, -(-K // group), N, generator=g, device="cuda") + 0.5) * 0.02).to(torch.bfloat16))
         s["bias"] = torch.randn(N, generator=g, device="cuda").to(torch.bfloat16) if case.get("epi", "none") != "none" else None
         per = 16 // torch.empty(0, dtype=TYPES[case["c"]]).element_size()
         s["c_buffer"] = torch.zeros(M, _up(N, per), dtype=TYPES[case["c"]], device="cuda")[:, :N]
@@ -208,7 +208,7 @@ def prepare(case, seed):
             s["offsets"] = torch.tensor(s["starts"], dtype=torch.int32, device="cuda")
     if own:
         import warp_specialized_tensor_gb300 as wst
-        s["ws"] = wst.tree_attention_workspace() if case["op"] == "attend" else wst.workspace()
+        s["ws"] = {"append": wst.workspace, "attend": wst.tree_attention_workspace}.get(case["op"], wst.gemm_w4_workspace)()
     return s
 
 
