@@ -5,7 +5,7 @@
  * The first three operations, each one hand-written CUDA kernel behind one call
  * (the declarations below hold the others: norm-fused GEMMs, IKBO attention,
  * expert parallelism, mixture-of-experts routing and its gradients, 8-bit
- * products with block scales):
+ * products with block scales, the operators of a decoding step):
  *
  *   wst_gemm_bf16            dense (optionally strided-batched) GEMM with an
  *                            optional fused bias / bias+SiLU epilogue.
@@ -646,6 +646,86 @@ wst_status wst_ikbo_attention_bf16(int num_users, int num_cand, int Lq, int H, i
 /* Workspace bytes for wst_ikbo_attention_bf16's split schedule (header,
  * per-CTA flags and one partial O/m/l slot per CTA, for up to 256 CTAs). */
 size_t wst_ikbo_attention_workspace_size(void);
+
+/*
+ * One step of decoding: new keys and values into a paged cache, attention of a
+ * step's tokens over it, products of few rows with 4-bit weights.
+ *
+ * A paged cache holds the keys (and, in an array of its own with the same
+ * strides, the values) of all sequences, bf16, in num_pages pages of page_size
+ * tokens:
+ *   element (page, token, head, d) at base + page*page_stride + token*token_stride
+ *                                     + head*head_stride + d
+ * so [page][token][head][d] and [page][head][token][d] are both possible, and
+ * keys and values may share pages.  Pointers are 16-byte aligned, strides (in
+ * elements) multiples of 16 bytes.  Slot s is token s % page_size of page
+ * s / page_size.
+ *
+ * wst_cache_append_bf16: for every token t < T with slots[t] >= 0
+ *   q_out[t][h] = R(q[t][h]),  slot of k_cache [h] = R(k[t][h]),
+ *   slot of v_cache [h] = v[t][h]
+ * R turns rot/2 pairs of the first rot components by positions[t]*inv_freq[j]
+ * (radians; evaluated as if exactly, for any 32-bit position), pair j being
+ * components (j, j + rot/2) (WST_ROPE_HALVES) or (2j, 2j + 1) (WST_ROPE_PAIRS):
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * in fp32, rounded once to bf16; the other components are copied.
+ *   q, k, v    x_type, element (t,h,d) at x + t*ldx + h*Dh + d; q may be NULL
+ *              (H and q_out are then not looked at)
+ *   positions  DEVICE int32 [T]; inv_freq DEVICE fp32 [rot/2], finite (both may
+ *              be NULL when rot == 0)
+ *   slots      DEVICE int32 [T]; a token with a negative slot is skipped: its
+ *              q_out is left as it was; one of num_pages*page_size or more is
+ *              skipped and latches WST_ERR_INVALID_ARG; of two tokens with one
+ *              slot either is stored, perhaps in parts
+ *   q_out      bf16, rows ldqo apart; it may be q itself (bf16, ldqo == ldq),
+ *              and must not overlap the other inputs or outputs
+ * Dh and rot are multiples of 16, Dh <= 256, else WST_ERR_UNSUPPORTED.
+ */
+typedef enum { WST_ROPE_HALVES = 0, WST_ROPE_PAIRS = 1 } wst_rope;
+
+wst_status wst_cache_append_bf16(int T, int H, int Hkv, int Dh, int rot, wst_rope style, const void* q, long ldq,
+                                 const void* k, long ldk, const void* v, long ldv, wst_dtype x_type,
+                                 const int* positions, const float* inv_freq, const int* slots, void* q_out,
+                                 long ldqo, void* k_cache, void* v_cache, int num_pages, int page_size,
+                                 long page_stride, long token_stride, long head_stride, void* workspace,
+                                 void* stream);
+
+/*
+ * Product of bf16 rows with 4-bit weights that have one scale for every
+ * `group` consecutive k.  For m < M, n < N:
+ *   C[m][n] = epi( sum_b s[b][n] sum_{k in group b} A[m][k] (w[n][k] - 8) (+ bias[n]) )
+ *   A       bf16 [M][K], leading dimension lda; M may be 0
+ *   W       4-bit numbers w in 0..15, two a byte: w[n][k] is the low (k even) or
+ *           high (k odd) half of byte W + n*ldw + k/2 (ldw in bytes)
+ *   scales  bf16, s[b][n] at scales + b*lds + n, b < ceil(K/group)
+ *   bias    bf16 [N], NULL unless epi > 0
+ *   C       c_type [M][N], leading dimension ldc
+ * group is 32, 64 or 128, else WST_ERR_UNSUPPORTED; K is arbitrary (a last group
+ * is what is left).  The weights are exact in bf16; products accumulate in fp32
+ * inside a group, the groups are scaled and added in fp32.  Pointers are 16-byte
+ * aligned, leading dimensions and strides multiples of 16 bytes.  Meant for the
+ * few rows of a decoding step: every 64 rows read the weights once.
+ * workspace: at least the 256-byte header, zero-filled once.  With
+ * wst_gemm_w4_workspace_size() bytes the K loops are cut so that every SM gets
+ * the same share (the pieces of a tile are added in a fixed order); smaller ones
+ * run whole tiles.
+ */
+wst_status wst_gemm_w4(int M, int N, int K, const void* A, long lda, const void* W, long ldw, const void* scales,
+                       long lds, int group, const void* bias, void* C, long ldc, wst_dtype c_type,
+                       wst_epilogue epi, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same for G groups of rows: rows [d_offsets[g], d_offsets[g+1]) of A and C
+ * with W + g*strideW_group (bytes), scales + g*strideS_group and
+ * bias + g*strideBias (offsets as in wst_grouped_gemm_bf16: rows behind the last
+ * group are left as they were). */
+wst_status wst_grouped_gemm_w4(int G, int M_total, int N, int K, const void* A, long lda, const void* W, long ldw,
+                               long strideW_group, const void* scales, long lds, long strideS_group, int group,
+                               const int* d_offsets, const void* bias, long strideBias, void* C, long ldc,
+                               wst_dtype c_type, wst_epilogue epi, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Workspace bytes with which the 4-bit products cut their K loops. */
+size_t wst_gemm_w4_workspace_size(void);
 
 /* Synchronize `stream`, then return and clear the first device-side error
  * latched in `workspace` (WST_OK if none). */

@@ -117,6 +117,7 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.wst_version.argtypes = []
         lib.wst_version.restype = ctypes.c_char_p
         moe.declare(lib)
+        decode.declare(lib)
         _lib = lib
         return lib
 
@@ -572,3 +573,11 @@ from . import moe  # noqa: E402  (uses the definitions above)
 from .moe import *  # noqa: E402,F401,F403
 
 __all__ += moe.__all__
+
+# ----------------------------------------------------------------------------
+# a decoding step: paged cache, attention over it, 4-bit weights
+# ----------------------------------------------------------------------------
+from . import decode  # noqa: E402
+from .decode import *  # noqa: E402,F401,F403
+
+__all__ += decode.__all__

@@ -123,6 +123,10 @@ struct AttnProblem {
   size_t ws_bytes;
 };
 
+// The arrays of a paged cache (include/wst.h, "One step of decoding"): Status.
+int check_cache(const char* what, const void* k_cache, const void* v_cache, int num_pages, int page_size, long page_stride,
+                long token_stride, long head_stride);
+
 int run_gemm(const GemmProblem& p, cudaStream_t stream);
 // s[b][n] = sum_k B[b][n][k] in fp32 for b < nb (LayerNorm fusion).
 // Passes over rows of bf16 data ahead of the norm GEMMs, one launch: the
