@@ -691,6 +691,52 @@ wst_status wst_cache_append_bf16(int T, int H, int Hkv, int Dh, int rot, wst_rop
                                  void* stream);
 
 /*
+ * Attention of a step's tokens over a paged cache that holds them already.
+ * Sequence b < B has the tokens [off[b], off[b+1]) of Q (n_b of them) behind
+ * context[b] cached ones; its key j is token j % page_size of page
+ * page_table[b][j / page_size], its i-th token being key context[b] + i.
+ * For token t = off[b] + i, head h and key head h / (H / Hkv):
+ *   O[t][h][:] = sum_j p_j V[j][:],  p = softmax of scale * Q[t][h][:] . K[j][:]
+ * over the keys j that token t sees: all of the context, and of the new tokens
+ * those whose bit is set in its mask (new token d: bit d % 32 of mask[t][d / 32]),
+ * or with mask NULL those up to itself (a chain; one token sees everything).  A
+ * token that sees no key gets zeros.  Keys that a token does not see take no part,
+ * whatever they hold (NaN or infinities in them or in the rest of a page included).
+ *   Q       bf16, element (t,h,d) at Q + t*ldq + h*Dh + d
+ *   d_q_offsets  DEVICE int32 [B+1], from 0, non-decreasing, at most T: rows behind
+ *           the last sequence are left as they were; d_context DEVICE int32 [B]
+ *   mask    DEVICE int32 [T][mask_words], rows ldm apart, or NULL
+ *   k_cache, v_cache  as wst_cache_append_bf16 leaves them
+ *   page_table  DEVICE int32 [B][max_pages], rows ldt apart; only the entries of a
+ *           sequence's keys are read
+ *   scale   finite, of at most 2e38
+ *   O       o_type, element (t,h,d) at O + t*ldo + h*Dh + d; it must not overlap the
+ *           inputs
+ * The probabilities are rounded to bf16 before the product with V; row maxima, sums
+ * and the output accumulate in fp32.  After a tree is verified, wst_permute_rows
+ * moves the accepted tokens' rows of the cache together.
+ * Supported: Dh 64 and 128, H / Hkv <= 128, page_size 8, 16, 32, 64 or a multiple of
+ * 128, max_pages * page_size <= 2^30, T <= 2^30 (else WST_ERR_UNSUPPORTED).
+ * Offsets, lengths or masks that break the rules (also context[b] + n_b above
+ * max_pages * page_size, or n_b above 32 * mask_words) are clamped and latch
+ * WST_ERR_BAD_OFFSETS; a page outside the cache reads as zeros and latches
+ * WST_ERR_INVALID_ARG.
+ * workspace: at least the 256-byte header, zero-filled once.  With
+ * wst_tree_attention_workspace_size() bytes sequences are cut so that every SM gets
+ * the same share of all keys (the pieces are added in a fixed order, by a second
+ * kernel); smaller ones give whole (sequence, key head, 128 query rows) to an SM.
+ */
+wst_status wst_tree_attention_bf16(int B, int T, int H, int Hkv, int Dh, const void* Q, long ldq,
+                                   const int* d_q_offsets, const int* d_context, const int* mask, int mask_words,
+                                   long ldm, const void* k_cache, const void* v_cache, int num_pages, int page_size,
+                                   long page_stride, long token_stride, long head_stride, const int* page_table,
+                                   int max_pages, long ldt, float scale, void* O, long ldo, wst_dtype o_type,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes with which wst_tree_attention_bf16 cuts sequences. */
+size_t wst_tree_attention_workspace_size(void);
+
+/*
  * Product of bf16 rows with 4-bit weights that have one scale for every
  * `group` consecutive k.  For m < M, n < N:
  *   C[m][n] = epi( sum_b s[b][n] sum_{k in group b} A[m][k] (w[n][k] - 8) (+ bias[n]) )

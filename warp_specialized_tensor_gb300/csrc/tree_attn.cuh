@@ -1,0 +1,857 @@
+// tree_attn.cuh -- attention of a step's tokens (a drafted tree, a chain, one token
+// for each sequence) over a paged cache, for sm_103a.
+//
+//   O[i][h] = sum_j p_ij V[j][h / group],  p = softmax over the j that i sees of
+//             scale * Q[i][h] . K[j][h / group]
+// Sequence b has context[b] cached tokens, which all of its n_b new tokens see, and
+// the new tokens themselves, of which a token sees those in its mask (or those up
+// to itself).  All of them lie in the cache, through the sequence's page table.
+//
+// The query rows of a sequence that share a key head (its tokens x the `group` heads
+// of that key head) are stacked into tiles of 128 rows, so K and V are read once per
+// tile: for a step of few tokens that read is the whole cost, and the 128-row products
+// hide under it even where most rows are empty (S and PV of 128 keys take 1,000
+// clocks of the tensor core, their 64 KB 2,800 clocks of an SM's share of HBM).
+//
+// Schedule: an item is (sequence, key head, tile), a block 128 keys.  The items'
+// blocks stand in one line, each CTA takes an equal share (work_split.cuh); the
+// lengths are on the device, so every CTA counts them at its start.  A piece of a cut
+// item leaves its un-normalised O, row maxima m and sums l in the workspace, and a
+// second kernel adds an item's pieces in ascending order of keys:
+//   m* = max m_i,  l* = sum l_i 2^(m_i - m*),  O = sum O_i 2^(m_i - m*) / l*
+// (its launch overlaps the first kernel's end; it is spread over all SMs, where the
+// last CTA of an item alone would read up to 152 pieces of 64 KB).
+//
+// Inside a CTA, per block (online softmax in base 2, cs = scale * log2 e):
+//   MMA      S = Q . K^T        Q and K from shared memory, 128 x 128 x Dh
+//   softmax  P = 2^(cs S - m) as bf16 over S's tensor memory; m moves only when the
+//            maximum has grown by more than 2^8, which rescales O and l
+//            (P <= 2^8, rounded to bf16: by at most 2^-8 of it; l sums the unrounded P)
+//   MMA      O += P . V         P from tensor memory, V from shared memory
+// Three S/P buffers, so S runs ahead of PV; two threads issue the products (a wait
+// costs ~160 clocks while products are in flight, and this way one's products run
+// under the other's wait).
+//
+// A block that ends behind the context (a sequence's last one or two) takes another
+// path: each row's visible keys come as 128 bits, scores outside them do not count
+// whatever they hold, and the rows of V outside the sequence are cleared in shared
+// memory, since 0 * NaN in the product would reach every row.  For the same reason a
+// new token's V that is not finite is cleared too and added again, at the end, to the
+// rows that see it.
+//
+// Roles (256 threads): warp 0 loads Q and K, warp 3 V (a lane per page of a block);
+// warp 1 issues S, warp 2 PV (and owns the tensor memory); warps 4-7 softmax and
+// output, thread = row = tensor memory lane.
+#pragma once
+
+#include "work_split.cuh"
+#include "wst_common.cuh"
+
+namespace wst {
+
+constexpr int kTreeBM = 128;
+constexpr int kTreeBN = 128;
+constexpr int kTreeThreads = 256;
+constexpr int kTreeSBufs = 3;
+constexpr int kTreeMaxCtas = 160;
+constexpr float kTreeGrow = 8.0f;       // log2 of how far P may exceed 1
+constexpr float kTreeGrowSum = 256.0f;  // 2^kTreeGrow
+
+template <int DH>
+struct TreeCfg {
+  static constexpr int kHalves = DH / 64;
+  static constexpr int kTile = kTreeBN * DH * 2;  // bytes of a Q tile or a block of K or V
+  static constexpr int kKStages = DH == 128 ? 3 : 6;
+  static constexpr int kVStages = DH == 128 ? 2 : 5;
+  static constexpr int kBars = 4 + 2 * kKStages + 2 * kVStages + 3 * kTreeSBufs + 1;
+  static constexpr size_t kSmem = 1024 + (size_t)(2 + kKStages + kVStages) * kTile + 1024;
+  static constexpr int kTmemO = kTreeSBufs * kTreeBN;
+  static_assert(kSmem <= 232448 && kTmemO + DH <= 512 && DH % 64 == 0, "shared memory, tensor memory");
+};
+
+// What the second kernel needs of a cut item; pieces 0: none.
+struct TreeCut {
+  int pieces;   // on CTAs c, c + 1, ...
+  int token0;   // the first row's token
+  int head0;    // the first row's head
+  int rows;
+};
+
+// Workspace after the header: TreeCut[kTreeMaxCtas], then two slots per CTA (the
+// second for an item that begins in its share): O as [Dh / 4][128 rows][4] fp32, m[128],
+// l[128].
+constexpr size_t kTreeCutOffset = kWsHeaderBytes;
+constexpr size_t kTreeSlotOffset = kTreeCutOffset + (size_t)kTreeMaxCtas * sizeof(TreeCut);
+constexpr size_t kTreeSlotFloats = (size_t)128 * kTreeBM + 2 * kTreeBM;
+constexpr size_t kTreeWorkspaceBytes = kTreeSlotOffset + 2 * (size_t)kTreeMaxCtas * kTreeSlotFloats * 4;
+static_assert(kTreeSlotOffset % 16 == 0, "alignment of the slots");
+
+struct TreeArgs {
+  int B, T, H, Hkv, group;
+  int tokens;             // of a tile: 128 / group
+  int page_size, max_pages;
+  int num_pages;
+  int chunk;              // keys of one copy: min(page_size, 128)
+  const int* q_offsets;
+  const int* context;
+  const int* mask;        // [T][mask_words] or NULL
+  int mask_words;
+  long long ldm;
+  const int* table;
+  long long ldt;
+  const __nv_bfloat16* v;  // for new tokens that are not finite
+  long long page_stride, token_stride, head_stride;
+  float cs;               // scale * log2(e)
+  void* O;
+  long long ldo;
+  WsHeader* ws;
+  int split;
+  TreeCut* cuts;
+  float* slots;
+  unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ void tree_tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+// 2^x on the special-function unit (2^-inf = +0).
+__device__ __forceinline__ float tree_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Packed pairs: (x0, x1) = (x0 * a + c, x1 * a + c); (r0, r1) += (y0, y1).
+__device__ __forceinline__ void tree_fma2(float& x0, float& x1, float a, float c) {
+  uint64_t x, av, cv;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(av) : "f"(a));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(cv) : "f"(c));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(x), "l"(av), "l"(cv));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
+}
+__device__ __forceinline__ void tree_add2(float& r0, float& r1, float y0, float y1) {
+  uint64_t r, y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(r0), "f"(r1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(y0), "f"(y1));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(r), "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
+}
+__device__ __forceinline__ void tree_tmem_store32(uint32_t taddr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+      "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]),
+      "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]),
+      "f"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tree_tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Product with the A operand in tensor memory.
+__device__ __forceinline__ void tree_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// sum over i < n of floor((a i + b) / 128), a <= 128, in O(log 128) steps: whole parts
+// are taken out, then the points under the line are counted along the other axis.
+__device__ __forceinline__ long long tree_floor_sum(long long n, long long a, long long b) {
+  long long m = 128, sum = 0;
+  while (n > 0) {
+    sum += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+    a %= m;
+    b %= m;
+    const long long top = a * n + b;  // (the line's value behind the last point, times m)
+    n = top / m;
+    b = top % m;
+    const long long swap = a;
+    a = m;
+    m = swap;
+    if (m == 0) break;
+  }
+  return sum;
+}
+
+// One sequence, as every role sees it (what breaks the rules is clamped; the checks
+// report it).
+struct TreeSeq {
+  int a, n;       // its rows of Q: tokens [a, a + n)
+  int ctx;
+  int tiles;
+  long long per_head;  // blocks of one key head's items
+
+  __device__ __forceinline__ void load(const TreeArgs& p, int b) {
+    const int o0 = __ldg(p.q_offsets + b), o1 = __ldg(p.q_offsets + b + 1), c = __ldg(p.context + b);
+    a = min(max(o0, 0), p.T);
+    n = min(max(o1, a), p.T) - a;
+    const long long most = (long long)p.max_pages * p.page_size - n;
+    ctx = (int)min((long long)max(c, 0), max(most, 0ll));
+    tiles = (n + p.tokens - 1) / p.tokens;
+    per_head = n == 0 ? 0 : before(p, tiles - 1) + blocks(p, tiles - 1);
+  }
+  // keys that some row of tile t may see, and their blocks
+  __device__ __forceinline__ int keys(const TreeArgs& p, int t) const {
+    return ctx + (p.mask ? n : min(n, (t + 1) * p.tokens));
+  }
+  __device__ __forceinline__ int blocks(const TreeArgs& p, int t) const { return (keys(p, t) + kTreeBN - 1) / kTreeBN; }
+  // blocks of the tiles before t (t < tiles)
+  __device__ __forceinline__ long long before(const TreeArgs& p, int t) const {
+    if (t == 0) return 0;
+    if (p.mask) return (long long)t * ((ctx + n + kTreeBN - 1) / kTreeBN);
+    return tree_floor_sum(t, p.tokens, (long long)ctx + p.tokens + kTreeBN - 1);
+  }
+};
+
+// A CTA's share, one fragment (consecutive blocks of one item) after another.
+struct TreeWalker {
+  long long x, hi;
+  int b, h, t;
+  long long base;   // first block of sequence b
+  bool fresh;       // (b, h, t) hold the item of block x
+  TreeSeq s;
+  // the fragment
+  long long item;   // the item's first block
+  int jb, je, nb;   // its blocks of the item's nb
+  int token0, ntok; // the tile's tokens
+  int keys;         // keys that the tile may see
+
+  __device__ __forceinline__ void init(const TreeArgs& p, long long lo, long long hi_, int b_, long long base_) {
+    x = lo;
+    hi = hi_;
+    b = b_;
+    base = base_;
+    if (x >= hi) return;
+    s.load(p, b);
+    const long long r = x - base;
+    h = (int)(r / s.per_head);
+    const long long at = r - h * s.per_head;
+    int lo_t = 0, hi_t = s.tiles - 1;  // the last tile with before(t) <= at
+    while (lo_t < hi_t) {
+      const int mid = (lo_t + hi_t + 1) / 2;
+      if (s.before(p, mid) <= at) lo_t = mid;
+      else hi_t = mid - 1;
+    }
+    t = lo_t;
+    item = base + h * s.per_head + s.before(p, t);
+    fresh = true;
+  }
+  __device__ __forceinline__ bool next(const TreeArgs& p) {
+    if (x >= hi) return false;
+    if (!fresh) {  // the item before this one has ended at x
+      if (++t == s.tiles) {
+        t = 0;
+        if (++h == p.Hkv) {
+          h = 0;
+          base += s.per_head * p.Hkv;
+          do s.load(p, ++b);  // (x < W: a sequence holds it)
+          while (s.n == 0);
+        }
+      }
+      item = x;
+    }
+    nb = s.blocks(p, t);
+    jb = (int)(x - item);
+    je = (int)min((long long)nb, jb + (hi - x));
+    token0 = s.a + t * p.tokens;
+    ntok = min(p.tokens, s.n - t * p.tokens);
+    keys = s.keys(p, t);
+    x += je - jb;
+    fresh = false;
+    return true;
+  }
+};
+
+static __device__ __noinline__ void tree_check(const TreeArgs& p) {
+  // (the threads of one CTA, a sequence each)
+  for (int b = (int)threadIdx.x; b < p.B; b += kTreeThreads) {
+    const int o0 = __ldg(p.q_offsets + b), o1 = __ldg(p.q_offsets + b + 1), c = __ldg(p.context + b);
+    const long long n = (long long)o1 - o0;
+    if ((b == 0 && o0 != 0) || n < 0 || o0 < 0 || o1 > p.T || c < 0 || c + n > (long long)p.max_pages * p.page_size ||
+        (p.mask && n > 32ll * p.mask_words))
+      latch_error(p.ws, kErrBadOffsets, 5);
+  }
+}
+
+// Bits 0..31: whether row `ti` of a sequence (its token's index there) sees keys
+// e .. e + 31 behind the context (e < 0: keys of the context).
+__device__ __forceinline__ uint32_t tree_visible(const TreeArgs& p, const TreeSeq& s, int ti, int e) {
+  const int end = p.mask ? s.n : ti + 1;  // no key from here on
+  const int left = end - e;
+  if (left <= 0) return 0u;
+  uint32_t bits = left >= 32 ? 0xffffffffu : (1u << left) - 1u;
+  if (p.mask && e + 31 >= 0) {
+    const int* row = p.mask + (long long)(s.a + ti) * p.ldm;
+    auto word = [&](int i) -> uint32_t { return i >= 0 && i < p.mask_words ? (uint32_t)__ldg(row + i) : 0u; };
+    const int at = e >> 5;  // floor
+    const uint32_t lo = at < 0 ? 0xffffffffu : word(at);
+    bits &= __funnelshift_r(lo, word(at + 1), (uint32_t)(e & 31));
+  }
+  return bits;
+}
+
+// The K or V blocks of the CTA's share into a ring, by one warp: lane c of a block's
+// copies takes chunk c (a page, or 128 keys of one).
+template <int DH, int STAGES, bool IS_K>
+__device__ __forceinline__ void tree_produce(const TreeArgs& p, TreeWalker w, const Guard& guard, const CUtensorMap* tm,
+                                             const CUtensorMap* tmQ, uint32_t ring, uint32_t full0, uint32_t empty0,
+                                             uint32_t q_ring, uint32_t q_full0, uint32_t q_done0) {
+  using Cfg = TreeCfg<DH>;
+  const uint32_t lane = lane_id();
+  const int per_block = kTreeBN / p.chunk;  // chunks: 1 .. 16
+  const int batch = 32 / per_block;         // blocks whose pages one load of the warp fetches
+  const int my_block = (int)lane / per_block, my_chunk = (int)lane % per_block;
+  int st = 0;
+  uint32_t ph = 1, it = 0;
+  for (; w.next(p); ++it) {
+    const int* row = p.table + (long long)w.b * p.ldt;
+    // page of this lane's chunk, `batch` blocks at a time; -1: nothing to load
+    auto fetch = [&](int j0) -> int {
+      const int j = j0 + my_block;
+      const int key = j * kTreeBN + my_chunk * p.chunk;
+      if (j >= w.je || key >= w.keys) return -1;
+      const int i = key / p.page_size;
+      return i < p.max_pages ? __ldg(row + i) : -1;
+    };
+    int ids = fetch(w.jb), ids_next = fetch(w.jb + batch);
+    if (IS_K) {
+      const uint32_t qb = it & 1u;
+      bool ok = true;
+      if (lane == 0) {
+        ok = it < 2 || wait_phase(guard, q_done0 + 8u * qb, ((it - 2u) >> 1) & 1u, (kRoleProducer << 16) | 0x900);
+        if (ok) {
+          mbar_arrive_expect_tx(q_full0 + 8u * qb, (uint32_t)(Cfg::kHalves * 128 * p.group * p.tokens));
+          for (int hf = 0; hf < Cfg::kHalves; ++hf)
+            tma_load_3d(q_ring + qb * Cfg::kTile + hf * (kTreeBM * 128), tmQ, q_full0 + 8u * qb, hf * 64, w.h * p.group, w.token0);
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
+    }
+    int i = 0;  // block of the batch
+    for (int j = w.jb; j < w.je; ++j) {
+      if (i == batch) {
+        i = 0;
+        ids = ids_next;
+        ids_next = fetch(j + batch);
+      }
+      const int left = w.keys - j * kTreeBN;
+      const int chunks = left >= kTreeBN ? per_block : (left + p.chunk - 1) / p.chunk;
+      const int page = __shfl_sync(0xffffffffu, ids, (i * per_block + (int)lane % per_block) & 31);
+      ++i;
+      bool ok = true;
+      if (lane == 0) {
+        ok = wait_phase(guard, empty0 + 8u * st, ph, (kRoleProducer << 16) | (IS_K ? 0 : 0x10) | st);
+        if (ok) mbar_arrive_expect_tx(full0 + 8u * st, (uint32_t)(chunks * p.chunk * DH * 2));
+      }
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
+      if ((int)lane < chunks) {
+        // (a page outside the cache reads as zeros)
+        if (page < 0 || page >= p.num_pages) latch_error(p.ws, 1u, (kRoleProducer << 16) | 0x20);
+        const int key = j * kTreeBN + (int)lane * p.chunk;
+        const uint32_t dst = ring + st * Cfg::kTile + (uint32_t)((int)lane * p.chunk * 128);
+        for (int hf = 0; hf < Cfg::kHalves; ++hf)
+          tree_tma_load_4d(dst + hf * (kTreeBN * 128), tm, full0 + 8u * st, hf * 64, key % p.page_size, w.h, page);
+      }
+      if (++st == STAGES) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
+  }
+}
+
+// tmQ {Dh, H, T}, boxes of 64 x group x (tokens of a tile); tmK, tmV {Dh, page_size,
+// Hkv, pages}, boxes of 64 x chunk x 1 x 1; 128-byte swizzle.
+template <int DH, bool OUT_F32>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    k_tree_attn(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const TreeArgs p) {
+  using Cfg = TreeCfg<DH>;
+  constexpr int KS = Cfg::kKStages, VS = Cfg::kVStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sQ = smem_addr(smem), sK = sQ + 2 * Cfg::kTile, sV = sK + KS * Cfg::kTile;
+  uint8_t* tail = smem + (2 + KS + VS) * Cfg::kTile;  // 1 KB
+  uint64_t* bars = reinterpret_cast<uint64_t*>(tail);
+  long long* scratch = reinterpret_cast<long long*>(tail + 320);
+  long long* found = scratch + 33;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(found + 2);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  volatile uint32_t* odd_v = tmem_slot + 2;  // [4]: fragment it & 3 met new tokens whose V is not finite
+  static_assert(Cfg::kBars * 8 <= 320 && 320 + 35 * 8 + 24 <= 1024, "the last kilobyte");
+  const int warp = (int)threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t bar0 = smem_addr(bars);
+  // q_full[2], q_done[2] (the softmax warps are done with a fragment), k_full, k_empty,
+  // v_full, v_empty, s_full[3], p_full[3], pv_done[3], o_empty
+  const uint32_t q_full = bar0, q_done = bar0 + 16, k_full = bar0 + 32, k_empty = k_full + 8 * KS;
+  const uint32_t v_full = k_empty + 8 * KS, v_empty = v_full + 8 * VS, s_full = v_empty + 8 * VS;
+  const uint32_t p_full = s_full + 8 * kTreeSBufs, pv_done = p_full + 8 * kTreeSBufs, o_empty = pv_done + 8 * kTreeSBufs;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 1);
+      mbar_init(q_done + 8 * i, 4);
+    }
+    for (int i = 0; i < KS; ++i) {
+      mbar_init(k_full + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(v_full + 8 * i, 1);
+      mbar_init(v_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < kTreeSBufs; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 4);
+      mbar_init(pv_done + 8 * i, 1);
+    }
+    mbar_init(o_empty, 4);
+    *abort_flag = 0u;
+    odd_v[0] = odd_v[1] = odd_v[2] = odd_v[3] = 0u;
+    found[0] = found[1] = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 2) {
+    tmem_alloc<1>(smem_addr(tmem_slot), 512);
+    tmem_relinquish<1>();
+  }
+  if (blockIdx.x == 0) tree_check(p);
+  // this CTA's share
+  auto count = [&](int b) -> long long {
+    TreeSeq s;
+    s.load(p, b);
+    return s.per_head * p.Hkv;
+  };
+  tc_fence_before_sync();
+  const long long W = block_total<kTreeThreads>(p.B, count, scratch);
+  tc_fence_after_sync();
+  const Share share{W, (int)max(1ll, min((long long)gridDim.x, W))};
+  long long lo = 0, hi = 0;
+  if ((int)blockIdx.x < share.G) {
+    lo = share.lo((int)blockIdx.x);
+    hi = share.lo((int)blockIdx.x + 1);
+  }
+  if (lo < hi) block_locate<kTreeThreads>(p.B, count, lo, scratch, found);
+  __syncthreads();
+  const uint32_t tmem_base = *tmem_slot;
+  const Guard guard{p.ws, abort_flag, p.timeout_ns};
+  TreeWalker w;
+  w.init(p, lo, hi, (int)found[0], found[1]);
+  if (!p.split && lo < hi) {
+    // Whole items only: those that begin in the share.
+    TreeWalker e = w;
+    if (w.item < w.x) {  // the first one began earlier
+      e.next(p);
+      e.x = e.item + e.nb;
+      w = e;
+    }
+    // the end: where the item that holds block hi - 1 ends
+    long long end = hi;
+    if (w.x < hi) {
+      e = w;
+      while (e.next(p)) end = e.item + e.nb;
+    }
+    w.hi = w.x < hi ? end : w.x;
+  }
+
+  if (warp == 0) {
+    tree_produce<DH, KS, true>(p, w, guard, &tmK, &tmQ, sK, k_full, k_empty, sQ, q_full, q_done);
+  } else if (warp == 3) {
+    tree_produce<DH, VS, false>(p, w, guard, &tmV, nullptr, sV, v_full, v_empty, 0, 0, 0);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ S = Q K^T
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kTreeBM, kTreeBN, false, false);
+      int ks = 0, sb = 0;
+      uint32_t kph = 0, sph = 0, it = 0;
+      long long done = 0;
+      bool ok = true;
+      for (; ok && w.next(p); ++it) {
+        const uint32_t qb = it & 1u;
+        if (!wait_phase(guard, q_full + 8 * qb, (it >> 1) & 1u, (kRoleMma << 16) | 0x800)) break;
+        const uint32_t q_at = sQ + qb * Cfg::kTile;
+        for (int j = w.jb; j < w.je; ++j, ++done) {
+          // the buffer's last P has been read (three blocks ago), and K is there
+          const bool p_ok = done < kTreeSBufs || mbar_test_wait(pv_done + 8 * sb, sph ^ 1u);
+          const bool k_ok = mbar_test_wait(k_full + 8 * ks, kph);
+          if ((!p_ok && !wait_phase(guard, pv_done + 8 * sb, sph ^ 1u, (kRoleMma << 16) | 0x400 | sb)) ||
+              (!k_ok && !wait_phase(guard, k_full + 8 * ks, kph, (kRoleMma << 16) | ks))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t k_at = sK + ks * Cfg::kTile;
+          const uint32_t d = tmem_base + (uint32_t)(kTreeBN * sb);
+#pragma unroll
+          for (int kk = 0; kk < DH / 16; ++kk) {
+            const uint32_t o = (uint32_t)((kk >> 2) * (kTreeBN * 128) + (kk & 3) * 32);
+            umma_bf16<1>(d, sdesc_sw128(q_at + o, 16, 1024), sdesc_sw128(k_at + o, 16, 1024), idesc, kk != 0 ? 1u : 0u);
+          }
+          umma_commit(s_full + 8 * sb);
+          umma_commit(k_empty + 8 * ks);
+          if (++ks == KS) {
+            ks = 0;
+            kph ^= 1u;
+          }
+          if (++sb == kTreeSBufs) {
+            sb = 0;
+            sph ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ O += P V
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kTreeBM, DH, false, true);
+      int vs = 0, sb = 0;
+      uint32_t vph = 0, sph = 0, it = 0;
+      bool ok = true;
+      for (; ok && w.next(p); ++it) {
+        for (int j = w.jb; j < w.je; ++j) {
+          const bool v_ok = mbar_test_wait(v_full + 8 * vs, vph);
+          const bool p_ok = mbar_test_wait(p_full + 8 * sb, sph);
+          if ((!v_ok && !wait_phase(guard, v_full + 8 * vs, vph, (kRoleMma << 16) | 0x10 | vs)) ||
+              (!p_ok && !wait_phase(guard, p_full + 8 * sb, sph, (kRoleMma << 16) | 0x200 | sb)) ||
+              (j == w.jb && !wait_phase(guard, o_empty, (it & 1u) ^ 1u, (kRoleMma << 16) | 0x300))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint64_t vd = sdesc_sw128(sV + vs * Cfg::kTile, kTreeBN * 128, 1024);
+          const uint32_t a = tmem_base + (uint32_t)(kTreeBN * sb);
+#pragma unroll
+          for (int kk = 0; kk < kTreeBN / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of V
+            tree_mma_ts(tmem_base + Cfg::kTmemO, a + (uint32_t)(kk * 8), vd + (uint32_t)(kk * 128), idesc,
+                        (j > w.jb || kk != 0) ? 1u : 0u);
+          umma_commit(pv_done + 8 * sb);
+          umma_commit(v_empty + 8 * vs);
+          if (++vs == VS) {
+            vs = 0;
+            vph ^= 1u;
+          }
+          if (++sb == kTreeSBufs) {
+            sb = 0;
+            sph ^= 1u;
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax, output
+    const int q = warp & 3;
+    const int row = q * 32 + (int)lane;
+    const uint32_t t_lane = tmem_base + ((uint32_t)(q * 32) << 16);
+    const uint32_t t_o = t_lane + Cfg::kTmemO;
+    const int my_tok = row / p.group, my_head = row - my_tok * p.group;
+    const float cs = p.cs;
+    int sb = 0, vs = 0;
+    uint32_t sph = 0, vph = 0, it = 0;
+    bool wrote_cut = false, ok = true;
+    for (; ok && w.next(p); ++it) {
+      const int rows = w.ntok * p.group;
+      const bool active = q * 32 < rows;  // (of the whole warp)
+      const int ti = w.t * p.tokens + my_tok;
+      float m = -INFINITY, l = 0.0f;
+      int last_sb = 0;
+      uint32_t last_ph = 0;
+      for (int j = w.jb; j < w.je; ++j) {
+        const bool inner = (j + 1) * kTreeBN <= w.s.ctx;  // every row sees every key
+        uint32_t vis[4] = {0u, 0u, 0u, 0u};
+        if (!inner && row < rows) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vis[i] = tree_visible(p, w.s, ti, j * kTreeBN - w.s.ctx + 32 * i);
+        }
+        if (!warp_wait_phase(guard, s_full + 8 * sb, sph, (kRoleEpilogue << 16) | sb)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        if (active) {
+          float s[kTreeBN];
+          float rs8[8];
+          const uint32_t t_s = t_lane + (uint32_t)(kTreeBN * sb);
+          auto load_scores = [&]() {
+#pragma unroll
+            for (int c = 0; c < kTreeBN / 32; ++c) tmem_load32(t_s + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
+          };
+          load_scores();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) rs8[i] = 0.0f;
+          auto sum8 = [&]() { return ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7])); };
+          bool done = false;
+          if (inner && j > w.jb) {
+            // With the maximum so far: every P is positive, so a row sum of at most 2^8
+            // proves that no P exceeds it and the maximum need not be looked for.
+#pragma unroll
+            for (int i = 0; i < kTreeBN / 2; ++i) {
+              tree_fma2(s[2 * i], s[2 * i + 1], cs, -m);
+              s[2 * i] = tree_ex2(s[2 * i]);
+              s[2 * i + 1] = tree_ex2(s[2 * i + 1]);
+              tree_add2(rs8[2 * (i & 3)], rs8[2 * (i & 3) + 1], s[2 * i], s[2 * i + 1]);
+            }
+            done = __all_sync(0xffffffffu, sum8() <= kTreeGrowSum || row >= rows) != 0;
+            if (!done) {
+              load_scores();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) rs8[i] = 0.0f;
+            }
+          }
+          if (!done) {
+            float e8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e8[i] = -INFINITY;
+            if (inner) {
+#pragma unroll
+              for (int i = 0; i < kTreeBN; ++i) {
+                s[i] *= cs;
+                e8[i & 7] = fmaxf(e8[i & 7], s[i]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kTreeBN; ++i) {
+                s[i] = (vis[i >> 5] >> (i & 31)) & 1u ? s[i] * cs : -INFINITY;
+                e8[i & 7] = fmaxf(e8[i & 7], s[i]);
+              }
+            }
+            const float mx = fmaxf(fmaxf(fmaxf(e8[0], e8[1]), fmaxf(e8[2], e8[3])), fmaxf(fmaxf(e8[4], e8[5]), fmaxf(e8[6], e8[7])));
+            if (j == w.jb) {
+              m = mx;  // the first PV product overwrites O
+            } else {
+              const bool grow = mx > m + kTreeGrow && row < rows;
+              if (__any_sync(0xffffffffu, grow)) {
+                if (!warp_wait_phase(guard, pv_done + 8 * last_sb, last_ph, (kRoleEpilogue << 16) | 0x100)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after_sync();
+                const float alpha = grow ? tree_ex2(m - mx) : 1.0f;
+                if (grow) {
+                  l *= alpha;
+                  m = mx;
+                }
+#pragma unroll
+                for (int c = 0; c < DH / 32; ++c) {
+                  float v[32];
+                  tmem_load32(t_o + c * 32, v);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) v[i] *= alpha;
+                  tree_tmem_store32(t_o + c * 32, v);
+                }
+                tree_tmem_store_wait();
+              }
+            }
+            // (a row that has seen no key yet: every P is 2^-inf)
+            const float ms = !inner && m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int i = 0; i < kTreeBN; ++i) {
+              s[i] = tree_ex2(s[i] - ms);
+              rs8[i & 7] += s[i];
+            }
+          }
+          l += sum8();
+#pragma unroll
+          for (int h2 = 0; h2 < kTreeBN / 64; ++h2) {
+            float pk[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) pk[c] = __uint_as_float(pack_bf16x2(s[64 * h2 + 2 * c], s[64 * h2 + 2 * c + 1]));
+            tree_tmem_store32(t_s + 32 * h2, pk);
+          }
+          tree_tmem_store_wait();
+        }
+        if (!inner) {
+          // V: clear the keys behind the sequence and what is not finite of the new
+          // tokens; thread = key.
+          if (!warp_wait_phase(guard, v_full + 8 * vs, vph, (kRoleEpilogue << 16) | 0x500)) {
+            ok = false;
+            break;
+          }
+          (void)mbar_try_wait(v_full + 8 * vs, vph);  // each lane sees the copies
+          const int key = j * kTreeBN + row;
+          if (key >= w.s.ctx) {
+            const bool out = key >= w.keys;
+            bool odd = false;
+            for (int hf = 0; hf < Cfg::kHalves; ++hf) {
+              const uint32_t at = sV + vs * Cfg::kTile + (uint32_t)(hf * (kTreeBN * 128) + row * 128);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const uint32_t a16 = at + (uint32_t)((c ^ (row & 7)) << 4);  // (the eight words in an order without bank conflicts)
+                if (out) {
+                  st_shared_v4(a16, 0u, 0u, 0u, 0u);
+                } else {
+                  uint32_t x[4];
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                               : "r"(a16)
+                               : "memory");
+                  bool bad = false;
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    if ((x[i] & 0x7f80u) == 0x7f80u) {
+                      x[i] &= 0xffff0000u;
+                      bad = true;
+                    }
+                    if ((x[i] & 0x7f800000u) == 0x7f800000u) {
+                      x[i] &= 0x0000ffffu;
+                      bad = true;
+                    }
+                  }
+                  if (bad) st_shared_v4(a16, x[0], x[1], x[2], x[3]);
+                  odd |= bad;
+                }
+              }
+            }
+            if (odd) odd_v[it & 3u] = 1u;
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * sb);
+        last_sb = sb;
+        last_ph = sph;
+        if (++sb == kTreeSBufs) {
+          sb = 0;
+          sph ^= 1u;
+        }
+        if (++vs == VS) {
+          vs = 0;
+          vph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (!warp_wait_phase(guard, pv_done + 8 * last_sb, last_ph, (kRoleEpilogue << 16) | 0x300)) {
+        ok = false;
+        break;
+      }
+      (void)mbar_try_wait(pv_done + 8 * last_sb, last_ph);  // each lane: odd_v was written before the products were issued
+      tc_fence_after_sync();
+      if (active) {
+        const bool whole = w.jb == 0 && w.je == w.nb;
+        const bool odd = odd_v[it & 3u] != 0u;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const long long at = (long long)(w.token0 + my_tok) * p.ldo + (long long)(w.h * p.group + my_head) * DH;
+        float* slot = whole ? nullptr : p.slots + (size_t)(2 * blockIdx.x + (w.jb == 0 ? 1 : 0)) * kTreeSlotFloats;
+#pragma unroll 1
+        for (int c = 0; c < DH / 32; ++c) {
+          float v[32];
+          tmem_load32(t_o + c * 32, v);
+          if (row < rows) {
+            if (odd) {
+              // new tokens of this fragment's blocks whose V is not finite, where the row sees them
+              for (int key = max(w.s.ctx, w.jb * kTreeBN); key < min(w.keys, w.je * kTreeBN); ++key) {
+                if (!(tree_visible(p, w.s, ti, key - w.s.ctx) & 1u)) continue;
+                const int pg = __ldg(p.table + (long long)w.b * p.ldt + min(key / p.page_size, p.max_pages - 1));
+                if (pg < 0 || pg >= p.num_pages) continue;
+                const __nv_bfloat16* vr = p.v + pg * p.page_stride + (key % p.page_size) * p.token_stride + w.h * p.head_stride + c * 32;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float y = __bfloat162float(vr[i]);
+                  if (!(fabsf(y) <= 3.4e38f)) v[i] += y;
+                }
+              }
+            }
+            if (whole) {
+              if (l == 0.0f) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.0f;  // the row sees nothing
+              }
+              if constexpr (OUT_F32) {
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.O) + at + c * 32);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+              } else {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.O) + at + c * 32);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  dst[i] = make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                                      pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv), pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+              }
+            } else {
+              float4* part = reinterpret_cast<float4*>(slot);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                __stcg(part + (c * 8 + i) * kTreeBM + row, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            }
+          }
+        }
+        if (!whole && row < rows) {
+          __stcg(slot + 128 * kTreeBM + row, m);
+          __stcg(slot + 128 * kTreeBM + kTreeBM + row, l);
+        }
+        if (!whole && w.jb == 0 && row == 0) {
+          p.cuts[blockIdx.x] =
+              TreeCut{share.owner(w.item + w.nb - 1) - (int)blockIdx.x + 1, w.token0, w.h * p.group, rows};
+          wrote_cut = true;
+        }
+      }
+      // The flag of the fragment after next: the products of this one are done, so every
+      // warp has left the fragment before it, and none enters that one before this warp
+      // has taken part in the next.
+      if (row == 0) odd_v[(it + 2u) & 3u] = 0u;
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(o_empty);
+        mbar_arrive(q_done + 8 * (it & 1u));
+      }
+    }
+    if (p.split && row == 0 && !wrote_cut) p.cuts[blockIdx.x].pieces = 0;
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc_fence_before_sync();
+  __syncthreads();
+  if (*abort_flag) {
+    for (int i = 0; i < 200; ++i) __nanosleep(1000);  // copies and products still in flight land first
+  }
+  tc_fence_after_sync();
+  if (warp == 2) tmem_dealloc<1>(tmem_base, 512);
+}
+
+// The cut items' pieces added up: blockIdx.x is the CTA in whose share an item
+// begins; a thread takes four components of a row.
+template <int DH, bool OUT_F32>
+__global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const TreeCut cut = p.cuts[blockIdx.x];
+  const int i = (int)(blockIdx.y * 256 + threadIdx.x);
+  const int row = i % kTreeBM, quad = i / kTreeBM;
+  if (cut.pieces == 0 || row >= cut.rows) return;
+  auto slot = [&](int k) { return p.slots + (size_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * kTreeSlotFloats; };
+  float m = -INFINITY;
+  for (int k = 0; k < cut.pieces; ++k) m = fmaxf(m, __ldcg(slot(k) + 128 * kTreeBM + row));
+  const float ms = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = 0; k < cut.pieces; ++k) {
+    const float* s = slot(k);
+    const float a = tree_ex2(__ldcg(s + 128 * kTreeBM + row) - ms);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + quad * kTreeBM + row);
+    l = fmaf(a, __ldcg(s + 128 * kTreeBM + kTreeBM + row), l);
+    o.x = fmaf(a, v.x, o.x);
+    o.y = fmaf(a, v.y, o.y);
+    o.z = fmaf(a, v.z, o.z);
+    o.w = fmaf(a, v.w, o.w);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const bool none = l == 0.0f;
+  const int tok = row / p.group, head = row - tok * p.group;
+  const long long at = (long long)(cut.token0 + tok) * p.ldo + (long long)(cut.head0 + head) * DH + quad * 4;
+  const float y0 = none ? 0.0f : o.x * inv, y1 = none ? 0.0f : o.y * inv, y2 = none ? 0.0f : o.z * inv, y3 = none ? 0.0f : o.w * inv;
+  if constexpr (OUT_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + at) = make_float4(y0, y1, y2, y3);
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + at) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
+}
+
+}  // namespace wst

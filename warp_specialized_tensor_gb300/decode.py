@@ -9,6 +9,7 @@ current stream unless one is given.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -17,6 +18,7 @@ from warp_specialized_tensor_gb300.moe import _dense, _need, _rows, _stream, _ty
 
 __all__ = [
     "ROPE_HALVES", "ROPE_PAIRS", "wst_cache_append_bf16",
+    "wst_tree_attention_bf16", "wst_tree_attention_workspace_size", "tree_attention_workspace",
     "wst_gemm_w4", "wst_grouped_gemm_w4", "wst_gemm_w4_workspace_size", "gemm_w4_workspace",
 ]
 
@@ -28,9 +30,11 @@ _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 
 def declare(lib) -> None:
     """Argument types of the functions bound here."""
-    P, I, L, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_long, ctypes.c_size_t
+    P, I, L, Z, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_long, ctypes.c_size_t, ctypes.c_float
     for name, res, args in (
             ("wst_cache_append_bf16", I, [I, I, I, I, I, I, P, L, P, L, P, L, I, P, P, P, P, L, P, P, I, I, L, L, L, P, P]),
+            ("wst_tree_attention_bf16", I, [I, I, I, I, I, P, L, P, P, P, I, L, P, P, I, I, L, L, L, P, I, L, F, P, L, I, P, Z, P]),
+            ("wst_tree_attention_workspace_size", Z, []),
             ("wst_gemm_w4", I, [I, I, I, P, L, P, L, P, L, I, P, P, L, I, I, P, Z, P]),
             ("wst_grouped_gemm_w4", I, [I, I, I, I, P, L, P, L, L, P, L, L, I, P, P, L, P, L, I, I, P, Z, P]),
             ("wst_gemm_w4_workspace_size", Z, [])):
@@ -107,6 +111,61 @@ def wst_cache_append_bf16(k, v, positions, slots, k_cache, v_cache, inv_freq=Non
         _w._ptr(q_out) if q is not None else None, ldqo, k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], k_cache.shape[1],
         sp, st_, sh, ws, _stream(stream, k))
     _w._check(st, "wst_cache_append_bf16")
+
+
+# ----------------------------------------------------------------------------
+# attention
+# ----------------------------------------------------------------------------
+def wst_tree_attention_workspace_size() -> int:
+    return int(_lib().wst_tree_attention_workspace_size())
+
+
+def tree_attention_workspace(device=None, stream=None) -> torch.Tensor:
+    """A zero-filled workspace with which wst_tree_attention_bf16 spreads long
+    sequences over all SMs; any workspace() works."""
+    ws = torch.empty(wst_tree_attention_workspace_size(), dtype=torch.uint8, device=device or "cuda")
+    _w.wst_workspace_init(ws, stream)
+    return ws
+
+
+def wst_tree_attention_bf16(Q, q_offsets, context, k_cache, v_cache, page_table, O, mask=None, scale=None, workspace=None,
+                            stream=None) -> None:
+    """Attention of the new tokens of B sequences over a paged cache that holds them
+    already, behind each sequence's context.
+
+    Q: bf16 [T, H, Dh]; q_offsets: device int32 [B+1], the tokens of each sequence;
+    context: device int32 [B], its cached tokens before them; k_cache, v_cache: bf16
+    [pages, page_size, Hkv, Dh]; page_table: int32 [B, max_pages]; O: bf16/fp32 [T, H,
+    Dh]; mask: int32 [T, words], bit d of a row set where the token sees its
+    sequence's new token d, or None (those up to itself); scale: 1/sqrt(Dh) if None.
+    A token that sees nothing gets zeros; rows behind q_offsets[B] are left as they
+    were."""
+    ldq, ldo = _heads(Q, "Q", _BF16), _heads(O, "O")
+    T, H, Dh = Q.shape
+    if O.shape != Q.shape:
+        raise ValueError("O must be like Q")
+    _need(page_table, "page_table", _I32, (2,))
+    B, max_pages = page_table.shape
+    sp, st_, sh = _cache(k_cache, v_cache)
+    Hkv = k_cache.shape[2]
+    if k_cache.shape[3] != Dh or Hkv == 0 or H % Hkv:
+        raise ValueError("k_cache must be [pages, page_size, Hkv, %d] with Hkv a divisor of %d, not %s" % (Dh, H, tuple(k_cache.shape)))
+    words = ldm = 0
+    if mask is not None:
+        _need(mask, "mask", _I32, (2,))
+        if mask.shape[0] != T:
+            raise ValueError("mask must be [T, words]")
+        words = mask.shape[1]
+        ldm = mask.stride(0) if T > 1 else words
+    if scale is None:
+        scale = 1.0 / math.sqrt(Dh)
+    ws, n = _ws(workspace)
+    st = _lib().wst_tree_attention_bf16(
+        B, T, H, Hkv, Dh, Q.data_ptr(), ldq, _dense(q_offsets, "q_offsets", _I32, (B + 1,)), _dense(context, "context", _I32, (B,)),
+        _w._ptr(mask), words, ldm, k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], k_cache.shape[1], sp, st_, sh,
+        page_table.data_ptr(), max_pages, page_table.stride(0) if B > 1 else max_pages, scale, O.data_ptr(), ldo, _type(O, "O"), ws, n,
+        _stream(stream, Q))
+    _w._check(st, "wst_tree_attention_bf16")
 
 
 # ----------------------------------------------------------------------------
