@@ -74,6 +74,20 @@ def test_scores_of_every_size(size, scale, Dh):
     check(c, scale=scale)
 
 
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("Dh", [64, 128])
+def test_keys_that_come_from_far_memory(page, Dh):
+    """Sequences of many blocks with the caches out of L2, so that V arrives long after its scores: blocks that are
+    cleaned behind a sequence's end while the ones before them are still read."""
+    c = Paged([(2048 + 66 * i, 1 + i % 3) for i in range(32)], 32, 8, Dh, page, "chain", seed=2)
+    want, size, most = c.want(1.0 / math.sqrt(Dh))
+    tol = c.tolerance(want, size, most, torch.float32)
+    for _ in range(3):
+        torch.randn(1 << 27, device="cuda")
+        out, status = run(c)
+        assert status == 0 and bool(((out.double() - want).abs() <= tol).all())
+
+
 def test_rows_that_see_nothing():
     c = Paged([(0, 40), (200, 5), (0, 3)], 4, 2, 128, 16, "any", seed=1)
     c.seen[0][::3] = False

@@ -26,8 +26,10 @@
 //   MMA      S = Q . K^T        Q and K from shared memory, 128 x 128 x Dh
 //   softmax  P = 2^(cs S - m) as bf16 over S's tensor memory; m moves only when the
 //            maximum has grown by more than 2^8, which rescales O and l
-//            (P <= 2^8, rounded to bf16: by at most 2^-8 of it; l sums the unrounded P)
-//   MMA      O += P . V         P from tensor memory, V from shared memory
+//            (P <= 2^8; l sums the unrounded P).  One bf16 is off by up to 2^-8 of P, which
+//            a bf16 output's own rounding covers; for fp32 output P is two bf16 (what the
+//            first leaves), off by 2^-16, in the two halves of S's columns
+//   MMA      O += P . V         P from tensor memory, V from shared memory (twice for two P)
 // Three S/P buffers, so S runs ahead of PV; two threads issue the products (a wait
 // costs ~160 clocks while products are in flight, and this way one's products run
 // under the other's wait).
@@ -534,6 +536,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int kk = 0; kk < kTreeBN / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of V
             tree_mma_ts(tmem_base + Cfg::kTmemO, a + (uint32_t)(kk * 8), vd + (uint32_t)(kk * 128), idesc,
                         (j > w.jb || kk != 0) ? 1u : 0u);
+          if constexpr (OUT_F32) {
+#pragma unroll
+            for (int kk = 0; kk < kTreeBN / 16; ++kk)
+              tree_mma_ts(tmem_base + Cfg::kTmemO, a + (uint32_t)(64 + kk * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
+          }
           umma_commit(pv_done + 8 * sb);
           umma_commit(v_empty + 8 * vs);
           if (++vs == VS) {
@@ -557,6 +564,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const float cs = p.cs;
     int sb = 0, vs = 0;
     uint32_t sph = 0, vph = 0, it = 0;
+    long long blocks = 0;  // before this one
     bool wrote_cut = false, ok = true;
     for (; ok && w.next(p); ++it) {
       const int rows = w.ntok * p.group;
@@ -664,14 +672,43 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int h2 = 0; h2 < kTreeBN / 64; ++h2) {
             float pk[32];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) pk[c] = __uint_as_float(pack_bf16x2(s[64 * h2 + 2 * c], s[64 * h2 + 2 * c + 1]));
+            for (int c = 0; c < 32; ++c) {
+              float& x0 = s[64 * h2 + 2 * c];
+              float& x1 = s[64 * h2 + 2 * c + 1];
+              const uint32_t hi = pack_bf16x2(x0, x1);
+              pk[c] = __uint_as_float(hi);
+              if constexpr (OUT_F32) {
+                x0 -= __uint_as_float(hi << 16);
+                x1 -= __uint_as_float(hi & 0xffff0000u);
+              }
+            }
             tree_tmem_store32(t_s + 32 * h2, pk);
+          }
+          if constexpr (OUT_F32) {
+#pragma unroll
+            for (int h2 = 0; h2 < kTreeBN / 64; ++h2) {
+              float pk[32];
+#pragma unroll
+              for (int c = 0; c < 32; ++c) pk[c] = __uint_as_float(pack_bf16x2(s[64 * h2 + 2 * c], s[64 * h2 + 2 * c + 1]));
+              tree_tmem_store32(t_s + 64 + 32 * h2, pk);
+            }
           }
           tree_tmem_store_wait();
         }
         if (!inner) {
           // V: clear the keys behind the sequence and what is not finite of the new
-          // tokens; thread = key.
+          // tokens; thread = key.  These warps wait for V here only, and a parity tells
+          // two phases apart: the stage's last use has to be over first.  (S_g was issued
+          // after PV_{g-3}: with three stages or more it is.)
+          static_assert(VS >= 2, "stages of V");
+          if constexpr (VS == 2) {
+            const bool wraps = sb < 2;  // block g - 2 used the buffers' round before this one
+            if (blocks >= 2 &&
+                !warp_wait_phase(guard, pv_done + 8 * (sb + 1 == kTreeSBufs ? 0 : sb + 1), wraps ? sph ^ 1u : sph, (kRoleEpilogue << 16) | 0x600)) {
+              ok = false;
+              break;
+            }
+          }
           if (!warp_wait_phase(guard, v_full + 8 * vs, vph, (kRoleEpilogue << 16) | 0x500)) {
             ok = false;
             break;
@@ -720,6 +757,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (lane == 0) mbar_arrive(p_full + 8 * sb);
         last_sb = sb;
         last_ph = sph;
+        ++blocks;
         if (++sb == kTreeSBufs) {
           sb = 0;
           sph ^= 1u;
