@@ -435,15 +435,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     return s.per_head * p.Hkv;
   };
   tc_fence_before_sync();
-  const long long W = block_total<kTreeThreads>(p.B, count, scratch);
+  BlockCount<long long, kTreeThreads> counted;
+  const long long W = counted.total(p.B, count, scratch);
   tc_fence_after_sync();
-  const Share share{W, (int)max(1ll, min((long long)gridDim.x, W))};
+  const Share<long long> share(W, (int)max(1ll, min((long long)gridDim.x, W)));
   long long lo = 0, hi = 0;
   if ((int)blockIdx.x < share.G) {
     lo = share.lo((int)blockIdx.x);
     hi = share.lo((int)blockIdx.x + 1);
   }
-  if (lo < hi) block_locate<kTreeThreads>(p.B, count, lo, scratch, found);
+  if (lo < hi) counted.locate(p.B, count, lo, scratch, found);
   __syncthreads();
   const uint32_t tmem_base = *tmem_slot;
   const Guard guard{p.ws, abort_flag, p.timeout_ns};

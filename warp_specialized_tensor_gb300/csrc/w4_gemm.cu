@@ -21,7 +21,7 @@ struct W4Problem {
   int group;
 };
 
-template <int NT>
+template <int NT, int GROUPS>
 int launch_w4(W4Problem& pr, const DeviceInfo& dev, cudaStream_t stream) {
   using Cfg = W4Cfg<NT>;
   W4Args& a = pr.a;
@@ -38,21 +38,28 @@ int launch_w4(W4Problem& pr, const DeviceInfo& dev, cudaStream_t stream) {
   {
     const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)a.M};
     const uint64_t str[1] = {(uint64_t)pr.lda * 2};
-    const uint32_t box[2] = {32, (uint32_t)Cfg::kTokens};
-    if ((st = encode_map(&tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pr.A, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B))) return st;
+    const uint32_t box[2] = {kW4K, (uint32_t)Cfg::kRows};
+    if ((st = encode_map(&tmA, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pr.A, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE))) return st;
   }
   {
     const uint64_t dims[3] = {(uint64_t)a.N, (uint64_t)kb, (uint64_t)a.G};
     const uint64_t str[2] = {(uint64_t)pr.lds * 2, (uint64_t)(a.G > 1 ? pr.strideS : pr.lds) * 2};
-    const uint32_t box[3] = {kW4Feats, (uint32_t)(kW4K / pr.group), 1};
+    const uint32_t box[3] = {kW4Feats, GROUPS, 1};
     if ((st = encode_map(&tmS, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, pr.scales, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE))) return st;
   }
-  auto kern = k_w4_gemm<NT>;
+  auto kern = k_w4_gemm<NT, GROUPS>;
   if ((st = ensure_smem_attr((const void*)kern, Cfg::kSmem))) return st;
   const int grid = std::min(dev.num_sms, kW4MaxCtas);
   kern<<<grid, Cfg::kThreads, Cfg::kSmem, stream>>>(tmW, tmA, tmS, a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ST_OK : cuda_fail(e, "launch k_w4_gemm");
+}
+
+template <int NT>
+int launch_w4_group(W4Problem& pr, const DeviceInfo& dev, cudaStream_t stream) {
+  if (pr.group == 128) return launch_w4<NT, 1>(pr, dev, stream);
+  if (pr.group == 64) return launch_w4<NT, 2>(pr, dev, stream);
+  return launch_w4<NT, 4>(pr, dev, stream);
 }
 
 int run_w4(const char* what, W4Problem& pr, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
@@ -89,21 +96,19 @@ int run_w4(const char* what, W4Problem& pr, void* workspace, size_t workspace_by
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.k_units = (a.K + kW4K - 1) / kW4K;
   a.n_tiles = (a.N + kW4Feats - 1) / kW4Feats;
-  a.steps = pr.group / 32;
-  a.scale_bytes = 256 * (kW4K / pr.group);
   a.split = workspace_bytes >= kW4WorkspaceBytes ? 1 : 0;
-  a.epoch = next_flag_epoch();
   a.ws = reinterpret_cast<WsHeader*>(ws);
-  a.tickets = reinterpret_cast<unsigned long long*>(ws + kW4TicketOffset);
-  a.slots = reinterpret_cast<float*>(ws + kW4SlotOffset);
+  a.slots = reinterpret_cast<float*>(ws + kWsHeaderBytes);
   a.timeout_ns = wait_timeout_ns();
-  // Column tiles of 8 rows: all rows of a dense product (up to 64), twice the mean of
-  // a group's.
+  // Rows that a tile takes: all of a dense product (up to 64), twice the mean of a group's.
   const long long rows = a.offsets ? 2 * (((long long)a.M + a.G - 1) / a.G) : a.M;
-  if (rows <= 8) return launch_w4<1>(pr, dev, stream);
-  if (rows <= 16) return launch_w4<2>(pr, dev, stream);
-  if (rows <= 32) return launch_w4<4>(pr, dev, stream);
-  return launch_w4<8>(pr, dev, stream);
+  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
+  const long long units = (((long long)a.M + 8 * nt - 1) / (8 * nt) + (a.offsets ? a.G : 0)) * a.n_tiles;
+  if (units > 0x7fffffffll / a.k_units) return reject(ST_UNSUPPORTED, "%s: G=%d M=%d N=%d K=%d: too large", what, a.G, a.M, a.N, a.K);
+  if (nt == 1) return launch_w4_group<1>(pr, dev, stream);
+  if (nt == 2) return launch_w4_group<2>(pr, dev, stream);
+  if (nt == 4) return launch_w4_group<4>(pr, dev, stream);
+  return launch_w4_group<8>(pr, dev, stream);
 }
 
 }  // namespace

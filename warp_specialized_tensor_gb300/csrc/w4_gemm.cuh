@@ -4,26 +4,29 @@
 //   C[m][n] = epi( sum_b s[b][n] sum_{k in b} A[m][k] (w[n][k] - 8) (+ bias[n]) )
 //
 // A decoding step's product reads its weights once for a few rows, so the weights'
-// bytes bound it, and what has to be cheap is turning a byte of them into operands:
-// about 90 instructions for the 1 KB that a warp takes at a time, against the 170
-// clocks that HBM needs for four such (one for each scheduler).  So:
-//  - A unit is 128 features x 128 k.  A TMA producer warp keeps a ring of units in
-//    flight (weights as they lie in memory, the rows' 128 k, the scales).
-//  - Sixteen warps in two sets (eight for 64 tokens) take the units in turn; a warp multiplies 16
-//    features with mma.sync (features as the instruction's 16 rows, 8 tokens per
-//    column tile).  tcgen05 wants 128 x 64-byte operand tiles in shared memory or
-//    tensor memory: the unpacked weights would have to be stored there and read
-//    again, four times the bytes of the packed ones, while a register fragment is
-//    used where it was made.
-//  - The sum over k may be taken in any order, so a fragment's k are the eight of one
-//    32-bit word of weights: (w >> 4i) & 0x000f000f are the numbers k = i and k = i + 4
-//    of it.  With 0x4300 over each they are the bf16 128 + w; minus 136, exact.  The
-//    rows' eight values are paired the same way by byte permutes.
+// bytes bound it: an SM's share of HBM brings a unit (128 features x 128 k, 8 KB) in 344
+// clocks, and in that time its 16,384 numbers have to be unpacked and multiplied.
+//  - The sum over k may be taken in any order: (w >> 4i) & 0x000f000f are the numbers i
+//    and i + 4 of a 32-bit word's eight; with 0x4300 over each they are the bf16 128 + w,
+//    minus 136 exact: 11 instructions a word, 704 of the 1,376 that four schedulers
+//    issue in 344 clocks.
+//  - mma.sync takes them from the registers where they were unpacked: a warp has 32
+//    features (two tiles of 16) and all the rows, 8 to a column tile.  (tcgen05 was built
+//    and measured: unpacked numbers go to tensor memory at 174 bytes a clock, a product
+//    of 16 k takes 45 clocks however few rows it has and 100 while other warps unpack
+//    and store: 800 clocks a unit.  At 64 rows the two would meet.)
+//  - The rows' values are put in the weights' order by warps of their own, where the
+//    instruction's fragments are one 16-byte load.
 //  - Accumulators of one group are scaled and added in fp32 when the group ends.
 //  - The tiles' units stand in one line and each CTA takes an equal share of it
 //    (work_split.cuh).  A tile that is cut is added up by the CTA that finishes it
 //    last, from fp32 partial sums in the workspace, in ascending order of k: the
 //    result does not depend on which CTA that is.
+//
+// Roles: sets of four multiplying warps, which take the units in turn (4 sets; 2 where
+// the rows' accumulators need the registers), then a warp that loads the weights, as they
+// lie in memory, one that loads the rows' 128 k and the scales (issuing a unit's four
+// copies takes a thread 340 clocks), and two that order the rows.
 #pragma once
 
 #include "work_split.cuh"
@@ -31,42 +34,43 @@
 
 namespace wst {
 
-constexpr int kW4Feats = 128;     // features of a tile: 8 warps x 16
-constexpr int kW4K = 128;         // k of a unit
+constexpr int kW4Feats = 128;  // features of a tile: 4 warps x 32
+constexpr int kW4K = 128;      // k of a unit
 constexpr int kW4WBytes = kW4Feats * kW4K / 2;
-constexpr int kW4SBytes = 1024;   // scales: 128 features x up to 4 groups, bf16
+constexpr int kW4SBytes = 1024;  // scales: 128 features x up to 4 groups, bf16
 constexpr int kW4MaxCtas = 160;
-constexpr int kW4Pitch = kW4Feats + 4;  // floats of a token's row of the output tile
+constexpr int kW4Pitch = kW4Feats + 4;  // floats of a row of a set's sums
 
-template <int NT>
+template <int NT>  // column tiles of 8 rows: 1, 2, 4, 8
 struct W4Cfg {
-  // Sets of 8 warps that take the units in turn.  (64 tokens' accumulators leave
-  // no room for the registers of a second set.)
-  static constexpr int kSets = NT == 8 ? 1 : 2;
-  static constexpr int kWarps = 8 * kSets;
-  static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kTokens = 8 * NT;
-  static constexpr int kABytes = kTokens * kW4K * 2;  // four boxes of 32 k
-  static constexpr int kStage = kW4WBytes + kABytes + kW4SBytes;
-  static constexpr int kOut = kTokens * kW4Pitch * 4;
-  static constexpr int kStages = (232448 - 1024 - 1024 - kOut) / kStage > 16 ? 16 : (232448 - 1024 - 1024 - kOut) / kStage;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kOut + 1024;
-  static_assert(kStage % 1024 == 0 && kStages >= 4 && kSmem <= 232448, "shared memory");
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kSets = NT <= 2 ? 4 : 2;
+  static constexpr int kMulThreads = 128 * kSets;
+  static constexpr int kThreads = kMulThreads + 128;
+  static constexpr int kABytes = kRows * kW4K * 2;
+  static constexpr int kStage = kW4WBytes + 2 * kABytes + kW4SBytes;  // A as loaded and as ordered
+  static constexpr int kRegions = kSets / 2;  // of sums: two sets share one
+  static constexpr int kSums = kRegions * kRows * kW4Pitch * 4;
+  static constexpr int kFit = (232448 - 2048 - kSums) / kStage;
+  // A stage belongs to one set (and one ordering warp): a barrier's parity tells two
+  // phases apart, and only who has waited for a phase may wait for the next.
+  static constexpr int kStages = kFit >= 12 ? 12 : kFit >= 8 ? 8 : 4;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kSums + 1024;
+  static_assert(kStage % 1024 == 0 && kSmem <= 232448 && kStages <= kFit && kStages % kSets == 0, "shared memory");
 };
 
-// Workspace after the header: tickets[kW4MaxCtas] (8 bytes each), then two slots of
-// partial sums per CTA: [64 tokens][128 features] fp32 each.
-constexpr size_t kW4TicketOffset = kWsHeaderBytes;
-constexpr size_t kW4SlotOffset = 256 * ((kW4TicketOffset + kW4MaxCtas * 8 + 255) / 256);
+// Workspace after the header: two slots of partial sums per CTA, [64 rows][128
+// features] fp32 each.  The pieces of the cut tiles are counted in the header's spare
+// words, which hold zeros between calls: a byte for each CTA (the tile that begins in
+// its share and ends in another's).
 constexpr size_t kW4SlotFloats = 64 * kW4Feats;
-constexpr size_t kW4WorkspaceBytes = kW4SlotOffset + 2 * (size_t)kW4MaxCtas * kW4SlotFloats * 4;
+constexpr size_t kW4WorkspaceBytes = kWsHeaderBytes + 2 * (size_t)kW4MaxCtas * kW4SlotFloats * 4;
+static_assert(kW4MaxCtas <= (int)sizeof(WsHeader::pad) && kW4MaxCtas < 256, "a byte for each CTA, counting up to all of them");
 
 struct W4Args {
   int G, M, N, K;
   int k_units;        // ceil(K / 128)
   int n_tiles;        // ceil(N / 128)
-  int steps;          // 32-k blocks per group: 1, 2 or 4
-  int scale_bytes;    // of a unit: 256 * groups of it
   const int* offsets; // NULL: one group of M rows
   const __nv_bfloat16* bias;
   long long stride_bias;
@@ -74,10 +78,8 @@ struct W4Args {
   long long ldc;
   int c_f32;
   int epi;
-  int split;          // the workspace holds tickets and slots
-  uint32_t epoch;     // this call's value in the tickets
+  int split;          // the workspace holds the slots
   WsHeader* ws;
-  unsigned long long* tickets;
   float* slots;
   unsigned long long timeout_ns;
 };
@@ -93,36 +95,34 @@ __device__ __forceinline__ void w4_rows(const W4Args& p, int g, int& a, int& b) 
 }
 
 static __device__ __noinline__ void w4_check_offsets(const W4Args& p) {
-  bool bad = __ldg(p.offsets) != 0;
-  int prev = 0;
-  for (int g = 0; g <= p.G && !bad; ++g) {
+  // (the threads of one CTA, an offset each)
+  for (int g = (int)threadIdx.x; g <= p.G; g += (int)blockDim.x) {
     const int v = __ldg(p.offsets + g);
-    if (v < prev || v > p.M) bad = true;
-    prev = v;
+    if (v < (g ? __ldg(p.offsets + g - 1) : 0) || v > p.M || (g == 0 && v != 0)) latch_error(p.ws, kErrBadOffsets, 3);
   }
-  if (bad) latch_error(p.ws, kErrBadOffsets, 3);
 }
 
 // A CTA's share, one fragment (consecutive units of one tile) after another.
 template <int NT>
 struct W4Walker {
-  long long x, hi;        // next unit, end of the share
+  int x, hi;          // next unit, end of the share
   int g;
-  long long base, count;  // group g's first unit and how many it has
-  int a, b;               // its rows
+  int base, count;    // group g's first unit and how many it has
+  int a, b;           // its rows
+  bool fresh;         // the tile of unit x has still to be found
   // the fragment
-  long long item;         // its tile's first unit
-  int tile, row0, rows, ua, ub;
+  int item;           // its tile's first unit
+  int tile, chunk, row0, rows, ua, ub;
 
-  __device__ __forceinline__ static long long units(const W4Args& p, int a, int b) {
-    return (long long)((b - a + 8 * NT - 1) / (8 * NT)) * p.n_tiles * p.k_units;
+  __device__ __forceinline__ static int units(const W4Args& p, int a, int b) {
+    return (b - a + 8 * NT - 1) / (8 * NT) * p.n_tiles * p.k_units;
   }
-  __device__ __forceinline__ void init(const W4Args& p, long long lo, long long hi_, int g_, long long base_) {
+  __device__ __forceinline__ void init(const W4Args& p, int lo, int hi_, int g_, int base_) {
     x = lo;
     hi = hi_;
     g = g_;
     base = base_;
-    count = 0;
+    fresh = true;
     if (x < hi) {
       w4_rows(p, g, a, b);
       count = units(p, a, b);
@@ -130,21 +130,33 @@ struct W4Walker {
   }
   __device__ __forceinline__ bool next(const W4Args& p) {
     if (x >= hi) return false;
+    bool moved = false;
     while (x >= base + count) {
       base += count;
       ++g;  // (x < W: a group holds it)
       w4_rows(p, g, a, b);
       count = units(p, a, b);
+      moved = true;
     }
     // tiles of features, and inside one the row chunks: those read the same weights
     const int chunks = (b - a + 8 * NT - 1) / (8 * NT);
-    const long long r = x - base;
-    const long long t = r / p.k_units;
-    ua = (int)(r - t * p.k_units);
-    ub = (int)min((long long)p.k_units, ua + (hi - x));
+    if (fresh) {
+      const int t = (x - base) / p.k_units;
+      ua = x - base - t * p.k_units;
+      tile = t / chunks;
+      chunk = t - tile * chunks;
+      fresh = false;
+    } else {  // the tile before this one has ended at x
+      ua = 0;
+      if (moved) tile = chunk = 0;
+      else if (++chunk == chunks) {
+        chunk = 0;
+        ++tile;
+      }
+    }
+    ub = min(p.k_units, ua + (hi - x));
     item = x - ua;
-    tile = (int)(t / chunks);
-    row0 = a + (int)(t - (long long)tile * chunks) * (8 * NT);
+    row0 = a + chunk * (8 * NT);
     rows = min(8 * NT, b - row0);
     x += ub - ua;
     return true;
@@ -157,21 +169,40 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t w, int i) {
   asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0x43084308u));  // 136
   return v;
 }
-__device__ __forceinline__ void w4_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t w4_lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+// d = a b (+ c): 16 features x 16 k, 16 k x 8 rows.
+__device__ __forceinline__ void w4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ uint4 w4_lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
+}
+// The 4 / GROUPS words of group q that a lane unpacks, of the row of weights at `row`
+// (its 16-byte words in the order that `swz` gives): lane t of four has the t-th part of
+// each group.
+template <int GROUPS>
+__device__ __forceinline__ void w4_words(uint32_t row, uint32_t swz, uint32_t t, uint32_t (&w)[4]) {
+  if constexpr (GROUPS == 1) {
+    const uint4 v = w4_lds128(row + ((t ^ swz) << 4));
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else if constexpr (GROUPS == 2) {
+#pragma unroll
+    for (uint32_t h = 0; h < 2; ++h)
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                   : "=r"(w[2 * h]), "=r"(w[2 * h + 1])
+                   : "r"(row + (((2 * h + (t >> 1)) ^ swz) << 4) + 8 * (t & 1))
+                   : "memory");
+  } else {
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q)
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[q]) : "r"(row + ((q ^ swz) << 4) + 4 * t) : "memory");
+  }
 }
 __device__ __forceinline__ float w4_lds_bf16(uint32_t a) {
   unsigned short v;
@@ -190,244 +221,356 @@ __device__ __forceinline__ float w4_activate(float v, int epi) {
   return v;
 }
 
-// Writes features f, f + 1 of token `tok` of a finished tile.
-__device__ __forceinline__ void w4_store(const W4Args& p, int g, int tile, int row, int f, float v0, float v1) {
-  const int n = tile * kW4Feats + f;
-  if (n >= p.N) return;
-  const bool two = n + 1 < p.N;
-  if (p.epi) {
-    const __nv_bfloat16* bias = p.bias + g * p.stride_bias + n;
-    v0 = w4_activate(v0 + __bfloat162float(bias[0]), p.epi);
-    if (two) v1 = w4_activate(v1 + __bfloat162float(bias[1]), p.epi);
+// Stores features f, f + 1 of a finished tile, row by row.
+struct W4Out {
+  int n;        // the first feature
+  int count;    // how many of the two there are
+  float b0, b1;
+  __device__ __forceinline__ W4Out(const W4Args& p, int g, int tile, int f) {
+    n = tile * kW4Feats + f;
+    count = min(max(p.N - n, 0), 2);
+    b0 = b1 = 0.0f;
+    if (p.epi) {
+      const __nv_bfloat16* bias = p.bias + g * p.stride_bias + n;
+      if (count > 0) b0 = __bfloat162float(bias[0]);
+      if (count > 1) b1 = __bfloat162float(bias[1]);
+    }
   }
-  const long long at = (long long)row * p.ldc + n;
-  if (p.c_f32) {
-    float* c = static_cast<float*>(p.C) + at;
-    if (two) *reinterpret_cast<float2*>(c) = make_float2(v0, v1);
-    else *c = v0;
-  } else {
-    __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.C) + at;
-    if (two) *reinterpret_cast<uint32_t*>(c) = pack_bf16x2(v0, v1);
-    else *c = __float2bfloat16_rn(v0);
+  __device__ __forceinline__ void store(const W4Args& p, int row, float2 v) const {
+    if (p.epi) {
+      v.x = w4_activate(v.x + b0, p.epi);
+      v.y = w4_activate(v.y + b1, p.epi);
+    }
+    const long long at = (long long)row * p.ldc + n;
+    if (p.c_f32) {
+      float* c = static_cast<float*>(p.C) + at;
+      if (count == 2) *reinterpret_cast<float2*>(c) = v;
+      else if (count == 1) *c = v.x;
+    } else {
+      __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.C) + at;
+      if (count == 2) *reinterpret_cast<uint32_t*>(c) = pack_bf16x2(v.x, v.y);
+      else if (count == 1) *c = __float2bfloat16_rn(v.x);
+    }
   }
+};
+
+// Counts one finished piece of the cut tile that begins in CTA c's share; true for the
+// last of `pieces`, which leaves zero.
+__device__ __forceinline__ bool w4_last_piece(WsHeader* ws, int c, int pieces) {
+  uint32_t* word = ws->pad + (c >> 2);
+  const int shift = 8 * (c & 3);
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(word), "r"(1u << shift) : "memory");
+  if ((int)((old >> shift) & 255u) + 1 != pieces) return false;
+  atomicSub(word, (uint32_t)pieces << shift);
+  return true;
 }
 
-// Counts one finished piece of a cut tile; true for the last of `pieces`.  A ticket
-// holds this call's value and the count: whatever an earlier operation left there
-// counts as zero, and the last piece leaves zero.
-__device__ __forceinline__ bool w4_last_piece(unsigned long long* ticket, uint32_t epoch, int pieces) {
-  unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(ticket);
-  while (true) {
-    const uint32_t n = (uint32_t)(old >> 32) == epoch ? (uint32_t)old : 0u;
-    const unsigned long long want = (int)n + 1 == pieces ? 0ull : ((unsigned long long)epoch << 32) | (n + 1u);
-    const unsigned long long got = atomicCAS(ticket, old, want);
-    if (got == old) return want == 0ull;
-    old = got;  // another piece was counted: at most `pieces` times
-  }
-}
+// What is left of a cut tile's piece when its sums are in the slot.
+struct W4Piece {
+  int c0, c1;  // the tile's first and last CTA
+  int g, tile, row0, rows;
+};
 
 // tmW {ceil(K/2) bytes, N, G}, boxes of 64 bytes x 128 features, 64-byte swizzle;
-// tmA {K, M}, boxes of 32 k x 8 NT rows, 64-byte swizzle; tmS {N, ceil(K/group), G},
-// boxes of 128 features x the groups of a unit.
-template <int NT>
+// tmA {K, M}, boxes of 128 k x 8 NT rows; tmS {N, ceil(K/group), G}, boxes of 128
+// features x GROUPS.
+template <int NT, int GROUPS>
 __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
     k_w4_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
               const __grid_constant__ CUtensorMap tmS, const W4Args p) {
   using Cfg = W4Cfg<NT>;
+  constexpr int ST = Cfg::kStages, SETS = Cfg::kSets, MT = Cfg::kMulThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* tile_out = reinterpret_cast<float*>(smem + Cfg::kStages * Cfg::kStage);  // [token][kW4Pitch]
-  __shared__ uint64_t bars[2 * 16];
-  __shared__ long long scratch[33], found[2];
-  __shared__ uint32_t abort_word, is_last;
+  const uint32_t ring = smem_addr(smem);
+  float* sums = reinterpret_cast<float*>(smem + ST * Cfg::kStage);  // [set][row][kW4Pitch]
+  __shared__ uint64_t bars[3 * 12];
+  __shared__ long long scratch[32], found[2];
+  __shared__ uint32_t abort_word, is_last[2];
   volatile uint32_t* abort_flag = &abort_word;
   const int warp = (int)threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
-  const uint32_t bar0 = smem_addr(bars);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (16 + s); };
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < Cfg::kStages; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 8);
+  // a_full (the rows are there), full (weights, scales and ordered rows are), empty
+  const uint32_t a_full = smem_addr(bars), full = a_full + 8 * ST, empty = full + 8 * ST;
+  if (warp == 4 * SETS && lane == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(a_full + 8 * i, 1);
+      mbar_init(full + 8 * i, 3);
+      mbar_init(empty + 8 * i, 4);
     }
     *abort_flag = 0u;
     found[0] = found[1] = 0;
     fence_mbar_init();
+  }
+  if (warp == 4 * SETS + 1 && lane == 0) {
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmS);
   }
-  // this CTA's share (block_total and block_locate end with barriers)
-  auto count = [&](int g) -> long long {
-    int a, b;
-    w4_rows(p, g, a, b);
-    return W4Walker<NT>::units(p, a, b);
-  };
-  const long long W = block_total<Cfg::kThreads>(p.G, count, scratch);
-  // whole tiles where the workspace holds no partial sums
-  const long long grain = p.split ? 1 : p.k_units;
-  const Share share{W / grain, (int)max(1ll, min((long long)gridDim.x, W / (2 * grain)))};
-  long long lo = 0, hi = 0;
-  if ((int)blockIdx.x < share.G) {
+  // this CTA's share; whole tiles where the workspace holds no partial sums
+  const int grain = p.split ? 1 : p.k_units;
+  int W, lo = 0, hi = 0;
+  if (p.offsets) {
+    BlockCount<long long, Cfg::kThreads> counted;
+    auto count = [&](int g) -> long long {
+      int a, b;
+      w4_rows(p, g, a, b);
+      return W4Walker<NT>::units(p, a, b);
+    };
+    const long long all = counted.total(p.G, count, scratch);
+    W = all > 0x7fffffff ? 0 : (int)all;  // (only offsets that go back and forth count so many: they are refused)
+    const Share<int> s(W / grain, max(1, min((int)gridDim.x, W / (2 * grain))));
+    if ((int)blockIdx.x < s.G) {
+      lo = s.lo((int)blockIdx.x) * grain;
+      hi = s.lo((int)blockIdx.x + 1) * grain;
+    }
+    if (lo < hi) counted.locate(p.G, count, (long long)lo, scratch, found);
+    if (blockIdx.x == 0) w4_check_offsets(p);
+  } else {
+    W = W4Walker<NT>::units(p, 0, p.M);
+  }
+  const Share<int> share(W / grain, max(1, min((int)gridDim.x, W / (2 * grain))));
+  if (!p.offsets && (int)blockIdx.x < share.G) {
     lo = share.lo((int)blockIdx.x) * grain;
     hi = share.lo((int)blockIdx.x + 1) * grain;
   }
-  if (lo < hi) block_locate<Cfg::kThreads>(p.G, count, lo, scratch, found);
-  __syncthreads();
+  // (the warp that loads the weights set the barriers up itself: without groups to find
+  // it need not wait for the others)
+  if (warp == 4 * SETS && !p.offsets) {
+    __syncwarp();
+    asm volatile("barrier.arrive 2, %0;" ::"n"(Cfg::kThreads) : "memory");
+  } else {
+    asm volatile("barrier.sync 2, %0;" ::"n"(Cfg::kThreads) : "memory");
+  }
   const Guard guard{p.ws, abort_flag, p.timeout_ns};
   W4Walker<NT> w;
-  w.init(p, lo, hi, (int)found[0], found[1]);
+  w.init(p, lo, hi, p.offsets ? (int)found[0] : 0, p.offsets ? (int)found[1] : 0);
 
-  if (warp == Cfg::kWarps) {
-    // ------------------------------------------------------------------ producer
+  if (warp == 4 * SETS || warp == 4 * SETS + 1) {
+    // ------------------------------------------------------------------ loads
     if (lane == 0) {
+      const bool weights = warp == 4 * SETS;
       int s = 0;
       uint32_t ph = 1;
       bool ok = true;
-      const uint32_t bytes = (uint32_t)(kW4WBytes + Cfg::kABytes + p.scale_bytes);
-      const int groups = p.scale_bytes / 256;
       while (ok && w.next(p)) {
         for (int u = w.ua; u < w.ub; ++u) {
-          if (!wait_phase(guard, empty_bar(s), ph, (kRoleProducer << 16) | s)) {
+          if (!wait_phase(guard, empty + 8 * s, ph, (kRoleProducer << 16) | s)) {
             ok = false;
             break;
           }
-          const uint32_t at = smem_addr(smem + s * Cfg::kStage);
-          mbar_arrive_expect_tx(full_bar(s), bytes);
-          tma_load_3d(at, &tmW, full_bar(s), u * (kW4K / 2), w.tile * kW4Feats, w.g);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            tma_load_2d(at + kW4WBytes + q * (Cfg::kABytes / 4), &tmA, full_bar(s), u * kW4K + 32 * q, w.row0);
-          tma_load_3d(at + kW4WBytes + Cfg::kABytes, &tmS, full_bar(s), w.tile * kW4Feats, u * groups, w.g);
-          if (++s == Cfg::kStages) {
+          const uint32_t at = ring + s * Cfg::kStage;
+          if (weights) {
+            mbar_arrive_expect_tx(full + 8 * s, (uint32_t)kW4WBytes);
+            tma_load_3d(at, &tmW, full + 8 * s, u * (kW4K / 2), w.tile * kW4Feats, w.g);
+          } else {
+            mbar_arrive_expect_tx(a_full + 8 * s, (uint32_t)Cfg::kABytes);
+            tma_load_2d(at + kW4WBytes, &tmA, a_full + 8 * s, u * kW4K, w.row0);
+            mbar_arrive_expect_tx(full + 8 * s, (uint32_t)(256 * GROUPS));
+            tma_load_3d(at + kW4WBytes + 2 * Cfg::kABytes, &tmS, full + 8 * s, w.tile * kW4Feats, u * GROUPS, w.g);
+          }
+          if (++s == ST) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
-    } else if (lane == 1 && blockIdx.x == 0 && p.offsets) {
-      w4_check_offsets(p);
+    }
+  } else if (warp >= 4 * SETS + 2) {
+    // ------------------------------------------------------------------ the rows' order
+    // Eight k of a row (16 bytes) are one lane's fragments for the eight numbers of a
+    // word: 0 4 1 5 2 6 3 7, to the place of [word q][column tile][lane].
+    const int mine = warp & 1;
+    int s = 0;
+    uint32_t ph = 0;
+    const int total = hi - lo;
+    for (int u = 0; u < total; ++u) {
+      if ((s & 1) == mine) {
+        if (!warp_wait_phase(guard, a_full + 8 * s, ph, (kRoleEpilogue << 16) | 0x100 | s)) break;
+        (void)mbar_try_wait(a_full + 8 * s, ph);  // each lane sees the copies
+        const uint32_t from = ring + s * Cfg::kStage + kW4WBytes, to = from + Cfg::kABytes;
+        constexpr int BATCH = NT == 1 ? 4 : 8;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 4 * NT; i0 += BATCH) {
+          uint4 v[BATCH];
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) v[i] = w4_lds128(from + (lane + 32u * (uint32_t)(i0 + i)) * 16);
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const uint32_t c = lane + 32u * (uint32_t)(i0 + i);  // 16-byte word: row c / 16, k 8 (c % 16) ..
+            const uint32_t row = c >> 4, kc = c & 15u;
+            const uint32_t q = GROUPS == 1 ? kc & 3u : GROUPS == 2 ? (kc >> 3) * 2 + (kc & 1u) : kc >> 2;
+            const uint32_t t = GROUPS == 1 ? kc >> 2 : GROUPS == 2 ? (kc >> 1) & 3u : kc & 3u;
+            st_shared_v4(to + (((q * NT + (row >> 3)) * 32 + (row & 7u) * 4 + t) << 4), __byte_perm(v[i].x, v[i].z, 0x5410),
+                         __byte_perm(v[i].x, v[i].z, 0x7632), __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632));
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + 8 * s);
+      }
+      if (++s == ST) {
+        s = 0;
+        ph ^= 1u;
+      }
     }
   } else {
-    // ------------------------------------------------------------------ multiplying warps
-    const int set = warp >> 3;
-    const int f0 = (warp & 7) * 16;               // the warp's features of a tile
-    const int fr = f0 + (int)(lane >> 2), t = (int)(lane & 3);
-    const uint32_t swz = (uint32_t)((lane >> 3) & 3);  // (row >> 1) & 3 of every row that the lane reads
-    const uint32_t w_at = (uint32_t)(fr * 64 + t * 4);
-    const uint32_t a_at = (uint32_t)(kW4WBytes + (lane >> 2) * 64 + (((uint32_t)t ^ swz) << 4));
-    const uint32_t s_at = (uint32_t)(kW4WBytes + Cfg::kABytes + fr * 2);
-    int s = 0, turn = 0;
+    // ------------------------------------------------------------------ products
+    const int set = warp >> 2, f0 = (warp & 3) * 32;
+    const uint32_t g8 = lane >> 2, t = lane & 3;
+    const uint32_t swz = (g8 >> 1) & 3u;  // (row >> 1) & 3 of every row that the lane reads
+    const uint32_t w_at = (uint32_t)(f0 + (int)g8) * 64, a_at = (uint32_t)(kW4WBytes + Cfg::kABytes) + lane * 16;
+    const uint32_t s_at = (uint32_t)(kW4WBytes + 2 * Cfg::kABytes) + (uint32_t)(f0 + (int)g8) * 2;
+    int s = 0;
     uint32_t ph = 0;
     bool ok = true;
+    W4Piece piece[2];
+    int pieces = 0;
     while (w.next(p)) {
-      float acc[NT][4];
+      float acc[2][NT][4];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.0f;
       for (int u = w.ua; u < w.ub; ++u) {
         // (a wait that gave up: the barriers and tickets below still count this CTA)
-        if (turn == set && ok) ok = warp_wait_phase(guard, full_bar(s), ph, (kRoleMma << 16) | s);
-        if (turn == set && ok) {
-          const uint32_t at = smem_addr(smem + s * Cfg::kStage);
-          float part[NT][4];
+        const bool own = s % SETS == set;
+        if (own && ok) ok = warp_wait_phase(guard, full + 8 * s, ph, (kRoleMma << 16) | s);
+        if (own && ok) {
+          const uint32_t at = ring + s * Cfg::kStage;
+          uint32_t word[2][2][4];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            w4_words<GROUPS>(at + w_at + m * 1024, swz, t, word[m][0]);
+            w4_words<GROUPS>(at + w_at + m * 1024 + 512, swz, t, word[m][1]);
+          }
+          float part[2][NT][4];
+          constexpr float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint32_t wq = at + w_at + (((uint32_t)q ^ swz) << 4);
-            const uint32_t w0 = w4_lds32(wq), w1 = w4_lds32(wq + 8 * 64);
-            const uint32_t a0 = w4_pair(w0, 0), a1 = w4_pair(w1, 0), a2 = w4_pair(w0, 1), a3 = w4_pair(w1, 1);
-            const uint32_t a4 = w4_pair(w0, 2), a5 = w4_pair(w1, 2), a6 = w4_pair(w0, 3), a7 = w4_pair(w1, 3);
-            const bool first = p.steps == 1 || (p.steps == 2 ? (q & 1) == 0 : q == 0);
-            if (first) {
+            const bool first = q % (4 / GROUPS) == 0, last = (q + 1) % (4 / GROUPS) == 0;
+            uint32_t a[2][2][4];  // [tile][half of the word][fragment]
 #pragma unroll
-              for (int i = 0; i < NT; ++i) part[i][0] = part[i][1] = part[i][2] = part[i][3] = 0.0f;
-            }
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                a[m][j][0] = w4_pair(word[m][0][q], 2 * j);
+                a[m][j][1] = w4_pair(word[m][1][q], 2 * j);
+                a[m][j][2] = w4_pair(word[m][0][q], 2 * j + 1);
+                a[m][j][3] = w4_pair(word[m][1][q], 2 * j + 1);
+              }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-              const uint4 x = w4_lds128(at + a_at + (uint32_t)(q * (Cfg::kABytes / 4) + i * 512));
-              w4_mma(part[i], a0, a1, a2, a3, __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632));
-              w4_mma(part[i], a4, a5, a6, a7, __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-            }
-            const bool last = p.steps == 1 || (p.steps == 2 ? (q & 1) == 1 : q == 3);
-            if (last) {
-              const uint32_t sq = at + s_at + (uint32_t)((p.steps == 1 ? q : p.steps == 2 ? q >> 1 : 0) * 256);
-              const float s0 = w4_lds_bf16(sq), s1 = w4_lds_bf16(sq + 16);
+              const uint4 x = w4_lds128(at + a_at + (uint32_t)((q * NT + i) * 512));
 #pragma unroll
-              for (int i = 0; i < NT; ++i) {
-                acc[i][0] = fmaf(s0, part[i][0], acc[i][0]);
-                acc[i][1] = fmaf(s0, part[i][1], acc[i][1]);
-                acc[i][2] = fmaf(s1, part[i][2], acc[i][2]);
-                acc[i][3] = fmaf(s1, part[i][3], acc[i][3]);
+              for (int m = 0; m < 2; ++m) {
+                if (first) w4_mma(part[m][i], a[m][0], x.x, x.y, zero);
+                else w4_mma(part[m][i], a[m][0], x.x, x.y, part[m][i]);
+                w4_mma(part[m][i], a[m][1], x.z, x.w, part[m][i]);
+              }
+            }
+            if (last) {
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                const uint32_t sq = at + s_at + (uint32_t)(q / (4 / GROUPS) * 256 + m * 32);
+                const float s0 = w4_lds_bf16(sq), s1 = w4_lds_bf16(sq + 16);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                  acc[m][i][0] = fmaf(s0, part[m][i][0], acc[m][i][0]);
+                  acc[m][i][1] = fmaf(s0, part[m][i][1], acc[m][i][1]);
+                  acc[m][i][2] = fmaf(s1, part[m][i][2], acc[m][i][2]);
+                  acc[m][i][3] = fmaf(s1, part[m][i][3], acc[m][i][3]);
+                }
               }
             }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(empty_bar(s));
+          if (lane == 0) mbar_arrive(empty + 8 * s);
         }
-        if (++turn == Cfg::kSets) turn = 0;
-        if (++s == Cfg::kStages) {
+        if (++s == ST) {
           s = 0;
           ph ^= 1u;
         }
       }
-      // The sets' sums: the last one's into shared memory, set 0 adds its own.
-      float* mine = tile_out + (2 * t) * kW4Pitch + fr;
-      w4_sync<32 * Cfg::kWarps>();  // the tile before this one has been read
-      if (set == Cfg::kSets - 1) {
+      // The sets' sums through shared memory: the second half of the sets stores its
+      // own, the first half adds.
+      float* o = sums + (set % Cfg::kRegions * Cfg::kRows + 2 * (int)t) * kW4Pitch + f0 + (int)g8;
+      w4_sync<MT>();  // the tile before this one has been read
+      if (set >= Cfg::kRegions) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          float* o = mine + i * 8 * kW4Pitch;
-          o[0] = acc[i][0];
-          o[kW4Pitch] = acc[i][1];
-          o[8] = acc[i][2];
-          o[kW4Pitch + 8] = acc[i][3];
-        }
-      }
-      if constexpr (Cfg::kSets == 2) {
-        w4_sync<32 * Cfg::kWarps>();
-        if (set == 0) {
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            float* o = mine + i * 8 * kW4Pitch;
-            o[0] += acc[i][0];
-            o[kW4Pitch] += acc[i][1];
-            o[8] += acc[i][2];
-            o[kW4Pitch + 8] += acc[i][3];
-          }
-        }
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[(8 * i + (j & 1)) * kW4Pitch + 16 * m + 8 * (j >> 1)] = acc[m][i][j];
       }
-      w4_sync<32 * Cfg::kWarps>();
-      const int f = 2 * (int)(threadIdx.x & 63), tok0 = (int)threadIdx.x >> 6;  // two features, every eighth token
-      if (w.ub - w.ua == p.k_units) {
-        for (int tok = tok0; tok < w.rows; tok += Cfg::kWarps / 2) {
-          const float2 v = *reinterpret_cast<const float2*>(tile_out + tok * kW4Pitch + f);
-          w4_store(p, w.g, w.tile, w.row0 + tok, f, v.x, v.y);
+      w4_sync<MT>();
+      if (set < Cfg::kRegions) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[(8 * i + (j & 1)) * kW4Pitch + 16 * m + 8 * (j >> 1)] += acc[m][i][j];
+      }
+      w4_sync<MT>();
+      // (thread: two features, every MT / 64-th row)
+      const int f = 2 * (int)(threadIdx.x & 63);
+      const bool whole = w.ub - w.ua == p.k_units;
+      const int c0 = whole ? 0 : share.owner(w.item);
+      // A piece of a cut tile goes into this CTA's slot (the second one if the tile begins
+      // in its share); it is counted when the share is done.
+      float* slot = p.slots + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0)) * kW4SlotFloats + f;
+      const W4Out out(p, w.g, w.tile, f);
+#pragma unroll 4
+      for (int row = (int)threadIdx.x >> 6; row < w.rows; row += MT / 64) {
+        float2 v = *reinterpret_cast<const float2*>(sums + row * kW4Pitch + f);
+        if constexpr (Cfg::kRegions == 2) {
+          const float2 x = *reinterpret_cast<const float2*>(sums + (Cfg::kRows + row) * kW4Pitch + f);
+          v.x += x.x;
+          v.y += x.y;
         }
-      } else {
-        // A piece of a cut tile: into this CTA's slot (the second one if the tile
-        // begins in its share), then the last of the tile's CTAs adds them up.
-        const int c0 = share.owner(w.item), c1 = share.owner(w.item + p.k_units - 1);
-        float* slot = p.slots + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0)) * kW4SlotFloats;
-        for (int tok = tok0; tok < w.rows; tok += Cfg::kWarps / 2)
-          __stcg(reinterpret_cast<float2*>(slot + tok * kW4Feats + f), *reinterpret_cast<const float2*>(tile_out + tok * kW4Pitch + f));
-        w4_sync<32 * Cfg::kWarps>();
-        if (threadIdx.x == 0) {
-          __threadfence();  // (after the barrier: all the warps' stores)
-          is_last = w4_last_piece(p.tickets + c0, p.epoch, c1 - c0 + 1) ? 1u : 0u;
-          __threadfence();
-        }
-        w4_sync<32 * Cfg::kWarps>();
-        if (is_last) {
-          for (int tok = tok0; tok < w.rows; tok += Cfg::kWarps / 2) {
-            float v0 = 0.0f, v1 = 0.0f;
-            for (int c = c0; c <= c1; ++c) {
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(
-                  p.slots + (size_t)(2 * c + (c == c0 ? 1 : 0)) * kW4SlotFloats + tok * kW4Feats + f));
-              v0 += v.x;
-              v1 += v.y;
+        if (whole) out.store(p, w.row0 + row, v);
+        else __stcg(reinterpret_cast<float2*>(slot + row * kW4Feats), v);
+      }
+      if (!whole) piece[pieces++ & 1] = W4Piece{c0, share.owner(w.item + p.k_units - 1), w.g, w.tile, w.row0, w.rows};
+    }
+    if (pieces) {
+      w4_sync<MT>();
+      if (threadIdx.x < 2 && (int)threadIdx.x < pieces) {
+        __threadfence();  // (after the barrier: all the warps' stores)
+        const W4Piece& x = threadIdx.x ? piece[1] : piece[0];
+        is_last[threadIdx.x] = w4_last_piece(p.ws, x.c0, x.c1 - x.c0 + 1) ? 1u : 0u;
+        __threadfence();
+      }
+      w4_sync<MT>();
+#pragma unroll 1
+      for (int k = 0; k < pieces; ++k) {
+        if (!is_last[k]) continue;
+        const W4Piece x = piece[k];
+        const int f = 2 * (int)(threadIdx.x & 63);
+        const W4Out out(p, x.g, x.tile, f);
+        // four rows at a time (rows behind the last one lie in the slots too), all pieces
+        for (int row0 = (int)threadIdx.x >> 6; row0 < x.rows; row0 += 4 * (MT / 64)) {
+          float2 v[4];
+          const float* from = p.slots + (size_t)row0 * kW4Feats + f;
+          constexpr int STEP = MT / 64 * kW4Feats;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = row0 + i * (MT / 64) < 64 ? __ldcg(reinterpret_cast<const float2*>(from + (size_t)(2 * x.c0 + 1) * kW4SlotFloats + i * STEP)) : make_float2(0.0f, 0.0f);
+#pragma unroll 4
+          for (int c = x.c0 + 1; c <= x.c1; ++c) {
+            const float* at = from + (size_t)(2 * c) * kW4SlotFloats;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 y = row0 + i * (MT / 64) < 64 ? __ldcg(reinterpret_cast<const float2*>(at + i * STEP)) : make_float2(0.0f, 0.0f);
+              v[i].x += y.x;
+              v[i].y += y.y;
             }
-            w4_store(p, w.g, w.tile, w.row0 + tok, f, v0, v1);
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (row0 + i * (MT / 64) < x.rows) out.store(p, x.row0 + row0 + i * (MT / 64), v[i]);
         }
       }
     }
