@@ -32,7 +32,7 @@ int launch_w4(W4Problem& pr, const DeviceInfo& dev, cudaStream_t stream) {
     // a stride of a dimension of one is never used, but has to be one that a map takes
     const uint64_t dims[3] = {(uint64_t)(a.K + 1) / 2, (uint64_t)a.N, (uint64_t)a.G};
     const uint64_t str[2] = {(uint64_t)pr.ldw, (uint64_t)(a.G > 1 ? pr.strideW : pr.ldw)};
-    const uint32_t box[3] = {kW4K / 2, kW4Feats, 1};
+    const uint32_t box[3] = {64, kW4Feats, 1};
     if ((st = encode_map(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pr.W, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B))) return st;
   }
   {
@@ -44,7 +44,7 @@ int launch_w4(W4Problem& pr, const DeviceInfo& dev, cudaStream_t stream) {
   {
     const uint64_t dims[3] = {(uint64_t)a.N, (uint64_t)kb, (uint64_t)a.G};
     const uint64_t str[2] = {(uint64_t)pr.lds * 2, (uint64_t)(a.G > 1 ? pr.strideS : pr.lds) * 2};
-    const uint32_t box[3] = {kW4Feats, GROUPS, 1};
+    const uint32_t box[3] = {kW4Feats, 2 * GROUPS, 1};
     if ((st = encode_map(&tmS, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, pr.scales, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE))) return st;
   }
   auto kern = k_w4_gemm<NT, GROUPS>;
@@ -95,6 +95,8 @@ int run_w4(const char* what, W4Problem& pr, void* workspace, size_t workspace_by
   if ((st = current_device_info(&dev))) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.k_units = (a.K + kW4K - 1) / kW4K;
+  while ((1ll << a.k_shift) < a.k_units) ++a.k_shift;
+  a.k_mul = (uint32_t)(((1ull << 32) * ((1ull << a.k_shift) - (uint64_t)a.k_units)) / (uint64_t)a.k_units + 1);
   a.n_tiles = (a.N + kW4Feats - 1) / kW4Feats;
   a.split = workspace_bytes >= kW4WorkspaceBytes ? 1 : 0;
   a.ws = reinterpret_cast<WsHeader*>(ws);

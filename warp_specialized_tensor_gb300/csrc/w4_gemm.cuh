@@ -4,18 +4,18 @@
 //   C[m][n] = epi( sum_b s[b][n] sum_{k in b} A[m][k] (w[n][k] - 8) (+ bias[n]) )
 //
 // A decoding step's product reads its weights once for a few rows, so the weights'
-// bytes bound it: an SM's share of HBM brings a unit (128 features x 128 k, 8 KB) in 344
-// clocks, and in that time its 16,384 numbers have to be unpacked and multiplied.
-//  - The sum over k may be taken in any order: (w >> 4i) & 0x000f000f are the numbers i
-//    and i + 4 of a 32-bit word's eight; with 0x4300 over each they are the bf16 128 + w,
-//    minus 136 exact: 11 instructions a word, 704 of the 1,376 that four schedulers
-//    issue in 344 clocks.
+// bytes bound it: an SM's share of HBM brings a unit (128 features x 256 k, 16 KB) in 690
+// clocks, and in that time its 32,768 numbers have to be unpacked and multiplied.
+//  - The sum over k may be taken in any order, so a fragment's pairs are the numbers i
+//    and i + 4 of a 32-bit word's eight, which a mask and one bf16 multiply-add unpack
+//    (w4_pair): 9 instructions a word, five of them on the integer pipe, which takes one
+//    every two clocks and bounds the rest (11 with shifts and 128 + w: 7 there).
 //  - mma.sync takes them from the registers where they were unpacked: a warp has 32
 //    features (two tiles of 16) and all the rows, 8 to a column tile.  (tcgen05 was built
 //    and measured: unpacked numbers go to tensor memory at 174 bytes a clock, a product
 //    of 16 k takes 45 clocks however few rows it has and 100 while other warps unpack
-//    and store: 800 clocks a unit.  At 64 rows the two would meet.)
-//  - The rows' values are put in the weights' order by warps of their own, where the
+//    and store: 1,600 clocks a unit.  At 64 rows the two would meet.)
+//  - The rows' values are put in the weights' order by a warp of its own, where the
 //    instruction's fragments are one 16-byte load.
 //  - Accumulators of one group are scaled and added in fp32 when the group ends.
 //  - The tiles' units stand in one line and each CTA takes an equal share of it
@@ -25,8 +25,9 @@
 //
 // Roles: sets of four multiplying warps, which take the units in turn (4 sets; 2 where
 // the rows' accumulators need the registers), then a warp that loads the weights, as they
-// lie in memory, one that loads the rows' 128 k and the scales (issuing a unit's four
-// copies takes a thread 340 clocks), and two that order the rows.
+// lie in memory, one that loads the rows' k and the scales (a copy and its barrier take
+// the issuing thread about 200 clocks), one that orders the rows, and one that adds the
+// sets' sums of a tile and stores it while they multiply the next.
 #pragma once
 
 #include "work_split.cuh"
@@ -35,9 +36,9 @@
 namespace wst {
 
 constexpr int kW4Feats = 128;  // features of a tile: 4 warps x 32
-constexpr int kW4K = 128;      // k of a unit
+constexpr int kW4K = 256;      // k of a unit: two halves of 128
 constexpr int kW4WBytes = kW4Feats * kW4K / 2;
-constexpr int kW4SBytes = 1024;  // scales: 128 features x up to 4 groups, bf16
+constexpr int kW4SBytes = 2048;  // scales: 128 features x up to 8 groups, bf16
 constexpr int kW4MaxCtas = 160;
 constexpr int kW4Pitch = kW4Feats + 4;  // floats of a row of a set's sums
 
@@ -48,15 +49,15 @@ struct W4Cfg {
   static constexpr int kMulThreads = 128 * kSets;
   static constexpr int kThreads = kMulThreads + 128;
   static constexpr int kABytes = kRows * kW4K * 2;
-  static constexpr int kStage = kW4WBytes + 2 * kABytes + kW4SBytes;  // A as loaded and as ordered
-  static constexpr int kRegions = kSets / 2;  // of sums: two sets share one
-  static constexpr int kSums = kRegions * kRows * kW4Pitch * 4;
+  static constexpr int kStage = kW4WBytes + kABytes + kW4SBytes;
+  static constexpr int kBufs = NT == 1 ? 2 : 1;  // of the sets' sums
+  static constexpr int kSums = kBufs * kSets * kRows * kW4Pitch * 4;
   static constexpr int kFit = (232448 - 2048 - kSums) / kStage;
-  // A stage belongs to one set (and one ordering warp): a barrier's parity tells two
-  // phases apart, and only who has waited for a phase may wait for the next.
-  static constexpr int kStages = kFit >= 12 ? 12 : kFit >= 8 ? 8 : 4;
+  // A stage belongs to one set: a barrier's parity tells two phases apart, and only who
+  // has waited for a phase may wait for the next.
+  static constexpr int kStages = kFit / kSets * kSets > 8 ? 8 : kFit / kSets * kSets;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kSums + 1024;
-  static_assert(kStage % 1024 == 0 && kSmem <= 232448 && kStages <= kFit && kStages % kSets == 0, "shared memory");
+  static_assert(kStage % 1024 == 0 && kSmem <= 232448 && kStages >= kSets, "shared memory");
 };
 
 // Workspace after the header: two slots of partial sums per CTA, [64 rows][128
@@ -69,7 +70,8 @@ static_assert(kW4MaxCtas <= (int)sizeof(WsHeader::pad) && kW4MaxCtas < 256, "a b
 
 struct W4Args {
   int G, M, N, K;
-  int k_units;        // ceil(K / 128)
+  int k_units;        // ceil(K / 256)
+  uint32_t k_mul, k_shift;  // x / k_units = (umulhi(x, k_mul) + x) >> k_shift for x < 2^31
   int n_tiles;        // ceil(N / 128)
   const int* offsets; // NULL: one group of M rows
   const __nv_bfloat16* bias;
@@ -141,9 +143,9 @@ struct W4Walker {
     // tiles of features, and inside one the row chunks: those read the same weights
     const int chunks = (b - a + 8 * NT - 1) / (8 * NT);
     if (fresh) {
-      const int t = (x - base) / p.k_units;
+      const int t = (int)((__umulhi((uint32_t)(x - base), p.k_mul) + (uint32_t)(x - base)) >> p.k_shift);
       ua = x - base - t * p.k_units;
-      tile = t / chunks;
+      tile = chunks == 1 ? t : t / chunks;
       chunk = t - tile * chunks;
       fresh = false;
     } else {  // the tile before this one has ended at x
@@ -163,10 +165,14 @@ struct W4Walker {
   }
 };
 
-// Two 4-bit numbers (bits 4i.. and 16 + 4i.. of w) minus 8, as bf16.
+// The numbers i and i + 4 of a word's eight, minus 8, in 64ths, as bf16.  Four bits at
+// the bottom of a bf16 read n 2^-133, four above them n 2^-129 (below 8 a subnormal, from
+// 8 on the first normals: the step is the same), so a mask and one multiplication and
+// addition do it, exact: n 2^-133 2^127 - 8/64, n 2^-129 2^123 - 8/64.
 __device__ __forceinline__ uint32_t w4_pair(uint32_t w, int i) {
-  uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;  // 128 + w
-  asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0x43084308u));  // 136
+  const uint32_t x = i < 2 ? w : w >> 8;
+  uint32_t v = x & (i & 1 ? 0x00f000f0u : 0x000f000fu);
+  asm("fma.rn.bf16x2 %0, %0, %1, %2;" : "+r"(v) : "r"(i & 1 ? 0x7d007d00u : 0x7f007f00u), "r"(0xbe00be00u));
   return v;
 }
 // d = a b (+ c): 16 features x 16 k, 16 k x 8 rows.
@@ -180,9 +186,9 @@ __device__ __forceinline__ uint4 w4_lds128(uint32_t a) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
-// The 4 / GROUPS words of group q that a lane unpacks, of the row of weights at `row`
-// (its 16-byte words in the order that `swz` gives): lane t of four has the t-th part of
-// each group.
+// The four words that a lane unpacks of 128 k of the row of weights at `row` (its
+// 16-byte words in the order that `swz` gives), where they hold GROUPS groups: lane t of
+// four has the t-th part of each group.
 template <int GROUPS>
 __device__ __forceinline__ void w4_words(uint32_t row, uint32_t swz, uint32_t t, uint32_t (&w)[4]) {
   if constexpr (GROUPS == 1) {
@@ -209,12 +215,6 @@ __device__ __forceinline__ float w4_lds_bf16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
   return __uint_as_float((uint32_t)v << 16);
 }
-// A barrier of the multiplying warps.
-template <int THREADS>
-__device__ __forceinline__ void w4_sync() {
-  asm volatile("barrier.sync 1, %0;" ::"n"(THREADS) : "memory");
-}
-
 __device__ __forceinline__ float w4_activate(float v, int epi) {
   if (epi == 2) return v / (1.0f + expf(-v));
   if (epi == 3) return v * normcdff(v);
@@ -273,31 +273,38 @@ struct W4Piece {
 };
 
 // tmW {ceil(K/2) bytes, N, G}, boxes of 64 bytes x 128 features, 64-byte swizzle;
-// tmA {K, M}, boxes of 128 k x 8 NT rows; tmS {N, ceil(K/group), G}, boxes of 128
-// features x GROUPS.
+// tmA {K, M}, boxes of 256 k x 8 NT rows; tmS {N, ceil(K/group), G}, boxes of 128
+// features x 2 GROUPS (GROUPS: the groups of 128 k).
 template <int NT, int GROUPS>
 __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
     k_w4_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
               const __grid_constant__ CUtensorMap tmS, const W4Args p) {
   using Cfg = W4Cfg<NT>;
-  constexpr int ST = Cfg::kStages, SETS = Cfg::kSets, MT = Cfg::kMulThreads;
+  constexpr int ST = Cfg::kStages, SETS = Cfg::kSets;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t ring = smem_addr(smem);
-  float* sums = reinterpret_cast<float*>(smem + ST * Cfg::kStage);  // [set][row][kW4Pitch]
-  __shared__ uint64_t bars[3 * 12];
+  float* sums = reinterpret_cast<float*>(smem + ST * Cfg::kStage);  // [buffer][set][row][kW4Pitch]
+  __shared__ uint64_t bars[3 * ST + 4];
   __shared__ long long scratch[32], found[2];
   __shared__ uint32_t abort_word, is_last[2];
+  __shared__ W4Piece piece[2];  // the cut tiles' pieces: at most the first and the last fragment
   volatile uint32_t* abort_flag = &abort_word;
   const int warp = (int)threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
-  // a_full (the rows are there), full (weights, scales and ordered rows are), empty
+  // a_full (the rows are there), full (weights, scales and ordered rows are), empty;
+  // sum_full, sum_empty of the sums' buffers
   const uint32_t a_full = smem_addr(bars), full = a_full + 8 * ST, empty = full + 8 * ST;
+  const uint32_t sum_full = empty + 8 * ST, sum_empty = sum_full + 16;
   if (warp == 4 * SETS && lane == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(a_full + 8 * i, 1);
       mbar_init(full + 8 * i, 3);
       mbar_init(empty + 8 * i, 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sum_full + 8 * i, 4 * SETS);
+      mbar_init(sum_empty + 8 * i, 1);
     }
     *abort_flag = 0u;
     found[0] = found[1] = 0;
@@ -364,11 +371,12 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
           if (weights) {
             mbar_arrive_expect_tx(full + 8 * s, (uint32_t)kW4WBytes);
             tma_load_3d(at, &tmW, full + 8 * s, u * (kW4K / 2), w.tile * kW4Feats, w.g);
+            tma_load_3d(at + kW4WBytes / 2, &tmW, full + 8 * s, u * (kW4K / 2) + 64, w.tile * kW4Feats, w.g);
           } else {
             mbar_arrive_expect_tx(a_full + 8 * s, (uint32_t)Cfg::kABytes);
             tma_load_2d(at + kW4WBytes, &tmA, a_full + 8 * s, u * kW4K, w.row0);
-            mbar_arrive_expect_tx(full + 8 * s, (uint32_t)(256 * GROUPS));
-            tma_load_3d(at + kW4WBytes + 2 * Cfg::kABytes, &tmS, full + 8 * s, w.tile * kW4Feats, u * GROUPS, w.g);
+            mbar_arrive_expect_tx(full + 8 * s, (uint32_t)(512 * GROUPS));
+            tma_load_3d(at + Cfg::kStage - kW4SBytes, &tmS, full + 8 * s, w.tile * kW4Feats, 2 * u * GROUPS, w.g);
           }
           if (++s == ST) {
             s = 0;
@@ -377,72 +385,129 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
         }
       }
     }
-  } else if (warp >= 4 * SETS + 2) {
+  } else if (warp == 4 * SETS + 2) {
     // ------------------------------------------------------------------ the rows' order
     // Eight k of a row (16 bytes) are one lane's fragments for the eight numbers of a
-    // word: 0 4 1 5 2 6 3 7, to the place of [word q][column tile][lane].
-    const int mine = warp & 1;
+    // word: 0 4 1 5 2 6 3 7.  They stay in their row of 512 bytes, [half][word q][lane t],
+    // odd rows with neighbouring q exchanged: the four lanes' words of two rows fill the
+    // banks once.
+    const uint32_t kc = lane & 15u;
+    const uint32_t q = GROUPS == 1 ? kc & 3u : GROUPS == 2 ? (kc >> 3) * 2 + (kc & 1u) : kc >> 2;
+    const uint32_t t = GROUPS == 1 ? kc >> 2 : GROUPS == 2 ? (kc >> 1) & 3u : kc & 3u;
+    const uint32_t place[2] = {((lane >> 4) * 16 + q * 4 + t) * 16, ((lane >> 4) * 16 + (q ^ 1u) * 4 + t) * 16};
     int s = 0;
     uint32_t ph = 0;
     const int total = hi - lo;
     for (int u = 0; u < total; ++u) {
-      if ((s & 1) == mine) {
-        if (!warp_wait_phase(guard, a_full + 8 * s, ph, (kRoleEpilogue << 16) | 0x100 | s)) break;
-        (void)mbar_try_wait(a_full + 8 * s, ph);  // each lane sees the copies
-        const uint32_t from = ring + s * Cfg::kStage + kW4WBytes, to = from + Cfg::kABytes;
-        constexpr int BATCH = NT == 1 ? 4 : 8;
+      if (!warp_wait_phase(guard, a_full + 8 * s, ph, (kRoleEpilogue << 16) | 0x100 | s)) break;
+      (void)mbar_try_wait(a_full + 8 * s, ph);  // each lane sees the copies
+      const uint32_t at = ring + s * Cfg::kStage + kW4WBytes;
 #pragma unroll 1
-        for (int i0 = 0; i0 < 4 * NT; i0 += BATCH) {
-          uint4 v[BATCH];
+      for (int i0 = 0; i0 < 8 * NT; i0 += 8) {
+        uint4 v[8];
 #pragma unroll
-          for (int i = 0; i < BATCH; ++i) v[i] = w4_lds128(from + (lane + 32u * (uint32_t)(i0 + i)) * 16);
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            const uint32_t c = lane + 32u * (uint32_t)(i0 + i);  // 16-byte word: row c / 16, k 8 (c % 16) ..
-            const uint32_t row = c >> 4, kc = c & 15u;
-            const uint32_t q = GROUPS == 1 ? kc & 3u : GROUPS == 2 ? (kc >> 3) * 2 + (kc & 1u) : kc >> 2;
-            const uint32_t t = GROUPS == 1 ? kc >> 2 : GROUPS == 2 ? (kc >> 1) & 3u : kc & 3u;
-            st_shared_v4(to + (((q * NT + (row >> 3)) * 32 + (row & 7u) * 4 + t) << 4), __byte_perm(v[i].x, v[i].z, 0x5410),
-                         __byte_perm(v[i].x, v[i].z, 0x7632), __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632));
-          }
-        }
+        for (int i = 0; i < 8; ++i) v[i] = w4_lds128(at + (uint32_t)((i0 + i) * (kW4K * 2)) + lane * 16);
         __syncwarp();
-        if (lane == 0) mbar_arrive(full + 8 * s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          st_shared_v4(at + (uint32_t)((i0 + i) * (kW4K * 2)) + place[i & 1], __byte_perm(v[i].x, v[i].z, 0x5410),
+                       __byte_perm(v[i].x, v[i].z, 0x7632), __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632));
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8 * s);
       if (++s == ST) {
         s = 0;
         ph ^= 1u;
       }
     }
+  } else if (warp == 4 * SETS + 3) {
+    // ------------------------------------------------------------------ tiles out
+    // (lane: four features)
+    const int f = 4 * (int)lane;
+    int buf = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    int pieces = 0;
+    while (w.next(p)) {
+      const bool whole = w.ub - w.ua == p.k_units;
+      const int c0 = whole ? 0 : share.owner(w.item);
+      // A piece of a cut tile goes into this CTA's slot (the second one if the tile begins
+      // in its share); it is counted when the share is done.
+      float* slot = p.slots + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0)) * kW4SlotFloats + f;
+      const W4Out out0(p, w.g, w.tile, f), out1(p, w.g, w.tile, f + 2);
+      // (a wait that gave up: the pieces are counted all the same)
+      ok = ok && warp_wait_phase(guard, sum_full + 8 * buf, ph, (kRoleEpilogue << 16) | 0x200 | buf);
+      if (ok) {
+        const float* from = sums + buf * (SETS * Cfg::kRows * kW4Pitch) + f;
+#pragma unroll 4
+        for (int row = 0; row < w.rows; ++row) {
+          float4 v = *reinterpret_cast<const float4*>(from + row * kW4Pitch);
+#pragma unroll
+          for (int k = 1; k < SETS; ++k) {
+            const float4 x = *reinterpret_cast<const float4*>(from + (k * Cfg::kRows + row) * kW4Pitch);
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
+          }
+          if (whole) {
+            out0.store(p, w.row0 + row, make_float2(v.x, v.y));
+            out1.store(p, w.row0 + row, make_float2(v.z, v.w));
+          } else {
+            __stcg(reinterpret_cast<float4*>(slot + row * kW4Feats), v);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sum_empty + 8 * buf);
+      }
+      if (!whole && lane == 0)
+        piece[pieces] = W4Piece{c0, share.owner(w.item + p.k_units - 1), w.g, w.tile, w.row0, w.rows};
+      pieces += whole ? 0 : 1;
+      if (++buf == Cfg::kBufs) {
+        buf = 0;
+        ph ^= 1u;
+      }
+    }
+    __syncwarp();
+    if ((int)lane < pieces) {
+      // (the count releases the whole warp's stores, which its barrier put before it)
+      is_last[lane] = w4_last_piece(p.ws, piece[lane].c0, piece[lane].c1 - piece[lane].c0 + 1) ? 1u : 0u;
+    }
+    if (lane >= (uint32_t)pieces && lane < 2) is_last[lane] = 0u;
   } else {
     // ------------------------------------------------------------------ products
     const int set = warp >> 2, f0 = (warp & 3) * 32;
     const uint32_t g8 = lane >> 2, t = lane & 3;
     const uint32_t swz = (g8 >> 1) & 3u;  // (row >> 1) & 3 of every row that the lane reads
-    const uint32_t w_at = (uint32_t)(f0 + (int)g8) * 64, a_at = (uint32_t)(kW4WBytes + Cfg::kABytes) + lane * 16;
-    const uint32_t s_at = (uint32_t)(kW4WBytes + 2 * Cfg::kABytes) + (uint32_t)(f0 + (int)g8) * 2;
-    int s = 0;
+    const uint32_t w_at = ring + (uint32_t)((f0 + (int)g8) * 64), s_at = ring + (uint32_t)(Cfg::kStage - kW4SBytes + (f0 + (int)g8) * 2);
+    uint32_t a_at[2];  // of even and odd q
+#pragma unroll
+    for (int q = 0; q < 2; ++q) a_at[q] = ring + (uint32_t)kW4WBytes + g8 * (kW4K * 2) + ((((uint32_t)q ^ (g8 & 1u)) * 4 + t) << 4);
+    int left = set;      // units until this set's next one
+    int s = set;         // its stage
     uint32_t ph = 0;
+    int buf = 0;
+    uint32_t sph = 1;
     bool ok = true;
-    W4Piece piece[2];
-    int pieces = 0;
     while (w.next(p)) {
       float acc[2][NT][4];
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.0f;
-      for (int u = w.ua; u < w.ub; ++u) {
-        // (a wait that gave up: the barriers and tickets below still count this CTA)
-        const bool own = s % SETS == set;
-        if (own && ok) ok = warp_wait_phase(guard, full + 8 * s, ph, (kRoleMma << 16) | s);
-        if (own && ok) {
-          const uint32_t at = ring + s * Cfg::kStage;
+      const int n = w.ub - w.ua;
+      for (; left < n; left += SETS) {
+        ok = ok && warp_wait_phase(guard, full + 8 * s, ph, (kRoleMma << 16) | s);
+        if (!ok) continue;
+#pragma unroll NT <= 2 ? 2 : 1
+        for (uint32_t half = 0; half < 2; ++half) {
+          const uint32_t at = (uint32_t)(s * Cfg::kStage);
+          const uint32_t hw = w_at + at + half * (kW4WBytes / 2), ha = at + half * (kW4K * 2 / 2), hs = s_at + at + half * (256 * GROUPS);
           uint32_t word[2][2][4];
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            w4_words<GROUPS>(at + w_at + m * 1024, swz, t, word[m][0]);
-            w4_words<GROUPS>(at + w_at + m * 1024 + 512, swz, t, word[m][1]);
+            w4_words<GROUPS>(hw + m * 1024, swz, t, word[m][0]);
+            w4_words<GROUPS>(hw + m * 1024 + 512, swz, t, word[m][1]);
           }
           float part[2][NT][4];
           constexpr float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -461,7 +526,7 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
               }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-              const uint4 x = w4_lds128(at + a_at + (uint32_t)((q * NT + i) * 512));
+              const uint4 x = w4_lds128(a_at[q & 1] + ha + (uint32_t)((q >> 1) * 128 + i * (8 * kW4K * 2)));
 #pragma unroll
               for (int m = 0; m < 2; ++m) {
                 if (first) w4_mma(part[m][i], a[m][0], x.x, x.y, zero);
@@ -472,7 +537,7 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
             if (last) {
 #pragma unroll
               for (int m = 0; m < 2; ++m) {
-                const uint32_t sq = at + s_at + (uint32_t)(q / (4 / GROUPS) * 256 + m * 32);
+                const uint32_t sq = hs + (uint32_t)(q / (4 / GROUPS) * 256 + m * 32);
                 const float s0 = w4_lds_bf16(sq), s1 = w4_lds_bf16(sq + 16);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
@@ -484,98 +549,68 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
               }
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty + 8 * s);
         }
-        if (++s == ST) {
-          s = 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + 8 * s);
+        s += SETS;
+        if (s >= ST) {
+          s = set;
           ph ^= 1u;
         }
       }
-      // The sets' sums through shared memory: the second half of the sets stores its
-      // own, the first half adds.
-      float* o = sums + (set % Cfg::kRegions * Cfg::kRows + 2 * (int)t) * kW4Pitch + f0 + (int)g8;
-      w4_sync<MT>();  // the tile before this one has been read
-      if (set >= Cfg::kRegions) {
+      left -= n;
+      // The tile's sums of this set, for the warp that stores it.
+      ok = ok && warp_wait_phase(guard, sum_empty + 8 * buf, sph, (kRoleMma << 16) | 0x400 | buf);
+      if (ok) {
+        float* o = sums + ((buf * SETS + set) * Cfg::kRows + 2 * (int)t) * kW4Pitch + f0 + (int)g8;
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[(8 * i + (j & 1)) * kW4Pitch + 16 * m + 8 * (j >> 1)] = acc[m][i][j];
+            for (int j = 0; j < 4; ++j)  // (the weights were in 64ths)
+              o[(8 * i + (j & 1)) * kW4Pitch + 16 * m + 8 * (j >> 1)] = 64.0f * acc[m][i][j];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sum_full + 8 * buf);
       }
-      w4_sync<MT>();
-      if (set < Cfg::kRegions) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[(8 * i + (j & 1)) * kW4Pitch + 16 * m + 8 * (j >> 1)] += acc[m][i][j];
-      }
-      w4_sync<MT>();
-      // (thread: two features, every MT / 64-th row)
-      const int f = 2 * (int)(threadIdx.x & 63);
-      const bool whole = w.ub - w.ua == p.k_units;
-      const int c0 = whole ? 0 : share.owner(w.item);
-      // A piece of a cut tile goes into this CTA's slot (the second one if the tile begins
-      // in its share); it is counted when the share is done.
-      float* slot = p.slots + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0)) * kW4SlotFloats + f;
-      const W4Out out(p, w.g, w.tile, f);
-#pragma unroll 4
-      for (int row = (int)threadIdx.x >> 6; row < w.rows; row += MT / 64) {
-        float2 v = *reinterpret_cast<const float2*>(sums + row * kW4Pitch + f);
-        if constexpr (Cfg::kRegions == 2) {
-          const float2 x = *reinterpret_cast<const float2*>(sums + (Cfg::kRows + row) * kW4Pitch + f);
-          v.x += x.x;
-          v.y += x.y;
-        }
-        if (whole) out.store(p, w.row0 + row, v);
-        else __stcg(reinterpret_cast<float2*>(slot + row * kW4Feats), v);
-      }
-      if (!whole) piece[pieces++ & 1] = W4Piece{c0, share.owner(w.item + p.k_units - 1), w.g, w.tile, w.row0, w.rows};
-    }
-    if (pieces) {
-      w4_sync<MT>();
-      if (threadIdx.x < 2 && (int)threadIdx.x < pieces) {
-        __threadfence();  // (after the barrier: all the warps' stores)
-        const W4Piece& x = threadIdx.x ? piece[1] : piece[0];
-        is_last[threadIdx.x] = w4_last_piece(p.ws, x.c0, x.c1 - x.c0 + 1) ? 1u : 0u;
-        __threadfence();
-      }
-      w4_sync<MT>();
-#pragma unroll 1
-      for (int k = 0; k < pieces; ++k) {
-        if (!is_last[k]) continue;
-        const W4Piece x = piece[k];
-        const int f = 2 * (int)(threadIdx.x & 63);
-        const W4Out out(p, x.g, x.tile, f);
-        // four rows at a time (rows behind the last one lie in the slots too), all pieces
-        for (int row0 = (int)threadIdx.x >> 6; row0 < x.rows; row0 += 4 * (MT / 64)) {
-          float2 v[4];
-          const float* from = p.slots + (size_t)row0 * kW4Feats + f;
-          constexpr int STEP = MT / 64 * kW4Feats;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = row0 + i * (MT / 64) < 64 ? __ldcg(reinterpret_cast<const float2*>(from + (size_t)(2 * x.c0 + 1) * kW4SlotFloats + i * STEP)) : make_float2(0.0f, 0.0f);
-#pragma unroll 4
-          for (int c = x.c0 + 1; c <= x.c1; ++c) {
-            const float* at = from + (size_t)(2 * c) * kW4SlotFloats;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 y = row0 + i * (MT / 64) < 64 ? __ldcg(reinterpret_cast<const float2*>(at + i * STEP)) : make_float2(0.0f, 0.0f);
-              v[i].x += y.x;
-              v[i].y += y.y;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (row0 + i * (MT / 64) < x.rows) out.store(p, x.row0 + row0 + i * (MT / 64), v[i]);
-        }
+      if (++buf == Cfg::kBufs) {
+        buf = 0;
+        sph ^= 1u;
       }
     }
   }
   __syncthreads();
+  // The cut tiles of which this CTA counted the last piece: all threads add.
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    if (!is_last[k]) continue;
+    const W4Piece x = piece[k];
+    const int f = 2 * (int)(threadIdx.x & 63);
+    const W4Out out(p, x.g, x.tile, f);
+    constexpr int TR = Cfg::kThreads / 64;  // rows at a time
+    // (four rows of a thread, those behind the last one too: the slots hold 64)
+    for (int row0 = (int)threadIdx.x >> 6; row0 < x.rows; row0 += 4 * TR) {
+      float2 v[4];
+      const float* from = p.slots + (size_t)row0 * kW4Feats + f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = row0 + i * TR < 64 ? __ldcg(reinterpret_cast<const float2*>(from + (size_t)(2 * x.c0 + 1) * kW4SlotFloats + i * TR * kW4Feats))
+                                  : make_float2(0.0f, 0.0f);
+#pragma unroll 4
+      for (int c = x.c0 + 1; c <= x.c1; ++c) {
+        const float* at = from + (size_t)(2 * c) * kW4SlotFloats;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = row0 + i * TR < 64 ? __ldcg(reinterpret_cast<const float2*>(at + i * TR * kW4Feats)) : make_float2(0.0f, 0.0f);
+          v[i].x += y.x;
+          v[i].y += y.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (row0 + i * TR < x.rows) out.store(p, x.row0 + row0 + i * TR, v[i]);
+    }
+  }
   if (*abort_flag) {
     for (int i = 0; i < 200; ++i) __nanosleep(1000);  // copies still in flight land first
   }
