@@ -53,9 +53,7 @@ struct W4Cfg {
   static constexpr int kBufs = NT == 1 ? 2 : 1;  // of the sets' sums
   static constexpr int kSums = kBufs * kSets * kRows * kW4Pitch * 4;
   static constexpr int kFit = (232448 - 2048 - kSums) / kStage;
-  // A stage belongs to one set: a barrier's parity tells two phases apart, and only who
-  // has waited for a phase may wait for the next.
-  static constexpr int kStages = kFit / kSets * kSets > 8 ? 8 : kFit / kSets * kSets;
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kSums + 1024;
   static_assert(kStage % 1024 == 0 && kSmem <= 232448 && kStages >= kSets, "shared memory");
 };
@@ -288,18 +286,23 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
   __shared__ uint64_t bars[3 * ST + 4];
   __shared__ long long scratch[32], found[2];
   __shared__ uint32_t abort_word, is_last[2];
-  __shared__ W4Piece piece[2];  // the cut tiles' pieces: at most the first and the last fragment
+  // the cut tiles' pieces (at most the first and the last fragment), the last fragment
+  // among them whether it is cut or not
+  __shared__ W4Piece piece[2];
+  __shared__ int pieces, last_buf;
   volatile uint32_t* abort_flag = &abort_word;
   const int warp = (int)threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
-  // a_full (the rows are there), full (weights, scales and ordered rows are), empty;
-  // sum_full, sum_empty of the sums' buffers
-  const uint32_t a_full = smem_addr(bars), full = a_full + 8 * ST, empty = full + 8 * ST;
+  // loaded, full (and the rows are in order), empty; sum_full, sum_empty of the sums'
+  // buffers.  A barrier's parity tells two phases apart, so who waits for a stage has to
+  // know that its last use is over.  The ordering warp hands the stages on one after the
+  // other, whatever order they arrive in: a set that has had unit u - SETS has had u - ST.
+  const uint32_t loaded = smem_addr(bars), full = loaded + 8 * ST, empty = full + 8 * ST;
   const uint32_t sum_full = empty + 8 * ST, sum_empty = sum_full + 16;
   if (warp == 4 * SETS && lane == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(a_full + 8 * i, 1);
-      mbar_init(full + 8 * i, 3);
+      mbar_init(loaded + 8 * i, 2);
+      mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -308,6 +311,7 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
     }
     *abort_flag = 0u;
     found[0] = found[1] = 0;
+    pieces = 0;
     fence_mbar_init();
   }
   if (warp == 4 * SETS + 1 && lane == 0) {
@@ -369,14 +373,13 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
           }
           const uint32_t at = ring + s * Cfg::kStage;
           if (weights) {
-            mbar_arrive_expect_tx(full + 8 * s, (uint32_t)kW4WBytes);
-            tma_load_3d(at, &tmW, full + 8 * s, u * (kW4K / 2), w.tile * kW4Feats, w.g);
-            tma_load_3d(at + kW4WBytes / 2, &tmW, full + 8 * s, u * (kW4K / 2) + 64, w.tile * kW4Feats, w.g);
+            mbar_arrive_expect_tx(loaded + 8 * s, (uint32_t)kW4WBytes);
+            tma_load_3d(at, &tmW, loaded + 8 * s, u * (kW4K / 2), w.tile * kW4Feats, w.g);
+            tma_load_3d(at + kW4WBytes / 2, &tmW, loaded + 8 * s, u * (kW4K / 2) + 64, w.tile * kW4Feats, w.g);
           } else {
-            mbar_arrive_expect_tx(a_full + 8 * s, (uint32_t)Cfg::kABytes);
-            tma_load_2d(at + kW4WBytes, &tmA, a_full + 8 * s, u * kW4K, w.row0);
-            mbar_arrive_expect_tx(full + 8 * s, (uint32_t)(512 * GROUPS));
-            tma_load_3d(at + Cfg::kStage - kW4SBytes, &tmS, full + 8 * s, w.tile * kW4Feats, 2 * u * GROUPS, w.g);
+            mbar_arrive_expect_tx(loaded + 8 * s, (uint32_t)(Cfg::kABytes + 512 * GROUPS));
+            tma_load_2d(at + kW4WBytes, &tmA, loaded + 8 * s, u * kW4K, w.row0);
+            tma_load_3d(at + Cfg::kStage - kW4SBytes, &tmS, loaded + 8 * s, w.tile * kW4Feats, 2 * u * GROUPS, w.g);
           }
           if (++s == ST) {
             s = 0;
@@ -399,8 +402,8 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
     uint32_t ph = 0;
     const int total = hi - lo;
     for (int u = 0; u < total; ++u) {
-      if (!warp_wait_phase(guard, a_full + 8 * s, ph, (kRoleEpilogue << 16) | 0x100 | s)) break;
-      (void)mbar_try_wait(a_full + 8 * s, ph);  // each lane sees the copies
+      if (!warp_wait_phase(guard, loaded + 8 * s, ph, (kRoleEpilogue << 16) | 0x100 | s)) break;
+      (void)mbar_try_wait(loaded + 8 * s, ph);  // each lane sees the copies
       const uint32_t at = ring + s * Cfg::kStage + kW4WBytes;
 #pragma unroll 1
       for (int i0 = 0; i0 < 8 * NT; i0 += 8) {
@@ -422,24 +425,29 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
     }
   } else if (warp == 4 * SETS + 3) {
     // ------------------------------------------------------------------ tiles out
-    // (lane: four features)
+    // All but the share's last one.  (lane: four features)
     const int f = 4 * (int)lane;
-    int buf = 0;
+    int buf = 0, cut = 0;
     uint32_t ph = 0;
     bool ok = true;
-    int pieces = 0;
     while (w.next(p)) {
       const bool whole = w.ub - w.ua == p.k_units;
-      const int c0 = whole ? 0 : share.owner(w.item);
+      const int c0 = whole ? (int)blockIdx.x : share.owner(w.item);
       // A piece of a cut tile goes into this CTA's slot (the second one if the tile begins
       // in its share); it is counted when the share is done.
+      if (!whole || w.x >= w.hi) {
+        if (lane == 0)
+          piece[cut] = W4Piece{c0, whole ? c0 : share.owner(w.item + p.k_units - 1), w.g, w.tile, w.row0, w.rows};
+        ++cut;
+        if (w.x >= w.hi) break;
+      }
       float* slot = p.slots + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0)) * kW4SlotFloats + f;
       const W4Out out0(p, w.g, w.tile, f), out1(p, w.g, w.tile, f + 2);
       // (a wait that gave up: the pieces are counted all the same)
       ok = ok && warp_wait_phase(guard, sum_full + 8 * buf, ph, (kRoleEpilogue << 16) | 0x200 | buf);
       if (ok) {
         const float* from = sums + buf * (SETS * Cfg::kRows * kW4Pitch) + f;
-#pragma unroll 4
+#pragma unroll 2
         for (int row = 0; row < w.rows; ++row) {
           float4 v = *reinterpret_cast<const float4*>(from + row * kW4Pitch);
 #pragma unroll
@@ -460,20 +468,15 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(sum_empty + 8 * buf);
       }
-      if (!whole && lane == 0)
-        piece[pieces] = W4Piece{c0, share.owner(w.item + p.k_units - 1), w.g, w.tile, w.row0, w.rows};
-      pieces += whole ? 0 : 1;
       if (++buf == Cfg::kBufs) {
         buf = 0;
         ph ^= 1u;
       }
     }
-    __syncwarp();
-    if ((int)lane < pieces) {
-      // (the count releases the whole warp's stores, which its barrier put before it)
-      is_last[lane] = w4_last_piece(p.ws, piece[lane].c0, piece[lane].c1 - piece[lane].c0 + 1) ? 1u : 0u;
+    if (lane == 0) {
+      pieces = cut;
+      last_buf = buf;
     }
-    if (lane >= (uint32_t)pieces && lane < 2) is_last[lane] = 0u;
   } else {
     // ------------------------------------------------------------------ products
     const int set = warp >> 2, f0 = (warp & 3) * 32;
@@ -554,7 +557,7 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
         if (lane == 0) mbar_arrive(empty + 8 * s);
         s += SETS;
         if (s >= ST) {
-          s = set;
+          s -= ST;
           ph ^= 1u;
         }
       }
@@ -580,35 +583,64 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
     }
   }
   __syncthreads();
-  // The cut tiles of which this CTA counted the last piece: all threads add.
-#pragma unroll 1
-  for (int k = 0; k < 2; ++k) {
-    if (!is_last[k]) continue;
-    const W4Piece x = piece[k];
-    const int f = 2 * (int)(threadIdx.x & 63);
+  // All threads: the sums of the last fragment (piece[pieces - 1]), then the cut tiles
+  // of which this CTA counts the last piece.  (thread: two features, every TR-th row)
+  constexpr int TR = Cfg::kThreads / 64;
+  const int f = 2 * (int)(threadIdx.x & 63), first_row = (int)threadIdx.x >> 6;
+  if (pieces > 0) {
+    const W4Piece x = piece[pieces - 1];
+    const bool whole = x.c0 == x.c1;
+    float* slot = p.slots + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == x.c0 ? 1 : 0)) * kW4SlotFloats + f;
+    const float* from = sums + last_buf * (SETS * Cfg::kRows * kW4Pitch) + f;
     const W4Out out(p, x.g, x.tile, f);
-    constexpr int TR = Cfg::kThreads / 64;  // rows at a time
-    // (four rows of a thread, those behind the last one too: the slots hold 64)
-    for (int row0 = (int)threadIdx.x >> 6; row0 < x.rows; row0 += 4 * TR) {
-      float2 v[4];
-      const float* from = p.slots + (size_t)row0 * kW4Feats + f;
+#pragma unroll 2
+    for (int row = first_row; row < x.rows; row += TR) {
+      float2 v = *reinterpret_cast<const float2*>(from + row * kW4Pitch);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = row0 + i * TR < 64 ? __ldcg(reinterpret_cast<const float2*>(from + (size_t)(2 * x.c0 + 1) * kW4SlotFloats + i * TR * kW4Feats))
-                                  : make_float2(0.0f, 0.0f);
+      for (int k = 1; k < SETS; ++k) {
+        const float2 y = *reinterpret_cast<const float2*>(from + (k * Cfg::kRows + row) * kW4Pitch);
+        v.x += y.x;
+        v.y += y.y;
+      }
+      if (whole) out.store(p, x.row0 + row, v);
+      else __stcg(reinterpret_cast<float2*>(slot + row * kW4Feats), v);
+    }
+    if (pieces == 2 || !whole) {  // (of two pieces the first is one of a cut tile)
+      __syncthreads();
+      if ((int)threadIdx.x < pieces) {
+        // (the count releases all threads' stores, which the barrier put before it)
+        const W4Piece& y = piece[threadIdx.x];
+        is_last[threadIdx.x] = y.c0 != y.c1 && w4_last_piece(p.ws, y.c0, y.c1 - y.c0 + 1) ? 1u : 0u;
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (int k = 0; k < pieces; ++k) {
+        if (!is_last[k]) continue;
+        const W4Piece y = piece[k];
+        const W4Out out(p, y.g, y.tile, f);
+        // (four rows of a thread, those behind the last one too: the slots hold 64)
+        for (int row0 = first_row; row0 < y.rows; row0 += 4 * TR) {
+          float2 v[4];
+          const float* at = p.slots + (size_t)row0 * kW4Feats + f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
-      for (int c = x.c0 + 1; c <= x.c1; ++c) {
-        const float* at = from + (size_t)(2 * c) * kW4SlotFloats;
+          for (int c = y.c0; c <= y.c1; ++c) {
+            const float* of = at + (size_t)(2 * c + (c == y.c0 ? 1 : 0)) * kW4SlotFloats;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 y = row0 + i * TR < 64 ? __ldcg(reinterpret_cast<const float2*>(at + i * TR * kW4Feats)) : make_float2(0.0f, 0.0f);
-          v[i].x += y.x;
-          v[i].y += y.y;
+            for (int i = 0; i < 4; ++i) {
+              if (row0 + i * TR < 64) {
+                const float2 z = __ldcg(reinterpret_cast<const float2*>(of + i * TR * kW4Feats));
+                v[i].x += z.x;
+                v[i].y += z.y;
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (row0 + i * TR < y.rows) out.store(p, y.row0 + row0 + i * TR, v[i]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (row0 + i * TR < x.rows) out.store(p, x.row0 + row0 + i * TR, v[i]);
     }
   }
   if (*abort_flag) {

@@ -46,8 +46,14 @@ def _lib():
     return _w._lib or _w.load_library()
 
 
+# As in the module's siblings, a good call pays for one look at each tensor; what is
+# wrong is looked for only when that fails.
 def _heads(t, name, dtype=None):
     """A CUDA tensor [T, heads, Dh] whose heads follow one another; returns the distance of its tokens."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype is dtype):
+        shape, st = t.shape, t.stride()
+        if len(st) == 3 and st[2] == 1 and st[1] == shape[2] and shape[0] > 1 and shape[1] > 0 and shape[2] > 1:
+            return st[0]
     _need(t, name, dtype, (3,))
     T, H, Dh = t.shape
     if (H > 1 and t.stride(1) != Dh) or (Dh > 1 and t.stride(2) != 1):
@@ -57,7 +63,13 @@ def _heads(t, name, dtype=None):
 
 
 def _cache(k_cache, v_cache):
-    """Checks the two arrays of a paged cache [pages, page_size, heads, Dh]; returns the strides of pages, tokens, heads."""
+    """Checks the two arrays of a paged cache [pages, page_size, heads, Dh]; returns its shape and the strides of pages,
+    tokens, heads."""
+    if (isinstance(k_cache, torch.Tensor) and isinstance(v_cache, torch.Tensor) and k_cache.is_cuda and v_cache.is_cuda
+            and k_cache.dtype is _BF16 and v_cache.dtype is _BF16):
+        shape, st = k_cache.shape, k_cache.stride()
+        if len(st) == 4 and st[3] == 1 and v_cache.stride() == st and v_cache.shape == shape and min(shape) > 1:
+            return shape, st[0], st[1], st[2]
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _need(t, name, _BF16, (4,))
         if t.shape[3] > 1 and t.stride(3) != 1:
@@ -72,7 +84,7 @@ def _cache(k_cache, v_cache):
         st = heads * sh
     if pages == 1:
         sp = max(page * st, heads * sh)
-    return sp, st, sh
+    return k_cache.shape, sp, st, sh
 
 
 # ----------------------------------------------------------------------------
@@ -93,14 +105,15 @@ def wst_cache_append_bf16(k, v, positions, slots, k_cache, v_cache, inv_freq=Non
     T, Hkv, Dh = k.shape
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("k and v must be alike")
-    if k_cache.dim() == 4 and tuple(k_cache.shape[2:]) != (Hkv, Dh):
-        raise ValueError("k_cache must be [pages, page_size, %d, %d], not %s" % (Hkv, Dh, tuple(k_cache.shape)))
-    sp, st_, sh = _cache(k_cache, v_cache)
+    shape, sp, st_, sh = _cache(k_cache, v_cache)
+    if shape[2] != Hkv or shape[3] != Dh:
+        raise ValueError("k_cache must be [pages, page_size, %d, %d], not %s" % (Hkv, Dh, tuple(shape)))
     H, ldq, ldqo = 0, 0, 0
     if q is not None:
         ldq, ldqo = _heads(q, "q"), _heads(q_out, "q_out", _BF16)
-        H = q.shape[1]
-        if q.shape != (T, H, Dh) or q_out.shape != q.shape or q.dtype != k.dtype:
+        qs = q.shape
+        H = qs[1]
+        if qs != (T, H, Dh) or q_out.shape != qs or q.dtype is not k.dtype:
             raise ValueError("q and q_out must be [T, H, Dh], q of k's type")
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     ws, _ = _ws(workspace)
@@ -108,7 +121,7 @@ def wst_cache_append_bf16(k, v, positions, slots, k_cache, v_cache, inv_freq=Non
         T, H, Hkv, Dh, rot, _STYLES[style] if isinstance(style, str) else int(style), _w._ptr(q), ldq, k.data_ptr(), ldk,
         v.data_ptr(), ldv, _type(k, "k"), None if positions is None else _dense(positions, "positions", _I32, (T,)),
         None if not rot else _dense(inv_freq, "inv_freq", _F32, (rot // 2,)), _dense(slots, "slots", _I32, (T,)),
-        _w._ptr(q_out) if q is not None else None, ldqo, k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], k_cache.shape[1],
+        _w._ptr(q_out) if q is not None else None, ldqo, k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1],
         sp, st_, sh, ws, _stream(stream, k))
     _w._check(st, "wst_cache_append_bf16")
 
@@ -144,25 +157,28 @@ def wst_tree_attention_bf16(Q, q_offsets, context, k_cache, v_cache, page_table,
     T, H, Dh = Q.shape
     if O.shape != Q.shape:
         raise ValueError("O must be like Q")
-    _need(page_table, "page_table", _I32, (2,))
+    if not (isinstance(page_table, torch.Tensor) and page_table.dtype is _I32 and page_table.is_cuda and page_table.dim() == 2
+            and page_table.stride(1) == 1):
+        _need(page_table, "page_table", _I32, (2,))
     B, max_pages = page_table.shape
-    sp, st_, sh = _cache(k_cache, v_cache)
-    Hkv = k_cache.shape[2]
-    if k_cache.shape[3] != Dh or Hkv == 0 or H % Hkv:
-        raise ValueError("k_cache must be [pages, page_size, Hkv, %d] with Hkv a divisor of %d, not %s" % (Dh, H, tuple(k_cache.shape)))
+    shape, sp, st_, sh = _cache(k_cache, v_cache)
+    Hkv = shape[2]
+    if shape[3] != Dh or Hkv == 0 or H % Hkv:
+        raise ValueError("k_cache must be [pages, page_size, Hkv, %d] with Hkv a divisor of %d, not %s" % (Dh, H, tuple(shape)))
     words = ldm = 0
     if mask is not None:
-        _need(mask, "mask", _I32, (2,))
-        if mask.shape[0] != T:
+        if not (isinstance(mask, torch.Tensor) and mask.dtype is _I32 and mask.is_cuda and mask.dim() == 2 and mask.stride(1) == 1):
+            _need(mask, "mask", _I32, (2,))
+        rows, words = mask.shape
+        if rows != T:
             raise ValueError("mask must be [T, words]")
-        words = mask.shape[1]
         ldm = mask.stride(0) if T > 1 else words
     if scale is None:
         scale = 1.0 / math.sqrt(Dh)
     ws, n = _ws(workspace)
     st = _lib().wst_tree_attention_bf16(
         B, T, H, Hkv, Dh, Q.data_ptr(), ldq, _dense(q_offsets, "q_offsets", _I32, (B + 1,)), _dense(context, "context", _I32, (B,)),
-        _w._ptr(mask), words, ldm, k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], k_cache.shape[1], sp, st_, sh,
+        _w._ptr(mask), words, ldm, k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], sp, st_, sh,
         page_table.data_ptr(), max_pages, page_table.stride(0) if B > 1 else max_pages, scale, O.data_ptr(), ldo, _type(O, "O"), ws, n,
         _stream(stream, Q))
     _w._check(st, "wst_tree_attention_bf16")
