@@ -23,11 +23,12 @@
 //    last, from fp32 partial sums in the workspace, in ascending order of k: the
 //    result does not depend on which CTA that is.
 //
-// Roles: sets of four multiplying warps, which take the units in turn (4 sets; 2 where
-// the rows' accumulators need the registers), then a warp that loads the weights, as they
-// lie in memory, one that loads the rows' k and the scales (a copy and its barrier take
-// the issuing thread about 200 clocks), one that orders the rows, and one that adds the
-// sets' sums of a tile and stores it while they multiply the next.
+// Roles: sets of four multiplying warps, which take the units in turn (4 sets; 3 or 2
+// where the rows' accumulators need the registers), then a warp that loads the weights,
+// as they lie in memory, one that loads the rows' k and the scales (a copy and its
+// barrier take the issuing thread about 200 clocks), one that adds the sets' sums of a
+// tile and stores it while they multiply the next, and one or two that order the rows (a
+// unit takes one 1,000 clocks at 8 rows, most of it latency).
 #pragma once
 
 #include "work_split.cuh"
@@ -45,9 +46,9 @@ constexpr int kW4Pitch = kW4Feats + 4;  // floats of a row of a set's sums
 template <int NT>  // column tiles of 8 rows: 1, 2, 4, 8
 struct W4Cfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kSets = NT <= 2 ? 4 : 2;
-  static constexpr int kMulThreads = 128 * kSets;
-  static constexpr int kThreads = kMulThreads + 128;
+  static constexpr int kSets = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int kOrder = NT <= 2 ? 2 : 1;  // ordering warps
+  static constexpr int kThreads = 128 * kSets + 32 * (3 + kOrder);
   static constexpr int kABytes = kRows * kW4K * 2;
   static constexpr int kStage = kW4WBytes + kABytes + kW4SBytes;
   static constexpr int kBufs = NT == 1 ? 2 : 1;  // of the sets' sums
@@ -213,7 +214,9 @@ __device__ __forceinline__ float w4_lds_bf16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
   return __uint_as_float((uint32_t)v << 16);
 }
-__device__ __forceinline__ float w4_activate(float v, int epi) {
+// (a call: inlined at every store it made the code of a tile's end several times as long,
+// and code that runs once a launch costs its fetching)
+static __device__ __noinline__ float w4_activate(float v, int epi) {
   if (epi == 2) return v / (1.0f + expf(-v));
   if (epi == 3) return v * normcdff(v);
   return v;
@@ -235,9 +238,11 @@ struct W4Out {
     }
   }
   __device__ __forceinline__ void store(const W4Args& p, int row, float2 v) const {
-    if (p.epi) {
-      v.x = w4_activate(v.x + b0, p.epi);
-      v.y = w4_activate(v.y + b1, p.epi);
+    v.x += b0;
+    v.y += b1;
+    if (p.epi > 1) {
+      v.x = w4_activate(v.x, p.epi);
+      v.y = w4_activate(v.y, p.epi);
     }
     const long long at = (long long)row * p.ldc + n;
     if (p.c_f32) {
@@ -295,8 +300,9 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
   const uint32_t lane = threadIdx.x & 31;
   // loaded, full (and the rows are in order), empty; sum_full, sum_empty of the sums'
   // buffers.  A barrier's parity tells two phases apart, so who waits for a stage has to
-  // know that its last use is over.  The ordering warp hands the stages on one after the
-  // other, whatever order they arrive in: a set that has had unit u - SETS has had u - ST.
+  // know that its last use is over.  The ordering warps hand the stages on one after the
+  // other, whatever order they arrive in: a set that has had unit u - SETS knows that unit
+  // u - ST was there.
   const uint32_t loaded = smem_addr(bars), full = loaded + 8 * ST, empty = full + 8 * ST;
   const uint32_t sum_full = empty + 8 * ST, sum_empty = sum_full + 16;
   if (warp == 4 * SETS && lane == 0) {
@@ -388,7 +394,7 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
         }
       }
     }
-  } else if (warp == 4 * SETS + 2) {
+  } else if (warp >= 4 * SETS + 3) {
     // ------------------------------------------------------------------ the rows' order
     // Eight k of a row (16 bytes) are one lane's fragments for the eight numbers of a
     // word: 0 4 1 5 2 6 3 7.  They stay in their row of 512 bytes, [half][word q][lane t],
@@ -398,12 +404,16 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
     const uint32_t q = GROUPS == 1 ? kc & 3u : GROUPS == 2 ? (kc >> 3) * 2 + (kc & 1u) : kc >> 2;
     const uint32_t t = GROUPS == 1 ? kc >> 2 : GROUPS == 2 ? (kc >> 1) & 3u : kc & 3u;
     const uint32_t place[2] = {((lane >> 4) * 16 + q * 4 + t) * 16, ((lane >> 4) * 16 + (q ^ 1u) * 4 + t) * 16};
-    int s = 0;
-    uint32_t ph = 0;
+    constexpr int ORDER = Cfg::kOrder;
+    static_assert(ST > ORDER && ST >= SETS, "who waits for a unit knows that the stage's last one is over");
     const int total = hi - lo;
-    for (int u = 0; u < total; ++u) {
-      if (!warp_wait_phase(guard, loaded + 8 * s, ph, (kRoleEpilogue << 16) | 0x100 | s)) break;
-      (void)mbar_try_wait(loaded + 8 * s, ph);  // each lane sees the copies
+    int s = warp - (4 * SETS + 3), prev = s == 0 ? ST - 1 : s - 1;  // the stages of unit u and of the one before
+    uint32_t ph = 0, prev_ph = s == 0 ? 1u : 0u;
+    for (int u = s; u < total; u += ORDER) {
+      bool there = mbar_try_wait(loaded + 8 * s, ph);  // (by each lane: it reads the copies)
+      if (!__all_sync(0xffffffffu, there) &&
+          !__all_sync(0xffffffffu, wait_phase(guard, loaded + 8 * s, ph, (kRoleEpilogue << 16) | 0x100 | s)))
+        break;
       const uint32_t at = ring + s * Cfg::kStage + kW4WBytes;
 #pragma unroll 1
       for (int i0 = 0; i0 < 8 * NT; i0 += 8) {
@@ -417,13 +427,22 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
                        __byte_perm(v[i].x, v[i].z, 0x7632), __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632));
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(full + 8 * s);
-      if (++s == ST) {
-        s = 0;
+      if (lane == 0) {
+        // in the units' order: after the unit before this one
+        if (ORDER > 1 && !wait_phase(guard, full + 8 * prev, prev_ph, (kRoleEpilogue << 16) | 0x180 | s)) there = false;
+        else mbar_arrive(full + 8 * s), there = true;
+      }
+      if (!__shfl_sync(0xffffffffu, there ? 1 : 0, 0)) break;
+      if ((s += ORDER) >= ST) {
+        s -= ST;
         ph ^= 1u;
       }
+      if ((prev += ORDER) >= ST) {
+        prev -= ST;
+        prev_ph ^= 1u;
+      }
     }
-  } else if (warp == 4 * SETS + 3) {
+  } else if (warp == 4 * SETS + 2) {
     // ------------------------------------------------------------------ tiles out
     // All but the share's last one.  (lane: four features)
     const int f = 4 * (int)lane;
@@ -447,22 +466,30 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
       ok = ok && warp_wait_phase(guard, sum_full + 8 * buf, ph, (kRoleEpilogue << 16) | 0x200 | buf);
       if (ok) {
         const float* from = sums + buf * (SETS * Cfg::kRows * kW4Pitch) + f;
-#pragma unroll 2
-        for (int row = 0; row < w.rows; ++row) {
-          float4 v = *reinterpret_cast<const float4*>(from + row * kW4Pitch);
+#pragma unroll 1
+        for (int row0 = 0; row0 < w.rows; row0 += 8) {  // (the buffer holds whole eights)
+          float4 v[8];
 #pragma unroll
-          for (int k = 1; k < SETS; ++k) {
-            const float4 x = *reinterpret_cast<const float4*>(from + (k * Cfg::kRows + row) * kW4Pitch);
-            v.x += x.x;
-            v.y += x.y;
-            v.z += x.z;
-            v.w += x.w;
-          }
-          if (whole) {
-            out0.store(p, w.row0 + row, make_float2(v.x, v.y));
-            out1.store(p, w.row0 + row, make_float2(v.z, v.w));
-          } else {
-            __stcg(reinterpret_cast<float4*>(slot + row * kW4Feats), v);
+          for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const float4*>(from + (row0 + i) * kW4Pitch);
+#pragma unroll
+          for (int k = 1; k < SETS; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 x = *reinterpret_cast<const float4*>(from + (k * Cfg::kRows + row0 + i) * kW4Pitch);
+              v[i].x += x.x;
+              v[i].y += x.y;
+              v[i].z += x.z;
+              v[i].w += x.w;
+            }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (row0 + i >= w.rows) break;
+            if (whole) {
+              out0.store(p, w.row0 + row0 + i, make_float2(v[i].x, v[i].y));
+              out1.store(p, w.row0 + row0 + i, make_float2(v[i].z, v[i].w));
+            } else {
+              __stcg(reinterpret_cast<float4*>(slot + (row0 + i) * kW4Feats), v[i]);
+            }
           }
         }
         __syncwarp();
@@ -586,24 +613,36 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
   // All threads: the sums of the last fragment (piece[pieces - 1]), then the cut tiles
   // of which this CTA counts the last piece.  (thread: two features, every TR-th row)
   constexpr int TR = Cfg::kThreads / 64;
-  const int f = 2 * (int)(threadIdx.x & 63), first_row = (int)threadIdx.x >> 6;
+  constexpr int PER = (Cfg::kRows + TR - 1) / TR < 6 ? (Cfg::kRows + TR - 1) / TR : 6;  // rows of a thread at a time
+  const int f = 2 * (int)(threadIdx.x & 63);
+  const int first_row = (int)threadIdx.x < 64 * TR ? (int)threadIdx.x >> 6 : Cfg::kRows;
   if (pieces > 0) {
     const W4Piece x = piece[pieces - 1];
     const bool whole = x.c0 == x.c1;
     float* slot = p.slots + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == x.c0 ? 1 : 0)) * kW4SlotFloats + f;
     const float* from = sums + last_buf * (SETS * Cfg::kRows * kW4Pitch) + f;
     const W4Out out(p, x.g, x.tile, f);
-#pragma unroll 2
-    for (int row = first_row; row < x.rows; row += TR) {
-      float2 v = *reinterpret_cast<const float2*>(from + row * kW4Pitch);
+#pragma unroll 1
+    for (int row0 = first_row; row0 < x.rows; row0 += PER * TR) {
+      float2 v[PER];
 #pragma unroll
-      for (int k = 1; k < SETS; ++k) {
-        const float2 y = *reinterpret_cast<const float2*>(from + (k * Cfg::kRows + row) * kW4Pitch);
-        v.x += y.x;
-        v.y += y.y;
+      for (int i = 0; i < PER; ++i) v[i] = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < SETS; ++k)
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (row0 + i * TR < Cfg::kRows) {
+            const float2 y = *reinterpret_cast<const float2*>(from + (k * Cfg::kRows + row0 + i * TR) * kW4Pitch);
+            v[i].x += y.x;
+            v[i].y += y.y;
+          }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int row = row0 + i * TR;
+        if (row >= x.rows) break;
+        if (whole) out.store(p, x.row0 + row, v[i]);
+        else __stcg(reinterpret_cast<float2*>(slot + row * kW4Feats), v[i]);
       }
-      if (whole) out.store(p, x.row0 + row, v);
-      else __stcg(reinterpret_cast<float2*>(slot + row * kW4Feats), v);
     }
     if (pieces == 2 || !whole) {  // (of two pieces the first is one of a cut tile)
       __syncthreads();
@@ -618,27 +657,28 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
         if (!is_last[k]) continue;
         const W4Piece y = piece[k];
         const W4Out out(p, y.g, y.tile, f);
-        // (four rows of a thread, those behind the last one too: the slots hold 64)
-        for (int row0 = first_row; row0 < y.rows; row0 += 4 * TR) {
-          float2 v[4];
+#pragma unroll 1
+        for (int row0 = first_row; row0 < y.rows; row0 += PER * TR) {
+          float2 v[PER];
           const float* at = p.slots + (size_t)row0 * kW4Feats + f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = make_float2(0.0f, 0.0f);
-#pragma unroll 4
+          for (int i = 0; i < PER; ++i) v[i] = make_float2(0.0f, 0.0f);
+#pragma unroll (PER == 1 ? 8 : 4)
           for (int c = y.c0; c <= y.c1; ++c) {
             const float* of = at + (size_t)(2 * c + (c == y.c0 ? 1 : 0)) * kW4SlotFloats;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (row0 + i * TR < 64) {
+            for (int i = 0; i < PER; ++i)
+              if (row0 + i * TR < Cfg::kRows) {  // (rows behind the last one too)
                 const float2 z = __ldcg(reinterpret_cast<const float2*>(of + i * TR * kW4Feats));
                 v[i].x += z.x;
                 v[i].y += z.y;
               }
-            }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (row0 + i * TR < y.rows) out.store(p, y.row0 + row0 + i * TR, v[i]);
+          for (int i = 0; i < PER; ++i) {
+            if (row0 + i * TR >= y.rows) break;
+            out.store(p, y.row0 + row0 + i * TR, v[i]);
+          }
         }
       }
     }
