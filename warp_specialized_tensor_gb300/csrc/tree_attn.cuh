@@ -8,12 +8,13 @@
 // to itself).  All of them lie in the cache, through the sequence's page table.
 //
 // The query rows of a sequence that share a key head (its tokens x the `group` heads
-// of that key head) are stacked into tiles of 128 rows, so K and V are read once per
-// tile: for a step of few tokens that read is the whole cost, and the 128-row products
-// hide under it even where most rows are empty (S and PV of 128 keys take 1,000
-// clocks of the tensor core, their 64 KB 2,800 clocks of an SM's share of HBM).
+// of that key head) are stacked into tiles of 128 rows, and a CTA takes one tile or two
+// (TILES) through a sequence's keys, so K and V are read once for them: for a step of few
+// tokens that read is the whole cost, and the 128-row products hide under it even where
+// most rows are empty (S and PV of 128 keys take a tile 1,000 clocks of the tensor core,
+// their 64 KB 2,800 clocks of an SM's share of HBM).
 //
-// Schedule: an item is (sequence, key head, tile), a block 128 keys.  The items'
+// Schedule: an item is (sequence, key head, TILES tiles), a block 128 keys.  The items'
 // blocks stand in one line, each CTA takes an equal share (work_split.cuh); the
 // lengths are on the device, so every CTA counts them at its start.  A piece of a cut
 // item leaves its un-normalised O, row maxima m and sums l in the workspace, and a
@@ -30,9 +31,11 @@
 //            a bf16 output's own rounding covers; for fp32 output P is two bf16 (what the
 //            first leaves), off by 2^-16, in the two halves of S's columns
 //   MMA      O += P . V         P from tensor memory, V from shared memory (twice for two P)
-// Three S/P buffers, so S runs ahead of PV; two threads issue the products (a wait
-// costs ~160 clocks while products are in flight, and this way one's products run
-// under the other's wait).
+// One tile has three S/P buffers, so S runs ahead of PV; two tiles have one each (tensor
+// memory holds two O as well), and one's softmax runs under the other's products.  Two
+// threads issue the products (a wait costs ~160 clocks while products are in flight, and
+// this way one's products run under the other's wait).  The softmax takes 64 scores at a
+// time and keeps its P packed, so that two tiles' threads fit the registers.
 //
 // A block that ends behind the context (a sequence's last one or two) takes another
 // path: each row's visible keys come as 128 bits, scores outside them do not count
@@ -41,9 +44,11 @@
 // new token's V that is not finite is cleared too and added again, at the end, to the
 // rows that see it.
 //
-// Roles (256 threads): warp 0 loads Q and K, warp 3 V (a lane per page of a block);
-// warp 1 issues S, warp 2 PV (and owns the tensor memory); warps 4-7 softmax and
-// output, thread = row = tensor memory lane.
+// Roles (128 + 128 TILES threads): warp 0 loads Q and K, warp 3 V (a lane per page of a
+// block); warp 1 issues S, warp 2 PV (and owns the tensor memory); warps 4-7 (and 8-11)
+// softmax and output of a tile, thread = row = tensor memory lane.  Each role walks the
+// share for itself and looks for its next fragment while it works on one: the lengths and
+// page numbers of another sequence are two dependent reads.
 #pragma once
 
 #include "work_split.cuh"
@@ -53,22 +58,23 @@ namespace wst {
 
 constexpr int kTreeBM = 128;
 constexpr int kTreeBN = 128;
-constexpr int kTreeThreads = 256;
-constexpr int kTreeSBufs = 3;
 constexpr int kTreeMaxCtas = 160;
 constexpr float kTreeGrow = 8.0f;       // log2 of how far P may exceed 1
 constexpr float kTreeGrowSum = 256.0f;  // 2^kTreeGrow
 
-template <int DH>
+template <int DH, int TILES>
 struct TreeCfg {
+  static constexpr int kThreads = 128 + 128 * TILES;
+  static constexpr int kSBufs = TILES == 1 ? 3 : 2;
+  static constexpr int kQBufs = TILES == 1 ? 2 : 1;  // of TILES tiles each
   static constexpr int kHalves = DH / 64;
   static constexpr int kTile = kTreeBN * DH * 2;  // bytes of a Q tile or a block of K or V
   static constexpr int kKStages = DH == 128 ? 3 : 6;
   static constexpr int kVStages = DH == 128 ? 2 : 5;
-  static constexpr int kBars = 4 + 2 * kKStages + 2 * kVStages + 3 * kTreeSBufs + 1;
+  static constexpr int kBars = 4 + 2 * kKStages + 2 * kVStages + 3 * kSBufs + TILES;
   static constexpr size_t kSmem = 1024 + (size_t)(2 + kKStages + kVStages) * kTile + 1024;
-  static constexpr int kTmemO = kTreeSBufs * kTreeBN;
-  static_assert(kSmem <= 232448 && kTmemO + DH <= 512 && DH % 64 == 0, "shared memory, tensor memory");
+  static constexpr int kTmemO = kSBufs * kTreeBN;
+  static_assert(kSmem <= 232448 && kTmemO + TILES * DH <= 512 && DH % 64 == 0, "shared memory, tensor memory");
 };
 
 // What the second kernel needs of a cut item; pieces 0: none.
@@ -76,21 +82,22 @@ struct TreeCut {
   int pieces;   // on CTAs c, c + 1, ...
   int token0;   // the first row's token
   int head0;    // the first row's head
-  int rows;
+  int ntok;     // the item's tokens
 };
 
-// Workspace after the header: TreeCut[kTreeMaxCtas], then two slots per CTA (the
-// second for an item that begins in its share): O as [Dh / 4][128 rows][4] fp32, m[128],
-// l[128].
+// Workspace after the header: TreeCut[kTreeMaxCtas], then two pairs of slots per CTA, one
+// slot for each tile (the second pair for an item that begins in its share): O as
+// [Dh / 4][128 rows][4] fp32, m[128], l[128].
 constexpr size_t kTreeCutOffset = kWsHeaderBytes;
 constexpr size_t kTreeSlotOffset = kTreeCutOffset + (size_t)kTreeMaxCtas * sizeof(TreeCut);
 constexpr size_t kTreeSlotFloats = (size_t)128 * kTreeBM + 2 * kTreeBM;
-constexpr size_t kTreeWorkspaceBytes = kTreeSlotOffset + 2 * (size_t)kTreeMaxCtas * kTreeSlotFloats * 4;
+constexpr size_t kTreeWorkspaceBytes = kTreeSlotOffset + 4 * (size_t)kTreeMaxCtas * kTreeSlotFloats * 4;
 static_assert(kTreeSlotOffset % 16 == 0, "alignment of the slots");
 
 struct TreeArgs {
   int B, T, H, Hkv, group;
-  int tokens;             // of a tile: 128 / group
+  int tile_tokens;        // 128 / group
+  int tokens;             // of an item: TILES tiles
   int page_size, max_pages;
   int num_pages;
   int chunk;              // keys of one copy: min(page_size, 128)
@@ -163,7 +170,7 @@ __device__ __forceinline__ void tree_mma_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// sum over i < n of floor((a i + b) / 128), a <= 128, in O(log 128) steps: whole parts
+// sum over i < n of floor((a i + b) / 128), in O(log 128) steps: whole parts
 // are taken out, then the points under the line are counted along the other axis.
 __device__ __forceinline__ long long tree_floor_sum(long long n, long long a, long long b) {
   long long m = 128, sum = 0;
@@ -187,8 +194,8 @@ __device__ __forceinline__ long long tree_floor_sum(long long n, long long a, lo
 struct TreeSeq {
   int a, n;       // its rows of Q: tokens [a, a + n)
   int ctx;
-  int tiles;
-  long long per_head;  // blocks of one key head's items
+  int tiles;           // items of a key head
+  long long per_head;  // their blocks
 
   __device__ __forceinline__ void load(const TreeArgs& p, int b) {
     const int o0 = __ldg(p.q_offsets + b), o1 = __ldg(p.q_offsets + b + 1), c = __ldg(p.context + b);
@@ -199,12 +206,12 @@ struct TreeSeq {
     tiles = (n + p.tokens - 1) / p.tokens;
     per_head = n == 0 ? 0 : before(p, tiles - 1) + blocks(p, tiles - 1);
   }
-  // keys that some row of tile t may see, and their blocks
+  // keys that some row of item t may see, and their blocks
   __device__ __forceinline__ int keys(const TreeArgs& p, int t) const {
     return ctx + (p.mask ? n : min(n, (t + 1) * p.tokens));
   }
   __device__ __forceinline__ int blocks(const TreeArgs& p, int t) const { return (keys(p, t) + kTreeBN - 1) / kTreeBN; }
-  // blocks of the tiles before t (t < tiles)
+  // blocks of the items before t (t < tiles)
   __device__ __forceinline__ long long before(const TreeArgs& p, int t) const {
     if (t == 0) return 0;
     if (p.mask) return (long long)t * ((ctx + n + kTreeBN - 1) / kTreeBN);
@@ -222,8 +229,8 @@ struct TreeWalker {
   // the fragment
   long long item;   // the item's first block
   int jb, je, nb;   // its blocks of the item's nb
-  int token0, ntok; // the tile's tokens
-  int keys;         // keys that the tile may see
+  int token0, ntok; // the item's tokens
+  int keys;         // keys that it may see
 
   __device__ __forceinline__ void init(const TreeArgs& p, long long lo, long long hi_, int b_, long long base_) {
     x = lo;
@@ -273,7 +280,7 @@ struct TreeWalker {
 
 static __device__ __noinline__ void tree_check(const TreeArgs& p) {
   // (the threads of one CTA, a sequence each)
-  for (int b = (int)threadIdx.x; b < p.B; b += kTreeThreads) {
+  for (int b = (int)threadIdx.x; b < p.B; b += (int)blockDim.x) {
     const int o0 = __ldg(p.q_offsets + b), o1 = __ldg(p.q_offsets + b + 1), c = __ldg(p.context + b);
     const long long n = (long long)o1 - o0;
     if ((b == 0 && o0 != 0) || n < 0 || o0 < 0 || o1 > p.T || c < 0 || c + n > (long long)p.max_pages * p.page_size ||
@@ -299,39 +306,53 @@ __device__ __forceinline__ uint32_t tree_visible(const TreeArgs& p, const TreeSe
   return bits;
 }
 
+// 64 consecutive fp32 columns of this thread's lane of tensor memory.
+__device__ __forceinline__ void tree_tmem_load64(uint32_t taddr, float (&v)[64]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) tmem_load32(taddr + 32 * h, *reinterpret_cast<float(*)[32]>(v + 32 * h));
+}
+
 // The K or V blocks of the CTA's share into a ring, by one warp: lane c of a block's
 // copies takes chunk c (a page, or 128 keys of one).
-template <int DH, int STAGES, bool IS_K>
+template <int DH, int TILES, int STAGES, bool IS_K>
 __device__ __forceinline__ void tree_produce(const TreeArgs& p, TreeWalker w, const Guard& guard, const CUtensorMap* tm,
                                              const CUtensorMap* tmQ, uint32_t ring, uint32_t full0, uint32_t empty0,
                                              uint32_t q_ring, uint32_t q_full0, uint32_t q_done0) {
-  using Cfg = TreeCfg<DH>;
+  using Cfg = TreeCfg<DH, TILES>;
+  constexpr uint32_t QB = Cfg::kQBufs;
   const uint32_t lane = lane_id();
   const int per_block = kTreeBN / p.chunk;  // chunks: 1 .. 16
   const int batch = 32 / per_block;         // blocks whose pages one load of the warp fetches
   const int my_block = (int)lane / per_block, my_chunk = (int)lane % per_block;
+  // page of this lane's chunk, `batch` blocks of a fragment at a time; -1: nothing to load
+  auto fetch = [&](const TreeWalker& f, int j0) -> int {
+    const int j = j0 + my_block;
+    const int key = j * kTreeBN + my_chunk * p.chunk;
+    if (j >= f.je || key >= f.keys) return -1;
+    const int i = key / p.page_size;
+    return i < p.max_pages ? __ldg(p.table + (long long)f.b * p.ldt + i) : -1;
+  };
   int st = 0;
   uint32_t ph = 1, it = 0;
-  for (; w.next(p); ++it) {
-    const int* row = p.table + (long long)w.b * p.ldt;
-    // page of this lane's chunk, `batch` blocks at a time; -1: nothing to load
-    auto fetch = [&](int j0) -> int {
-      const int j = j0 + my_block;
-      const int key = j * kTreeBN + my_chunk * p.chunk;
-      if (j >= w.je || key >= w.keys) return -1;
-      const int i = key / p.page_size;
-      return i < p.max_pages ? __ldg(row + i) : -1;
-    };
-    int ids = fetch(w.jb), ids_next = fetch(w.jb + batch);
+  bool has = w.next(p);
+  int ids = has ? fetch(w, w.jb) : -1;
+  TreeWalker nx = w;
+  bool has_next = false;
+  int ids_first = -1;
+  for (; has; w = nx, has = has_next, ids = ids_first, ++it) {
+    int ids_next = fetch(w, w.jb + batch);
     if (IS_K) {
-      const uint32_t qb = it & 1u;
+      const uint32_t qb = it % QB;
       bool ok = true;
       if (lane == 0) {
-        ok = it < 2 || wait_phase(guard, q_done0 + 8u * qb, ((it - 2u) >> 1) & 1u, (kRoleProducer << 16) | 0x900);
+        ok = it < QB || wait_phase(guard, q_done0 + 8u * qb, ((it - QB) / QB) & 1u, (kRoleProducer << 16) | 0x900);
         if (ok) {
-          mbar_arrive_expect_tx(q_full0 + 8u * qb, (uint32_t)(Cfg::kHalves * 128 * p.group * p.tokens));
-          for (int hf = 0; hf < Cfg::kHalves; ++hf)
-            tma_load_3d(q_ring + qb * Cfg::kTile + hf * (kTreeBM * 128), tmQ, q_full0 + 8u * qb, hf * 64, w.h * p.group, w.token0);
+          const int tiles = TILES == 1 || w.ntok <= p.tile_tokens ? 1 : 2;
+          mbar_arrive_expect_tx(q_full0 + 8u * qb, (uint32_t)(tiles * Cfg::kHalves * 128 * p.group * p.tile_tokens));
+          for (int t = 0; t < tiles; ++t)
+            for (int hf = 0; hf < Cfg::kHalves; ++hf)
+              tma_load_3d(q_ring + (qb * TILES + t) * Cfg::kTile + hf * (kTreeBM * 128), tmQ, q_full0 + 8u * qb, hf * 64, w.h * p.group,
+                          w.token0 + t * p.tile_tokens);
         }
       }
       if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
@@ -341,7 +362,7 @@ __device__ __forceinline__ void tree_produce(const TreeArgs& p, TreeWalker w, co
       if (i == batch) {
         i = 0;
         ids = ids_next;
-        ids_next = fetch(j + batch);
+        ids_next = fetch(w, j + batch);
       }
       const int left = w.keys - j * kTreeBN;
       const int chunks = left >= kTreeBN ? per_block : (left + p.chunk - 1) / p.chunk;
@@ -365,41 +386,47 @@ __device__ __forceinline__ void tree_produce(const TreeArgs& p, TreeWalker w, co
         st = 0;
         ph ^= 1u;
       }
+      if (j == min(w.jb + 1, w.je - 1)) {  // the next fragment, while copies of this one are in flight
+        nx = w;
+        has_next = nx.next(p);
+        ids_first = has_next ? fetch(nx, nx.jb) : -1;
+      }
     }
   }
 }
 
 // tmQ {Dh, H, T}, boxes of 64 x group x (tokens of a tile); tmK, tmV {Dh, page_size,
 // Hkv, pages}, boxes of 64 x chunk x 1 x 1; 128-byte swizzle.
-template <int DH, bool OUT_F32>
-__global__ void __launch_bounds__(kTreeThreads, 1)
+template <int DH, int TILES, bool OUT_F32>
+__global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const TreeArgs p) {
-  using Cfg = TreeCfg<DH>;
-  constexpr int KS = Cfg::kKStages, VS = Cfg::kVStages;
+  using Cfg = TreeCfg<DH, TILES>;
+  constexpr int KS = Cfg::kKStages, VS = Cfg::kVStages, SB = Cfg::kSBufs;
+  constexpr uint32_t QB = Cfg::kQBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_addr(smem), sK = sQ + 2 * Cfg::kTile, sV = sK + KS * Cfg::kTile;
   uint8_t* tail = smem + (2 + KS + VS) * Cfg::kTile;  // 1 KB
   uint64_t* bars = reinterpret_cast<uint64_t*>(tail);
   long long* scratch = reinterpret_cast<long long*>(tail + 320);
-  long long* found = scratch + 33;
+  long long* found = scratch + 32;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(found + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* odd_v = tmem_slot + 2;  // [4]: fragment it & 3 met new tokens whose V is not finite
-  static_assert(Cfg::kBars * 8 <= 320 && 320 + 35 * 8 + 24 <= 1024, "the last kilobyte");
+  static_assert(Cfg::kBars * 8 <= 320 && 320 + 34 * 8 + 24 <= 1024, "the last kilobyte");
   const int warp = (int)threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
-  const uint32_t bar0 = smem_addr(bars);
   // q_full[2], q_done[2] (the softmax warps are done with a fragment), k_full, k_empty,
-  // v_full, v_empty, s_full[3], p_full[3], pv_done[3], o_empty
+  // v_full, v_empty, s_full[SB], p_full[SB], pv_done[SB], o_empty[TILES]
+  const uint32_t bar0 = smem_addr(bars);
   const uint32_t q_full = bar0, q_done = bar0 + 16, k_full = bar0 + 32, k_empty = k_full + 8 * KS;
   const uint32_t v_full = k_empty + 8 * KS, v_empty = v_full + 8 * VS, s_full = v_empty + 8 * VS;
-  const uint32_t p_full = s_full + 8 * kTreeSBufs, pv_done = p_full + 8 * kTreeSBufs, o_empty = pv_done + 8 * kTreeSBufs;
+  const uint32_t p_full = s_full + 8 * SB, pv_done = p_full + 8 * SB, o_empty = pv_done + 8 * SB;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1);
-      mbar_init(q_done + 8 * i, 4);
+      mbar_init(q_done + 8 * i, 4 * TILES);
     }
     for (int i = 0; i < KS; ++i) {
       mbar_init(k_full + 8 * i, 1);
@@ -409,12 +436,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_empty + 8 * i, 1);
     }
-    for (int i = 0; i < kTreeSBufs; ++i) {
+    for (int i = 0; i < SB; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 4);
       mbar_init(pv_done + 8 * i, 1);
     }
-    mbar_init(o_empty, 4);
+    for (int i = 0; i < TILES; ++i) mbar_init(o_empty + 8 * i, 4);
     *abort_flag = 0u;
     odd_v[0] = odd_v[1] = odd_v[2] = odd_v[3] = 0u;
     found[0] = found[1] = 0;
@@ -435,7 +462,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     return s.per_head * p.Hkv;
   };
   tc_fence_before_sync();
-  BlockCount<long long, kTreeThreads> counted;
+  BlockCount<long long, Cfg::kThreads> counted;
   const long long W = counted.total(p.B, count, scratch);
   tc_fence_after_sync();
   const Share<long long> share(W, (int)max(1ll, min((long long)gridDim.x, W)));
@@ -468,47 +495,51 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   }
 
   if (warp == 0) {
-    tree_produce<DH, KS, true>(p, w, guard, &tmK, &tmQ, sK, k_full, k_empty, sQ, q_full, q_done);
+    tree_produce<DH, TILES, KS, true>(p, w, guard, &tmK, &tmQ, sK, k_full, k_empty, sQ, q_full, q_done);
   } else if (warp == 3) {
-    tree_produce<DH, VS, false>(p, w, guard, &tmV, nullptr, sV, v_full, v_empty, 0, 0, 0);
+    tree_produce<DH, TILES, VS, false>(p, w, guard, &tmV, nullptr, sV, v_full, v_empty, 0, 0, 0);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ S = Q K^T
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(kTreeBM, kTreeBN, false, false);
       int ks = 0, sb = 0;
-      uint32_t kph = 0, sph = 0, it = 0;
-      long long done = 0;
+      uint32_t kph = 0, it = 0;
+      uint32_t used = 0, sph = 0;  // bit b: buffer b has been used, and the parity of its next use
       bool ok = true;
       for (; ok && w.next(p); ++it) {
-        const uint32_t qb = it & 1u;
-        if (!wait_phase(guard, q_full + 8 * qb, (it >> 1) & 1u, (kRoleMma << 16) | 0x800)) break;
-        const uint32_t q_at = sQ + qb * Cfg::kTile;
-        for (int j = w.jb; j < w.je; ++j, ++done) {
-          // the buffer's last P has been read (three blocks ago), and K is there
-          const bool p_ok = done < kTreeSBufs || mbar_test_wait(pv_done + 8 * sb, sph ^ 1u);
-          const bool k_ok = mbar_test_wait(k_full + 8 * ks, kph);
-          if ((!p_ok && !wait_phase(guard, pv_done + 8 * sb, sph ^ 1u, (kRoleMma << 16) | 0x400 | sb)) ||
-              (!k_ok && !wait_phase(guard, k_full + 8 * ks, kph, (kRoleMma << 16) | ks))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
+        const uint32_t qb = it % QB;
+        if (!wait_phase(guard, q_full + 8 * qb, (it / QB) & 1u, (kRoleMma << 16) | 0x800)) break;
+        const int tiles = TILES == 1 || w.ntok <= p.tile_tokens ? 1 : 2;
+        for (int j = w.jb; ok && j < w.je; ++j) {
           const uint32_t k_at = sK + ks * Cfg::kTile;
-          const uint32_t d = tmem_base + (uint32_t)(kTreeBN * sb);
+          for (int t = 0; t < tiles; ++t) {
+            const int b = TILES == 1 ? sb : t;
+            // the buffer's last P has been read, and K is there
+            const bool p_ok = !((used >> b) & 1u) || mbar_test_wait(pv_done + 8 * b, ((sph >> b) & 1u) ^ 1u);
+            const bool k_ok = t > 0 || mbar_test_wait(k_full + 8 * ks, kph);
+            if ((!p_ok && !wait_phase(guard, pv_done + 8 * b, ((sph >> b) & 1u) ^ 1u, (kRoleMma << 16) | 0x400 | b)) ||
+                (!k_ok && !wait_phase(guard, k_full + 8 * ks, kph, (kRoleMma << 16) | ks))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t q_at = sQ + (qb * TILES + t) * Cfg::kTile;
+            const uint32_t d = tmem_base + (uint32_t)(kTreeBN * b);
 #pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk) {
-            const uint32_t o = (uint32_t)((kk >> 2) * (kTreeBN * 128) + (kk & 3) * 32);
-            umma_bf16<1>(d, sdesc_sw128(q_at + o, 16, 1024), sdesc_sw128(k_at + o, 16, 1024), idesc, kk != 0 ? 1u : 0u);
+            for (int kk = 0; kk < DH / 16; ++kk) {
+              const uint32_t o = (uint32_t)((kk >> 2) * (kTreeBN * 128) + (kk & 3) * 32);
+              umma_bf16<1>(d, sdesc_sw128(q_at + o, 16, 1024), sdesc_sw128(k_at + o, 16, 1024), idesc, kk != 0 ? 1u : 0u);
+            }
+            umma_commit(s_full + 8 * b);
+            used |= 1u << b;
+            sph ^= 1u << b;
+            if (TILES == 1 && ++sb == SB) sb = 0;
           }
-          umma_commit(s_full + 8 * sb);
+          if (!ok) break;
           umma_commit(k_empty + 8 * ks);
           if (++ks == KS) {
             ks = 0;
             kph ^= 1u;
-          }
-          if (++sb == kTreeSBufs) {
-            sb = 0;
-            sph ^= 1u;
           }
         }
       }
@@ -518,59 +549,71 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(kTreeBM, DH, false, true);
       int vs = 0, sb = 0;
-      uint32_t vph = 0, sph = 0, it = 0;
+      uint32_t vph = 0;
+      uint32_t sph = 0;            // bit b: parity of buffer b's next use
+      uint32_t oph = (1u << TILES) - 1u;  // bit t: parity of O t's next release
       bool ok = true;
-      for (; ok && w.next(p); ++it) {
-        for (int j = w.jb; j < w.je; ++j) {
-          const bool v_ok = mbar_test_wait(v_full + 8 * vs, vph);
-          const bool p_ok = mbar_test_wait(p_full + 8 * sb, sph);
-          if ((!v_ok && !wait_phase(guard, v_full + 8 * vs, vph, (kRoleMma << 16) | 0x10 | vs)) ||
-              (!p_ok && !wait_phase(guard, p_full + 8 * sb, sph, (kRoleMma << 16) | 0x200 | sb)) ||
-              (j == w.jb && !wait_phase(guard, o_empty, (it & 1u) ^ 1u, (kRoleMma << 16) | 0x300))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
+      while (ok && w.next(p)) {
+        const int tiles = TILES == 1 || w.ntok <= p.tile_tokens ? 1 : 2;
+        for (int j = w.jb; ok && j < w.je; ++j) {
           const uint64_t vd = sdesc_sw128(sV + vs * Cfg::kTile, kTreeBN * 128, 1024);
-          const uint32_t a = tmem_base + (uint32_t)(kTreeBN * sb);
+          for (int t = 0; t < tiles; ++t) {
+            const int b = TILES == 1 ? sb : t;
+            const bool v_ok = t > 0 || mbar_test_wait(v_full + 8 * vs, vph);
+            const bool p_ok = mbar_test_wait(p_full + 8 * b, (sph >> b) & 1u);
+            if ((!v_ok && !wait_phase(guard, v_full + 8 * vs, vph, (kRoleMma << 16) | 0x10 | vs)) ||
+                (!p_ok && !wait_phase(guard, p_full + 8 * b, (sph >> b) & 1u, (kRoleMma << 16) | 0x200 | b)) ||
+                (j == w.jb && !wait_phase(guard, o_empty + 8 * t, (oph >> t) & 1u, (kRoleMma << 16) | 0x300 | t))) {
+              ok = false;
+              break;
+            }
+            if (j == w.jb) oph ^= 1u << t;
+            tc_fence_after_sync();
+            const uint32_t a = tmem_base + (uint32_t)(kTreeBN * b), d = tmem_base + (uint32_t)(Cfg::kTmemO + t * DH);
 #pragma unroll
-          for (int kk = 0; kk < kTreeBN / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of V
-            tree_mma_ts(tmem_base + Cfg::kTmemO, a + (uint32_t)(kk * 8), vd + (uint32_t)(kk * 128), idesc,
-                        (j > w.jb || kk != 0) ? 1u : 0u);
-          if constexpr (OUT_F32) {
+            for (int kk = 0; kk < kTreeBN / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of V
+              tree_mma_ts(d, a + (uint32_t)(kk * 8), vd + (uint32_t)(kk * 128), idesc, (j > w.jb || kk != 0) ? 1u : 0u);
+            if constexpr (OUT_F32) {
 #pragma unroll
-            for (int kk = 0; kk < kTreeBN / 16; ++kk)
-              tree_mma_ts(tmem_base + Cfg::kTmemO, a + (uint32_t)(64 + kk * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
+              for (int kk = 0; kk < kTreeBN / 16; ++kk) tree_mma_ts(d, a + (uint32_t)(64 + kk * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
+            }
+            umma_commit(pv_done + 8 * b);
+            sph ^= 1u << b;
+            if (TILES == 1 && ++sb == SB) sb = 0;
           }
-          umma_commit(pv_done + 8 * sb);
+          if (!ok) break;
           umma_commit(v_empty + 8 * vs);
           if (++vs == VS) {
             vs = 0;
             vph ^= 1u;
-          }
-          if (++sb == kTreeSBufs) {
-            sb = 0;
-            sph ^= 1u;
           }
         }
       }
     }
   } else {
     // ------------------------------------------------------------------ softmax, output
+    const int t = TILES == 1 ? 0 : (warp >> 2) - 1;  // the tile
     const int q = warp & 3;
     const int row = q * 32 + (int)lane;
     const uint32_t t_lane = tmem_base + ((uint32_t)(q * 32) << 16);
-    const uint32_t t_o = t_lane + Cfg::kTmemO;
+    const uint32_t t_o = t_lane + Cfg::kTmemO + t * DH;
     const int my_tok = row / p.group, my_head = row - my_tok * p.group;
     const float cs = p.cs;
-    int sb = 0, vs = 0;
+    int sb = t, vs = 0;
     uint32_t sph = 0, vph = 0, it = 0;
     long long blocks = 0;  // before this one
     bool wrote_cut = false, ok = true;
     for (; ok && w.next(p); ++it) {
-      const int rows = w.ntok * p.group;
+      const int rows = min(p.tile_tokens, w.ntok - t * p.tile_tokens) * p.group;
+      if (TILES == 2 && rows <= 0) {
+        // A fragment without this tile: over when its Q is there (so that the barrier's
+        // phases are told apart).
+        ok = warp_wait_phase(guard, q_full + 8 * (it % QB), (it / QB) & 1u, (kRoleEpilogue << 16) | 0x700);
+        if (ok && lane == 0) mbar_arrive(q_done + 8 * (it % QB));
+        continue;
+      }
       const bool active = q * 32 < rows;  // (of the whole warp)
-      const int ti = w.t * p.tokens + my_tok;
+      const int ti = w.t * p.tokens + t * p.tile_tokens + my_tok;
       float m = -INFINITY, l = 0.0f;
       int last_sb = 0;
       uint32_t last_ph = 0;
@@ -587,53 +630,64 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         tc_fence_after_sync();
         if (active) {
-          float s[kTreeBN];
-          float rs8[8];
           const uint32_t t_s = t_lane + (uint32_t)(kTreeBN * sb);
-          auto load_scores = [&]() {
+          uint32_t hi[kTreeBN / 2];                     // P as pairs of bf16
+          uint32_t lo[OUT_F32 ? kTreeBN / 2 : 1];       // and what they leave
+          float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          // P = 2^(cs S - top) of 64 scores.  `once`: with one rounding, which is against
+          // the exact product (a score that equals a rounded top is off by its rounding:
+          // nothing for all of a row's alike, unless the scores pass 2^24).
+          auto probabilities = [&](int h, float top, bool masked, bool once) {
+            float x[64];
+            tree_tmem_load64(t_s + 64 * h, x);
 #pragma unroll
-            for (int c = 0; c < kTreeBN / 32; ++c) tmem_load32(t_s + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
+            for (int i = 0; i < 32; ++i) {
+              if (once) {
+                tree_fma2(x[2 * i], x[2 * i + 1], cs, -top);
+              } else {
+                x[2 * i] = __fadd_rn(__fmul_rn(x[2 * i], cs), -top);
+                x[2 * i + 1] = __fadd_rn(__fmul_rn(x[2 * i + 1], cs), -top);
+              }
+              x[2 * i] = tree_ex2(x[2 * i]);
+              x[2 * i + 1] = tree_ex2(x[2 * i + 1]);
+              if (masked) {
+                const uint32_t v = vis[2 * h + (i >> 4)] >> (2 * (i & 15));
+                if (!(v & 1u)) x[2 * i] = 0.0f;
+                if (!(v & 2u)) x[2 * i + 1] = 0.0f;
+              }
+              tree_add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], x[2 * i], x[2 * i + 1]);
+              const uint32_t y = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+              hi[32 * h + i] = y;
+              if constexpr (OUT_F32)
+                lo[32 * h + i] = pack_bf16x2(x[2 * i] - __uint_as_float(y << 16), x[2 * i + 1] - __uint_as_float(y & 0xffff0000u));
+            }
           };
-          load_scores();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) rs8[i] = 0.0f;
-          auto sum8 = [&]() { return ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7])); };
+          auto sum = [&]() { return (rs[0] + rs[1]) + (rs[2] + rs[3]); };
           bool done = false;
-          if (inner && j > w.jb) {
+          if (inner && j > w.jb && __all_sync(0xffffffffu, fabsf(m) < 1.0e6f || row >= rows)) {
             // With the maximum so far: every P is positive, so a row sum of at most 2^8
             // proves that no P exceeds it and the maximum need not be looked for.
-#pragma unroll
-            for (int i = 0; i < kTreeBN / 2; ++i) {
-              tree_fma2(s[2 * i], s[2 * i + 1], cs, -m);
-              s[2 * i] = tree_ex2(s[2 * i]);
-              s[2 * i + 1] = tree_ex2(s[2 * i + 1]);
-              tree_add2(rs8[2 * (i & 3)], rs8[2 * (i & 3) + 1], s[2 * i], s[2 * i + 1]);
-            }
-            done = __all_sync(0xffffffffu, sum8() <= kTreeGrowSum || row >= rows) != 0;
-            if (!done) {
-              load_scores();
-#pragma unroll
-              for (int i = 0; i < 8; ++i) rs8[i] = 0.0f;
-            }
+            probabilities(0, m, false, true);
+            probabilities(1, m, false, true);
+            done = __all_sync(0xffffffffu, sum() <= kTreeGrowSum || row >= rows) != 0;
+            if (!done) rs[0] = rs[1] = rs[2] = rs[3] = 0.0f;
           }
           if (!done) {
-            float e8[8];
+            float e[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              float x[64];
+              tree_tmem_load64(t_s + 64 * h, x);
+              if (inner) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e8[i] = -INFINITY;
-            if (inner) {
+                for (int i = 0; i < 64; ++i) e[i & 3] = fmaxf(e[i & 3], __fmul_rn(x[i], cs));
+              } else {
+                const uint32_t v0 = h ? vis[2] : vis[0], v1 = h ? vis[3] : vis[1];
 #pragma unroll
-              for (int i = 0; i < kTreeBN; ++i) {
-                s[i] *= cs;
-                e8[i & 7] = fmaxf(e8[i & 7], s[i]);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < kTreeBN; ++i) {
-                s[i] = (vis[i >> 5] >> (i & 31)) & 1u ? s[i] * cs : -INFINITY;
-                e8[i & 7] = fmaxf(e8[i & 7], s[i]);
+                for (int i = 0; i < 64; ++i) e[i & 3] = ((i < 32 ? v0 : v1) >> (i & 31)) & 1u ? fmaxf(e[i & 3], __fmul_rn(x[i], cs)) : e[i & 3];
               }
             }
-            const float mx = fmaxf(fmaxf(fmaxf(e8[0], e8[1]), fmaxf(e8[2], e8[3])), fmaxf(fmaxf(e8[4], e8[5]), fmaxf(e8[6], e8[7])));
+            const float mx = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
             if (j == w.jb) {
               m = mx;  // the first PV product overwrites O
             } else {
@@ -649,7 +703,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                   l *= alpha;
                   m = mx;
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < DH / 32; ++c) {
                   float v[32];
                   tmem_load32(t_o + c * 32, v);
@@ -660,52 +714,33 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 tree_tmem_store_wait();
               }
             }
-            // (a row that has seen no key yet: every P is 2^-inf)
-            const float ms = !inner && m == -INFINITY ? 0.0f : m;
-#pragma unroll
-            for (int i = 0; i < kTreeBN; ++i) {
-              s[i] = tree_ex2(s[i] - ms);
-              rs8[i & 7] += s[i];
-            }
+            // (a row that has seen no key yet: its P are all masked)
+            const float top = !inner && m == -INFINITY ? 0.0f : m;
+            probabilities(0, top, !inner, false);
+            probabilities(1, top, !inner, false);
           }
-          l += sum8();
+          l += sum();
 #pragma unroll
-          for (int h2 = 0; h2 < kTreeBN / 64; ++h2) {
-            float pk[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              float& x0 = s[64 * h2 + 2 * c];
-              float& x1 = s[64 * h2 + 2 * c + 1];
-              const uint32_t hi = pack_bf16x2(x0, x1);
-              pk[c] = __uint_as_float(hi);
-              if constexpr (OUT_F32) {
-                x0 -= __uint_as_float(hi << 16);
-                x1 -= __uint_as_float(hi & 0xffff0000u);
-              }
-            }
-            tree_tmem_store32(t_s + 32 * h2, pk);
-          }
+          for (int h = 0; h < 2; ++h)
+            tree_tmem_store32(t_s + 32 * h, *reinterpret_cast<const float(*)[32]>(hi + 32 * h));
           if constexpr (OUT_F32) {
 #pragma unroll
-            for (int h2 = 0; h2 < kTreeBN / 64; ++h2) {
-              float pk[32];
-#pragma unroll
-              for (int c = 0; c < 32; ++c) pk[c] = __uint_as_float(pack_bf16x2(s[64 * h2 + 2 * c], s[64 * h2 + 2 * c + 1]));
-              tree_tmem_store32(t_s + 64 + 32 * h2, pk);
-            }
+            for (int h = 0; h < 2; ++h)
+              tree_tmem_store32(t_s + 64 + 32 * h, *reinterpret_cast<const float(*)[32]>(lo + 32 * h));
           }
           tree_tmem_store_wait();
         }
-        if (!inner) {
+        if (!inner && t == 0) {
           // V: clear the keys behind the sequence and what is not finite of the new
-          // tokens; thread = key.  These warps wait for V here only, and a parity tells
-          // two phases apart: the stage's last use has to be over first.  (S_g was issued
-          // after PV_{g-3}: with three stages or more it is.)
+          // tokens; thread = key.  (The other tile's product with this V is issued after
+          // this one's.)  These warps wait for V here only, and a parity tells two phases
+          // apart: the stage's last use has to be over first.  (S_g was issued after
+          // PV_{g-3}, with two tiles after PV_{g-1}: with more stages than two it is.)
           static_assert(VS >= 2, "stages of V");
-          if constexpr (VS == 2) {
+          if constexpr (VS == 2 && TILES == 1) {
             const bool wraps = sb < 2;  // block g - 2 used the buffers' round before this one
             if (blocks >= 2 &&
-                !warp_wait_phase(guard, pv_done + 8 * (sb + 1 == kTreeSBufs ? 0 : sb + 1), wraps ? sph ^ 1u : sph, (kRoleEpilogue << 16) | 0x600)) {
+                !warp_wait_phase(guard, pv_done + 8 * (sb + 1 == SB ? 0 : sb + 1), wraps ? sph ^ 1u : sph, (kRoleEpilogue << 16) | 0x600)) {
               ok = false;
               break;
             }
@@ -759,7 +794,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         last_sb = sb;
         last_ph = sph;
         ++blocks;
-        if (++sb == kTreeSBufs) {
+        if (TILES == 2) {
+          sph ^= 1u;
+        } else if (++sb == SB) {
           sb = 0;
           sph ^= 1u;
         }
@@ -779,8 +816,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const bool whole = w.jb == 0 && w.je == w.nb;
         const bool odd = odd_v[it & 3u] != 0u;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const long long at = (long long)(w.token0 + my_tok) * p.ldo + (long long)(w.h * p.group + my_head) * DH;
-        float* slot = whole ? nullptr : p.slots + (size_t)(2 * blockIdx.x + (w.jb == 0 ? 1 : 0)) * kTreeSlotFloats;
+        const long long at = (long long)(w.token0 + t * p.tile_tokens + my_tok) * p.ldo + (long long)(w.h * p.group + my_head) * DH;
+        float* slot = whole ? nullptr : p.slots + (size_t)((2 * blockIdx.x + (w.jb == 0 ? 1 : 0)) * 2 + t) * kTreeSlotFloats;
 #pragma unroll 1
         for (int c = 0; c < DH / 32; ++c) {
           float v[32];
@@ -828,24 +865,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           __stcg(slot + 128 * kTreeBM + row, m);
           __stcg(slot + 128 * kTreeBM + kTreeBM + row, l);
         }
-        if (!whole && w.jb == 0 && row == 0) {
+        if (!whole && w.jb == 0 && row == 0 && t == 0) {
           p.cuts[blockIdx.x] =
-              TreeCut{share.owner(w.item + w.nb - 1) - (int)blockIdx.x + 1, w.token0, w.h * p.group, rows};
+              TreeCut{share.owner(w.item + w.nb - 1) - (int)blockIdx.x + 1, w.token0, w.h * p.group, w.ntok};
           wrote_cut = true;
         }
       }
       // The flag of the fragment after next: the products of this one are done, so every
       // warp has left the fragment before it, and none enters that one before this warp
       // has taken part in the next.
-      if (row == 0) odd_v[(it + 2u) & 3u] = 0u;
+      if (row == 0 && t == 0) odd_v[(it + 2u) & 3u] = 0u;
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(o_empty);
-        mbar_arrive(q_done + 8 * (it & 1u));
+        mbar_arrive(o_empty + 8 * t);
+        mbar_arrive(q_done + 8 * (it % QB));
       }
     }
-    if (p.split && row == 0 && !wrote_cut) p.cuts[blockIdx.x].pieces = 0;
+    if (p.split && row == 0 && t == 0 && !wrote_cut) p.cuts[blockIdx.x].pieces = 0;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before_sync();
@@ -858,15 +895,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 }
 
 // The cut items' pieces added up: blockIdx.x is the CTA in whose share an item
-// begins; a thread takes four components of a row.
+// begins, blockIdx.z the tile; a thread takes four components of a row.
 template <int DH, bool OUT_F32>
 __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const TreeCut cut = p.cuts[blockIdx.x];
   const int i = (int)(blockIdx.y * 256 + threadIdx.x);
-  const int row = i % kTreeBM, quad = i / kTreeBM;
-  if (cut.pieces == 0 || row >= cut.rows) return;
-  auto slot = [&](int k) { return p.slots + (size_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * kTreeSlotFloats; };
+  const int row = i % kTreeBM, quad = i / kTreeBM, t = (int)blockIdx.z;
+  if (cut.pieces == 0 || row >= min(p.tile_tokens, cut.ntok - t * p.tile_tokens) * p.group) return;
+  auto slot = [&](int k) { return p.slots + (size_t)((2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * 2 + t) * kTreeSlotFloats; };
   float m = -INFINITY;
   for (int k = 0; k < cut.pieces; ++k) m = fmaxf(m, __ldcg(slot(k) + 128 * kTreeBM + row));
   const float ms = m == -INFINITY ? 0.0f : m;
@@ -886,7 +923,7 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const bool none = l == 0.0f;
   const int tok = row / p.group, head = row - tok * p.group;
-  const long long at = (long long)(cut.token0 + tok) * p.ldo + (long long)(cut.head0 + head) * DH + quad * 4;
+  const long long at = (long long)(cut.token0 + t * p.tile_tokens + tok) * p.ldo + (long long)(cut.head0 + head) * DH + quad * 4;
   const float y0 = none ? 0.0f : o.x * inv, y1 = none ? 0.0f : o.y * inv, y2 = none ? 0.0f : o.z * inv, y3 = none ? 0.0f : o.w * inv;
   if constexpr (OUT_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + at) = make_float4(y0, y1, y2, y3);
   else
