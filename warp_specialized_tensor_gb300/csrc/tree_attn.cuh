@@ -34,8 +34,7 @@
 // One tile has three S/P buffers, so S runs ahead of PV; two tiles have one each (tensor
 // memory holds two O as well), and one's softmax runs under the other's products.  Two
 // threads issue the products (a wait costs ~160 clocks while products are in flight, and
-// this way one's products run under the other's wait).  The softmax takes 64 scores at a
-// time and keeps its P packed, so that two tiles' threads fit the registers.
+// this way one's products run under the other's wait).
 //
 // A block that ends behind the context (a sequence's last one or two) takes another
 // path: each row's visible keys come as 128 bits, scores outside them do not count
@@ -170,23 +169,32 @@ __device__ __forceinline__ void tree_mma_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// sum over i < n of floor((a i + b) / 128), in O(log 128) steps: whole parts
-// are taken out, then the points under the line are counted along the other axis.
-__device__ __forceinline__ long long tree_floor_sum(long long n, long long a, long long b) {
-  long long m = 128, sum = 0;
-  while (n > 0) {
-    sum += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
-    a %= m;
-    b %= m;
-    const long long top = a * n + b;  // (the line's value behind the last point, times m)
+// sum over i < n of floor((a i + b) / 128), n < 2^23, a <= 256, b < 2^31: whole parts are
+// taken out, then the points under the line are counted along the other axis, until none
+// are left (a logarithm of 128 steps; the quotients fit 32 bits).
+__device__ __forceinline__ long long tree_floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+  long long sum = (long long)(a >> 7) * ((long long)n * (n - 1) / 2) + (long long)(b >> 7) * n;
+  a &= 127u;
+  b &= 127u;
+  uint32_t m = 128;
+  while (true) {
+    const uint32_t top = a * n + b;  // (the line's value behind the last point, times m)
     n = top / m;
-    b = top % m;
-    const long long swap = a;
-    a = m;
-    m = swap;
-    if (m == 0) break;
+    if (n == 0) return sum;
+    b = top - n * m;
+    const uint32_t whole = m / a;  // (a > 0: else top < m)
+    const uint32_t rest = m - whole * a;
+    m = a;
+    a = rest;
+    sum += (long long)whole * ((long long)n * (n - 1) / 2) + (long long)(b / m) * n;
+    b %= m;
   }
-  return sum;
+}
+
+// r / d, in 32 bits where both fit (nearly always)
+__device__ __forceinline__ long long tree_div(long long r, long long d) {
+  if (((r | d) >> 32) == 0) return (long long)((uint32_t)r / (uint32_t)d);
+  return r / d;
 }
 
 // One sequence, as every role sees it (what breaks the rules is clamped; the checks
@@ -215,7 +223,7 @@ struct TreeSeq {
   __device__ __forceinline__ long long before(const TreeArgs& p, int t) const {
     if (t == 0) return 0;
     if (p.mask) return (long long)t * ((ctx + n + kTreeBN - 1) / kTreeBN);
-    return tree_floor_sum(t, p.tokens, (long long)ctx + p.tokens + kTreeBN - 1);
+    return tree_floor_sum((uint32_t)t, (uint32_t)p.tokens, (uint32_t)(ctx + p.tokens + kTreeBN - 1));
   }
 };
 
@@ -240,7 +248,7 @@ struct TreeWalker {
     if (x >= hi) return;
     s.load(p, b);
     const long long r = x - base;
-    h = (int)(r / s.per_head);
+    h = (int)tree_div(r, s.per_head);
     const long long at = r - h * s.per_head;
     int lo_t = 0, hi_t = s.tiles - 1;  // the last tile with before(t) <= at
     while (lo_t < hi_t) {
@@ -306,10 +314,31 @@ __device__ __forceinline__ uint32_t tree_visible(const TreeArgs& p, const TreeSe
   return bits;
 }
 
-// 64 consecutive fp32 columns of this thread's lane of tensor memory.
-__device__ __forceinline__ void tree_tmem_load64(uint32_t taddr, float (&v)[64]) {
+// 32 consecutive columns of this thread's lane of tensor memory, without the wait.
+__device__ __forceinline__ void tree_tmem_load32(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+        "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+        "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for the thread's loads; v passes through, so that no use of it moves ahead.
+__device__ __forceinline__ void tree_tmem_load_wait(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int h = 0; h < 2; ++h) tmem_load32(taddr + 32 * h, *reinterpret_cast<float(*)[32]>(v + 32 * h));
+  for (int i = 0; i < 128; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void tree_tmem_store16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 
 // The K or V blocks of the CTA's share into a ring, by one warp: lane c of a block's
@@ -324,12 +353,12 @@ __device__ __forceinline__ void tree_produce(const TreeArgs& p, TreeWalker w, co
   const int per_block = kTreeBN / p.chunk;  // chunks: 1 .. 16
   const int batch = 32 / per_block;         // blocks whose pages one load of the warp fetches
   const int my_block = (int)lane / per_block, my_chunk = (int)lane % per_block;
+  const int page_blocks = p.page_size / kTreeBN;  // blocks of a page (0: a page is a chunk)
   // page of this lane's chunk, `batch` blocks of a fragment at a time; -1: nothing to load
   auto fetch = [&](const TreeWalker& f, int j0) -> int {
     const int j = j0 + my_block;
-    const int key = j * kTreeBN + my_chunk * p.chunk;
-    if (j >= f.je || key >= f.keys) return -1;
-    const int i = key / p.page_size;
+    if (j >= f.je || j * kTreeBN + my_chunk * p.chunk >= f.keys) return -1;
+    const int i = page_blocks ? j / page_blocks : j * per_block + my_chunk;
     return i < p.max_pages ? __ldg(p.table + (long long)f.b * p.ldt + i) : -1;
   };
   int st = 0;
@@ -358,6 +387,7 @@ __device__ __forceinline__ void tree_produce(const TreeArgs& p, TreeWalker w, co
       if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
     }
     int i = 0;  // block of the batch
+    int in_page = page_blocks ? w.jb % page_blocks : 0;
     for (int j = w.jb; j < w.je; ++j) {
       if (i == batch) {
         i = 0;
@@ -366,7 +396,7 @@ __device__ __forceinline__ void tree_produce(const TreeArgs& p, TreeWalker w, co
       }
       const int left = w.keys - j * kTreeBN;
       const int chunks = left >= kTreeBN ? per_block : (left + p.chunk - 1) / p.chunk;
-      const int page = __shfl_sync(0xffffffffu, ids, (i * per_block + (int)lane % per_block) & 31);
+      const int page = __shfl_sync(0xffffffffu, ids, (i * per_block + my_chunk) & 31);
       ++i;
       bool ok = true;
       if (lane == 0) {
@@ -377,11 +407,11 @@ __device__ __forceinline__ void tree_produce(const TreeArgs& p, TreeWalker w, co
       if ((int)lane < chunks) {
         // (a page outside the cache reads as zeros)
         if (page < 0 || page >= p.num_pages) latch_error(p.ws, 1u, (kRoleProducer << 16) | 0x20);
-        const int key = j * kTreeBN + (int)lane * p.chunk;
         const uint32_t dst = ring + st * Cfg::kTile + (uint32_t)((int)lane * p.chunk * 128);
         for (int hf = 0; hf < Cfg::kHalves; ++hf)
-          tree_tma_load_4d(dst + hf * (kTreeBN * 128), tm, full0 + 8u * st, hf * 64, key % p.page_size, w.h, page);
+          tree_tma_load_4d(dst + hf * (kTreeBN * 128), tm, full0 + 8u * st, hf * 64, in_page * kTreeBN, w.h, page);
       }
+      if (++in_page >= page_blocks) in_page = 0;
       if (++st == STAGES) {
         st = 0;
         ph ^= 1u;
@@ -572,10 +602,12 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
             const uint32_t a = tmem_base + (uint32_t)(kTreeBN * b), d = tmem_base + (uint32_t)(Cfg::kTmemO + t * DH);
 #pragma unroll
             for (int kk = 0; kk < kTreeBN / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of V
-              tree_mma_ts(d, a + (uint32_t)(kk * 8), vd + (uint32_t)(kk * 128), idesc, (j > w.jb || kk != 0) ? 1u : 0u);
+              tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc,
+                          (j > w.jb || kk != 0) ? 1u : 0u);
             if constexpr (OUT_F32) {
 #pragma unroll
-              for (int kk = 0; kk < kTreeBN / 16; ++kk) tree_mma_ts(d, a + (uint32_t)(64 + kk * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
+              for (int kk = 0; kk < kTreeBN / 16; ++kk)
+                tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + 16 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
             }
             umma_commit(pv_done + 8 * b);
             sph ^= 1u << b;
@@ -619,11 +651,6 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
       uint32_t last_ph = 0;
       for (int j = w.jb; j < w.je; ++j) {
         const bool inner = (j + 1) * kTreeBN <= w.s.ctx;  // every row sees every key
-        uint32_t vis[4] = {0u, 0u, 0u, 0u};
-        if (!inner && row < rows) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) vis[i] = tree_visible(p, w.s, ti, j * kTreeBN - w.s.ctx + 32 * i);
-        }
         if (!warp_wait_phase(guard, s_full + 8 * sb, sph, (kRoleEpilogue << 16) | sb)) {
           ok = false;
           break;
@@ -631,63 +658,68 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
         tc_fence_after_sync();
         if (active) {
           const uint32_t t_s = t_lane + (uint32_t)(kTreeBN * sb);
-          uint32_t hi[kTreeBN / 2];                     // P as pairs of bf16
-          uint32_t lo[OUT_F32 ? kTreeBN / 2 : 1];       // and what they leave
+          // P of 32 keys goes over their scores: 16 columns of bf16 pairs, then (fp32
+          // output) 16 of what those leave.
           float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          // P = 2^(cs S - top) of 64 scores.  `once`: with one rounding, which is against
-          // the exact product (a score that equals a rounded top is off by its rounding:
-          // nothing for all of a row's alike, unless the scores pass 2^24).
-          auto probabilities = [&](int h, float top, bool masked, bool once) {
-            float x[64];
-            tree_tmem_load64(t_s + 64 * h, x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (once) {
-                tree_fma2(x[2 * i], x[2 * i + 1], cs, -top);
-              } else {
-                x[2 * i] = __fadd_rn(__fmul_rn(x[2 * i], cs), -top);
-                x[2 * i + 1] = __fadd_rn(__fmul_rn(x[2 * i + 1], cs), -top);
-              }
-              x[2 * i] = tree_ex2(x[2 * i]);
-              x[2 * i + 1] = tree_ex2(x[2 * i + 1]);
-              if (masked) {
-                const uint32_t v = vis[2 * h + (i >> 4)] >> (2 * (i & 15));
-                if (!(v & 1u)) x[2 * i] = 0.0f;
-                if (!(v & 2u)) x[2 * i + 1] = 0.0f;
-              }
-              tree_add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], x[2 * i], x[2 * i + 1]);
-              const uint32_t y = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-              hi[32 * h + i] = y;
-              if constexpr (OUT_F32)
-                lo[32 * h + i] = pack_bf16x2(x[2 * i] - __uint_as_float(y << 16), x[2 * i + 1] - __uint_as_float(y & 0xffff0000u));
-            }
-          };
           auto sum = [&]() { return (rs[0] + rs[1]) + (rs[2] + rs[3]); };
           bool done = false;
           if (inner && j > w.jb && __all_sync(0xffffffffu, fabsf(m) < 1.0e6f || row >= rows)) {
             // With the maximum so far: every P is positive, so a row sum of at most 2^8
-            // proves that no P exceeds it and the maximum need not be looked for.
-            probabilities(0, m, false, true);
-            probabilities(1, m, false, true);
+            // proves that no P exceeds it and the maximum need not be looked for.  (cs S - m
+            // is rounded once, m is a rounded product: their difference is the same factor
+            // for all of a row, and small while m is.)
+            float x[kTreeBN];
+#pragma unroll
+            for (int c = 0; c < kTreeBN / 32; ++c) tree_tmem_load32(t_s + 32 * c, x + 32 * c);
+            tree_tmem_load_wait(x);
+            uint32_t hi[kTreeBN / 2], lo[OUT_F32 ? kTreeBN / 2 : 1];
+#pragma unroll
+            for (int i = 0; i < kTreeBN / 2; ++i) {
+              float& x0 = x[2 * i];
+              float& x1 = x[2 * i + 1];
+              tree_fma2(x0, x1, cs, -m);
+              x0 = tree_ex2(x0);
+              x1 = tree_ex2(x1);
+              tree_add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], x0, x1);
+              hi[i] = pack_bf16x2(x0, x1);
+              if constexpr (OUT_F32) lo[i] = pack_bf16x2(x0 - __uint_as_float(hi[i] << 16), x1 - __uint_as_float(hi[i] & 0xffff0000u));
+            }
             done = __all_sync(0xffffffffu, sum() <= kTreeGrowSum || row >= rows) != 0;
-            if (!done) rs[0] = rs[1] = rs[2] = rs[3] = 0.0f;
+            if (done) {
+#pragma unroll
+              for (int c = 0; c < kTreeBN / 32; ++c) {
+                tree_tmem_store16(t_s + 32 * c, hi + 16 * c);
+                if constexpr (OUT_F32) tree_tmem_store16(t_s + 32 * c + 16, lo + 16 * c);
+              }
+            } else {
+              rs[0] = rs[1] = rs[2] = rs[3] = 0.0f;
+            }
           }
           if (!done) {
-            float e[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              float x[64];
-              tree_tmem_load64(t_s + 64 * h, x);
-              if (inner) {
+            // Any other block, 32 keys at a time (loops: this code runs a few times in a
+            // fragment, and unrolled it took longer to fetch than to run).  First cs S,
+            // -inf where the row sees nothing, back over the scores.
+            uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+            if (!inner && row < rows) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) e[i & 3] = fmaxf(e[i & 3], __fmul_rn(x[i], cs));
-              } else {
-                const uint32_t v0 = h ? vis[2] : vis[0], v1 = h ? vis[3] : vis[1];
-#pragma unroll
-                for (int i = 0; i < 64; ++i) e[i & 3] = ((i < 32 ? v0 : v1) >> (i & 31)) & 1u ? fmaxf(e[i & 3], __fmul_rn(x[i], cs)) : e[i & 3];
-              }
+              for (int i = 0; i < 4; ++i) vis[i] = tree_visible(p, w.s, ti, j * kTreeBN - w.s.ctx + 32 * i);
             }
-            const float mx = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < kTreeBN / 32; ++c) {
+              float x[32];
+              tmem_load32(t_s + 32 * c, x);
+              const uint32_t v = c < 2 ? (c ? vis[1] : vis[0]) : (c > 2 ? vis[3] : vis[2]);
+              float e[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                x[i] = v & (1u << i) ? x[i] * cs : -INFINITY;
+                e[i & 3] = fmaxf(e[i & 3], x[i]);
+              }
+              mx = fmaxf(mx, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])));
+              tree_tmem_store32(t_s + 32 * c, x);
+            }
+            tree_tmem_store_wait();
             if (j == w.jb) {
               m = mx;  // the first PV product overwrites O
             } else {
@@ -714,20 +746,28 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
                 tree_tmem_store_wait();
               }
             }
-            // (a row that has seen no key yet: its P are all masked)
+            // (a row that has seen no key yet: all its scores are -inf, its P zero)
             const float top = !inner && m == -INFINITY ? 0.0f : m;
-            probabilities(0, top, !inner, false);
-            probabilities(1, top, !inner, false);
+#pragma unroll 1
+            for (int c = 0; c < kTreeBN / 32; ++c) {
+              float x[32];
+              tmem_load32(t_s + 32 * c, x);
+              uint32_t hi[16], lo[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float& x0 = x[2 * i];
+                float& x1 = x[2 * i + 1];
+                x0 = tree_ex2(x0 - top);
+                x1 = tree_ex2(x1 - top);
+                tree_add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], x0, x1);
+                hi[i] = pack_bf16x2(x0, x1);
+                if constexpr (OUT_F32) lo[i] = pack_bf16x2(x0 - __uint_as_float(hi[i] << 16), x1 - __uint_as_float(hi[i] & 0xffff0000u));
+              }
+              tree_tmem_store16(t_s + 32 * c, hi);
+              if constexpr (OUT_F32) tree_tmem_store16(t_s + 32 * c + 16, lo);
+            }
           }
           l += sum();
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            tree_tmem_store32(t_s + 32 * h, *reinterpret_cast<const float(*)[32]>(hi + 32 * h));
-          if constexpr (OUT_F32) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              tree_tmem_store32(t_s + 64 + 32 * h, *reinterpret_cast<const float(*)[32]>(lo + 32 * h));
-          }
           tree_tmem_store_wait();
         }
         if (!inner && t == 0) {
