@@ -153,7 +153,7 @@ wst_status wst_tree_attention_bf16(int B, int T, int H, int Hkv, int Dh, const v
   a.slots = reinterpret_cast<float*>(ws + kTreeSlotOffset);
   a.timeout_ns = wait_timeout_ns();
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Two tiles to a CTA where the mean sequence has more rows than one.
+  // Two tiles of an item together where the mean sequence has more rows than one.
   if (T > (long long)B * a.tile_tokens)
     return (wst_status)launch_tree_tiles<2>(a, Dh, o_type == WST_F32, Q, ldq, k_cache, v_cache, dev, s);
   return (wst_status)launch_tree_tiles<1>(a, Dh, o_type == WST_F32, Q, ldq, k_cache, v_cache, dev, s);

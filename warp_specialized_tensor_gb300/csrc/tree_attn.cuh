@@ -14,11 +14,11 @@
 // most rows are empty (S and PV of 128 keys take a tile 1,000 clocks of the tensor core,
 // their 64 KB 2,800 clocks of an SM's share of HBM).
 //
-// Schedule: an item is (sequence, key head, TILES tiles), a block 128 keys.  The items'
-// blocks stand in one line, each CTA takes an equal share (work_split.cuh); the
-// lengths are on the device, so every CTA counts them at its start.  A piece of a cut
-// item leaves its un-normalised O, row maxima m and sums l in the workspace, and a
-// second kernel adds an item's pieces in ascending order of keys:
+// Schedule: an item is (sequence, key head, one or two tiles), a block 128 keys.  The
+// items' blocks stand in one line, each CTA takes an equal share (work_split.cuh); the
+// lengths are on the device, so every CTA counts them at its start.
+// A piece of a cut item leaves its un-normalised O, row maxima m and sums l in the
+// workspace, and a second kernel adds an item's pieces in ascending order of keys:
 //   m* = max m_i,  l* = sum l_i 2^(m_i - m*),  O = sum O_i 2^(m_i - m*) / l*
 // (its launch overlaps the first kernel's end; it is spread over all SMs, where the
 // last CTA of an item alone would read up to 152 pieces of 64 KB).
@@ -31,10 +31,13 @@
 //            a bf16 output's own rounding covers; for fp32 output P is two bf16 (what the
 //            first leaves), off by 2^-16, in the two halves of S's columns
 //   MMA      O += P . V         P from tensor memory, V from shared memory (twice for two P)
-// One tile has three S/P buffers, so S runs ahead of PV; two tiles have one each (tensor
-// memory holds two O as well), and one's softmax runs under the other's products.  Two
-// threads issue the products (a wait costs ~160 clocks while products are in flight, and
-// this way one's products run under the other's wait).
+// From a score's product to the next in its buffer a tile goes through S, softmax, PV and
+// three handshakes, 5,000 clocks, of which the softmax is a third: so one tile has three
+// S/P buffers of 128 keys, and two tiles have two each of 64 keys (tensor memory holds two
+// O as well), and S runs ahead of PV.  (Two tiles with one buffer of 128 keys each: 138 us
+// for 16 sequences with trees of 64 tokens on 8,192.  Two items at a time, each with its
+// own keys, instead of one: 147 us for 32 sequences of 4,096 against 82.)  Two threads
+// issue the products, so that one's run under the other's wait.
 //
 // A block that ends behind the context (a sequence's last one or two) takes another
 // path: each row's visible keys come as 128 bits, scores outside them do not count
@@ -43,11 +46,11 @@
 // new token's V that is not finite is cleared too and added again, at the end, to the
 // rows that see it.
 //
-// Roles (128 + 128 TILES threads): warp 0 loads Q and K, warp 3 V (a lane per page of a
-// block); warp 1 issues S, warp 2 PV (and owns the tensor memory); warps 4-7 (and 8-11)
-// softmax and output of a tile, thread = row = tensor memory lane.  Each role walks the
-// share for itself and looks for its next fragment while it works on one: the lengths and
-// page numbers of another sequence are two dependent reads.
+// Roles (128 + 128 TILES threads): warp 0 loads K, warp 3 V (a lane per page of a block);
+// warp 1 issues S, warp 2 PV (and owns the tensor memory); warps 4-7 (and 8-11) are a
+// tile's softmax and output, thread = row = tensor memory lane, and load its Q.  Each role
+// walks the share for itself; the loaders fetch the page numbers of their next item while
+// they work on one (two dependent reads).
 #pragma once
 
 #include "work_split.cuh"
@@ -64,21 +67,21 @@ constexpr float kTreeGrowSum = 256.0f;  // 2^kTreeGrow
 template <int DH, int TILES>
 struct TreeCfg {
   static constexpr int kThreads = 128 + 128 * TILES;
-  static constexpr int kSBufs = TILES == 1 ? 3 : 2;
-  static constexpr int kQBufs = TILES == 1 ? 2 : 1;  // of TILES tiles each
+  static constexpr int kSub = TILES == 1 ? kTreeBN : kTreeBN / 2;  // keys of a product
+  static constexpr int kSBufs = TILES == 1 ? 3 : 4;
   static constexpr int kHalves = DH / 64;
   static constexpr int kTile = kTreeBN * DH * 2;  // bytes of a Q tile or a block of K or V
   static constexpr int kKStages = DH == 128 ? 3 : 6;
   static constexpr int kVStages = DH == 128 ? 2 : 5;
-  static constexpr int kBars = 4 + 2 * kKStages + 2 * kVStages + 3 * kSBufs + TILES;
+  static constexpr int kBars = 2 * kKStages + 2 * kVStages + 2 + 3 * kSBufs + TILES;
   static constexpr size_t kSmem = 1024 + (size_t)(2 + kKStages + kVStages) * kTile + 1024;
-  static constexpr int kTmemO = kSBufs * kTreeBN;
+  static constexpr int kTmemO = kSBufs * kSub;
   static_assert(kSmem <= 232448 && kTmemO + TILES * DH <= 512 && DH % 64 == 0, "shared memory, tensor memory");
 };
 
 // What the second kernel needs of a cut item; pieces 0: none.
 struct TreeCut {
-  int pieces;   // on CTAs c, c + 1, ...
+  int pieces;   // of CTAs c, c + 1, ...
   int token0;   // the first row's token
   int head0;    // the first row's head
   int ntok;     // the item's tokens
@@ -96,7 +99,7 @@ static_assert(kTreeSlotOffset % 16 == 0, "alignment of the slots");
 struct TreeArgs {
   int B, T, H, Hkv, group;
   int tile_tokens;        // 128 / group
-  int tokens;             // of an item: TILES tiles
+  int tokens;             // of an item: one tile's or two tiles'
   int page_size, max_pages;
   int num_pages;
   int chunk;              // keys of one copy: min(page_size, 128)
@@ -328,10 +331,11 @@ __device__ __forceinline__ void tree_tmem_load32(uint32_t taddr, float* v) {
       : "memory");
 }
 // Waits for the thread's loads; v passes through, so that no use of it moves ahead.
+template <int N>
 __device__ __forceinline__ void tree_tmem_load_wait(float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 128; ++i) asm volatile("" : "+f"(v[i]));
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 __device__ __forceinline__ void tree_tmem_store16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -341,86 +345,123 @@ __device__ __forceinline__ void tree_tmem_store16(uint32_t taddr, const uint32_t
       : "memory");
 }
 
-// The K or V blocks of the CTA's share into a ring, by one warp: lane c of a block's
+// Waits for a phase: tests for a while (a suspended wait takes longer to wake), then as
+// the others do.
+__device__ __forceinline__ bool tree_wait(const Guard& g, uint32_t bar, uint32_t parity, uint32_t info) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_test_wait(bar, parity)) return true;
+  return wait_slow(g, bar, parity, info, false);
+}
+
+// The blocks of the share's K or V, for the warp that loads them: lane c of a block's
 // copies takes chunk c (a page, or 128 keys of one).
-template <int DH, int TILES, int STAGES, bool IS_K>
-__device__ __forceinline__ void tree_produce(const TreeArgs& p, TreeWalker w, const Guard& guard, const CUtensorMap* tm,
-                                             const CUtensorMap* tmQ, uint32_t ring, uint32_t full0, uint32_t empty0,
-                                             uint32_t q_ring, uint32_t q_full0, uint32_t q_done0) {
-  using Cfg = TreeCfg<DH, TILES>;
-  constexpr uint32_t QB = Cfg::kQBufs;
-  const uint32_t lane = lane_id();
-  const int per_block = kTreeBN / p.chunk;  // chunks: 1 .. 16
-  const int batch = 32 / per_block;         // blocks whose pages one load of the warp fetches
-  const int my_block = (int)lane / per_block, my_chunk = (int)lane % per_block;
-  const int page_blocks = p.page_size / kTreeBN;  // blocks of a page (0: a page is a chunk)
-  // page of this lane's chunk, `batch` blocks of a fragment at a time; -1: nothing to load
-  auto fetch = [&](const TreeWalker& f, int j0) -> int {
-    const int j = j0 + my_block;
-    if (j >= f.je || j * kTreeBN + my_chunk * p.chunk >= f.keys) return -1;
-    const int i = page_blocks ? j / page_blocks : j * per_block + my_chunk;
+template <int DH>
+struct TreeLoads {
+  TreeWalker w, nx;
+  bool has, has_next;
+  int ids, ids_next, ids_first;  // page of this lane's chunk, `batch` blocks at a time; -1: nothing to load
+  int i, j, in_page;
+
+  __device__ __forceinline__ static int fetch(const TreeArgs& p, const TreeWalker& f, int j0) {
+    const int per_block = kTreeBN / p.chunk, page_blocks = p.page_size / kTreeBN;
+    const int block = (int)lane_id() / per_block, chunk = (int)lane_id() - block * per_block;
+    const int j = j0 + block;
+    if (j >= f.je || j * kTreeBN + chunk * p.chunk >= f.keys) return -1;
+    const int i = page_blocks ? j / page_blocks : j * per_block + chunk;
     return i < p.max_pages ? __ldg(p.table + (long long)f.b * p.ldt + i) : -1;
-  };
-  int st = 0;
-  uint32_t ph = 1, it = 0;
-  bool has = w.next(p);
-  int ids = has ? fetch(w, w.jb) : -1;
-  TreeWalker nx = w;
-  bool has_next = false;
-  int ids_first = -1;
-  for (; has; w = nx, has = has_next, ids = ids_first, ++it) {
-    int ids_next = fetch(w, w.jb + batch);
-    if (IS_K) {
-      const uint32_t qb = it % QB;
-      bool ok = true;
-      if (lane == 0) {
-        ok = it < QB || wait_phase(guard, q_done0 + 8u * qb, ((it - QB) / QB) & 1u, (kRoleProducer << 16) | 0x900);
-        if (ok) {
-          const int tiles = TILES == 1 || w.ntok <= p.tile_tokens ? 1 : 2;
-          mbar_arrive_expect_tx(q_full0 + 8u * qb, (uint32_t)(tiles * Cfg::kHalves * 128 * p.group * p.tile_tokens));
-          for (int t = 0; t < tiles; ++t)
-            for (int hf = 0; hf < Cfg::kHalves; ++hf)
-              tma_load_3d(q_ring + (qb * TILES + t) * Cfg::kTile + hf * (kTreeBM * 128), tmQ, q_full0 + 8u * qb, hf * 64, w.h * p.group,
-                          w.token0 + t * p.tile_tokens);
-        }
-      }
-      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
+  }
+  __device__ __forceinline__ void enter(const TreeArgs& p) {
+    const int page_blocks = p.page_size / kTreeBN;
+    ids = ids_first;
+    ids_next = fetch(p, w, w.jb + 32 / (kTreeBN / p.chunk));
+    i = 0;
+    j = w.jb;
+    in_page = page_blocks ? j % page_blocks : 0;
+  }
+  __device__ __forceinline__ void start(const TreeArgs& p, const TreeWalker& from) {
+    w = from;
+    has = w.next(p);
+    if (!has) return;
+    ids_first = fetch(p, w, w.jb);
+    enter(p);
+  }
+  // One block into stage `st` (whose barriers are full and empty); false: gave up.
+  __device__ __forceinline__ bool step(const TreeArgs& p, const Guard& guard, const CUtensorMap* tm, uint32_t dst, uint32_t full,
+                                       uint32_t empty, uint32_t parity, uint32_t info) {
+    const uint32_t lane = lane_id();
+    const int per_block = kTreeBN / p.chunk, batch = 32 / per_block;  // chunks of a block: 1 .. 16
+    if (i == batch) {
+      i = 0;
+      ids = ids_next;
+      ids_next = fetch(p, w, j + batch);
     }
-    int i = 0;  // block of the batch
-    int in_page = page_blocks ? w.jb % page_blocks : 0;
-    for (int j = w.jb; j < w.je; ++j) {
-      if (i == batch) {
-        i = 0;
-        ids = ids_next;
-        ids_next = fetch(w, j + batch);
+    const int left = w.keys - j * kTreeBN;
+    const int chunks = left >= kTreeBN ? per_block : (left + p.chunk - 1) / p.chunk;
+    const int page = __shfl_sync(0xffffffffu, ids, (i * per_block + (int)(lane & (uint32_t)(per_block - 1))) & 31);
+    ++i;
+    bool ok = true;
+    if (lane == 0) {
+      ok = wait_phase(guard, empty, parity, info);
+      if (ok) mbar_arrive_expect_tx(full, (uint32_t)(chunks * p.chunk * DH * 2));
+    }
+    if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return false;
+    if ((int)lane < chunks) {
+      // (a page outside the cache reads as zeros)
+      if (page < 0 || page >= p.num_pages) latch_error(p.ws, 1u, (kRoleProducer << 16) | 0x20);
+      const uint32_t to = dst + (uint32_t)((int)lane * p.chunk * 128);
+      for (int hf = 0; hf < DH / 64; ++hf)
+        tree_tma_load_4d(to + hf * (kTreeBN * 128), tm, full, hf * 64, in_page * kTreeBN, w.h, page);
+    }
+    if (++in_page >= p.page_size / kTreeBN) in_page = 0;
+    if (j == min(w.jb + 1, w.je - 1)) {  // the next item, while copies of this one are in flight
+      nx = w;
+      has_next = nx.next(p);
+      ids_first = has_next ? fetch(p, nx, nx.jb) : -1;
+    }
+    if (++j == w.je) {
+      w = nx;
+      has = has_next;
+      if (has) enter(p);
+    }
+    return true;
+  }
+};
+
+template <int DH, int STAGES>
+__device__ __forceinline__ void tree_load(const TreeArgs& p, const TreeWalker& w, const Guard& guard, const CUtensorMap* tm,
+                                          uint32_t ring, uint32_t full0, uint32_t empty0, uint32_t info) {
+  TreeLoads<DH> s;
+  s.start(p, w);
+  int st = 0;
+  uint32_t ph = 1;
+  while (s.has) {
+    if (!s.step(p, guard, tm, ring + st * (kTreeBN * DH * 2), full0 + 8u * st, empty0 + 8u * st, ph, info | (uint32_t)st)) return;
+    if (++st == STAGES) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+}
+
+// Calls f(tile, block, part of its keys, buffer, first, last) for each product of the CTA
+// in the order of their issue, until f is false; first and last: of the products that
+// share a block of K and V.
+template <int TILES, class F>
+__device__ __forceinline__ void tree_products(const TreeArgs& p, TreeWalker& w, const F& f) {
+  int b = 0;
+  while (w.next(p)) {
+    if constexpr (TILES == 1) {
+      for (int j = w.jb; j < w.je; ++j) {
+        if (!f(0, j, 0, b, true, true)) return;
+        if (++b == 3) b = 0;
       }
-      const int left = w.keys - j * kTreeBN;
-      const int chunks = left >= kTreeBN ? per_block : (left + p.chunk - 1) / p.chunk;
-      const int page = __shfl_sync(0xffffffffu, ids, (i * per_block + my_chunk) & 31);
-      ++i;
-      bool ok = true;
-      if (lane == 0) {
-        ok = wait_phase(guard, empty0 + 8u * st, ph, (kRoleProducer << 16) | (IS_K ? 0 : 0x10) | st);
-        if (ok) mbar_arrive_expect_tx(full0 + 8u * st, (uint32_t)(chunks * p.chunk * DH * 2));
-      }
-      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return;
-      if ((int)lane < chunks) {
-        // (a page outside the cache reads as zeros)
-        if (page < 0 || page >= p.num_pages) latch_error(p.ws, 1u, (kRoleProducer << 16) | 0x20);
-        const uint32_t dst = ring + st * Cfg::kTile + (uint32_t)((int)lane * p.chunk * 128);
-        for (int hf = 0; hf < Cfg::kHalves; ++hf)
-          tree_tma_load_4d(dst + hf * (kTreeBN * 128), tm, full0 + 8u * st, hf * 64, in_page * kTreeBN, w.h, page);
-      }
-      if (++in_page >= page_blocks) in_page = 0;
-      if (++st == STAGES) {
-        st = 0;
-        ph ^= 1u;
-      }
-      if (j == min(w.jb + 1, w.je - 1)) {  // the next fragment, while copies of this one are in flight
-        nx = w;
-        has_next = nx.next(p);
-        ids_first = has_next ? fetch(nx, nx.jb) : -1;
-      }
+    } else {
+      const int tiles = w.ntok <= p.tile_tokens ? 1 : 2;
+      for (int j = w.jb; j < w.je; ++j)
+        for (int sub = 0; sub < 2; ++sub)
+          for (int t = 0; t < tiles; ++t)
+            if (!f(t, j, sub, 2 * t + sub, sub == 0 && t == 0, sub == 1 && t == tiles - 1)) return;
     }
   }
 }
@@ -432,8 +473,7 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const TreeArgs p) {
   using Cfg = TreeCfg<DH, TILES>;
-  constexpr int KS = Cfg::kKStages, VS = Cfg::kVStages, SB = Cfg::kSBufs;
-  constexpr uint32_t QB = Cfg::kQBufs;
+  constexpr int KS = Cfg::kKStages, VS = Cfg::kVStages, SB = Cfg::kSBufs, SUB = Cfg::kSub;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_addr(smem), sK = sQ + 2 * Cfg::kTile, sV = sK + KS * Cfg::kTile;
@@ -443,21 +483,19 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
   long long* found = scratch + 32;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(found + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  volatile uint32_t* odd_v = tmem_slot + 2;  // [4]: fragment it & 3 met new tokens whose V is not finite
+  // [4]: it + 1 where the share's item `it`, in place it & 3, met new tokens whose V is not
+  // finite
+  volatile uint32_t* odd_v = tmem_slot + 2;
   static_assert(Cfg::kBars * 8 <= 320 && 320 + 34 * 8 + 24 <= 1024, "the last kilobyte");
   const int warp = (int)threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
-  // q_full[2], q_done[2] (the softmax warps are done with a fragment), k_full, k_empty,
-  // v_full, v_empty, s_full[SB], p_full[SB], pv_done[SB], o_empty[TILES]
+  // k_full, k_empty, v_full, v_empty, q_full[2] (one tile: of items in turn), then of the
+  // S/P buffers s_full, p_full, pv_done, then of the tiles o_empty
   const uint32_t bar0 = smem_addr(bars);
-  const uint32_t q_full = bar0, q_done = bar0 + 16, k_full = bar0 + 32, k_empty = k_full + 8 * KS;
-  const uint32_t v_full = k_empty + 8 * KS, v_empty = v_full + 8 * VS, s_full = v_empty + 8 * VS;
-  const uint32_t p_full = s_full + 8 * SB, pv_done = p_full + 8 * SB, o_empty = pv_done + 8 * SB;
+  const uint32_t k_full = bar0, k_empty = k_full + 8 * KS, v_full = k_empty + 8 * KS, v_empty = v_full + 8 * VS;
+  const uint32_t q_full = v_empty + 8 * VS, s_full = q_full + 16, p_full = s_full + 8 * SB, pv_done = p_full + 8 * SB;
+  const uint32_t o_empty = pv_done + 8 * SB;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + 8 * i, 1);
-      mbar_init(q_done + 8 * i, 4 * TILES);
-    }
     for (int i = 0; i < KS; ++i) {
       mbar_init(k_full + 8 * i, 1);
       mbar_init(k_empty + 8 * i, 1);
@@ -466,14 +504,15 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_empty + 8 * i, 1);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(q_full + 8 * i, 1);
     for (int i = 0; i < SB; ++i) {
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, 4);
+      mbar_init(p_full + 8 * i, 4);  // the tile's softmax warps
       mbar_init(pv_done + 8 * i, 1);
     }
     for (int i = 0; i < TILES; ++i) mbar_init(o_empty + 8 * i, 4);
     *abort_flag = 0u;
-    odd_v[0] = odd_v[1] = odd_v[2] = odd_v[3] = 0u;
+    for (int i = 0; i < 4; ++i) odd_v[i] = 0u;
     found[0] = found[1] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
@@ -525,102 +564,87 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
   }
 
   if (warp == 0) {
-    tree_produce<DH, TILES, KS, true>(p, w, guard, &tmK, &tmQ, sK, k_full, k_empty, sQ, q_full, q_done);
+    tree_load<DH, KS>(p, w, guard, &tmK, sK, k_full, k_empty, kRoleProducer << 16);
   } else if (warp == 3) {
-    tree_produce<DH, TILES, VS, false>(p, w, guard, &tmV, nullptr, sV, v_full, v_empty, 0, 0, 0);
+    tree_load<DH, VS>(p, w, guard, &tmV, sV, v_full, v_empty, (kRoleProducer << 16) | 0x10);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ S = Q K^T
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(kTreeBM, kTreeBN, false, false);
-      int ks = 0, sb = 0;
-      uint32_t kph = 0, it = 0;
-      uint32_t used = 0, sph = 0;  // bit b: buffer b has been used, and the parity of its next use
-      bool ok = true;
-      for (; ok && w.next(p); ++it) {
-        const uint32_t qb = it % QB;
-        if (!wait_phase(guard, q_full + 8 * qb, (it / QB) & 1u, (kRoleMma << 16) | 0x800)) break;
-        const int tiles = TILES == 1 || w.ntok <= p.tile_tokens ? 1 : 2;
-        for (int j = w.jb; ok && j < w.je; ++j) {
-          const uint32_t k_at = sK + ks * Cfg::kTile;
-          for (int t = 0; t < tiles; ++t) {
-            const int b = TILES == 1 ? sb : t;
-            // the buffer's last P has been read, and K is there
-            const bool p_ok = !((used >> b) & 1u) || mbar_test_wait(pv_done + 8 * b, ((sph >> b) & 1u) ^ 1u);
-            const bool k_ok = t > 0 || mbar_test_wait(k_full + 8 * ks, kph);
-            if ((!p_ok && !wait_phase(guard, pv_done + 8 * b, ((sph >> b) & 1u) ^ 1u, (kRoleMma << 16) | 0x400 | b)) ||
-                (!k_ok && !wait_phase(guard, k_full + 8 * ks, kph, (kRoleMma << 16) | ks))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-            const uint32_t q_at = sQ + (qb * TILES + t) * Cfg::kTile;
-            const uint32_t d = tmem_base + (uint32_t)(kTreeBN * b);
+      constexpr uint32_t idesc = idesc_bf16_f32(kTreeBM, SUB, false, false);
+      int ks = 0;
+      uint32_t kph = 0;
+      uint32_t used = 0, sph = 0;  // bit b: buffer b has been used; the parity of its next use
+      uint32_t qph = 0;            // bit i: parity of Q buffer i's next item
+      int qb = 0;                  // (one tile) its item's Q buffer
+      tree_products<TILES>(p, w, [&](int t, int j, int sub, int b, bool first, bool last) -> bool {
+        if (j == w.jb && sub == 0) {
+          if (TILES == 2) qb = t;
+          if (!tree_wait(guard, q_full + 8 * qb, (qph >> qb) & 1u, (kRoleMma << 16) | 0x800 | qb)) return false;
+          qph ^= 1u << qb;
+        }
+        // the buffer's last P has been read, and K is there
+        if (((used >> b) & 1u) && !tree_wait(guard, pv_done + 8 * b, ((sph >> b) & 1u) ^ 1u, (kRoleMma << 16) | 0x400 | b)) return false;
+        if (first && !tree_wait(guard, k_full + 8 * ks, kph, (kRoleMma << 16) | ks)) return false;
+        tc_fence_after_sync();
+        const uint32_t q_at = sQ + (TILES == 2 ? t : qb) * Cfg::kTile, k_at = sK + ks * Cfg::kTile + sub * (SUB * 128);
+        const uint32_t d = tmem_base + (uint32_t)(SUB * b);
 #pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk) {
-              const uint32_t o = (uint32_t)((kk >> 2) * (kTreeBN * 128) + (kk & 3) * 32);
-              umma_bf16<1>(d, sdesc_sw128(q_at + o, 16, 1024), sdesc_sw128(k_at + o, 16, 1024), idesc, kk != 0 ? 1u : 0u);
-            }
-            umma_commit(s_full + 8 * b);
-            used |= 1u << b;
-            sph ^= 1u << b;
-            if (TILES == 1 && ++sb == SB) sb = 0;
-          }
-          if (!ok) break;
+        for (int kk = 0; kk < DH / 16; ++kk) {
+          const uint32_t o = (uint32_t)((kk >> 2) * (kTreeBN * 128) + (kk & 3) * 32);
+          umma_bf16<1>(d, sdesc_sw128(q_at + o, 16, 1024), sdesc_sw128(k_at + o, 16, 1024), idesc, kk != 0 ? 1u : 0u);
+        }
+        umma_commit(s_full + 8 * b);
+        used |= 1u << b;
+        sph ^= 1u << b;
+        if (last) {
           umma_commit(k_empty + 8 * ks);
           if (++ks == KS) {
             ks = 0;
             kph ^= 1u;
           }
+          if (TILES == 1 && j == w.je - 1) qb ^= 1;
         }
-      }
+        return true;
+      });
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------------ O += P V
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(kTreeBM, DH, false, true);
-      int vs = 0, sb = 0;
+      int vs = 0;
       uint32_t vph = 0;
-      uint32_t sph = 0;            // bit b: parity of buffer b's next use
-      uint32_t oph = (1u << TILES) - 1u;  // bit t: parity of O t's next release
-      bool ok = true;
-      while (ok && w.next(p)) {
-        const int tiles = TILES == 1 || w.ntok <= p.tile_tokens ? 1 : 2;
-        for (int j = w.jb; ok && j < w.je; ++j) {
-          const uint64_t vd = sdesc_sw128(sV + vs * Cfg::kTile, kTreeBN * 128, 1024);
-          for (int t = 0; t < tiles; ++t) {
-            const int b = TILES == 1 ? sb : t;
-            const bool v_ok = t > 0 || mbar_test_wait(v_full + 8 * vs, vph);
-            const bool p_ok = mbar_test_wait(p_full + 8 * b, (sph >> b) & 1u);
-            if ((!v_ok && !wait_phase(guard, v_full + 8 * vs, vph, (kRoleMma << 16) | 0x10 | vs)) ||
-                (!p_ok && !wait_phase(guard, p_full + 8 * b, (sph >> b) & 1u, (kRoleMma << 16) | 0x200 | b)) ||
-                (j == w.jb && !wait_phase(guard, o_empty + 8 * t, (oph >> t) & 1u, (kRoleMma << 16) | 0x300 | t))) {
-              ok = false;
-              break;
-            }
-            if (j == w.jb) oph ^= 1u << t;
-            tc_fence_after_sync();
-            const uint32_t a = tmem_base + (uint32_t)(kTreeBN * b), d = tmem_base + (uint32_t)(Cfg::kTmemO + t * DH);
+      uint32_t sph = 0, oph = 3u;  // bits: parities of the buffers' next P, of the tiles' next release of O
+      tree_products<TILES>(p, w, [&](int t, int j, int sub, int b, bool first, bool last) -> bool {
+        if (first && !tree_wait(guard, v_full + 8 * vs, vph, (kRoleMma << 16) | 0x10 | vs)) return false;
+        const bool begins = j == w.jb && sub == 0;
+        if (begins) {
+          if (!tree_wait(guard, o_empty + 8 * t, (oph >> t) & 1u, (kRoleMma << 16) | 0x300 | t)) return false;
+          oph ^= 1u << t;
+        }
+        if (!tree_wait(guard, p_full + 8 * b, (sph >> b) & 1u, (kRoleMma << 16) | 0x200 | b)) return false;
+        tc_fence_after_sync();
+        // 16 keys: 8 columns of P, 2 KB of V
+        const uint64_t vd = sdesc_sw128(sV + vs * Cfg::kTile, kTreeBN * 128, 1024) + (uint32_t)(sub * (SUB / 16) * 128);
+        const uint32_t a = tmem_base + (uint32_t)(SUB * b), d = tmem_base + (uint32_t)(Cfg::kTmemO + t * DH);
 #pragma unroll
-            for (int kk = 0; kk < kTreeBN / 16; ++kk)  // 16 keys: 8 columns of P, 2 KB of V
-              tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc,
-                          (j > w.jb || kk != 0) ? 1u : 0u);
-            if constexpr (OUT_F32) {
+        for (int kk = 0; kk < SUB / 16; ++kk)
+          tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc, (!begins || kk != 0) ? 1u : 0u);
+        if constexpr (OUT_F32) {
 #pragma unroll
-              for (int kk = 0; kk < kTreeBN / 16; ++kk)
-                tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + 16 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
-            }
-            umma_commit(pv_done + 8 * b);
-            sph ^= 1u << b;
-            if (TILES == 1 && ++sb == SB) sb = 0;
-          }
-          if (!ok) break;
+          for (int kk = 0; kk < SUB / 16; ++kk)
+            tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + 16 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
+        }
+        umma_commit(pv_done + 8 * b);
+        sph ^= 1u << b;
+        if (last) {
           umma_commit(v_empty + 8 * vs);
           if (++vs == VS) {
             vs = 0;
             vph ^= 1u;
           }
         }
-      }
+        return true;
+      });
     }
   } else {
     // ------------------------------------------------------------------ softmax, output
@@ -631,50 +655,79 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
     const uint32_t t_o = t_lane + Cfg::kTmemO + t * DH;
     const int my_tok = row / p.group, my_head = row - my_tok * p.group;
     const float cs = p.cs;
-    int sb = t, vs = 0;
-    uint32_t sph = 0, vph = 0, it = 0;
-    long long blocks = 0;  // before this one
+    const long long x_first = w.x;
+    int b = 2 * t;               // S/P buffer of the next product,
+    uint32_t bph = 0;            // its parity,
+    int last_b = 0;              // and those of the product before
+    uint32_t last_ph = 0, it = 0;  // (it: items of the share, those without this tile too)
     bool wrote_cut = false, ok = true;
-    for (; ok && w.next(p); ++it) {
-      const int rows = min(p.tile_tokens, w.ntok - t * p.tile_tokens) * p.group;
-      if (TILES == 2 && rows <= 0) {
-        // A fragment without this tile: over when its Q is there (so that the barrier's
-        // phases are told apart).
-        ok = warp_wait_phase(guard, q_full + 8 * (it % QB), (it / QB) & 1u, (kRoleEpilogue << 16) | 0x700);
-        if (ok && lane == 0) mbar_arrive(q_done + 8 * (it % QB));
-        continue;
+    // the tile's rows of item x (none: the item has one tile only), and their Q
+    auto rows_of = [&](const TreeWalker& x) { return min(p.tile_tokens, x.ntok - t * p.tile_tokens) * p.group; };
+    auto load_q = [&](const TreeWalker& x, int qb) {
+      if (q == 0 && lane == 0) {
+        mbar_arrive_expect_tx(q_full + 8 * qb, (uint32_t)(Cfg::kHalves * 128 * p.group * p.tile_tokens));
+        for (int hf = 0; hf < Cfg::kHalves; ++hf)
+          tma_load_3d(sQ + qb * Cfg::kTile + hf * (kTreeBM * 128), &tmQ, q_full + 8 * qb, hf * 64, x.h * p.group,
+                      x.token0 + t * p.tile_tokens);
+      }
+    };
+    // (an item without this tile is passed over)
+    auto advance = [&](TreeWalker& x) -> bool {
+      while (x.next(p)) {
+        if (rows_of(x) > 0) return true;
+        ++it;
+      }
+      return false;
+    };
+    bool has = advance(w);
+    if (has) load_q(w, t);
+    TreeWalker nx = w;
+    bool has_next = false;
+    for (; ok && has; w = nx, has = has_next, ++it) {
+      const uint32_t it_now = it;
+      const int rows = rows_of(w);
+      if (TILES == 1) {  // the next item's Q, into the other buffer: the item before this one is over
+        nx = w;
+        has_next = advance(nx);
+        if (has_next) load_q(nx, (int)((it_now + 1u) & 1u));
       }
       const bool active = q * 32 < rows;  // (of the whole warp)
       const int ti = w.t * p.tokens + t * p.tile_tokens + my_tok;
       float m = -INFINITY, l = 0.0f;
-      int last_sb = 0;
-      uint32_t last_ph = 0;
-      for (int j = w.jb; j < w.je; ++j) {
-        const bool inner = (j + 1) * kTreeBN <= w.s.ctx;  // every row sees every key
-        if (!warp_wait_phase(guard, s_full + 8 * sb, sph, (kRoleEpilogue << 16) | sb)) {
+      for (int js = w.jb * (kTreeBN / SUB); js < w.je * (kTreeBN / SUB); ++js) {
+        const int j = js / (kTreeBN / SUB), sub = js % (kTreeBN / SUB), key0 = js * SUB;
+        const bool begins = j == w.jb && sub == 0;
+        const bool inner = key0 + SUB <= w.s.ctx;  // every row sees every key
+        if (!__all_sync(0xffffffffu, tree_wait(guard, s_full + 8 * b, bph, (kRoleEpilogue << 16) | b))) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
+        if (TILES == 2 && js == w.je * (kTreeBN / SUB) - 1) {
+          // The item's last product with Q is done: the next item's can come.
+          nx = w;
+          has_next = advance(nx);
+          if (has_next) load_q(nx, t);
+        }
+        const uint32_t t_s = t_lane + (uint32_t)(SUB * b);
         if (active) {
-          const uint32_t t_s = t_lane + (uint32_t)(kTreeBN * sb);
           // P of 32 keys goes over their scores: 16 columns of bf16 pairs, then (fp32
           // output) 16 of what those leave.
           float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           auto sum = [&]() { return (rs[0] + rs[1]) + (rs[2] + rs[3]); };
           bool done = false;
-          if (inner && j > w.jb && __all_sync(0xffffffffu, fabsf(m) < 1.0e6f || row >= rows)) {
+          if (inner && !begins && __all_sync(0xffffffffu, fabsf(m) < 1.0e6f || row >= rows)) {
             // With the maximum so far: every P is positive, so a row sum of at most 2^8
             // proves that no P exceeds it and the maximum need not be looked for.  (cs S - m
             // is rounded once, m is a rounded product: their difference is the same factor
             // for all of a row, and small while m is.)
-            float x[kTreeBN];
+            float x[SUB];
 #pragma unroll
-            for (int c = 0; c < kTreeBN / 32; ++c) tree_tmem_load32(t_s + 32 * c, x + 32 * c);
-            tree_tmem_load_wait(x);
-            uint32_t hi[kTreeBN / 2], lo[OUT_F32 ? kTreeBN / 2 : 1];
+            for (int c = 0; c < SUB / 32; ++c) tree_tmem_load32(t_s + 32 * c, x + 32 * c);
+            tree_tmem_load_wait<SUB>(x);
+            uint32_t hi[SUB / 2], lo[OUT_F32 ? SUB / 2 : 1];
 #pragma unroll
-            for (int i = 0; i < kTreeBN / 2; ++i) {
+            for (int i = 0; i < SUB / 2; ++i) {
               float& x0 = x[2 * i];
               float& x1 = x[2 * i + 1];
               tree_fma2(x0, x1, cs, -m);
@@ -687,7 +740,7 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
             done = __all_sync(0xffffffffu, sum() <= kTreeGrowSum || row >= rows) != 0;
             if (done) {
 #pragma unroll
-              for (int c = 0; c < kTreeBN / 32; ++c) {
+              for (int c = 0; c < SUB / 32; ++c) {
                 tree_tmem_store16(t_s + 32 * c, hi + 16 * c);
                 if constexpr (OUT_F32) tree_tmem_store16(t_s + 32 * c + 16, lo + 16 * c);
               }
@@ -699,14 +752,14 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
             // Any other block, 32 keys at a time (loops: this code runs a few times in a
             // fragment, and unrolled it took longer to fetch than to run).  First cs S,
             // -inf where the row sees nothing, back over the scores.
-            uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+            uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};  // (of SUB / 32 words)
             if (!inner && row < rows) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) vis[i] = tree_visible(p, w.s, ti, j * kTreeBN - w.s.ctx + 32 * i);
+              for (int i = 0; i < SUB / 32; ++i) vis[i] = tree_visible(p, w.s, ti, key0 - w.s.ctx + 32 * i);
             }
             float mx = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < kTreeBN / 32; ++c) {
+            for (int c = 0; c < SUB / 32; ++c) {
               float x[32];
               tmem_load32(t_s + 32 * c, x);
               const uint32_t v = c < 2 ? (c ? vis[1] : vis[0]) : (c > 2 ? vis[3] : vis[2]);
@@ -720,12 +773,12 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
               tree_tmem_store32(t_s + 32 * c, x);
             }
             tree_tmem_store_wait();
-            if (j == w.jb) {
+            if (begins) {
               m = mx;  // the first PV product overwrites O
             } else {
               const bool grow = mx > m + kTreeGrow && row < rows;
               if (__any_sync(0xffffffffu, grow)) {
-                if (!warp_wait_phase(guard, pv_done + 8 * last_sb, last_ph, (kRoleEpilogue << 16) | 0x100)) {
+                if (!warp_wait_phase(guard, pv_done + 8 * last_b, last_ph, (kRoleEpilogue << 16) | 0x100)) {
                   ok = false;
                   break;
                 }
@@ -749,7 +802,7 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
             // (a row that has seen no key yet: all its scores are -inf, its P zero)
             const float top = !inner && m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
-            for (int c = 0; c < kTreeBN / 32; ++c) {
+            for (int c = 0; c < SUB / 32; ++c) {
               float x[32];
               tmem_load32(t_s + 32 * c, x);
               uint32_t hi[16], lo[16];
@@ -770,26 +823,24 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
           l += sum();
           tree_tmem_store_wait();
         }
-        if (!inner && t == 0) {
-          // V: clear the keys behind the sequence and what is not finite of the new
-          // tokens; thread = key.  (The other tile's product with this V is issued after
-          // this one's.)  These warps wait for V here only, and a parity tells two phases
-          // apart: the stage's last use has to be over first.  (S_g was issued after
-          // PV_{g-3}, with two tiles after PV_{g-1}: with more stages than two it is.)
+        if (t == 0 && sub == 0 && (j + 1) * kTreeBN > w.s.ctx) {
+          // V: clear the block's keys behind the sequence and what is not finite of the new
+          // tokens; thread = key.  (The block's other products with V are issued after this
+          // one.)  These warps wait for V here only, and a parity tells two phases apart:
+          // the stage's last use has to be over.  With two tiles PV of the block before this
+          // one is; with one, PV three blocks ago, and two stages need two.
+          const long long g = w.item + j - x_first;  // the share's blocks use the stages in turn
           static_assert(VS >= 2, "stages of V");
-          if constexpr (VS == 2 && TILES == 1) {
-            const bool wraps = sb < 2;  // block g - 2 used the buffers' round before this one
-            if (blocks >= 2 &&
-                !warp_wait_phase(guard, pv_done + 8 * (sb + 1 == SB ? 0 : sb + 1), wraps ? sph ^ 1u : sph, (kRoleEpilogue << 16) | 0x600)) {
-              ok = false;
-              break;
-            }
-          }
-          if (!warp_wait_phase(guard, v_full + 8 * vs, vph, (kRoleEpilogue << 16) | 0x500)) {
+          if (TILES == 1 && VS == 2 && g >= 2 &&
+              !__all_sync(0xffffffffu, tree_wait(guard, pv_done + 8 * (int)((g - 2) % 3), (uint32_t)((g - 2) / 3) & 1u, (kRoleEpilogue << 16) | 0x600))) {
             ok = false;
             break;
           }
-          (void)mbar_try_wait(v_full + 8 * vs, vph);  // each lane sees the copies
+          const int vs = (int)(g % VS);
+          if (!__all_sync(0xffffffffu, tree_wait(guard, v_full + 8 * vs, (uint32_t)(g / VS) & 1u, (kRoleEpilogue << 16) | 0x500 | vs))) {
+            ok = false;
+            break;
+          }
           const int key = j * kTreeBN + row;
           if (key >= w.s.ctx) {
             const bool out = key >= w.keys;
@@ -824,40 +875,38 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
                 }
               }
             }
-            if (odd) odd_v[it & 3u] = 1u;
+            if (odd) odd_v[it_now & 3u] = it_now + 1u;
           }
           fence_proxy_async_smem();
         }
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * sb);
-        last_sb = sb;
-        last_ph = sph;
-        ++blocks;
-        if (TILES == 2) {
-          sph ^= 1u;
-        } else if (++sb == SB) {
-          sb = 0;
-          sph ^= 1u;
-        }
-        if (++vs == VS) {
-          vs = 0;
-          vph ^= 1u;
+        if (lane == 0) mbar_arrive(p_full + 8 * b);
+        last_b = b;
+        last_ph = bph;
+        if constexpr (TILES == 1) {
+          if (++b == 3) {
+            b = 0;
+            bph ^= 1u;
+          }
+        } else {
+          b ^= 1;
+          if (sub == 1) bph ^= 1u;
         }
       }
       if (!ok) break;
-      if (!warp_wait_phase(guard, pv_done + 8 * last_sb, last_ph, (kRoleEpilogue << 16) | 0x300)) {
+      // (each lane: odd_v was written before the products were issued)
+      if (!__all_sync(0xffffffffu, tree_wait(guard, pv_done + 8 * last_b, last_ph, (kRoleEpilogue << 16) | 0x300 | last_b))) {
         ok = false;
         break;
       }
-      (void)mbar_try_wait(pv_done + 8 * last_sb, last_ph);  // each lane: odd_v was written before the products were issued
       tc_fence_after_sync();
       if (active) {
         const bool whole = w.jb == 0 && w.je == w.nb;
-        const bool odd = odd_v[it & 3u] != 0u;
+        const bool odd = odd_v[it_now & 3u] > it_now;  // (a later item's: looked into too)
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const long long at = (long long)(w.token0 + t * p.tile_tokens + my_tok) * p.ldo + (long long)(w.h * p.group + my_head) * DH;
-        float* slot = whole ? nullptr : p.slots + (size_t)((2 * blockIdx.x + (w.jb == 0 ? 1 : 0)) * 2 + t) * kTreeSlotFloats;
+        float* slot = whole ? nullptr : p.slots + (size_t)(4 * blockIdx.x + (w.jb == 0 ? 2 : 0) + t) * kTreeSlotFloats;
 #pragma unroll 1
         for (int c = 0; c < DH / 32; ++c) {
           float v[32];
@@ -906,20 +955,14 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
           __stcg(slot + 128 * kTreeBM + kTreeBM + row, l);
         }
         if (!whole && w.jb == 0 && row == 0 && t == 0) {
-          p.cuts[blockIdx.x] =
-              TreeCut{share.owner(w.item + w.nb - 1) - (int)blockIdx.x + 1, w.token0, w.h * p.group, w.ntok};
+          p.cuts[blockIdx.x] = TreeCut{share.owner(w.item + w.nb - 1) - (int)blockIdx.x + 1, w.token0, w.h * p.group, w.ntok};
           wrote_cut = true;
         }
       }
-      // The flag of the fragment after next: the products of this one are done, so every
-      // warp has left the fragment before it, and none enters that one before this warp
-      // has taken part in the next.
-      if (row == 0 && t == 0) odd_v[(it + 2u) & 3u] = 0u;
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(o_empty + 8 * t);
-        mbar_arrive(q_done + 8 * (it % QB));
       }
     }
     if (p.split && row == 0 && t == 0 && !wrote_cut) p.cuts[blockIdx.x].pieces = 0;
@@ -934,8 +977,8 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
   if (warp == 2) tmem_dealloc<1>(tmem_base, 512);
 }
 
-// The cut items' pieces added up: blockIdx.x is the CTA in whose share an item
-// begins, blockIdx.z the tile; a thread takes four components of a row.
+// The cut items' pieces added up: blockIdx.x is the CTA in whose share an item begins,
+// blockIdx.z the tile; a thread takes four components of a row.
 template <int DH, bool OUT_F32>
 __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -943,7 +986,9 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
   const int i = (int)(blockIdx.y * 256 + threadIdx.x);
   const int row = i % kTreeBM, quad = i / kTreeBM, t = (int)blockIdx.z;
   if (cut.pieces == 0 || row >= min(p.tile_tokens, cut.ntok - t * p.tile_tokens) * p.group) return;
-  auto slot = [&](int k) { return p.slots + (size_t)((2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * 2 + t) * kTreeSlotFloats; };
+  auto slot = [&](int k) {
+    return p.slots + (size_t)(4 * (blockIdx.x + k) + (k == 0 ? 2 : 0) + t) * kTreeSlotFloats;
+  };
   float m = -INFINITY;
   for (int k = 0; k < cut.pieces; ++k) m = fmaxf(m, __ldcg(slot(k) + 128 * kTreeBM + row));
   const float ms = m == -INFINITY ? 0.0f : m;
