@@ -11,17 +11,16 @@ namespace wst {
 
 namespace {
 
-template <int DH, int TILES, bool OUT_F32>
-int launch_tree(TreeArgs a, const void* Q, long long ldq, const void* K, const void* V, const DeviceInfo& dev,
+template <int DH, bool OUT_F32>
+int launch_tree(const TreeArgs& a, const void* Q, long long ldq, const void* K, const void* V, const DeviceInfo& dev,
                 cudaStream_t stream) {
-  using Cfg = TreeCfg<DH, TILES>;
-  a.tokens = TILES * a.tile_tokens;
+  using Cfg = TreeCfg<DH>;
   int st;
   CUtensorMap tmQ, tmK, tmV;
   {
     const uint64_t dims[3] = {(uint64_t)DH, (uint64_t)a.H, (uint64_t)a.T};
     const uint64_t str[2] = {(uint64_t)DH * 2, (uint64_t)ldq * 2};
-    const uint32_t box[3] = {64, (uint32_t)a.group, (uint32_t)a.tile_tokens};
+    const uint32_t box[3] = {64, (uint32_t)a.group, (uint32_t)a.tokens};
     if ((st = encode_map(&tmQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, Q, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))) return st;
   }
   const uint64_t dims[4] = {(uint64_t)DH, (uint64_t)a.page_size, (uint64_t)a.Hkv, (uint64_t)a.num_pages};
@@ -29,10 +28,10 @@ int launch_tree(TreeArgs a, const void* Q, long long ldq, const void* K, const v
   const uint32_t box[4] = {64, (uint32_t)a.chunk, 1, 1};
   if ((st = encode_map(&tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, K, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))) return st;
   if ((st = encode_map(&tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, V, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))) return st;
-  auto kern = k_tree_attn<DH, TILES, OUT_F32>;
+  auto kern = k_tree_attn<DH, OUT_F32>;
   if ((st = ensure_smem_attr((const void*)kern, Cfg::kSmem))) return st;
   const int grid = std::min(dev.num_sms, kTreeMaxCtas);
-  kern<<<grid, Cfg::kThreads, Cfg::kSmem, stream>>>(tmQ, tmK, tmV, a);
+  kern<<<grid, kTreeThreads, Cfg::kSmem, stream>>>(tmQ, tmK, tmV, a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch k_tree_attn");
   if (!a.split) return ST_OK;
@@ -41,21 +40,13 @@ int launch_tree(TreeArgs a, const void* Q, long long ldq, const void* K, const v
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)(DH / 4 * kTreeBM / 256), (unsigned)TILES);
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)(DH / 4 * kTreeBM / 256), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, k_tree_merge<DH, OUT_F32>, a);
   return e == cudaSuccess ? ST_OK : cuda_fail(e, "launch k_tree_merge");
-}
-
-template <int TILES>
-int launch_tree_tiles(const TreeArgs& a, int Dh, bool f32, const void* Q, long long ldq, const void* K, const void* V,
-                      const DeviceInfo& dev, cudaStream_t stream) {
-  if (Dh == 128)
-    return f32 ? launch_tree<128, TILES, true>(a, Q, ldq, K, V, dev, stream) : launch_tree<128, TILES, false>(a, Q, ldq, K, V, dev, stream);
-  return f32 ? launch_tree<64, TILES, true>(a, Q, ldq, K, V, dev, stream) : launch_tree<64, TILES, false>(a, Q, ldq, K, V, dev, stream);
 }
 
 }  // namespace
@@ -128,7 +119,8 @@ wst_status wst_tree_attention_bf16(int B, int T, int H, int Hkv, int Dh, const v
   a.H = H;
   a.Hkv = Hkv;
   a.group = group;
-  a.tile_tokens = kTreeBM / group;
+  a.tokens = kTreeBM / group;
+  a.lines = T > a.tokens ? 2 : 1;
   a.page_size = page_size;
   a.max_pages = max_pages;
   a.num_pages = num_pages;
@@ -153,10 +145,11 @@ wst_status wst_tree_attention_bf16(int B, int T, int H, int Hkv, int Dh, const v
   a.slots = reinterpret_cast<float*>(ws + kTreeSlotOffset);
   a.timeout_ns = wait_timeout_ns();
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Two tiles of an item together where the mean sequence has more rows than one.
-  if (T > (long long)B * a.tile_tokens)
-    return (wst_status)launch_tree_tiles<2>(a, Dh, o_type == WST_F32, Q, ldq, k_cache, v_cache, dev, s);
-  return (wst_status)launch_tree_tiles<1>(a, Dh, o_type == WST_F32, Q, ldq, k_cache, v_cache, dev, s);
+  if (Dh == 128)
+    return (wst_status)(o_type == WST_F32 ? launch_tree<128, true>(a, Q, ldq, k_cache, v_cache, dev, s)
+                                          : launch_tree<128, false>(a, Q, ldq, k_cache, v_cache, dev, s));
+  return (wst_status)(o_type == WST_F32 ? launch_tree<64, true>(a, Q, ldq, k_cache, v_cache, dev, s)
+                                        : launch_tree<64, false>(a, Q, ldq, k_cache, v_cache, dev, s));
 }
 
 }  // extern "C"

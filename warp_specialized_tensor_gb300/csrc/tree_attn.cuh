@@ -8,15 +8,19 @@
 // to itself).  All of them lie in the cache, through the sequence's page table.
 //
 // The query rows of a sequence that share a key head (its tokens x the `group` heads
-// of that key head) are stacked into tiles of 128 rows, and a CTA takes one tile or two
-// (TILES) through a sequence's keys, so K and V are read once for them: for a step of few
-// tokens that read is the whole cost, and the 128-row products hide under it even where
-// most rows are empty (S and PV of 128 keys take a tile 1,000 clocks of the tensor core,
-// their 64 KB 2,800 clocks of an SM's share of HBM).
+// of that key head) are stacked into tiles of 128 rows, and K and V are read once per
+// tile: for a step of few tokens that read is the whole cost, and the 128-row products
+// hide under it even where most rows are empty (S and PV of 128 keys take 1,000 clocks of
+// the tensor core, their 64 KB 2,800 clocks of an SM's share of HBM).
 //
-// Schedule: an item is (sequence, key head, one or two tiles), a block 128 keys.  The
-// items' blocks stand in one line, each CTA takes an equal share (work_split.cuh); the
-// lengths are on the device, so every CTA counts them at its start.
+// Schedule: an item is (sequence, key head, tile), a block 128 keys.  The items' blocks
+// stand in one line, each CTA takes an equal share (work_split.cuh); the lengths are on the
+// device, so every CTA counts them at its start.  The line holds the even tiles of all
+// sequences, then the odd ones: the two tiles of a sequence are worked on at the same time
+// by two CTAs, and one of them finds K and V in L2.  (In the sequences' order one CTA took
+// a tile after the other and both came from HBM: 138 us for 16 trees of 64 tokens on 8,192,
+// 800 MB.  Two tiles at a time in one CTA, 129 us, read 400 MB but wait for each other's
+// products: tensor memory holds one S/P buffer for each of two tiles, three for one.)
 // A piece of a cut item leaves its un-normalised O, row maxima m and sums l in the
 // workspace, and a second kernel adds an item's pieces in ascending order of keys:
 //   m* = max m_i,  l* = sum l_i 2^(m_i - m*),  O = sum O_i 2^(m_i - m*) / l*
@@ -31,13 +35,11 @@
 //            a bf16 output's own rounding covers; for fp32 output P is two bf16 (what the
 //            first leaves), off by 2^-16, in the two halves of S's columns
 //   MMA      O += P . V         P from tensor memory, V from shared memory (twice for two P)
-// From a score's product to the next in its buffer a tile goes through S, softmax, PV and
-// three handshakes, 5,000 clocks, of which the softmax is a third: so one tile has three
-// S/P buffers of 128 keys, and two tiles have two each of 64 keys (tensor memory holds two
-// O as well), and S runs ahead of PV.  (Two tiles with one buffer of 128 keys each: 138 us
-// for 16 sequences with trees of 64 tokens on 8,192.  Two items at a time, each with its
-// own keys, instead of one: 147 us for 32 sequences of 4,096 against 82.)  Two threads
-// issue the products, so that one's run under the other's wait.
+// From a score's product to the next in its buffer it is S, softmax, PV and three
+// handshakes, 5,000 clocks, of which the softmax is a third: three S/P buffers let S run
+// ahead of PV.  (Two items at a time with one buffer each: 147 us for 32 sequences of
+// 4,096 against 82.)  Two threads issue the products, so that one's run under the other's
+// wait.
 //
 // A block that ends behind the context (a sequence's last one or two) takes another
 // path: each row's visible keys come as 128 bits, scores outside them do not count
@@ -46,11 +48,11 @@
 // new token's V that is not finite is cleared too and added again, at the end, to the
 // rows that see it.
 //
-// Roles (128 + 128 TILES threads): warp 0 loads K, warp 3 V (a lane per page of a block);
-// warp 1 issues S, warp 2 PV (and owns the tensor memory); warps 4-7 (and 8-11) are a
-// tile's softmax and output, thread = row = tensor memory lane, and load its Q.  Each role
-// walks the share for itself; the loaders fetch the page numbers of their next item while
-// they work on one (two dependent reads).
+// Roles (256 threads): warp 0 loads K, warp 3 V (a lane per page of a block); warp 1
+// issues S, warp 2 PV (and owns the tensor memory); warps 4-7 are the softmax and the
+// output, thread = row = tensor memory lane, and load Q.  Each role walks the share for
+// itself; the loaders fetch the page numbers of their next item while they work on one
+// (two dependent reads).
 #pragma once
 
 #include "work_split.cuh"
@@ -64,19 +66,18 @@ constexpr int kTreeMaxCtas = 160;
 constexpr float kTreeGrow = 8.0f;       // log2 of how far P may exceed 1
 constexpr float kTreeGrowSum = 256.0f;  // 2^kTreeGrow
 
-template <int DH, int TILES>
+constexpr int kTreeThreads = 256;
+constexpr int kTreeSBufs = 3;
+
+template <int DH>
 struct TreeCfg {
-  static constexpr int kThreads = 128 + 128 * TILES;
-  static constexpr int kSub = TILES == 1 ? kTreeBN : kTreeBN / 2;  // keys of a product
-  static constexpr int kSBufs = TILES == 1 ? 3 : 4;
-  static constexpr int kHalves = DH / 64;
   static constexpr int kTile = kTreeBN * DH * 2;  // bytes of a Q tile or a block of K or V
   static constexpr int kKStages = DH == 128 ? 3 : 6;
   static constexpr int kVStages = DH == 128 ? 2 : 5;
-  static constexpr int kBars = 2 * kKStages + 2 * kVStages + 2 + 3 * kSBufs + TILES;
+  static constexpr int kBars = 2 * kKStages + 2 * kVStages + 2 + 3 * kTreeSBufs + 1;
   static constexpr size_t kSmem = 1024 + (size_t)(2 + kKStages + kVStages) * kTile + 1024;
-  static constexpr int kTmemO = kSBufs * kSub;
-  static_assert(kSmem <= 232448 && kTmemO + TILES * DH <= 512 && DH % 64 == 0, "shared memory, tensor memory");
+  static constexpr int kTmemO = kTreeSBufs * kTreeBN;
+  static_assert(kSmem <= 232448 && kTmemO + DH <= 512 && DH % 64 == 0, "shared memory, tensor memory");
 };
 
 // What the second kernel needs of a cut item; pieces 0: none.
@@ -87,19 +88,18 @@ struct TreeCut {
   int ntok;     // the item's tokens
 };
 
-// Workspace after the header: TreeCut[kTreeMaxCtas], then two pairs of slots per CTA, one
-// slot for each tile (the second pair for an item that begins in its share): O as
-// [Dh / 4][128 rows][4] fp32, m[128], l[128].
+// Workspace after the header: TreeCut[kTreeMaxCtas], then two slots per CTA (the second
+// for an item that begins in its share): O as [Dh / 4][128 rows][4] fp32, m[128], l[128].
 constexpr size_t kTreeCutOffset = kWsHeaderBytes;
 constexpr size_t kTreeSlotOffset = kTreeCutOffset + (size_t)kTreeMaxCtas * sizeof(TreeCut);
 constexpr size_t kTreeSlotFloats = (size_t)128 * kTreeBM + 2 * kTreeBM;
-constexpr size_t kTreeWorkspaceBytes = kTreeSlotOffset + 4 * (size_t)kTreeMaxCtas * kTreeSlotFloats * 4;
+constexpr size_t kTreeWorkspaceBytes = kTreeSlotOffset + 2 * (size_t)kTreeMaxCtas * kTreeSlotFloats * 4;
 static_assert(kTreeSlotOffset % 16 == 0, "alignment of the slots");
 
 struct TreeArgs {
   int B, T, H, Hkv, group;
-  int tile_tokens;        // 128 / group
-  int tokens;             // of an item: one tile's or two tiles'
+  int tokens;             // of a tile: 128 / group
+  int lines;              // 2: even tiles, then odd ones; 1: no sequence has two
   int page_size, max_pages;
   int num_pages;
   int chunk;              // keys of one copy: min(page_size, 128)
@@ -200,56 +200,62 @@ __device__ __forceinline__ long long tree_div(long long r, long long d) {
   return r / d;
 }
 
-// One sequence, as every role sees it (what breaks the rules is clamped; the checks
-// report it).
+// One sequence's even or odd tiles (v: all sequences' even ones, then their odd ones), as
+// every role sees it (what breaks the rules is clamped; the checks report it).
 struct TreeSeq {
-  int a, n;       // its rows of Q: tokens [a, a + n)
+  int b, odd;
+  int a, n;            // its rows of Q: tokens [a, a + n)
   int ctx;
-  int tiles;           // items of a key head
-  long long per_head;  // their blocks
+  int tiles;           // even (or odd) ones
+  long long per_head;  // their blocks, of one key head
 
-  __device__ __forceinline__ void load(const TreeArgs& p, int b) {
+  __device__ __forceinline__ void load(const TreeArgs& p, int v) {
+    odd = v >= p.B ? 1 : 0;
+    b = v - odd * p.B;
     const int o0 = __ldg(p.q_offsets + b), o1 = __ldg(p.q_offsets + b + 1), c = __ldg(p.context + b);
     a = min(max(o0, 0), p.T);
     n = min(max(o1, a), p.T) - a;
     const long long most = (long long)p.max_pages * p.page_size - n;
     ctx = (int)min((long long)max(c, 0), max(most, 0ll));
-    tiles = (n + p.tokens - 1) / p.tokens;
-    per_head = n == 0 ? 0 : before(p, tiles - 1) + blocks(p, tiles - 1);
+    const int all = n <= p.tokens ? (n > 0 ? 1 : 0) : (n + p.tokens - 1) / p.tokens;
+    tiles = p.lines == 1 ? all : (all - odd + 1) >> 1;
+    per_head = tiles == 0 ? 0 : before(p, tiles - 1) + blocks(p, tiles - 1);
   }
-  // keys that some row of item t may see, and their blocks
-  __device__ __forceinline__ int keys(const TreeArgs& p, int t) const {
-    return ctx + (p.mask ? n : min(n, (t + 1) * p.tokens));
+  // the sequence's first token of its i-th tile here
+  __device__ __forceinline__ int token(const TreeArgs& p, int i) const { return (p.lines * i + odd) * p.tokens; }
+  // keys that some row of the tile may see, and their blocks
+  __device__ __forceinline__ int keys(const TreeArgs& p, int i) const {
+    return ctx + (p.mask ? n : min(n, token(p, i) + p.tokens));
   }
-  __device__ __forceinline__ int blocks(const TreeArgs& p, int t) const { return (keys(p, t) + kTreeBN - 1) / kTreeBN; }
-  // blocks of the items before t (t < tiles)
-  __device__ __forceinline__ long long before(const TreeArgs& p, int t) const {
-    if (t == 0) return 0;
-    if (p.mask) return (long long)t * ((ctx + n + kTreeBN - 1) / kTreeBN);
-    return tree_floor_sum((uint32_t)t, (uint32_t)p.tokens, (uint32_t)(ctx + p.tokens + kTreeBN - 1));
+  __device__ __forceinline__ int blocks(const TreeArgs& p, int i) const { return (keys(p, i) + kTreeBN - 1) / kTreeBN; }
+  // blocks of the tiles before the i-th
+  __device__ __forceinline__ long long before(const TreeArgs& p, int i) const {
+    if (i == 0) return 0;
+    if (p.mask) return (long long)i * ((ctx + n + kTreeBN - 1) / kTreeBN);
+    return tree_floor_sum((uint32_t)i, (uint32_t)(p.lines * p.tokens), (uint32_t)(ctx + (odd + 1) * p.tokens + kTreeBN - 1));
   }
 };
 
 // A CTA's share, one fragment (consecutive blocks of one item) after another.
 struct TreeWalker {
   long long x, hi;
-  int b, h, t;
-  long long base;   // first block of sequence b
-  bool fresh;       // (b, h, t) hold the item of block x
+  int v, h, t;
+  long long base;   // first block of v
+  bool fresh;       // (v, h, t) hold the item of block x
   TreeSeq s;
   // the fragment
   long long item;   // the item's first block
   int jb, je, nb;   // its blocks of the item's nb
-  int token0, ntok; // the item's tokens
+  int token0, ntok; // the tile's tokens
   int keys;         // keys that it may see
 
-  __device__ __forceinline__ void init(const TreeArgs& p, long long lo, long long hi_, int b_, long long base_) {
+  __device__ __forceinline__ void init(const TreeArgs& p, long long lo, long long hi_, int v_, long long base_) {
     x = lo;
     hi = hi_;
-    b = b_;
+    v = v_;
     base = base_;
     if (x >= hi) return;
-    s.load(p, b);
+    s.load(p, v);
     const long long r = x - base;
     h = (int)tree_div(r, s.per_head);
     const long long at = r - h * s.per_head;
@@ -271,8 +277,8 @@ struct TreeWalker {
         if (++h == p.Hkv) {
           h = 0;
           base += s.per_head * p.Hkv;
-          do s.load(p, ++b);  // (x < W: a sequence holds it)
-          while (s.n == 0);
+          do s.load(p, ++v);  // (x < W: a sequence holds it)
+          while (s.tiles == 0);
         }
       }
       item = x;
@@ -280,8 +286,8 @@ struct TreeWalker {
     nb = s.blocks(p, t);
     jb = (int)(x - item);
     je = (int)min((long long)nb, jb + (hi - x));
-    token0 = s.a + t * p.tokens;
-    ntok = min(p.tokens, s.n - t * p.tokens);
+    token0 = s.a + s.token(p, t);
+    ntok = min(p.tokens, s.n - s.token(p, t));
     keys = s.keys(p, t);
     x += je - jb;
     fresh = false;
@@ -369,7 +375,7 @@ struct TreeLoads {
     const int j = j0 + block;
     if (j >= f.je || j * kTreeBN + chunk * p.chunk >= f.keys) return -1;
     const int i = page_blocks ? j / page_blocks : j * per_block + chunk;
-    return i < p.max_pages ? __ldg(p.table + (long long)f.b * p.ldt + i) : -1;
+    return i < p.max_pages ? __ldg(p.table + (long long)f.s.b * p.ldt + i) : -1;
   }
   __device__ __forceinline__ void enter(const TreeArgs& p) {
     const int page_blocks = p.page_size / kTreeBN;
@@ -444,36 +450,14 @@ __device__ __forceinline__ void tree_load(const TreeArgs& p, const TreeWalker& w
   }
 }
 
-// Calls f(tile, block, part of its keys, buffer, first, last) for each product of the CTA
-// in the order of their issue, until f is false; first and last: of the products that
-// share a block of K and V.
-template <int TILES, class F>
-__device__ __forceinline__ void tree_products(const TreeArgs& p, TreeWalker& w, const F& f) {
-  int b = 0;
-  while (w.next(p)) {
-    if constexpr (TILES == 1) {
-      for (int j = w.jb; j < w.je; ++j) {
-        if (!f(0, j, 0, b, true, true)) return;
-        if (++b == 3) b = 0;
-      }
-    } else {
-      const int tiles = w.ntok <= p.tile_tokens ? 1 : 2;
-      for (int j = w.jb; j < w.je; ++j)
-        for (int sub = 0; sub < 2; ++sub)
-          for (int t = 0; t < tiles; ++t)
-            if (!f(t, j, sub, 2 * t + sub, sub == 0 && t == 0, sub == 1 && t == tiles - 1)) return;
-    }
-  }
-}
-
 // tmQ {Dh, H, T}, boxes of 64 x group x (tokens of a tile); tmK, tmV {Dh, page_size,
 // Hkv, pages}, boxes of 64 x chunk x 1 x 1; 128-byte swizzle.
-template <int DH, int TILES, bool OUT_F32>
-__global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
+template <int DH, bool OUT_F32>
+__global__ void __launch_bounds__(kTreeThreads, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const TreeArgs p) {
-  using Cfg = TreeCfg<DH, TILES>;
-  constexpr int KS = Cfg::kKStages, VS = Cfg::kVStages, SB = Cfg::kSBufs, SUB = Cfg::kSub;
+  using Cfg = TreeCfg<DH>;
+  constexpr int KS = Cfg::kKStages, VS = Cfg::kVStages, SB = kTreeSBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_addr(smem), sK = sQ + 2 * Cfg::kTile, sV = sK + KS * Cfg::kTile;
@@ -489,8 +473,8 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
   static_assert(Cfg::kBars * 8 <= 320 && 320 + 34 * 8 + 24 <= 1024, "the last kilobyte");
   const int warp = (int)threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
-  // k_full, k_empty, v_full, v_empty, q_full[2] (one tile: of items in turn), then of the
-  // S/P buffers s_full, p_full, pv_done, then of the tiles o_empty
+  // k_full, k_empty, v_full, v_empty, q_full[2] (of items in turn), then of the S/P buffers
+  // s_full, p_full, pv_done, then o_empty
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t k_full = bar0, k_empty = k_full + 8 * KS, v_full = k_empty + 8 * KS, v_empty = v_full + 8 * VS;
   const uint32_t q_full = v_empty + 8 * VS, s_full = q_full + 16, p_full = s_full + 8 * SB, pv_done = p_full + 8 * SB;
@@ -507,10 +491,10 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
     for (int i = 0; i < 2; ++i) mbar_init(q_full + 8 * i, 1);
     for (int i = 0; i < SB; ++i) {
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, 4);  // the tile's softmax warps
+      mbar_init(p_full + 8 * i, 4);  // the softmax warps
       mbar_init(pv_done + 8 * i, 1);
     }
-    for (int i = 0; i < TILES; ++i) mbar_init(o_empty + 8 * i, 4);
+    mbar_init(o_empty, 4);
     *abort_flag = 0u;
     for (int i = 0; i < 4; ++i) odd_v[i] = 0u;
     found[0] = found[1] = 0;
@@ -525,14 +509,14 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
   }
   if (blockIdx.x == 0) tree_check(p);
   // this CTA's share
-  auto count = [&](int b) -> long long {
+  auto count = [&](int v) -> long long {
     TreeSeq s;
-    s.load(p, b);
+    s.load(p, v);
     return s.per_head * p.Hkv;
   };
   tc_fence_before_sync();
-  BlockCount<long long, Cfg::kThreads> counted;
-  const long long W = counted.total(p.B, count, scratch);
+  BlockCount<long long, kTreeThreads> counted;
+  const long long W = counted.total(p.lines * p.B, count, scratch);
   tc_fence_after_sync();
   const Share<long long> share(W, (int)max(1ll, min((long long)gridDim.x, W)));
   long long lo = 0, hi = 0;
@@ -540,7 +524,7 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
     lo = share.lo((int)blockIdx.x);
     hi = share.lo((int)blockIdx.x + 1);
   }
-  if (lo < hi) counted.locate(p.B, count, lo, scratch, found);
+  if (lo < hi) counted.locate(p.lines * p.B, count, lo, scratch, found);
   __syncthreads();
   const uint32_t tmem_base = *tmem_slot;
   const Guard guard{p.ws, abort_flag, p.timeout_ns};
@@ -570,164 +554,144 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ S = Q K^T
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(kTreeBM, SUB, false, false);
-      int ks = 0;
-      uint32_t kph = 0;
-      uint32_t used = 0, sph = 0;  // bit b: buffer b has been used; the parity of its next use
-      uint32_t qph = 0;            // bit i: parity of Q buffer i's next item
-      int qb = 0;                  // (one tile) its item's Q buffer
-      tree_products<TILES>(p, w, [&](int t, int j, int sub, int b, bool first, bool last) -> bool {
-        if (j == w.jb && sub == 0) {
-          if (TILES == 2) qb = t;
-          if (!tree_wait(guard, q_full + 8 * qb, (qph >> qb) & 1u, (kRoleMma << 16) | 0x800 | qb)) return false;
-          qph ^= 1u << qb;
-        }
-        // the buffer's last P has been read, and K is there
-        if (((used >> b) & 1u) && !tree_wait(guard, pv_done + 8 * b, ((sph >> b) & 1u) ^ 1u, (kRoleMma << 16) | 0x400 | b)) return false;
-        if (first && !tree_wait(guard, k_full + 8 * ks, kph, (kRoleMma << 16) | ks)) return false;
-        tc_fence_after_sync();
-        const uint32_t q_at = sQ + (TILES == 2 ? t : qb) * Cfg::kTile, k_at = sK + ks * Cfg::kTile + sub * (SUB * 128);
-        const uint32_t d = tmem_base + (uint32_t)(SUB * b);
+      constexpr uint32_t idesc = idesc_bf16_f32(kTreeBM, kTreeBN, false, false);
+      int ks = 0, b = 0;
+      uint32_t kph = 0, bph = 0, it = 0;
+      bool used = false, ok = true;  // used: every buffer has been
+      for (; ok && w.next(p); ++it) {
+        const uint32_t qb = it & 1u;
+        if (!tree_wait(guard, q_full + 8 * qb, (it >> 1) & 1u, (kRoleMma << 16) | 0x800 | qb)) break;
+        const uint32_t q_at = sQ + qb * Cfg::kTile;
+        for (int j = w.jb; j < w.je; ++j) {
+          // the buffer's last P has been read, and K is there
+          if ((used && !tree_wait(guard, pv_done + 8 * b, bph ^ 1u, (kRoleMma << 16) | 0x400 | b)) ||
+              !tree_wait(guard, k_full + 8 * ks, kph, (kRoleMma << 16) | ks)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t k_at = sK + ks * Cfg::kTile, d = tmem_base + (uint32_t)(kTreeBN * b);
 #pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-          const uint32_t o = (uint32_t)((kk >> 2) * (kTreeBN * 128) + (kk & 3) * 32);
-          umma_bf16<1>(d, sdesc_sw128(q_at + o, 16, 1024), sdesc_sw128(k_at + o, 16, 1024), idesc, kk != 0 ? 1u : 0u);
-        }
-        umma_commit(s_full + 8 * b);
-        used |= 1u << b;
-        sph ^= 1u << b;
-        if (last) {
+          for (int kk = 0; kk < DH / 16; ++kk) {
+            const uint32_t o = (uint32_t)((kk >> 2) * (kTreeBN * 128) + (kk & 3) * 32);
+            umma_bf16<1>(d, sdesc_sw128(q_at + o, 16, 1024), sdesc_sw128(k_at + o, 16, 1024), idesc, kk != 0 ? 1u : 0u);
+          }
+          umma_commit(s_full + 8 * b);
           umma_commit(k_empty + 8 * ks);
           if (++ks == KS) {
             ks = 0;
             kph ^= 1u;
           }
-          if (TILES == 1 && j == w.je - 1) qb ^= 1;
+          if (++b == SB) {
+            b = 0;
+            bph ^= 1u;
+            used = true;
+          }
         }
-        return true;
-      });
+      }
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------------ O += P V
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(kTreeBM, DH, false, true);
-      int vs = 0;
-      uint32_t vph = 0;
-      uint32_t sph = 0, oph = 3u;  // bits: parities of the buffers' next P, of the tiles' next release of O
-      tree_products<TILES>(p, w, [&](int t, int j, int sub, int b, bool first, bool last) -> bool {
-        if (first && !tree_wait(guard, v_full + 8 * vs, vph, (kRoleMma << 16) | 0x10 | vs)) return false;
-        const bool begins = j == w.jb && sub == 0;
-        if (begins) {
-          if (!tree_wait(guard, o_empty + 8 * t, (oph >> t) & 1u, (kRoleMma << 16) | 0x300 | t)) return false;
-          oph ^= 1u << t;
-        }
-        if (!tree_wait(guard, p_full + 8 * b, (sph >> b) & 1u, (kRoleMma << 16) | 0x200 | b)) return false;
-        tc_fence_after_sync();
-        // 16 keys: 8 columns of P, 2 KB of V
-        const uint64_t vd = sdesc_sw128(sV + vs * Cfg::kTile, kTreeBN * 128, 1024) + (uint32_t)(sub * (SUB / 16) * 128);
-        const uint32_t a = tmem_base + (uint32_t)(SUB * b), d = tmem_base + (uint32_t)(Cfg::kTmemO + t * DH);
+      int vs = 0, b = 0;
+      uint32_t vph = 0, bph = 0, oph = 1;
+      bool ok = true;
+      while (ok && w.next(p)) {
+        for (int j = w.jb; j < w.je; ++j) {
+          if (!tree_wait(guard, v_full + 8 * vs, vph, (kRoleMma << 16) | 0x10 | vs) ||
+              (j == w.jb && !tree_wait(guard, o_empty, oph, (kRoleMma << 16) | 0x300)) ||
+              !tree_wait(guard, p_full + 8 * b, bph, (kRoleMma << 16) | 0x200 | b)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          // 16 keys: 8 columns of P, 2 KB of V
+          const uint64_t vd = sdesc_sw128(sV + vs * Cfg::kTile, kTreeBN * 128, 1024);
+          const uint32_t a = tmem_base + (uint32_t)(kTreeBN * b), d = tmem_base + Cfg::kTmemO;
 #pragma unroll
-        for (int kk = 0; kk < SUB / 16; ++kk)
-          tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc, (!begins || kk != 0) ? 1u : 0u);
-        if constexpr (OUT_F32) {
+          for (int kk = 0; kk < kTreeBN / 16; ++kk)
+            tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc,
+                        (j > w.jb || kk != 0) ? 1u : 0u);
+          if constexpr (OUT_F32) {
 #pragma unroll
-          for (int kk = 0; kk < SUB / 16; ++kk)
-            tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + 16 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
-        }
-        umma_commit(pv_done + 8 * b);
-        sph ^= 1u << b;
-        if (last) {
+            for (int kk = 0; kk < kTreeBN / 16; ++kk)
+              tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + 16 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
+          }
+          umma_commit(pv_done + 8 * b);
           umma_commit(v_empty + 8 * vs);
           if (++vs == VS) {
             vs = 0;
             vph ^= 1u;
           }
+          if (++b == SB) {
+            b = 0;
+            bph ^= 1u;
+          }
         }
-        return true;
-      });
+        oph ^= 1u;
+      }
     }
   } else {
     // ------------------------------------------------------------------ softmax, output
-    const int t = TILES == 1 ? 0 : (warp >> 2) - 1;  // the tile
     const int q = warp & 3;
     const int row = q * 32 + (int)lane;
     const uint32_t t_lane = tmem_base + ((uint32_t)(q * 32) << 16);
-    const uint32_t t_o = t_lane + Cfg::kTmemO + t * DH;
+    const uint32_t t_o = t_lane + Cfg::kTmemO;
     const int my_tok = row / p.group, my_head = row - my_tok * p.group;
     const float cs = p.cs;
     const long long x_first = w.x;
-    int b = 2 * t;               // S/P buffer of the next product,
-    uint32_t bph = 0;            // its parity,
-    int last_b = 0;              // and those of the product before
-    uint32_t last_ph = 0, it = 0;  // (it: items of the share, those without this tile too)
+    int b = 0;                     // S/P buffer of the next product,
+    uint32_t bph = 0;              // its parity,
+    int last_b = 0;                // and those of the product before
+    uint32_t last_ph = 0, it = 0;  // (it: items of the share)
     bool wrote_cut = false, ok = true;
-    // the tile's rows of item x (none: the item has one tile only), and their Q
-    auto rows_of = [&](const TreeWalker& x) { return min(p.tile_tokens, x.ntok - t * p.tile_tokens) * p.group; };
-    auto load_q = [&](const TreeWalker& x, int qb) {
+    auto load_q = [&](const TreeWalker& x, uint32_t qb) {
       if (q == 0 && lane == 0) {
-        mbar_arrive_expect_tx(q_full + 8 * qb, (uint32_t)(Cfg::kHalves * 128 * p.group * p.tile_tokens));
-        for (int hf = 0; hf < Cfg::kHalves; ++hf)
-          tma_load_3d(sQ + qb * Cfg::kTile + hf * (kTreeBM * 128), &tmQ, q_full + 8 * qb, hf * 64, x.h * p.group,
-                      x.token0 + t * p.tile_tokens);
+        mbar_arrive_expect_tx(q_full + 8 * qb, (uint32_t)(DH / 64 * 128 * p.group * p.tokens));
+        for (int hf = 0; hf < DH / 64; ++hf)
+          tma_load_3d(sQ + qb * Cfg::kTile + hf * (kTreeBM * 128), &tmQ, q_full + 8 * qb, hf * 64, x.h * p.group, x.token0);
       }
     };
-    // (an item without this tile is passed over)
-    auto advance = [&](TreeWalker& x) -> bool {
-      while (x.next(p)) {
-        if (rows_of(x) > 0) return true;
-        ++it;
-      }
-      return false;
-    };
-    bool has = advance(w);
-    if (has) load_q(w, t);
+    bool has = w.next(p);
+    if (has) load_q(w, 0);
     TreeWalker nx = w;
     bool has_next = false;
     for (; ok && has; w = nx, has = has_next, ++it) {
-      const uint32_t it_now = it;
-      const int rows = rows_of(w);
-      if (TILES == 1) {  // the next item's Q, into the other buffer: the item before this one is over
-        nx = w;
-        has_next = advance(nx);
-        if (has_next) load_q(nx, (int)((it_now + 1u) & 1u));
-      }
+      const int rows = w.ntok * p.group;
+      // the next item's Q, into the other buffer: the item before this one is over
+      nx = w;
+      has_next = nx.next(p);
+      if (has_next) load_q(nx, (it + 1u) & 1u);
       const bool active = q * 32 < rows;  // (of the whole warp)
-      const int ti = w.t * p.tokens + t * p.tile_tokens + my_tok;
+      const int ti = w.s.token(p, w.t) + my_tok;
       float m = -INFINITY, l = 0.0f;
-      for (int js = w.jb * (kTreeBN / SUB); js < w.je * (kTreeBN / SUB); ++js) {
-        const int j = js / (kTreeBN / SUB), sub = js % (kTreeBN / SUB), key0 = js * SUB;
-        const bool begins = j == w.jb && sub == 0;
-        const bool inner = key0 + SUB <= w.s.ctx;  // every row sees every key
+      for (int j = w.jb; j < w.je; ++j) {
+        const bool inner = (j + 1) * kTreeBN <= w.s.ctx;  // every row sees every key
         if (!__all_sync(0xffffffffu, tree_wait(guard, s_full + 8 * b, bph, (kRoleEpilogue << 16) | b))) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        if (TILES == 2 && js == w.je * (kTreeBN / SUB) - 1) {
-          // The item's last product with Q is done: the next item's can come.
-          nx = w;
-          has_next = advance(nx);
-          if (has_next) load_q(nx, t);
-        }
-        const uint32_t t_s = t_lane + (uint32_t)(SUB * b);
+        const uint32_t t_s = t_lane + (uint32_t)(kTreeBN * b);
         if (active) {
           // P of 32 keys goes over their scores: 16 columns of bf16 pairs, then (fp32
           // output) 16 of what those leave.
           float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           auto sum = [&]() { return (rs[0] + rs[1]) + (rs[2] + rs[3]); };
           bool done = false;
-          if (inner && !begins && __all_sync(0xffffffffu, fabsf(m) < 1.0e6f || row >= rows)) {
+          if (inner && j > w.jb && __all_sync(0xffffffffu, fabsf(m) < 1.0e6f || row >= rows)) {
             // With the maximum so far: every P is positive, so a row sum of at most 2^8
             // proves that no P exceeds it and the maximum need not be looked for.  (cs S - m
             // is rounded once, m is a rounded product: their difference is the same factor
             // for all of a row, and small while m is.)
-            float x[SUB];
+            float x[kTreeBN];
 #pragma unroll
-            for (int c = 0; c < SUB / 32; ++c) tree_tmem_load32(t_s + 32 * c, x + 32 * c);
-            tree_tmem_load_wait<SUB>(x);
-            uint32_t hi[SUB / 2], lo[OUT_F32 ? SUB / 2 : 1];
+            for (int c = 0; c < kTreeBN / 32; ++c) tree_tmem_load32(t_s + 32 * c, x + 32 * c);
+            tree_tmem_load_wait<kTreeBN>(x);
+            uint32_t hi[kTreeBN / 2], lo[OUT_F32 ? kTreeBN / 2 : 1];
 #pragma unroll
-            for (int i = 0; i < SUB / 2; ++i) {
+            for (int i = 0; i < kTreeBN / 2; ++i) {
               float& x0 = x[2 * i];
               float& x1 = x[2 * i + 1];
               tree_fma2(x0, x1, cs, -m);
@@ -740,7 +704,7 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
             done = __all_sync(0xffffffffu, sum() <= kTreeGrowSum || row >= rows) != 0;
             if (done) {
 #pragma unroll
-              for (int c = 0; c < SUB / 32; ++c) {
+              for (int c = 0; c < kTreeBN / 32; ++c) {
                 tree_tmem_store16(t_s + 32 * c, hi + 16 * c);
                 if constexpr (OUT_F32) tree_tmem_store16(t_s + 32 * c + 16, lo + 16 * c);
               }
@@ -752,14 +716,14 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
             // Any other block, 32 keys at a time (loops: this code runs a few times in a
             // fragment, and unrolled it took longer to fetch than to run).  First cs S,
             // -inf where the row sees nothing, back over the scores.
-            uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};  // (of SUB / 32 words)
+            uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
             if (!inner && row < rows) {
 #pragma unroll
-              for (int i = 0; i < SUB / 32; ++i) vis[i] = tree_visible(p, w.s, ti, key0 - w.s.ctx + 32 * i);
+              for (int i = 0; i < kTreeBN / 32; ++i) vis[i] = tree_visible(p, w.s, ti, j * kTreeBN - w.s.ctx + 32 * i);
             }
             float mx = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < SUB / 32; ++c) {
+            for (int c = 0; c < kTreeBN / 32; ++c) {
               float x[32];
               tmem_load32(t_s + 32 * c, x);
               const uint32_t v = c < 2 ? (c ? vis[1] : vis[0]) : (c > 2 ? vis[3] : vis[2]);
@@ -773,7 +737,7 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
               tree_tmem_store32(t_s + 32 * c, x);
             }
             tree_tmem_store_wait();
-            if (begins) {
+            if (j == w.jb) {
               m = mx;  // the first PV product overwrites O
             } else {
               const bool grow = mx > m + kTreeGrow && row < rows;
@@ -802,7 +766,7 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
             // (a row that has seen no key yet: all its scores are -inf, its P zero)
             const float top = !inner && m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
-            for (int c = 0; c < SUB / 32; ++c) {
+            for (int c = 0; c < kTreeBN / 32; ++c) {
               float x[32];
               tmem_load32(t_s + 32 * c, x);
               uint32_t hi[16], lo[16];
@@ -823,16 +787,15 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
           l += sum();
           tree_tmem_store_wait();
         }
-        if (t == 0 && sub == 0 && (j + 1) * kTreeBN > w.s.ctx) {
+        if (!inner) {
           // V: clear the block's keys behind the sequence and what is not finite of the new
-          // tokens; thread = key.  (The block's other products with V are issued after this
-          // one.)  These warps wait for V here only, and a parity tells two phases apart:
-          // the stage's last use has to be over.  With two tiles PV of the block before this
-          // one is; with one, PV three blocks ago, and two stages need two.
+          // tokens; thread = key.  These warps wait for V here only, and a parity tells two
+          // phases apart: the stage's last use has to be over.  PV of three blocks ago is (its
+          // buffer holds this S), and two stages need that of two.
           const long long g = w.item + j - x_first;  // the share's blocks use the stages in turn
-          static_assert(VS >= 2, "stages of V");
-          if (TILES == 1 && VS == 2 && g >= 2 &&
-              !__all_sync(0xffffffffu, tree_wait(guard, pv_done + 8 * (int)((g - 2) % 3), (uint32_t)((g - 2) / 3) & 1u, (kRoleEpilogue << 16) | 0x600))) {
+          static_assert(VS >= 2 && SB == 3, "stages of V");
+          if (VS == 2 && g >= 2 &&
+              !__all_sync(0xffffffffu, tree_wait(guard, pv_done + 8 * (int)((g - 2) % SB), (uint32_t)((g - 2) / SB) & 1u, (kRoleEpilogue << 16) | 0x600))) {
             ok = false;
             break;
           }
@@ -845,7 +808,7 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
           if (key >= w.s.ctx) {
             const bool out = key >= w.keys;
             bool odd = false;
-            for (int hf = 0; hf < Cfg::kHalves; ++hf) {
+            for (int hf = 0; hf < DH / 64; ++hf) {
               const uint32_t at = sV + vs * Cfg::kTile + (uint32_t)(hf * (kTreeBN * 128) + row * 128);
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
@@ -875,7 +838,7 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
                 }
               }
             }
-            if (odd) odd_v[it_now & 3u] = it_now + 1u;
+            if (odd) odd_v[it & 3u] = it + 1u;
           }
           fence_proxy_async_smem();
         }
@@ -884,14 +847,9 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
         if (lane == 0) mbar_arrive(p_full + 8 * b);
         last_b = b;
         last_ph = bph;
-        if constexpr (TILES == 1) {
-          if (++b == 3) {
-            b = 0;
-            bph ^= 1u;
-          }
-        } else {
-          b ^= 1;
-          if (sub == 1) bph ^= 1u;
+        if (++b == SB) {
+          b = 0;
+          bph ^= 1u;
         }
       }
       if (!ok) break;
@@ -903,10 +861,10 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
       tc_fence_after_sync();
       if (active) {
         const bool whole = w.jb == 0 && w.je == w.nb;
-        const bool odd = odd_v[it_now & 3u] > it_now;  // (a later item's: looked into too)
+        const bool odd = odd_v[it & 3u] > it;  // (a later item's: looked into too)
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const long long at = (long long)(w.token0 + t * p.tile_tokens + my_tok) * p.ldo + (long long)(w.h * p.group + my_head) * DH;
-        float* slot = whole ? nullptr : p.slots + (size_t)(4 * blockIdx.x + (w.jb == 0 ? 2 : 0) + t) * kTreeSlotFloats;
+        const long long at = (long long)(w.token0 + my_tok) * p.ldo + (long long)(w.h * p.group + my_head) * DH;
+        float* slot = whole ? nullptr : p.slots + (size_t)(2 * blockIdx.x + (w.jb == 0 ? 1 : 0)) * kTreeSlotFloats;
 #pragma unroll 1
         for (int c = 0; c < DH / 32; ++c) {
           float v[32];
@@ -916,7 +874,7 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
               // new tokens of this fragment's blocks whose V is not finite, where the row sees them
               for (int key = max(w.s.ctx, w.jb * kTreeBN); key < min(w.keys, w.je * kTreeBN); ++key) {
                 if (!(tree_visible(p, w.s, ti, key - w.s.ctx) & 1u)) continue;
-                const int pg = __ldg(p.table + (long long)w.b * p.ldt + min(key / p.page_size, p.max_pages - 1));
+                const int pg = __ldg(p.table + (long long)w.s.b * p.ldt + min(key / p.page_size, p.max_pages - 1));
                 if (pg < 0 || pg >= p.num_pages) continue;
                 const __nv_bfloat16* vr = p.v + pg * p.page_stride + (key % p.page_size) * p.token_stride + w.h * p.head_stride + c * 32;
 #pragma unroll
@@ -954,7 +912,7 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
           __stcg(slot + 128 * kTreeBM + row, m);
           __stcg(slot + 128 * kTreeBM + kTreeBM + row, l);
         }
-        if (!whole && w.jb == 0 && row == 0 && t == 0) {
+        if (!whole && w.jb == 0 && row == 0) {
           p.cuts[blockIdx.x] = TreeCut{share.owner(w.item + w.nb - 1) - (int)blockIdx.x + 1, w.token0, w.h * p.group, w.ntok};
           wrote_cut = true;
         }
@@ -962,10 +920,10 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(o_empty + 8 * t);
+        mbar_arrive(o_empty);
       }
     }
-    if (p.split && row == 0 && t == 0 && !wrote_cut) p.cuts[blockIdx.x].pieces = 0;
+    if (p.split && row == 0 && !wrote_cut) p.cuts[blockIdx.x].pieces = 0;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before_sync();
@@ -977,17 +935,17 @@ __global__ void __launch_bounds__(TreeCfg<DH, TILES>::kThreads, 1)
   if (warp == 2) tmem_dealloc<1>(tmem_base, 512);
 }
 
-// The cut items' pieces added up: blockIdx.x is the CTA in whose share an item begins,
-// blockIdx.z the tile; a thread takes four components of a row.
+// The cut items' pieces added up: blockIdx.x is the CTA in whose share an item begins; a
+// thread takes four components of a row.
 template <int DH, bool OUT_F32>
 __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const TreeCut cut = p.cuts[blockIdx.x];
   const int i = (int)(blockIdx.y * 256 + threadIdx.x);
-  const int row = i % kTreeBM, quad = i / kTreeBM, t = (int)blockIdx.z;
-  if (cut.pieces == 0 || row >= min(p.tile_tokens, cut.ntok - t * p.tile_tokens) * p.group) return;
+  const int row = i % kTreeBM, quad = i / kTreeBM;
+  if (cut.pieces == 0 || row >= cut.ntok * p.group) return;
   auto slot = [&](int k) {
-    return p.slots + (size_t)(4 * (blockIdx.x + k) + (k == 0 ? 2 : 0) + t) * kTreeSlotFloats;
+    return p.slots + (size_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * kTreeSlotFloats;
   };
   float m = -INFINITY;
   for (int k = 0; k < cut.pieces; ++k) m = fmaxf(m, __ldcg(slot(k) + 128 * kTreeBM + row));
@@ -1008,7 +966,7 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const bool none = l == 0.0f;
   const int tok = row / p.group, head = row - tok * p.group;
-  const long long at = (long long)(cut.token0 + t * p.tile_tokens + tok) * p.ldo + (long long)(cut.head0 + head) * DH + quad * 4;
+  const long long at = (long long)(cut.token0 + tok) * p.ldo + (long long)(cut.head0 + head) * DH + quad * 4;
   const float y0 = none ? 0.0f : o.x * inv, y1 = none ? 0.0f : o.y * inv, y2 = none ? 0.0f : o.z * inv, y3 = none ? 0.0f : o.w * inv;
   if constexpr (OUT_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.O) + at) = make_float4(y0, y1, y2, y3);
   else
