@@ -29,8 +29,8 @@
 //
 // Inside a CTA, per block (online softmax in base 2, cs = scale * log2 e):
 //   MMA      S = Q . K^T        Q and K from shared memory, 128 x 128 x Dh
-//   softmax  P = 2^(cs S - m) as bf16 over S's tensor memory; m moves only when the
-//            maximum has grown by more than 2^8, which rescales O and l
+//   softmax  P = 2^(cs S - m) as bf16 over S's tensor memory; m is a whole number that
+//            moves only when a score exceeds it by more than 8, which rescales O and l
 //            (P <= 2^8; l sums the unrounded P).  One bf16 is off by up to 2^-8 of P, which
 //            a bf16 output's own rounding covers; for fp32 output P is two bf16 (what the
 //            first leaves), off by 2^-16, in the two halves of S's columns
@@ -675,116 +675,129 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tc_fence_after_sync();
         const uint32_t t_s = t_lane + (uint32_t)(kTreeBN * b);
         if (active) {
+          // 64 keys at a time, in a loop: code that fits the instruction cache's first level
+          // (unrolled over the block, a warp waited for instructions a fourth of the time).
           // P of 32 keys goes over their scores: 16 columns of bf16 pairs, then (fp32
           // output) 16 of what those leave.
-          float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          auto sum = [&]() { return (rs[0] + rs[1]) + (rs[2] + rs[3]); };
-          bool done = false;
-          if (inner && j > w.jb && __all_sync(0xffffffffu, fabsf(m) < 1.0e6f || row >= rows)) {
-            // With the maximum so far: every P is positive, so a row sum of at most 2^8
-            // proves that no P exceeds it and the maximum need not be looked for.  (cs S - m
-            // is rounded once, m is a rounded product: their difference is the same factor
-            // for all of a row, and small while m is.)
-            float x[kTreeBN];
+          uint32_t vis[4] = {0u, 0u, 0u, 0u};
+          if (!inner && row < rows) {
 #pragma unroll
-            for (int c = 0; c < kTreeBN / 32; ++c) tree_tmem_load32(t_s + 32 * c, x + 32 * c);
-            tree_tmem_load_wait<kTreeBN>(x);
-            uint32_t hi[kTreeBN / 2], lo[OUT_F32 ? kTreeBN / 2 : 1];
-#pragma unroll
-            for (int i = 0; i < kTreeBN / 2; ++i) {
-              float& x0 = x[2 * i];
-              float& x1 = x[2 * i + 1];
-              tree_fma2(x0, x1, cs, -m);
-              x0 = tree_ex2(x0);
-              x1 = tree_ex2(x1);
-              tree_add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], x0, x1);
-              hi[i] = pack_bf16x2(x0, x1);
-              if constexpr (OUT_F32) lo[i] = pack_bf16x2(x0 - __uint_as_float(hi[i] << 16), x1 - __uint_as_float(hi[i] & 0xffff0000u));
-            }
-            done = __all_sync(0xffffffffu, sum() <= kTreeGrowSum || row >= rows) != 0;
-            if (done) {
-#pragma unroll
-              for (int c = 0; c < kTreeBN / 32; ++c) {
-                tree_tmem_store16(t_s + 32 * c, hi + 16 * c);
-                if constexpr (OUT_F32) tree_tmem_store16(t_s + 32 * c + 16, lo + 16 * c);
-              }
-            } else {
-              rs[0] = rs[1] = rs[2] = rs[3] = 0.0f;
-            }
+            for (int i = 0; i < 4; ++i) vis[i] = tree_visible(p, w.s, ti, j * kTreeBN - w.s.ctx + 32 * i);
           }
-          if (!done) {
-            // Any other block, 32 keys at a time (loops: this code runs a few times in a
-            // fragment, and unrolled it took longer to fetch than to run).  First cs S,
-            // -inf where the row sees nothing, back over the scores.
-            uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-            if (!inner && row < rows) {
-#pragma unroll
-              for (int i = 0; i < kTreeBN / 32; ++i) vis[i] = tree_visible(p, w.s, ti, j * kTreeBN - w.s.ctx + 32 * i);
-            }
-            float mx = -INFINITY;
+          float sum = 0.0f;
 #pragma unroll 1
-            for (int c = 0; c < kTreeBN / 32; ++c) {
-              float x[32];
-              tmem_load32(t_s + 32 * c, x);
-              const uint32_t v = c < 2 ? (c ? vis[1] : vis[0]) : (c > 2 ? vis[3] : vis[2]);
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t t_c = t_s + 64 * c;
+            const uint32_t v0 = c ? vis[2] : vis[0], v1 = c ? vis[3] : vis[1];
+            float x[64];
+            auto load = [&]() {
+              tree_tmem_load32(t_c, x);
+              tree_tmem_load32(t_c + 32, x + 32);
+              tree_tmem_load_wait<64>(x);
+            };
+            // the largest cs S that the row sees of these keys, rounded up: maxima are whole
+            // numbers, so that a change of one scales by a power of two, exactly
+            auto maximum = [&]() {
               float e[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              if (inner) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) e[i & 3] = fmaxf(e[i & 3], __fmul_rn(x[i], cs));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) e[i & 3] = (i < 32 ? v0 : v1) & (1u << (i & 31)) ? fmaxf(e[i & 3], __fmul_rn(x[i], cs)) : e[i & 3];
+              }
+              return ceilf(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])));
+            };
+            load();
+            // A row without a maximum yet (its first keys): theirs.  Its O is zero so far, or
+            // is overwritten.
+            if (__any_sync(0xffffffffu, m == -INFINITY && row < rows)) {
+              const float mx = maximum();
+              if (m == -INFINITY) m = mx;
+            }
+            uint32_t hi[32], lo[OUT_F32 ? 32 : 1];
+            auto probabilities = [&]() -> float {
+              // (no key seen yet: all scores are -inf, P zero)
+              const float top = !inner && m == -INFINITY ? 0.0f : m;
+              float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              if (__all_sync(0xffffffffu, fabsf(top) < 1.0e6f || row >= rows)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) tree_fma2(x[2 * i], x[2 * i + 1], cs, -top);
+              } else {  // (the difference to the exact product, for scores that pass 2^24)
+#pragma unroll
+                for (int i = 0; i < 64; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], cs), -top);
+              }
+              if (!inner) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) x[i] = (i < 32 ? v0 : v1) & (1u << (i & 31)) ? x[i] : -INFINITY;
+              }
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                x[i] = v & (1u << i) ? x[i] * cs : -INFINITY;
-                e[i & 3] = fmaxf(e[i & 3], x[i]);
-              }
-              mx = fmaxf(mx, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])));
-              tree_tmem_store32(t_s + 32 * c, x);
-            }
-            tree_tmem_store_wait();
-            if (j == w.jb) {
-              m = mx;  // the first PV product overwrites O
-            } else {
-              const bool grow = mx > m + kTreeGrow && row < rows;
-              if (__any_sync(0xffffffffu, grow)) {
-                if (!warp_wait_phase(guard, pv_done + 8 * last_b, last_ph, (kRoleEpilogue << 16) | 0x100)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after_sync();
-                const float alpha = grow ? tree_ex2(m - mx) : 1.0f;
-                if (grow) {
-                  l *= alpha;
-                  m = mx;
-                }
-#pragma unroll 1
-                for (int c = 0; c < DH / 32; ++c) {
-                  float v[32];
-                  tmem_load32(t_o + c * 32, v);
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) v[i] *= alpha;
-                  tree_tmem_store32(t_o + c * 32, v);
-                }
-                tree_tmem_store_wait();
-              }
-            }
-            // (a row that has seen no key yet: all its scores are -inf, its P zero)
-            const float top = !inner && m == -INFINITY ? 0.0f : m;
-#pragma unroll 1
-            for (int c = 0; c < kTreeBN / 32; ++c) {
-              float x[32];
-              tmem_load32(t_s + 32 * c, x);
-              uint32_t hi[16], lo[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
                 float& x0 = x[2 * i];
                 float& x1 = x[2 * i + 1];
-                x0 = tree_ex2(x0 - top);
-                x1 = tree_ex2(x1 - top);
+                x0 = tree_ex2(x0);
+                x1 = tree_ex2(x1);
                 tree_add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], x0, x1);
                 hi[i] = pack_bf16x2(x0, x1);
                 if constexpr (OUT_F32) lo[i] = pack_bf16x2(x0 - __uint_as_float(hi[i] << 16), x1 - __uint_as_float(hi[i] & 0xffff0000u));
               }
-              tree_tmem_store16(t_s + 32 * c, hi);
-              if constexpr (OUT_F32) tree_tmem_store16(t_s + 32 * c + 16, lo);
+              return (rs[0] + rs[1]) + (rs[2] + rs[3]);
+            };
+            float part = probabilities();
+            // Every P is positive: a sum of at most 2^8 proves that none exceeds it and the
+            // maximum need not be looked for.
+            if (!__all_sync(0xffffffffu, part <= kTreeGrowSum || row >= rows)) {
+              load();
+              const float mx = maximum();
+              const bool grow = mx > m + kTreeGrow && row < rows;
+              if (__any_sync(0xffffffffu, grow)) {
+                const float alpha = grow ? tree_ex2(m - mx) : 1.0f;
+                if (grow) {
+                  l *= alpha;
+                  sum *= alpha;
+                  m = mx;
+                }
+                if (j > w.jb) {  // (the first PV product overwrites O)
+                  if (!__all_sync(0xffffffffu, tree_wait(guard, pv_done + 8 * last_b, last_ph, (kRoleEpilogue << 16) | 0x100))) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after_sync();
+#pragma unroll 1
+                  for (int d = 0; d < DH / 32; ++d) {
+                    float v[32];
+                    tmem_load32(t_o + d * 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= alpha;
+                    tree_tmem_store32(t_o + d * 32, v);
+                  }
+                }
+                if (c == 1) {  // the block's first 64 P, with the old maximum
+#pragma unroll 1
+                  for (int d = 0; d < 2; ++d) {
+                    float v[32];
+                    tmem_load32(t_s + 32 * d, v);
+#pragma unroll
+                    for (int i = 0; i < (OUT_F32 ? 32 : 16); ++i) {
+                      const uint32_t y = __float_as_uint(v[i]);
+                      v[i] = __uint_as_float(pack_bf16x2(__uint_as_float(y << 16) * alpha, __uint_as_float(y & 0xffff0000u) * alpha));
+                    }
+                    tree_tmem_store32(t_s + 32 * d, v);
+                  }
+                }
+                tree_tmem_store_wait();
+              }
+              part = probabilities();
+            }
+            sum += part;
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              tree_tmem_store16(t_c + 32 * d, hi + 16 * d);
+              if constexpr (OUT_F32) tree_tmem_store16(t_c + 32 * d + 16, lo + 16 * d);
             }
           }
-          l += sum();
+          if (!ok) break;
+          l += sum;
           tree_tmem_store_wait();
         }
         if (!inner) {
