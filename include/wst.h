@@ -716,9 +716,7 @@ wst_status wst_cache_append_bf16(int T, int H, int Hkv, int Dh, int rot, wst_rop
  * where O is fp32); row maxima, sums and the output accumulate in fp32.  After a tree is verified, wst_permute_rows
  * moves the accepted tokens' rows of the cache together.
  * Supported: Dh 64 and 128, H / Hkv <= 128, page_size 8, 16, 32, 64 or a multiple of
- * 128, max_pages * page_size <= 2^30, T <= 2^30, and fewer than 2^31 blocks of 128 keys
- * if every tile of 128 query rows of every key head read max_pages pages (else
- * WST_ERR_UNSUPPORTED).
+ * 128, max_pages * page_size <= 2^30, T <= 2^30 (else WST_ERR_UNSUPPORTED).
  * Offsets, lengths or masks that break the rules (also context[b] + n_b above
  * max_pages * page_size, or n_b above 32 * mask_words) are clamped and latch
  * WST_ERR_BAD_OFFSETS; a page outside the cache reads as zeros and latches

@@ -174,25 +174,30 @@ __device__ __forceinline__ void tree_mma_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 
 // sum over i < n of floor((a i + b) / 128), n < 2^23, a <= 256, b < 2^31: whole parts are
 // taken out, then the points under the line are counted along the other axis, until none
-// are left (a logarithm of 128 steps; the quotients fit 32 bits, and so does the sum: the
-// host has refused what could make it larger).
-__device__ __forceinline__ int tree_floor_sum(uint32_t n, uint32_t a, uint32_t b) {
-  uint32_t sum = (a >> 7) * (uint32_t)((uint64_t)n * (n - 1) / 2) + (b >> 7) * n;
+// are left (a logarithm of 128 steps; the quotients fit 32 bits).
+__device__ __forceinline__ long long tree_floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+  long long sum = (long long)(a >> 7) * ((long long)n * (n - 1) / 2) + (long long)(b >> 7) * n;
   a &= 127u;
   b &= 127u;
   uint32_t m = 128;
   while (true) {
     const uint32_t top = a * n + b;  // (the line's value behind the last point, times m)
     n = top / m;
-    if (n == 0) return (int)sum;
+    if (n == 0) return sum;
     b = top - n * m;
     const uint32_t whole = m / a;  // (a > 0: else top < m)
     const uint32_t rest = m - whole * a;
     m = a;
     a = rest;
-    sum += whole * (uint32_t)((uint64_t)n * (n - 1) / 2) + (b / m) * n;
+    sum += (long long)whole * ((long long)n * (n - 1) / 2) + (long long)(b / m) * n;
     b %= m;
   }
+}
+
+// r / d, in 32 bits where both fit (nearly always)
+__device__ __forceinline__ long long tree_div(long long r, long long d) {
+  if (((r | d) >> 32) == 0) return (long long)((uint32_t)r / (uint32_t)d);
+  return r / d;
 }
 
 // One sequence's even or odd tiles (v: all sequences' even ones, then their odd ones), as
@@ -202,7 +207,7 @@ struct TreeSeq {
   int a, n;            // its rows of Q: tokens [a, a + n)
   int ctx;
   int tiles;           // even (or odd) ones
-  int per_head;        // their blocks, of one key head
+  long long per_head;  // their blocks, of one key head
 
   __device__ __forceinline__ void load(const TreeArgs& p, int v) {
     odd = v >= p.B ? 1 : 0;
@@ -210,7 +215,8 @@ struct TreeSeq {
     const int o0 = __ldg(p.q_offsets + b), o1 = __ldg(p.q_offsets + b + 1), c = __ldg(p.context + b);
     a = min(max(o0, 0), p.T);
     n = min(max(o1, a), p.T) - a;
-    ctx = min(max(c, 0), max(p.max_pages * p.page_size - n, 0));
+    const long long most = (long long)p.max_pages * p.page_size - n;
+    ctx = (int)min((long long)max(c, 0), max(most, 0ll));
     const int all = n <= p.tokens ? (n > 0 ? 1 : 0) : (n + p.tokens - 1) / p.tokens;
     tiles = p.lines == 1 ? all : (all - odd + 1) >> 1;
     per_head = tiles == 0 ? 0 : before(p, tiles - 1) + blocks(p, tiles - 1);
@@ -223,36 +229,36 @@ struct TreeSeq {
   }
   __device__ __forceinline__ int blocks(const TreeArgs& p, int i) const { return (keys(p, i) + kTreeBN - 1) / kTreeBN; }
   // blocks of the tiles before the i-th
-  __device__ __forceinline__ int before(const TreeArgs& p, int i) const {
+  __device__ __forceinline__ long long before(const TreeArgs& p, int i) const {
     if (i == 0) return 0;
-    if (p.mask) return i * ((ctx + n + kTreeBN - 1) / kTreeBN);
+    if (p.mask) return (long long)i * ((ctx + n + kTreeBN - 1) / kTreeBN);
     return tree_floor_sum((uint32_t)i, (uint32_t)(p.lines * p.tokens), (uint32_t)(ctx + (odd + 1) * p.tokens + kTreeBN - 1));
   }
 };
 
 // A CTA's share, one fragment (consecutive blocks of one item) after another.
 struct TreeWalker {
-  int x, hi;
+  long long x, hi;
   int v, h, t;
-  int base;         // first block of v
+  long long base;   // first block of v
   bool fresh;       // (v, h, t) hold the item of block x
   TreeSeq s;
   // the fragment
-  int item;         // the item's first block
+  long long item;   // the item's first block
   int jb, je, nb;   // its blocks of the item's nb
   int token0, ntok; // the tile's tokens
   int keys;         // keys that it may see
 
-  __device__ __forceinline__ void init(const TreeArgs& p, int lo, int hi_, int v_, int base_) {
+  __device__ __forceinline__ void init(const TreeArgs& p, long long lo, long long hi_, int v_, long long base_) {
     x = lo;
     hi = hi_;
     v = v_;
     base = base_;
     if (x >= hi) return;
     s.load(p, v);
-    const int r = x - base;
-    h = r / s.per_head;
-    const int at = r - h * s.per_head;
+    const long long r = x - base;
+    h = (int)tree_div(r, s.per_head);
+    const long long at = r - h * s.per_head;
     int lo_t = 0, hi_t = s.tiles - 1;  // the last tile with before(t) <= at
     while (lo_t < hi_t) {
       const int mid = (lo_t + hi_t + 1) / 2;
@@ -278,8 +284,8 @@ struct TreeWalker {
       item = x;
     }
     nb = s.blocks(p, t);
-    jb = x - item;
-    je = min(nb, jb + (hi - x));
+    jb = (int)(x - item);
+    je = (int)min((long long)nb, jb + (hi - x));
     token0 = s.a + s.token(p, t);
     ntok = min(p.tokens, s.n - s.token(p, t));
     keys = s.keys(p, t);
@@ -506,25 +512,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   auto count = [&](int v) -> long long {
     TreeSeq s;
     s.load(p, v);
-    return (long long)s.per_head * p.Hkv;
+    return s.per_head * p.Hkv;
   };
   tc_fence_before_sync();
   BlockCount<long long, kTreeThreads> counted;
-  const long long all = counted.total(p.lines * p.B, count, scratch);
+  const long long W = counted.total(p.lines * p.B, count, scratch);
   tc_fence_after_sync();
-  const int W = all > 0x7fffffff ? 0 : (int)all;  // (only offsets that go back and forth count so many: they are refused)
-  const Share<int> share(W, max(1, min((int)gridDim.x, W)));
-  int lo = 0, hi = 0;
+  const Share<long long> share(W, (int)max(1ll, min((long long)gridDim.x, W)));
+  long long lo = 0, hi = 0;
   if ((int)blockIdx.x < share.G) {
     lo = share.lo((int)blockIdx.x);
     hi = share.lo((int)blockIdx.x + 1);
   }
-  if (lo < hi) counted.locate(p.lines * p.B, count, (long long)lo, scratch, found);
+  if (lo < hi) counted.locate(p.lines * p.B, count, lo, scratch, found);
   __syncthreads();
   const uint32_t tmem_base = *tmem_slot;
   const Guard guard{p.ws, abort_flag, p.timeout_ns};
   TreeWalker w;
-  w.init(p, lo, hi, (int)found[0], (int)found[1]);
+  w.init(p, lo, hi, (int)found[0], found[1]);
   if (!p.split && lo < hi) {
     // Whole items only: those that begin in the share.
     TreeWalker e = w;
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       w = e;
     }
     // the end: where the item that holds block hi - 1 ends
-    int end = hi;
+    long long end = hi;
     if (w.x < hi) {
       e = w;
       while (e.next(p)) end = e.item + e.nb;
@@ -635,7 +640,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint32_t t_o = t_lane + Cfg::kTmemO;
     const int my_tok = row / p.group, my_head = row - my_tok * p.group;
     const float cs = p.cs;
-    const int x_first = w.x;
+    const long long x_first = w.x;
     int b = 0;                     // S/P buffer of the next product,
     uint32_t bph = 0;              // its parity,
     int last_b = 0;                // and those of the product before
@@ -800,14 +805,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           // tokens; thread = key.  These warps wait for V here only, and a parity tells two
           // phases apart: the stage's last use has to be over.  PV of three blocks ago is (its
           // buffer holds this S), and two stages need that of two.
-          const int g = w.item + j - x_first;  // the share's blocks use the stages in turn
+          const long long g = w.item + j - x_first;  // the share's blocks use the stages in turn
           static_assert(VS >= 2 && SB == 3, "stages of V");
           if (VS == 2 && g >= 2 &&
-              !__all_sync(0xffffffffu, tree_wait(guard, pv_done + 8 * ((g - 2) % SB), (uint32_t)((g - 2) / SB) & 1u, (kRoleEpilogue << 16) | 0x600))) {
+              !__all_sync(0xffffffffu, tree_wait(guard, pv_done + 8 * (int)((g - 2) % SB), (uint32_t)((g - 2) / SB) & 1u, (kRoleEpilogue << 16) | 0x600))) {
             ok = false;
             break;
           }
-          const int vs = g % VS;
+          const int vs = (int)(g % VS);
           if (!__all_sync(0xffffffffu, tree_wait(guard, v_full + 8 * vs, (uint32_t)(g / VS) & 1u, (kRoleEpilogue << 16) | 0x500 | vs))) {
             ok = false;
             break;
@@ -948,15 +953,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // rows alone fill the blocks), then the first of them adds up what the ways have found.
 template <int DH, bool OUT_F32>
 __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
-  __shared__ float found[256 * 6];  // m, l, O of a thread
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const TreeCut cut = p.cuts[blockIdx.x];
   const int rows = cut.ntok * p.group;
   if (cut.pieces == 0) return;
   int ways = 1;
   while (ways < 8 && 2 * ways * rows <= kTreeBM && ways < cut.pieces) ways *= 2;
-  const int here = 256 / ways;  // quads of rows of this block
-  const int way = (int)threadIdx.x / here, i = (int)blockIdx.y * here + (int)threadIdx.x % here;
+  const int per = 32 / ways;  // quads of rows of a warp
+  const int way = (int)lane_id() / per, i = (int)(blockIdx.y * 8 + threadIdx.x / 32) * per + (int)lane_id() % per;
   const int quad = i / rows, row = i - quad * rows;
   const bool on = quad < DH / 4;
   auto slot = [&](int k) { return p.slots + (size_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * kTreeSlotFloats; };
@@ -969,12 +973,15 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
       float4 v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const bool there = k0 + k * ways < cut.pieces;
-        const float* s = slot(there ? k0 + k * ways : way);
-        mk[k] = __ldcg(s + 128 * kTreeBM + row);
-        lk[k] = __ldcg(s + 128 * kTreeBM + kTreeBM + row);
-        v[k] = __ldcg(reinterpret_cast<const float4*>(s) + quad * kTreeBM + row);
-        if (!there) mk[k] = -INFINITY;
+        mk[k] = -INFINITY;
+        lk[k] = 0.0f;
+        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k0 + k * ways < cut.pieces) {
+          const float* s = slot(k0 + k * ways);
+          mk[k] = __ldcg(s + 128 * kTreeBM + row);
+          lk[k] = __ldcg(s + 128 * kTreeBM + kTreeBM + row);
+          v[k] = __ldcg(reinterpret_cast<const float4*>(s) + quad * kTreeBM + row);
+        }
       }
       const float top = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), m);
       const float ms = top == -INFINITY ? 0.0f : top;
@@ -986,7 +993,6 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
       o.w *= self;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (k0 + k * ways >= cut.pieces) break;
         const float a = tree_ex2(mk[k] - ms);
         l = fmaf(a, lk[k], l);
         o.x = fmaf(a, v[k].x, o.x);
@@ -997,32 +1003,17 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
       m = top;
     }
   }
-  if (ways > 1) {
-    float* mine = found + threadIdx.x;  // (a number's values of all threads in a row)
-    mine[0] = m;
-    mine[256] = l;
-    mine[512] = o.x;
-    mine[768] = o.y;
-    mine[1024] = o.z;
-    mine[1280] = o.w;
-    __syncthreads();
-    if (way > 0) return;
-    float top = m;
-    for (int k = 1; k < ways; ++k) top = fmaxf(top, mine[k * here]);
-    const float ms = top == -INFINITY ? 0.0f : top;
-    l = 0.0f;
-    o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = 0; k < ways; ++k) {
-      const float* z = mine + k * here;
-      const float a = tree_ex2(z[0] - ms);
-      l = fmaf(a, z[256], l);
-      o.x = fmaf(a, z[512], o.x);
-      o.y = fmaf(a, z[768], o.y);
-      o.z = fmaf(a, z[1024], o.z);
-      o.w = fmaf(a, z[1280], o.w);
-    }
+  for (int d = per; d < 32; d *= 2) {
+    const float mo = __shfl_xor_sync(0xffffffffu, m, d), lo = __shfl_xor_sync(0xffffffffu, l, d);
+    const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, o.x, d), __shfl_xor_sync(0xffffffffu, o.y, d),
+                                 __shfl_xor_sync(0xffffffffu, o.z, d), __shfl_xor_sync(0xffffffffu, o.w, d));
+    const float top = fmaxf(m, mo), ms = top == -INFINITY ? 0.0f : top;
+    const float a = tree_ex2(m - ms), c = tree_ex2(mo - ms);
+    m = top;
+    l = l * a + lo * c;
+    o = make_float4(o.x * a + y.x * c, o.y * a + y.y * c, o.z * a + y.z * c, o.w * a + y.w * c);
   }
-  if (!on) return;
+  if (!on || way > 0) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const bool none = l == 0.0f;
   const int tok = row / p.group, head = row - tok * p.group;
