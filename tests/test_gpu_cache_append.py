@@ -51,6 +51,10 @@ CASES = [  # T, H, Hkv, Dh, rot, style, page, layout, type
     (300, 64, 8, 128, 128, "halves", 64, "plain", torch.float32),
     (2000, 2, 2, 16, 0, "halves", 16, "plain", torch.bfloat16),
     (9, 5, 5, 48, 32, "pairs", 3, "heads", torch.bfloat16),
+    # several tokens to a step of a block, also with angles for eight only, and a last step of fewer
+    (4001, 2, 1, 64, 32, "pairs", 16, "plain", torch.float32),
+    (12347, 1, 1, 256, 256, "halves", 16, "heads", torch.bfloat16),
+    (20011, 1, 1, 48, 48, "pairs", 8, "both", torch.bfloat16),
 ]
 
 
