@@ -713,8 +713,10 @@ wst_status wst_cache_append_bf16(int T, int H, int Hkv, int Dh, int rot, wst_rop
  *   O       o_type, element (t,h,d) at O + t*ldo + h*Dh + d; it must not overlap the
  *           inputs
  * The probabilities enter the product with V as bf16 (as two bf16, good to 2^-16,
- * where O is fp32); row maxima, sums and the output accumulate in fp32.  After a tree is verified, wst_permute_rows
- * moves the accepted tokens' rows of the cache together.
+ * where O is fp32); row maxima, sums and the output accumulate in fp32.
+ * After a tree is verified, two calls of wst_permute_rows move the accepted tokens'
+ * rows of a cache together: into an array of their own and back behind the context
+ * (a row's new place may be another's old one).
  * Supported: Dh 64 and 128, H / Hkv <= 128, page_size 8, 16, 32, 64 or a multiple of
  * 128, max_pages * page_size <= 2^30, T <= 2^30 (else WST_ERR_UNSUPPORTED).
  * Offsets, lengths or masks that break the rules (also context[b] + n_b above
