@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks<X>) k_cache_appe
   const int half = p.rot / 2;
   const int per_head = p.Dh / 16;
   const int units = (p.H + 2 * p.Hkv) * per_head;
+  early_wait();
   unsigned long long turn = 0;  // this thread's angle: turns per position, as a 64-bit fraction
   if (tid < half) {
     double x = (double)__ldg(p.inv_freq + tid) * 0.15915494309189533577;  // 1 / (2 pi)
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks<X>) k_cache_appe
   // A thread's angle is the same for all its tokens; `angles` tokens at a time.
   const int angles = half ? kAppendThreads / half : 0;
   const int k_angle = half ? tid / half : 0, j_angle = tid - k_angle * half;
+  early_wait();
   unsigned long long turn = 0;
   if (k_angle < angles) {
     double x = (double)__ldg(p.inv_freq + j_angle) * 0.15915494309189533577;
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks<X>) k_cache_appe
 }
 
 template <typename X>
-void launch_append(AppendArgs a, bool pairs, int num_sms, cudaStream_t stream) {
+cudaError_t launch_append(AppendArgs a, bool pairs, int num_sms, cudaStream_t stream) {
   // Blocks for all SMs first, then tokens to a step: as many as their units and angles
   // allow, no more than make the steps of a block equally long.  (Eight times the blocks, a
   // step each, take 97 us and 15 us for the two prompts named above.)
@@ -273,7 +275,7 @@ void launch_append(AppendArgs a, bool pairs, int num_sms, cudaStream_t stream) {
   const int grid = std::min((a.T + a.tokens - 1) / a.tokens, blocks);
   const auto kern = a.tokens > 1 ? (pairs ? k_cache_append_several<X, true> : k_cache_append_several<X, false>)
                                  : (pairs ? k_cache_append<X, true> : k_cache_append<X, false>);
-  kern<<<grid, kAppendThreads, 0, stream>>>(a);
+  return launch_early(kern, dim3((unsigned)grid), kAppendThreads, 0, stream, a);
 }
 
 }  // namespace
@@ -377,9 +379,8 @@ wst_status wst_cache_append_bf16(int T, int H, int Hkv, int Dh, int rot, wst_rop
   a.head_stride = head_stride;
   a.ws = static_cast<WsHeader*>(workspace);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (x_type == WST_F32) launch_append<float>(a, style == WST_ROPE_PAIRS, dev.num_sms, s);
-  else launch_append<__nv_bfloat16>(a, style == WST_ROPE_PAIRS, dev.num_sms, s);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = x_type == WST_F32 ? launch_append<float>(a, style == WST_ROPE_PAIRS, dev.num_sms, s)
+                                          : launch_append<__nv_bfloat16>(a, style == WST_ROPE_PAIRS, dev.num_sms, s);
   return e == cudaSuccess ? WST_OK : (wst_status)cuda_fail(e, "launch k_cache_append");
 }
 

@@ -31,21 +31,10 @@ int launch_tree(const TreeArgs& a, const void* Q, long long ldq, const void* K, 
   auto kern = k_tree_attn<DH, OUT_F32>;
   if ((st = ensure_smem_attr((const void*)kern, Cfg::kSmem))) return st;
   const int grid = std::min(dev.num_sms, kTreeMaxCtas);
-  kern<<<grid, kTreeThreads, Cfg::kSmem, stream>>>(tmQ, tmK, tmV, a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_early(kern, dim3((unsigned)grid), kTreeThreads, Cfg::kSmem, stream, tmQ, tmK, tmV, a);
   if (e != cudaSuccess) return cuda_fail(e, "launch k_tree_attn");
   if (!a.split) return ST_OK;
-  // The second kernel's blocks may start while the first one ends; they wait for it.
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)(DH / 4 * kTreeBM / 256), 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k_tree_merge<DH, OUT_F32>, a);
+  e = launch_early(k_tree_merge<DH, OUT_F32>, dim3((unsigned)grid, (unsigned)(DH / 4 * kTreeBM / 256)), 256, 0, stream, a);
   return e == cudaSuccess ? ST_OK : cuda_fail(e, "launch k_tree_merge");
 }
 

@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     tmem_alloc<1>(smem_addr(tmem_slot), 512);
     tmem_relinquish<1>();
   }
+  early_wait();
   if (blockIdx.x == 0) tree_check(p);
   // this CTA's share
   auto count = [&](int v) -> long long {
@@ -938,7 +939,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     if (p.split && row == 0 && !wrote_cut) p.cuts[blockIdx.x].pieces = 0;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before_sync();
   __syncthreads();
   if (*abort_flag) {
@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // rows alone fill the blocks), then the first of them adds up what the ways have found.
 template <int DH, bool OUT_F32>
 __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  early_wait();
   const TreeCut cut = p.cuts[blockIdx.x];
   const int rows = cut.ntok * p.group;
   if (cut.pieces == 0) return;

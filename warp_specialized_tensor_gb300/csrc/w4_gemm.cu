@@ -50,8 +50,7 @@ int launch_w4(W4Problem& pr, const DeviceInfo& dev, cudaStream_t stream) {
   auto kern = k_w4_gemm<NT, GROUPS>;
   if ((st = ensure_smem_attr((const void*)kern, Cfg::kSmem))) return st;
   const int grid = std::min(dev.num_sms, kW4MaxCtas);
-  kern<<<grid, Cfg::kThreads, Cfg::kSmem, stream>>>(tmW, tmA, tmS, a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(kern, dim3((unsigned)grid), Cfg::kThreads, Cfg::kSmem, stream, tmW, tmA, tmS, a);
   return e == cudaSuccess ? ST_OK : cuda_fail(e, "launch k_w4_gemm");
 }
 

@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmS);
   }
+  early_wait();
   // this CTA's share; whole tiles where the workspace holds no partial sums
   const int grain = p.split ? 1 : p.k_units;
   int W, lo = 0, hi = 0;

@@ -14,6 +14,14 @@ enum : uint32_t {
   kErrBadOffsets = 6,
 };
 
+// For kernels started by launch_early.  early_wait: the kernel before this one in the
+// stream is over and its stores are visible; the kernel after this one may set itself up
+// from here on (its blocks come once all of this kernel's are on the SMs).
+__device__ __forceinline__ void early_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // First 256 bytes of every workspace.
 struct WsHeader {
   uint32_t error;       // first latched device error (0 = none)

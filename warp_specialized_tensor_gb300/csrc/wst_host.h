@@ -68,6 +68,24 @@ bool take_fault_injection();
 // device and size).  Returns Status.
 int ensure_smem_attr(const void* kernel, size_t bytes);
 
+// Launch a kernel whose blocks may come onto the SMs while the kernel before it in the
+// stream ends: it sets itself up and then waits (griddepcontrol.wait) before it reads or
+// writes anything that another kernel might.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Encode a tiled tensor map (rank 2 or 3).  dims / box innermost first,
 // strides_bytes has rank-1 entries.  Returns Status.
 int encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ptr,
