@@ -187,28 +187,6 @@ int check_device_ptr(const void* p, const char* name) {
 }
 
 int check_operand(const void* p, const char* name) {
-  // The driver's query of the two attributes that matter: a good operand pays for no
-  // more (0.2 us a pointer where the runtime's full query takes about 1 us).  What it
-  // does not show to be device memory of the current device goes through the full one.
-  using AttributesFn = CUresult (*)(unsigned int, CUpointer_attribute*, void**, CUdeviceptr);
-  static const AttributesFn attributes = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess) {
-      cudaGetLastError();
-      return AttributesFn(nullptr);
-    }
-    return q == cudaDriverEntryPointSuccess ? reinterpret_cast<AttributesFn>(fn) : AttributesFn(nullptr);
-  }();
-  if (attributes && p) {
-    unsigned int type = 0;
-    int ordinal = -1, current = -2;
-    CUpointer_attribute which[2] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL};
-    void* values[2] = {&type, &ordinal};
-    if (attributes(2, which, values, reinterpret_cast<CUdeviceptr>(p)) == CUDA_SUCCESS && type == CU_MEMORYTYPE_DEVICE &&
-        cudaGetDevice(&current) == cudaSuccess && ordinal == current)
-      return ST_OK;
-  }
   cudaPointerAttributes at{};
   int st = device_attributes(p, name, at);
   if (st) return st;

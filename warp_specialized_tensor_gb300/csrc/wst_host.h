@@ -86,7 +86,7 @@ cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Encode a tiled tensor map (rank 2 or 3).  dims / box innermost first,
+// Encode a tiled tensor map (rank 2 to 4).  dims / box innermost first,
 // strides_bytes has rank-1 entries.  Returns Status.
 int encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ptr,
                const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
