@@ -99,10 +99,12 @@ class Paged:
         return out, size, most
 
     def tolerance(self, out, size, most, dtype):
-        """P is off by half a step of bf16 (for fp32 output by half a step of what a first bf16 leaves, 2^-16); a score's Dh products are added with an error of at most 2^-22 of their
-        sizes in each of Dh/16 steps, a score's error counts twice (P and the sum of P), 2^x and the scaling are good
-        to 2^-21; an output adds 8 steps of at most 2^-22 for every 128 keys; then the rounding of the result."""
+        """P is off by half a step of bf16 (for fp32 output by half a step of the last of three bf16, at most 2^-24); a
+        score's Dh products are added with an error of at most 2^-22 of their sizes in each of Dh/16 steps, a score's
+        error counts twice (P and the sum of P), 2^x and the scaling are good to 2^-21; an output adds 8 steps (three
+        times 8 for three parts) of at most 2^-22 for every 128 keys; then the rounding of the result."""
         blocks = max(c + n for c, n in self.lens) / 128 + 2
-        part = (2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -16) + 2 * (self.Dh / 16 * 2.0 ** -22 * most + 2.0 ** -21 * (1 + most)) + 8 * blocks * 2.0 ** -22
+        parts = 1 if dtype is torch.bfloat16 else 3
+        part = 2.0 ** (-8 * parts) + 2 * (self.Dh / 16 * 2.0 ** -22 * most + 2.0 ** -21 * (1 + most)) + 8 * parts * blocks * 2.0 ** -22
         half = 2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -24
         return part * size + half * (out.abs() + part * size)

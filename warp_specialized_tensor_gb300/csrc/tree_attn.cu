@@ -14,7 +14,7 @@ namespace {
 template <int DH, bool OUT_F32>
 int launch_tree(const TreeArgs& a, const void* Q, long long ldq, const void* K, const void* V, const DeviceInfo& dev,
                 cudaStream_t stream) {
-  using Cfg = TreeCfg<DH>;
+  using Cfg = TreeCfg<DH, OUT_F32 ? 3 : 1>;
   int st;
   CUtensorMap tmQ, tmK, tmV;
   {

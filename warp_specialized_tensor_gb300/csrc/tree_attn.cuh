@@ -32,12 +32,12 @@
 //   softmax  P = 2^(cs S - m) as bf16 over S's tensor memory; m is a whole number that
 //            moves only when a score exceeds it by more than 8, which rescales O and l
 //            (P <= 2^8; l sums the unrounded P).  One bf16 is off by up to 2^-8 of P, which
-//            a bf16 output's own rounding covers; for fp32 output P is two bf16 (what the
-//            first leaves), off by 2^-16, in the two halves of S's columns
-//   MMA      O += P . V         P from tensor memory, V from shared memory (twice for two P)
+//            a bf16 output's own rounding covers; for fp32 output P is three bf16, each what
+//            the ones before leave, off by 2^-24 together
+//   MMA      O += P . V         P from tensor memory, V from shared memory (for each part of P)
 // From a score's product to the next in its buffer it is S, softmax, PV and three
-// handshakes, 5,000 clocks, of which the softmax is a third: three S/P buffers let S run
-// ahead of PV.  (Two items at a time with one buffer each: 147 us for 32 sequences of
+// handshakes, 5,000 clocks, of which the softmax is a third: three S/P buffers (two of the
+// wider ones of fp32 output) let S run ahead of PV.  (Two items at a time with one buffer each: 147 us for 32 sequences of
 // 4,096 against 82.)  Two threads issue the products, so that one's run under the other's
 // wait.
 //
@@ -67,16 +67,20 @@ constexpr float kTreeGrow = 8.0f;       // log2 of how far P may exceed 1
 constexpr float kTreeGrowSum = 256.0f;  // 2^kTreeGrow
 
 constexpr int kTreeThreads = 256;
-constexpr int kTreeSBufs = 3;
 
-template <int DH>
+// PARTS: bf16 numbers that hold one P, 1 for bf16 output, 3 for fp32.
+template <int DH, int PARTS>
 struct TreeCfg {
   static constexpr int kTile = kTreeBN * DH * 2;  // bytes of a Q tile or a block of K or V
   static constexpr int kKStages = DH == 128 ? 3 : 6;
   static constexpr int kVStages = DH == 128 ? 2 : 5;
-  static constexpr int kBars = 2 * kKStages + 2 * kVStages + 2 + 3 * kTreeSBufs + 1;
+  // S/P buffers and their columns of tensor memory: the first two parts of P lie over S,
+  // the third behind it
+  static constexpr int kSBufs = PARTS == 1 ? 3 : 2;
+  static constexpr int kSCols = PARTS == 1 ? kTreeBN : kTreeBN + kTreeBN / 2;
+  static constexpr int kBars = 2 * kKStages + 2 * kVStages + 2 + 3 * kSBufs + 1;
   static constexpr size_t kSmem = 1024 + (size_t)(2 + kKStages + kVStages) * kTile + 1024;
-  static constexpr int kTmemO = kTreeSBufs * kTreeBN;
+  static constexpr int kTmemO = kSBufs * kSCols;
   static_assert(kSmem <= 232448 && kTmemO + DH <= 512 && DH % 64 == 0, "shared memory, tensor memory");
 };
 
@@ -456,8 +460,9 @@ template <int DH, bool OUT_F32>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const TreeArgs p) {
-  using Cfg = TreeCfg<DH>;
-  constexpr int KS = Cfg::kKStages, VS = Cfg::kVStages, SB = kTreeSBufs;
+  constexpr int PARTS = OUT_F32 ? 3 : 1;
+  using Cfg = TreeCfg<DH, PARTS>;
+  constexpr int KS = Cfg::kKStages, VS = Cfg::kVStages, SB = Cfg::kSBufs, COLS = Cfg::kSCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_addr(smem), sK = sQ + 2 * Cfg::kTile, sV = sK + KS * Cfg::kTile;
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             break;
           }
           tc_fence_after_sync();
-          const uint32_t k_at = sK + ks * Cfg::kTile, d = tmem_base + (uint32_t)(kTreeBN * b);
+          const uint32_t k_at = sK + ks * Cfg::kTile, d = tmem_base + (uint32_t)(COLS * b);
 #pragma unroll
           for (int kk = 0; kk < DH / 16; ++kk) {
             const uint32_t o = (uint32_t)((kk >> 2) * (kTreeBN * 128) + (kk & 3) * 32);
@@ -609,15 +614,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           tc_fence_after_sync();
           // 16 keys: 8 columns of P, 2 KB of V
           const uint64_t vd = sdesc_sw128(sV + vs * Cfg::kTile, kTreeBN * 128, 1024);
-          const uint32_t a = tmem_base + (uint32_t)(kTreeBN * b), d = tmem_base + Cfg::kTmemO;
+          const uint32_t a = tmem_base + (uint32_t)(COLS * b), d = tmem_base + Cfg::kTmemO;
 #pragma unroll
           for (int kk = 0; kk < kTreeBN / 16; ++kk)
             tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc,
                         (j > w.jb || kk != 0) ? 1u : 0u);
-          if constexpr (OUT_F32) {
+          if constexpr (PARTS == 3) {
 #pragma unroll
             for (int kk = 0; kk < kTreeBN / 16; ++kk)
               tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + 16 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
+#pragma unroll
+            for (int kk = 0; kk < kTreeBN / 16; ++kk)
+              tree_mma_ts(d, a + (uint32_t)(kTreeBN + kk * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
           }
           umma_commit(pv_done + 8 * b);
           umma_commit(v_empty + 8 * vs);
@@ -674,12 +682,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           break;
         }
         tc_fence_after_sync();
-        const uint32_t t_s = t_lane + (uint32_t)(kTreeBN * b);
+        const uint32_t t_s = t_lane + (uint32_t)(COLS * b);
         if (active) {
-          // 64 keys at a time, in a loop: code that fits the instruction cache's first level
-          // (unrolled over the block, a warp waited for instructions a fourth of the time).
-          // P of 32 keys goes over their scores: 16 columns of bf16 pairs, then (fp32
-          // output) 16 of what those leave.
+          // 64 keys at a time (fp32 output: 32, for its parts' registers), in a loop: code
+          // that fits the instruction cache's first level (unrolled over the block, a warp
+          // waited for instructions a fourth of the time).  P of 32 keys goes over their
+          // scores: 16 columns of bf16 pairs, then (fp32 output) 16 of what those leave; what
+          // both leave goes behind the scores.
+          constexpr int WIDTH = PARTS == 1 ? 64 : 32;
           uint32_t vis[4] = {0u, 0u, 0u, 0u};
           if (!inner && row < rows) {
 #pragma unroll
@@ -687,14 +697,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           float sum = 0.0f;
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t t_c = t_s + 64 * c;
-            const uint32_t v0 = c ? vis[2] : vis[0], v1 = c ? vis[3] : vis[1];
-            float x[64];
+          for (int c = 0; c < kTreeBN / WIDTH; ++c) {
+            const uint32_t t_c = t_s + WIDTH * c;
+            uint32_t v0 = c == 0 ? vis[0] : vis[2], v1 = c == 0 ? vis[1] : vis[3];
+            if (PARTS == 3 && (c & 1)) v0 = c == 1 ? vis[1] : vis[3];
+            float x[WIDTH];
             auto load = [&]() {
-              tree_tmem_load32(t_c, x);
-              tree_tmem_load32(t_c + 32, x + 32);
-              tree_tmem_load_wait<64>(x);
+#pragma unroll
+              for (int d = 0; d < WIDTH / 32; ++d) tree_tmem_load32(t_c + 32 * d, x + 32 * d);
+              tree_tmem_load_wait<WIDTH>(x);
             };
             // the largest cs S that the row sees of these keys, rounded up: maxima are whole
             // numbers, so that a change of one scales by a power of two, exactly
@@ -702,10 +713,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               float e[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
               if (inner) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) e[i & 3] = fmaxf(e[i & 3], __fmul_rn(x[i], cs));
+                for (int i = 0; i < WIDTH; ++i) e[i & 3] = fmaxf(e[i & 3], __fmul_rn(x[i], cs));
               } else {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) e[i & 3] = (i < 32 ? v0 : v1) & (1u << (i & 31)) ? fmaxf(e[i & 3], __fmul_rn(x[i], cs)) : e[i & 3];
+                for (int i = 0; i < WIDTH; ++i) e[i & 3] = (i < 32 ? v0 : v1) & (1u << (i & 31)) ? fmaxf(e[i & 3], __fmul_rn(x[i], cs)) : e[i & 3];
               }
               return ceilf(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])));
             };
@@ -716,31 +727,35 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               const float mx = maximum();
               if (m == -INFINITY) m = mx;
             }
-            uint32_t hi[32], lo[OUT_F32 ? 32 : 1];
+            uint32_t hi[WIDTH / 2], mid[PARTS == 3 ? 16 : 1], lo[PARTS == 3 ? 16 : 1];
             auto probabilities = [&]() -> float {
               // (no key seen yet: all scores are -inf, P zero)
               const float top = !inner && m == -INFINITY ? 0.0f : m;
               float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
               if (__all_sync(0xffffffffu, fabsf(top) < 1.0e6f || row >= rows)) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) tree_fma2(x[2 * i], x[2 * i + 1], cs, -top);
+                for (int i = 0; i < WIDTH / 2; ++i) tree_fma2(x[2 * i], x[2 * i + 1], cs, -top);
               } else {  // (the difference to the exact product, for scores that pass 2^24)
 #pragma unroll
-                for (int i = 0; i < 64; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], cs), -top);
+                for (int i = 0; i < WIDTH; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], cs), -top);
               }
               if (!inner) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) x[i] = (i < 32 ? v0 : v1) & (1u << (i & 31)) ? x[i] : -INFINITY;
+                for (int i = 0; i < WIDTH; ++i) x[i] = (i < 32 ? v0 : v1) & (1u << (i & 31)) ? x[i] : -INFINITY;
               }
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
+              for (int i = 0; i < WIDTH / 2; ++i) {
                 float& x0 = x[2 * i];
                 float& x1 = x[2 * i + 1];
                 x0 = tree_ex2(x0);
                 x1 = tree_ex2(x1);
                 tree_add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], x0, x1);
                 hi[i] = pack_bf16x2(x0, x1);
-                if constexpr (OUT_F32) lo[i] = pack_bf16x2(x0 - __uint_as_float(hi[i] << 16), x1 - __uint_as_float(hi[i] & 0xffff0000u));
+                if constexpr (PARTS == 3) {  // (the differences are exact)
+                  const float r0 = x0 - __uint_as_float(hi[i] << 16), r1 = x1 - __uint_as_float(hi[i] & 0xffff0000u);
+                  mid[i] = pack_bf16x2(r0, r1);
+                  lo[i] = pack_bf16x2(r0 - __uint_as_float(mid[i] << 16), r1 - __uint_as_float(mid[i] & 0xffff0000u));
+                }
               }
               return (rs[0] + rs[1]) + (rs[2] + rs[3]);
             };
@@ -773,18 +788,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     tree_tmem_store32(t_o + d * 32, v);
                   }
                 }
-                if (c == 1) {  // the block's first 64 P, with the old maximum
-#pragma unroll 1
-                  for (int d = 0; d < 2; ++d) {
-                    float v[32];
-                    tmem_load32(t_s + 32 * d, v);
+                // the block's P so far, with the old maximum: WIDTH columns of every step (of
+                // which bf16 output uses half), and of the third parts half as many
+                auto rescale = [&](uint32_t at) {
+                  float v[32];
+                  tmem_load32(at, v);
 #pragma unroll
-                    for (int i = 0; i < (OUT_F32 ? 32 : 16); ++i) {
-                      const uint32_t y = __float_as_uint(v[i]);
-                      v[i] = __uint_as_float(pack_bf16x2(__uint_as_float(y << 16) * alpha, __uint_as_float(y & 0xffff0000u) * alpha));
-                    }
-                    tree_tmem_store32(t_s + 32 * d, v);
+                  for (int i = 0; i < (PARTS == 1 ? 16 : 32); ++i) {
+                    const uint32_t y = __float_as_uint(v[i]);
+                    v[i] = __uint_as_float(pack_bf16x2(__uint_as_float(y << 16) * alpha, __uint_as_float(y & 0xffff0000u) * alpha));
                   }
+                  tree_tmem_store32(at, v);
+                };
+#pragma unroll 1
+                for (int d = 0; d < c * (WIDTH / 32); ++d) rescale(t_s + 32 * d);
+                if (PARTS == 3 && c > 0) {  // (of this step too, which are written anew)
+                  rescale(t_s + kTreeBN);
+                  if (c > 1) rescale(t_s + kTreeBN + 32);
                 }
                 tree_tmem_store_wait();
               }
@@ -792,9 +812,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             sum += part;
 #pragma unroll
-            for (int d = 0; d < 2; ++d) {
-              tree_tmem_store16(t_c + 32 * d, hi + 16 * d);
-              if constexpr (OUT_F32) tree_tmem_store16(t_c + 32 * d + 16, lo + 16 * d);
+            for (int d = 0; d < WIDTH / 32; ++d) tree_tmem_store16(t_c + 32 * d, hi + 16 * d);
+            if constexpr (PARTS == 3) {
+              tree_tmem_store16(t_c + 16, mid);
+              tree_tmem_store16(t_s + kTreeBN + 16 * c, lo);
             }
           }
           if (!ok) break;
@@ -804,10 +825,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (!inner) {
           // V: clear the block's keys behind the sequence and what is not finite of the new
           // tokens; thread = key.  These warps wait for V here only, and a parity tells two
-          // phases apart: the stage's last use has to be over.  PV of three blocks ago is (its
+          // phases apart: the stage's last use has to be over.  PV of SB blocks ago is (its
           // buffer holds this S), and two stages need that of two.
           const long long g = w.item + j - x_first;  // the share's blocks use the stages in turn
-          static_assert(VS >= 2 && SB == 3, "stages of V");
+          static_assert(VS >= 2 && (VS == 2 || VS >= SB), "stages of V");
           if (VS == 2 && g >= 2 &&
               !__all_sync(0xffffffffu, tree_wait(guard, pv_done + 8 * (int)((g - 2) % SB), (uint32_t)((g - 2) / SB) & 1u, (kRoleEpilogue << 16) | 0x600))) {
             ok = false;

@@ -1,9 +1,10 @@
 // work_split.cuh -- equal shares of a sequence of blocks, for kernels whose items
 // (tiles, heads of a sequence) have lengths that only the device knows.
 //
-// The items' blocks stand in one line of W blocks, of which each of G CTAs takes W / G
-// in order, the first W % G of them one more.  An item that lies in several shares is
-// worked on in pieces, one per CTA, in ascending order of both.
+// The items' blocks stand in one line of W blocks, of which CTA c of G takes those from
+// floor(c W / G) on: the shares that are one longer are spread evenly, so that with an even
+// G the line's second half is cut where its first one is.  An item that lies in several
+// shares is worked on in pieces, one per CTA, in ascending order of both.
 #pragma once
 
 #include <cstdint>
@@ -16,11 +17,18 @@ struct Share {
   int G;  // at most W (1 if W is 0)
   I q, r;
   __device__ __forceinline__ Share(I w, int g) : W(w), G(g), q(w / g), r(w - (w / g) * g) {}
-  __device__ __forceinline__ I lo(int c) const { return c * q + (c < r ? (I)c : r); }
-  // the CTA that holds block x < W
+  // (r < G: 32 bits hold the product)
+  __device__ __forceinline__ I lo(int c) const { return c * q + (I)((uint32_t)c * (uint32_t)r / (uint32_t)G); }
+  // the CTA that holds block x < W: the last c with c W <= (x + 1) G - 1
   __device__ __forceinline__ int owner(I x) const {
-    const I longer = r * (q + 1);
-    return (int)(x < longer ? x / (q + 1) : r + (x - longer) / q);
+    if constexpr (sizeof(I) == 4) return (int)(((uint64_t)((uint32_t)x + 1u) * (uint32_t)G - 1u) / (uint32_t)W);
+    int c = 0, last = G - 1;
+    while (c < last) {
+      const int mid = (c + last + 1) / 2;
+      if (lo(mid) <= x) c = mid;
+      else last = mid - 1;
+    }
+    return c;
   }
 };
 
