@@ -16,11 +16,14 @@
 // Schedule: an item is (sequence, key head, tile), a block 128 keys.  The items' blocks
 // stand in one line, each CTA takes an equal share (work_split.cuh); the lengths are on the
 // device, so every CTA counts them at its start.  The line holds the even tiles of all
-// sequences, then the odd ones: the two tiles of a sequence are worked on at the same time
-// by two CTAs, and one of them finds K and V in L2.  (In the sequences' order one CTA took
-// a tile after the other and both came from HBM: 138 us for 16 trees of 64 tokens on 8,192,
-// 800 MB.  Two tiles at a time in one CTA, 129 us, read 400 MB but wait for each other's
-// products: tensor memory holds one S/P buffer for each of two tiles, three for one.)
+// sequences, then the odd ones: the two tiles of a sequence are worked on by two CTAs at
+// nearly the same time, and the later one finds K and V in L2.  The cut between the lines is
+// shifted (Share's lead) so that the two are up to 24 blocks apart: at the same time both
+// miss L2 and read HBM.  (16 trees of 64 tokens on up to 8,192, 400 MB of K and V: 128 us;
+// with leads of 0, 4, 8, 16 141, 138, 136, 132, and 740 MB read at 0; in the
+// sequences' order one CTA took a tile after the other, 138 us and 800 MB.)  Two tiles of a
+// sequence in one CTA read 400 MB but wait for each other's products, 129 us: tensor memory
+// holds one S/P buffer for each of two tiles, three for one.
 // A piece of a cut item leaves its un-normalised O, row maxima m and sums l in the
 // workspace, and a second kernel adds an item's pieces in a fixed order:
 //   m* = max m_i,  l* = sum l_i 2^(m_i - m*),  O = sum O_i 2^(m_i - m*) / l*
@@ -67,6 +70,7 @@ constexpr float kTreeGrow = 8.0f;       // log2 of how far P may exceed 1
 constexpr float kTreeGrowSum = 256.0f;  // 2^kTreeGrow
 
 constexpr int kTreeThreads = 256;
+constexpr int kTreeLead = 24;  // blocks, of one line before the other
 
 // PARTS: bf16 numbers that hold one P, 1 for bf16 output, 3 for fp32.
 template <int DH, int PARTS>
@@ -524,7 +528,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   BlockCount<long long, kTreeThreads> counted;
   const long long W = counted.total(p.lines * p.B, count, scratch);
   tc_fence_after_sync();
-  const Share<long long> share(W, (int)max(1ll, min((long long)gridDim.x, W)));
+  const int G = (int)max(1ll, min((long long)gridDim.x, W));
+  const Share<long long> share(W, G, p.lines == 2 ? (int)min((long long)kTreeLead, W / G / 2) : 0);
   long long lo = 0, hi = 0;
   if ((int)blockIdx.x < share.G) {
     lo = share.lo((int)blockIdx.x);

@@ -16,12 +16,15 @@ struct Share {
   I W;
   int G;  // at most W (1 if W is 0)
   I q, r;
-  __device__ __forceinline__ Share(I w, int g) : W(w), G(g), q(w / g), r(w - (w / g) * g) {}
+  int lead;  // blocks that the cut in the middle is late by, the ones around it in proportion; q > lead
+  __device__ __forceinline__ Share(I w, int g, int lead_ = 0) : W(w), G(g), q(w / g), r(w - (w / g) * g), lead(lead_) {}
   // (r < G: 32 bits hold the product)
-  __device__ __forceinline__ I lo(int c) const { return c * q + (I)((uint32_t)c * (uint32_t)r / (uint32_t)G); }
-  // the CTA that holds block x < W: the last c with c W <= (x + 1) G - 1
+  __device__ __forceinline__ I lo(int c) const {
+    return c * q + (I)(((uint32_t)c * (uint32_t)r + 2u * (uint32_t)lead * (uint32_t)(c < G - c ? c : G - c)) / (uint32_t)G);
+  }
+  // the CTA that holds block x < W: the last c with lo(c) <= x (c W <= (x + 1) G - 1)
   __device__ __forceinline__ int owner(I x) const {
-    if constexpr (sizeof(I) == 4) return (int)(((uint64_t)((uint32_t)x + 1u) * (uint32_t)G - 1u) / (uint32_t)W);
+    if (sizeof(I) == 4 && lead == 0) return (int)(((uint64_t)((uint32_t)x + 1u) * (uint32_t)G - 1u) / (uint32_t)W);
     int c = 0, last = G - 1;
     while (c < last) {
       const int mid = (c + last + 1) / 2;
