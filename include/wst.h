@@ -718,7 +718,8 @@ wst_status wst_cache_append_bf16(int T, int H, int Hkv, int Dh, int rot, wst_rop
  * rows of a cache together: into an array of their own and back behind the context
  * (a row's new place may be another's old one).
  * Supported: Dh 64 and 128, H / Hkv <= 128, page_size 8, 16, 32, 64 or a multiple of
- * 128, max_pages * page_size <= 2^30, T <= 2^30 (else WST_ERR_UNSUPPORTED).
+ * 128, max_pages * page_size <= 2^30, T <= 2^30, B <= 2^29 (else
+ * WST_ERR_UNSUPPORTED).
  * Offsets, lengths or masks that break the rules (also context[b] + n_b above
  * max_pages * page_size, or n_b above 32 * mask_words) are clamped and latch
  * WST_ERR_BAD_OFFSETS; a page outside the cache reads as zeros and latches
@@ -748,8 +749,9 @@ size_t wst_tree_attention_workspace_size(void);
  *   scales  bf16, s[b][n] at scales + b*lds + n, b < ceil(K/group)
  *   bias    bf16 [N], NULL unless epi > 0
  *   C       c_type [M][N], leading dimension ldc
- * group is 32, 64 or 128, else WST_ERR_UNSUPPORTED; K is arbitrary (a last group
- * is what is left).  The weights are exact in bf16; products accumulate in fp32
+ * group is 32, 64 or 128, sizes below 2^31 - 1024, else WST_ERR_UNSUPPORTED (also
+ * where the tiles' blocks of 256 k exceed 2^31); K is arbitrary (a last group is
+ * what is left).  The weights are exact in bf16; products accumulate in fp32
  * inside a group, the groups are scaled and added in fp32.  Pointers are 16-byte
  * aligned, leading dimensions and strides multiples of 16 bytes.  Meant for the
  * few rows of a decoding step: every 64 rows read the weights once.

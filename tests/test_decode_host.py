@@ -56,7 +56,7 @@ ATTEND = dict(B=2, T=8, H=8, Hkv=2, Dh=128, Q=FAKE, ldq=1024, off=FAKE, ctx=FAKE
     (dict(page=4), UNSUPPORTED), (dict(page=24), UNSUPPORTED), (dict(page=192), UNSUPPORTED), (dict(page=0), INVALID),
     (dict(pages=0), INVALID), (dict(pages=2 ** 28), UNSUPPORTED), (dict(ps=0), INVALID), (dict(ts=0), INVALID), (dict(hs=0), INVALID),
     (dict(ps=-8), INVALID), (dict(ts=260), ALIGN), (dict(max_pages=0), INVALID), (dict(max_pages=2 ** 27, ldt=2 ** 27), UNSUPPORTED),
-    (dict(T=2 ** 30 + 1), UNSUPPORTED), (dict(ot=2), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
+    (dict(T=2 ** 30 + 1), UNSUPPORTED), (dict(B=2 ** 29 + 1), UNSUPPORTED), (dict(ot=2), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(scale=3e38), INVALID), (dict(Q=None), INVALID), (dict(O=None), INVALID), (dict(off=None), INVALID), (dict(ctx=None), INVALID),
     (dict(table=None), INVALID), (dict(kc=None), INVALID), (dict(vc=None), INVALID), (dict(ws=None), INVALID), (dict(ldq=1016), INVALID),
     (dict(ldo=1016), INVALID), (dict(ldt=1), INVALID), (dict(words=0), INVALID), (dict(words=3, ldm=2), INVALID), (dict(Q=FAKE + 8), ALIGN),
@@ -93,6 +93,7 @@ GROUP4 = dict(G=4, M=8, N=128, K=256, A=FAKE, lda=256, W=FAKE, ldw=128, stW=128 
 @pytest.mark.parametrize("change,code", [
     (dict(G=0), INVALID), (dict(M=-1), INVALID), (dict(off=None), INVALID), (dict(off=FAKE + 2), ALIGN), (dict(stW=-16), INVALID),
     (dict(stW=8), ALIGN), (dict(stS=-8), INVALID), (dict(stS=4), ALIGN), (dict(epi=1, bias=FAKE, stBias=-1), INVALID), (dict(ct=5), INVALID),
+    (dict(G=2 ** 31 - 1000), UNSUPPORTED),
     (dict(G=2 ** 24, N=2 ** 20, lds=2 ** 20, ldc=2 ** 20), INVALID),  # (too large too, which only the device's sizes decide)
     (dict(), INVALID)])
 def test_grouped_gemm_rejects(lib, change, code):

@@ -72,8 +72,8 @@ wst_status wst_tree_attention_bf16(int B, int T, int H, int Hkv, int Dh, const v
   if (page_stride < 1 || token_stride < 1 || head_stride < 1)
     return (wst_status)reject(ST_INVALID_ARG, "tree attention: the cache's strides must be positive");
   if (max_pages < 1 && B > 0) return (wst_status)reject(ST_INVALID_ARG, "tree attention: max_pages=%d", max_pages);
-  if ((long long)max_pages * page_size > (1ll << 30) || T > (1 << 30))
-    return (wst_status)reject(ST_UNSUPPORTED, "tree attention: T=%d, %d pages of %d a sequence: too long", T, max_pages, page_size);
+  if ((long long)max_pages * page_size > (1ll << 30) || T > (1 << 30) || B > (1 << 29))
+    return (wst_status)reject(ST_UNSUPPORTED, "tree attention: B=%d T=%d, %d pages of %d a sequence: too large", B, T, max_pages, page_size);
   if (o_type != WST_F32 && o_type != WST_BF16) return (wst_status)reject(ST_INVALID_ARG, "tree attention: unknown o_type %d", (int)o_type);
   if (!(std::fabs(scale) <= 2.0e38f))  // (times log2(e) it has to be finite too)
     return (wst_status)reject(ST_INVALID_ARG, "tree attention: scale must be finite, at most 2e38");

@@ -65,8 +65,8 @@ int run_w4(const char* what, W4Problem& pr, void* workspace, size_t workspace_by
   W4Args& a = pr.a;
   if (a.N < 1 || a.K < 1 || a.M < 0 || a.G < 1)
     return reject(ST_INVALID_ARG, "%s: sizes out of range (G=%d M=%d N=%d K=%d)", what, a.G, a.M, a.N, a.K);
-  if (a.N > 0x7fffffff - 1024 || a.K > 0x7fffffff - 1024 || a.M > 0x7fffffff - 1024)
-    return reject(ST_UNSUPPORTED, "%s: M=%d N=%d K=%d: too large", what, a.M, a.N, a.K);
+  if (a.N > 0x7fffffff - 1024 || a.K > 0x7fffffff - 1024 || a.M > 0x7fffffff - 1024 || a.G > 0x7fffffff - 1024)
+    return reject(ST_UNSUPPORTED, "%s: G=%d M=%d N=%d K=%d: too large", what, a.G, a.M, a.N, a.K);
   if (pr.group != 32 && pr.group != 64 && pr.group != 128)
     return reject(ST_UNSUPPORTED, "%s: group=%d: this build supports 32, 64 and 128", what, pr.group);
   if (a.epi < 0 || a.epi > 3) return reject(ST_INVALID_ARG, "%s: unknown epilogue %d", what, a.epi);

