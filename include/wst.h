@@ -754,7 +754,7 @@ size_t wst_tree_attention_workspace_size(void);
  * what is left).  The weights are exact in bf16; products accumulate in fp32
  * inside a group, the groups are scaled and added in fp32.  Pointers are 16-byte
  * aligned, leading dimensions and strides multiples of 16 bytes.  Meant for the
- * few rows of a decoding step: every 64 rows read the weights once.
+ * few rows of a decoding step: every 32 rows read the weights once.
  * workspace: at least the 256-byte header, zero-filled once.  With
  * wst_gemm_w4_workspace_size() bytes the K loops are cut so that every SM gets
  * the same share (the pieces of a tile are added in a fixed order); smaller ones

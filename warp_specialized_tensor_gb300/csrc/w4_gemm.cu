@@ -101,15 +101,20 @@ int run_w4(const char* what, W4Problem& pr, void* workspace, size_t workspace_by
   a.ws = reinterpret_cast<WsHeader*>(ws);
   a.slots = reinterpret_cast<float*>(ws + kWsHeaderBytes);
   a.timeout_ns = wait_timeout_ns();
-  // Rows that a tile takes: all of a dense product (up to 64), twice the mean of a group's.
+  // Column tiles of 8 rows in a tile: as many as the rows need (twice the mean of a group's),
+  // up to 4; fewer while that leaves a CTA at most 14 units, whose length then counts for
+  // less than the sums that are merged.  (64 x 2,048 x 2,048 7.7, 9.1, 9.0 us with 1, 2, 4;
+  // 64 x 4,096 x 4,096 22.6, 13.5, 14.2; 32 x 8,192 x 8,192 34.9, 22.3, 22.1.  Tiles of 64
+  // rows, 8, took 48 us for 64 x 8,192 x 8,192 where 4 takes 38.)
   const long long rows = a.offsets ? 2 * (((long long)a.M + a.G - 1) / a.G) : a.M;
-  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
-  const long long units = (((long long)a.M + 8 * nt - 1) / (8 * nt) + (a.offsets ? a.G : 0)) * a.n_tiles;
+  int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  auto tiles = [&](int n) { return (((long long)a.M + 8 * n - 1) / (8 * n) + (a.offsets ? a.G : 0)) * a.n_tiles; };
+  while (nt > 1 && tiles(nt / 2) <= 14ll * dev.num_sms / a.k_units) nt /= 2;
+  const long long units = tiles(nt);
   if (units > 0x7fffffffll / a.k_units) return reject(ST_UNSUPPORTED, "%s: G=%d M=%d N=%d K=%d: too large", what, a.G, a.M, a.N, a.K);
   if (nt == 1) return launch_w4_group<1>(pr, dev, stream);
   if (nt == 2) return launch_w4_group<2>(pr, dev, stream);
-  if (nt == 4) return launch_w4_group<4>(pr, dev, stream);
-  return launch_w4_group<8>(pr, dev, stream);
+  return launch_w4_group<4>(pr, dev, stream);
 }
 
 }  // namespace

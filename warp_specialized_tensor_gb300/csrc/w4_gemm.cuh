@@ -14,7 +14,7 @@
 //    features (two tiles of 16) and all the rows, 8 to a column tile.  (tcgen05 was built
 //    and measured: unpacked numbers go to tensor memory at 174 bytes a clock, a product
 //    of 16 k takes 45 clocks however few rows it has and 100 while other warps unpack
-//    and store: 1,600 clocks a unit.  At 64 rows the two would meet.)
+//    and store: 1,600 clocks a unit.)
 //  - The rows' values are put in the weights' order by a warp of its own, where the
 //    instruction's fragments are one 16-byte load.
 //  - Accumulators of one group are scaled and added in fp32 when the group ends.
@@ -29,9 +29,10 @@
 // barrier take the issuing thread about 200 clocks), one that adds the sets' sums of a
 // tile and stores it while they multiply the next, and one or two that order the rows (a
 // unit takes one 1,000 clocks at 8 rows, most of it latency).
-// Measured: 1 x 4,096 x 4,096 10.8 us (8.7 MB; about 9 us do not depend on the size), 16 x 8,192 x 8,192 with bias and SiLU 21 us (35 MB),
-// 64 rows of 64 experts, 1,536 x 4,096, 32 us (111 MB at 3.4 TB/s): a unit takes a CTA 750
-// clocks at 8 rows and 1,000 at 16, of the integer pipe and the rows' order.
+// Measured: 1 x 4,096 x 4,096 8.0 us (8.7 MB; a launch 2, the first loads and the merge of
+// four pieces the most of the rest), 16 x 8,192 x 8,192 with bias and SiLU 17.2 us (35 MB at
+// 2.0 TB/s), 64 rows of 64 experts, 1,536 x 4,096, 32 us (111 MB at 3.5 TB/s): a unit takes a
+// CTA 750 clocks at 8 rows and 1,000 at 16, of the integer pipe and the rows' order.
 #pragma once
 
 #include "work_split.cuh"
@@ -46,7 +47,7 @@ constexpr int kW4SBytes = 2048;  // scales: 128 features x up to 8 groups, bf16
 constexpr int kW4MaxCtas = 160;
 constexpr int kW4Pitch = kW4Feats + 4;  // floats of a row of a set's sums
 
-template <int NT>  // column tiles of 8 rows: 1, 2, 4, 8
+template <int NT>  // column tiles of 8 rows: 1, 2, 4
 struct W4Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kSets = NT == 1 ? 4 : NT == 2 ? 3 : 2;
@@ -62,11 +63,11 @@ struct W4Cfg {
   static_assert(kStage % 1024 == 0 && kSmem <= 232448 && kStages >= kSets, "shared memory");
 };
 
-// Workspace after the header: two slots of partial sums per CTA, [64 rows][128
+// Workspace after the header: two slots of partial sums per CTA, [32 rows][128
 // features] fp32 each.  The pieces of the cut tiles are counted in the header's spare
 // words, which hold zeros between calls: a byte for each CTA (the tile that begins in
 // its share and ends in another's).
-constexpr size_t kW4SlotFloats = 64 * kW4Feats;
+constexpr size_t kW4SlotFloats = 32 * kW4Feats;
 constexpr size_t kW4WorkspaceBytes = kWsHeaderBytes + 2 * (size_t)kW4MaxCtas * kW4SlotFloats * 4;
 static_assert(kW4MaxCtas <= (int)sizeof(WsHeader::pad) && kW4MaxCtas < 256, "a byte for each CTA, counting up to all of them");
 
@@ -272,6 +273,18 @@ __device__ __forceinline__ bool w4_last_piece(WsHeader* ws, int c, int pieces) {
   return true;
 }
 
+// CTAs that share W units.  Where every tile can have one, each has the same number of them
+// (of at least two units): then no share spans two tiles, whose sums a CTA would hand over
+// one after the other, and no tile is cut at odd places.  (1 x 4,096 x 4,096 8.0 us on 128
+// CTAs against 10.8 on all, 16 x 8,192 x 8,192 17.2 against 21.0, 61 x 1,531 x 2,744 9.7
+// against 13.2; of 13 sizes none became slower.)
+__device__ __forceinline__ int w4_ctas(const W4Args& p, int W) {
+  const int tiles = W / p.k_units, grid = (int)gridDim.x;
+  if (!p.split || tiles == 0) return max(1, min(grid, tiles));
+  if (tiles <= grid) return tiles * max(1, min(grid / tiles, p.k_units / 2));
+  return min(grid, W / 2);
+}
+
 // What is left of a cut tile's piece when its sums are in the slot.
 struct W4Piece {
   int c0, c1;  // the tile's first and last CTA
@@ -341,7 +354,7 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
     };
     const long long all = counted.total(p.G, count, scratch);
     W = all > 0x7fffffff ? 0 : (int)all;  // (only offsets that go back and forth count so many: they are refused)
-    const Share<int> s(W / grain, max(1, min((int)gridDim.x, W / (2 * grain))));
+    const Share<int> s(W / grain, w4_ctas(p, W));
     if ((int)blockIdx.x < s.G) {
       lo = s.lo((int)blockIdx.x) * grain;
       hi = s.lo((int)blockIdx.x + 1) * grain;
@@ -351,7 +364,7 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
   } else {
     W = W4Walker<NT>::units(p, 0, p.M);
   }
-  const Share<int> share(W / grain, max(1, min((int)gridDim.x, W / (2 * grain))));
+  const Share<int> share(W / grain, w4_ctas(p, W));
   if (!p.offsets && (int)blockIdx.x < share.G) {
     lo = share.lo((int)blockIdx.x) * grain;
     hi = share.lo((int)blockIdx.x + 1) * grain;

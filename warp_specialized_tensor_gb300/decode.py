@@ -216,7 +216,7 @@ def wst_gemm_w4(A, W, scales, C, group=128, bias=None, epi="none", workspace=Non
 
     A: bf16 [M, K]; W: uint8 [N, ceil(K/2)], two numbers a byte, the even k in the low
     half; scales: bf16 [ceil(K/group), N]; group 32, 64 or 128; C: bf16/fp32 [M, N];
-    bias: bf16 [N].  For few rows: every 64 rows read the weights once."""
+    bias: bf16 [N].  For few rows: every 32 rows read the weights once."""
     lda, ldw, lds, ldc = _w4_operands(A, W, scales, C, group, 2)
     (M, K), N = A.shape, W.shape[0]
     e = _w._epi(epi)
