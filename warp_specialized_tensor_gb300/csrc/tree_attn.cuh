@@ -20,7 +20,7 @@
 // nearly the same time, and the later one finds K and V in L2.  The cut between the lines is
 // shifted (Share's lead) so that the two are up to 24 blocks apart: at the same time both
 // miss L2 and read HBM.  (16 trees of 64 tokens on up to 8,192, 400 MB of K and V: 128 us;
-// with leads of 0, 4, 8, 16 141, 138, 136, 132, and 740 MB read at 0; in the
+// with leads of 0, 4, 8, 16 141, 138, 136, 132, and 740 MB read at 0, 500 at 24; in the
 // sequences' order one CTA took a tile after the other, 138 us and 800 MB.)  Two tiles of a
 // sequence in one CTA read 400 MB but wait for each other's products, 129 us: tensor memory
 // holds one S/P buffer for each of two tiles, three for one.
