@@ -44,7 +44,7 @@
  *    wst_ikbo_linear_compress_noalloc.
  *  - `stream` is a cudaStream_t (NULL = the legacy default stream).  Every
  *    call is asynchronous: it validates its arguments on the host, enqueues
- *    one kernel on `stream`, and returns.
+ *    its kernel (a few calls: two) on `stream`, and returns.
  *  - bf16 is IEEE-style bfloat16; accumulation is fp32; bf16 outputs are
  *    rounded to nearest even.
  *  - Alignment: every matrix pointer is 16-byte aligned and every leading
