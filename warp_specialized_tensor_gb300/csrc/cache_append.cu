@@ -14,8 +14,8 @@
 // step's sines and cosines into shared memory while their first two units of data are in
 // flight.  A unit is 16 components of a head: two 16-byte words of bf16, the two halves of
 // eight pairs.  Measured: 16,384 tokens of 32 + 2 x 8 heads of 128, bf16: 71.6 us, 403 MB at
-// 5.6 TB/s (a plain copy reaches 6.8); 5,003 of 14 + 2 x 2 heads of 64, fp32: 9.8 us, 33 MB (a
-// token to a step 19.8 us, three of four threads without a unit); 32 tokens 2.7 us, of which a
+// 5.6 TB/s (a plain copy reaches 6.8); 5,003 of 14 + 2 x 2 heads of 64, fp32: 10.0 us, 33 MB (a
+// token to a step 19.8 us, three of four threads without a unit); 32 tokens 2.6 us, of which a
 // launch is 2.
 #include <algorithm>
 
