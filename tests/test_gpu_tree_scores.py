@@ -1,0 +1,82 @@
+"""wst_tree_attention_bf16 with scores that fp32 holds exactly, so that what is left of the error is the probabilities':
+maxima that grow in the middle of a block, and the parts in which fp32 output takes P."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import warp_specialized_tensor_gb300 as wst
+from tree_ref import Paged
+
+pytestmark = pytest.mark.gpu
+
+LN2 = float(np.float32(math.log(2.0)))  # times log2(e), rounded to fp32, it is 1: a score is an exponent of 2
+                                        # (off by less than 2^-28 of it)
+
+
+def run(c, dtype, scale, whole=True):
+    out = torch.full((c.T, c.H, c.Dh), 3.0, dtype=dtype, device="cuda")
+    ws = wst.tree_attention_workspace() if whole else wst.workspace()
+    wst.wst_tree_attention_bf16(c.q, c.offsets, c.context, c.k_cache, c.v_cache, c.table, out, mask=c.mask, scale=scale, workspace=ws)
+    assert wst.wst_sync_status(ws) == 0
+    return out
+
+
+def exact_scores(lens, H, Hkv, Dh, page, mask, seed, every, rise):
+    """Row (t, h) scores fine + rise * (how often its maximum has grown): two products of bf16 numbers whose sum 24 bits
+    hold.  It grows at four of every `every`-th key (not the same ones for each head); `fine` lies in (-4, 0] in 64ths.
+    A component of V is 1 for one key of the sequence and 0 for the others, so an output is that key's probability."""
+    c = Paged(lens, H, Hkv, Dh, page, mask, seed=seed)
+    rng = np.random.default_rng(seed)
+    group = H // Hkv
+    assert 2 * group <= Dh
+    c.q.zero_()
+    for h in range(H):
+        c.q[:, h, 2 * (h % group)] = 1.0
+        c.q[:, h, 2 * (h % group) + 1] = 1.0
+    for b, (ctx, n) in enumerate(lens):
+        N = ctx + n
+        steps = -(-N // every)
+        K, V = np.zeros((N, Hkv, Dh)), np.zeros((N, Hkv, Dh))
+        for h in range(H):
+            grows = np.zeros(steps, dtype=bool)
+            grows[1 + rng.permutation(steps - 1)[:4]] = True  # (no more: below 2^-126 there is no P)
+            K[:, h // group, 2 * (h % group)] = rise * np.cumsum(grows)[np.arange(N) // every]
+            K[:, h // group, 2 * (h % group) + 1] = -rng.integers(0, 256, N) / 64.0
+        for h in range(Hkv):
+            keys = rng.permutation(N)[:Dh]
+            V[keys, h, np.arange(keys.size)] = 1.0
+        c.K[b] = torch.from_numpy(K).cuda().bfloat16()
+        c.V[b] = torch.from_numpy(V).cuda().bfloat16()
+        assert torch.equal(c.K[b].double().cpu(), torch.from_numpy(K))
+    c.fill()
+    return c
+
+
+CASES = [  # lens, H, Hkv, Dh, page, mask, whole workspace
+    ([(508, 5), (130, 3), (64, 1)], 8, 2, 128, 64, "chain", True),
+    ([(508, 5), (130, 3), (64, 1)], 8, 2, 64, 16, "chain", False),
+    ([(250, 70), (0, 64)], 16, 2, 128, 32, "tree", True),
+    ([(900, 9)], 4, 1, 64, 128, "any", True),
+    ([(0, 200), (96, 33)], 2, 1, 128, 16, "chain", True),
+]
+
+
+@pytest.mark.parametrize("every,rise", [(32, 10.0), (64, 20.0), (96, 12.0)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens,H,Hkv,Dh,page,mask,whole", CASES, ids=["case%d" % i for i in range(len(CASES))])
+def test_probabilities_of_exact_scores(lens, H, Hkv, Dh, page, mask, whole, dtype, every, rise):
+    """The whole relative error of an output, which is one probability p / l, in units of 2^-24:
+    2^x is good to 2^-22, for p and for the terms of l: 8; l adds the terms of one size (what came before a growth counts
+    2^-10 and less) in chains of 8 and their sums (7 + 2), over the 4 steps of a block and up to 8 blocks, a rounding each:
+    21; the scale, 2^-28 of an exponent below 128 times ln 2: 6; 1 / l, its product, the join of two pieces: 6; the three
+    bf16 of p: 1, their products with 1, added with 2^-22 each: 8.  That is 50 or 2^-18.3; two parts of p would be off by
+    up to 2^-16, 256.  bf16 output: P and the result are each off by 2^-8, l adds 8 terms more in a chain."""
+    c = exact_scores(lens, H, Hkv, Dh, page, mask, len(lens) + Dh + int(rise), every, rise)
+    out = run(c, dtype, LN2, whole)
+    want, _, _ = c.want(LN2)
+    bound = 50 * 2.0 ** -24 if dtype is torch.float32 else 2.0 ** -8 + (1 + 2.0 ** -8) * 2.0 ** -8 + 60 * 2.0 ** -24
+    err = (out.double() - want).abs()
+    assert bool((err <= want * bound).all()), float((err / want.clamp_min(1e-300)).max())
+    assert float(want[want > 0].min()) > 2.0 ** -100

@@ -798,7 +798,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                   }
                 }
                 // the block's P so far, with the old maximum: WIDTH columns of every step (of
-                // which bf16 output uses half), and of the third parts half as many
+                // which bf16 output uses half), and of the third parts half as many.  The steps
+                // before have stored it, and only this wait puts those stores before the loads.
+                if (c > 0) tree_tmem_store_wait();
                 auto rescale = [&](uint32_t at) {
                   float v[32];
                   tmem_load32(at, v);
