@@ -443,6 +443,7 @@ __global__ void __launch_bounds__(W4Cfg<NT>::kThreads, 1)
           st_shared_v4(at + (uint32_t)((i0 + i) * (kW4K * 2)) + place[i & 1], __byte_perm(v[i].x, v[i].z, 0x5410),
                        __byte_perm(v[i].x, v[i].z, 0x7632), __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632));
       }
+      fence_proxy_async_smem();  // (the stage's next copy comes by the other proxy: barriers alone do not put these stores before it)
       __syncwarp();
       if (lane == 0) {
         // in the units' order: after the unit before this one
