@@ -700,8 +700,10 @@ wst_status wst_cache_append_bf16(int T, int H, int Hkv, int Dh, int rot, wst_rop
  * over the keys j that token t sees: all of the context, and of the new tokens
  * those whose bit is set in its mask (new token d: bit d % 32 of mask[t][d / 32]),
  * or with mask NULL those up to itself (a chain; one token sees everything).  A
- * token that sees no key gets zeros.  Keys that a token does not see take no part,
- * whatever they hold (NaN or infinities in them or in the rest of a page included).
+ * token that sees no key gets zeros.  Scores are fp32 (a larger one is infinite); a key
+ * that scores -inf weighs nothing, and a row of nothing else is zeros as well.  Keys that
+ * a token does not see take no part, whatever they hold (NaN or infinities in them or in
+ * the rest of a page included).
  *   Q       bf16, element (t,h,d) at Q + t*ldq + h*Dh + d
  *   d_q_offsets  DEVICE int32 [B+1], from 0, non-decreasing, at most T: rows behind
  *           the last sequence are left as they were; d_context DEVICE int32 [B]

@@ -80,3 +80,41 @@ def test_probabilities_of_exact_scores(lens, H, Hkv, Dh, page, mask, whole, dtyp
     err = (out.double() - want).abs()
     assert bool((err <= want * bound).all()), float((err / want.clamp_min(1e-300)).max())
     assert float(want[want > 0].min()) > 2.0 ** -100
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("Dh,whole", [(128, True), (64, False)])
+@pytest.mark.parametrize("first,last,value", [(0, 32, -float("inf")), (0, 64, -float("inf")), (0, 128, -float("inf")), (0, 900, -float("inf")),
+                                              (0, 200, -3e38), (1000, 1500, -3e38)])
+def test_context_whose_scores_are_infinite(first, last, value, Dh, whole, dtype):
+    """Keys [first, last) of the context score -inf (held so, or beyond fp32: -3e38 * 4): they weigh nothing, wherever a
+    block or a share begins."""
+    lens = [(700, 3), (2500, 1), (1023, 2), (128, 1), (40, 5)]
+    c = Paged(lens, 8, 2, Dh, 16, "chain", seed=last)
+    c.q[:, :, 0] = 4.0
+
+    def keys(x):
+        for b, (n, _) in enumerate(lens):
+            c.K[b][first:min(last, n), :, 0] = x
+    keys(0.0)
+    _, _, most = c.want(1.0 / math.sqrt(Dh))
+    keys(-1e30)  # (whose weight 64 bits do not hold either)
+    want, size, _ = c.want(1.0 / math.sqrt(Dh))
+    keys(value)
+    c.fill()
+    out = run(c, dtype, 1.0 / math.sqrt(Dh), whole)
+    tol = c.tolerance(want, size, most, dtype)
+    assert bool(((out.double() - want).abs() <= tol).all())
+
+
+def test_rows_whose_scores_are_all_infinite():
+    """Nothing of weight: zeros, as where a row sees nothing; the sequences beside it as they were."""
+    lens = [(300, 2), (127, 1), (255, 1), (0, 3)]
+    c = Paged(lens, 4, 2, 128, 32, "chain", seed=1)
+    c.q[:, :, 0] = 1.0
+    clean = run(c, torch.float32, None)
+    for b in (1, 2, 3):
+        c.K[b][..., 0] = -float("inf")
+    c.fill()
+    out = run(c, torch.float32, None)
+    assert torch.equal(out[:2], clean[:2]) and bool((out[2:] == 0).all())

@@ -738,8 +738,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             uint32_t hi[WIDTH / 2], mid[PARTS == 3 ? 16 : 1], lo[PARTS == 3 ? 16 : 1];
             auto probabilities = [&]() -> float {
-              // (no key seen yet: all scores are -inf, P zero)
-              const float top = !inner && m == -INFINITY ? 0.0f : m;
+              // (no key seen yet, or none whose score is above -inf: P zero)
+              const float top = m == -INFINITY ? 0.0f : m;
               float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
               if (__all_sync(0xffffffffu, fabsf(top) < 1.0e6f || row >= rows)) {
 #pragma unroll
