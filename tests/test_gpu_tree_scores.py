@@ -118,3 +118,21 @@ def test_rows_whose_scores_are_all_infinite():
     c.fill()
     out = run(c, torch.float32, None)
     assert torch.equal(out[:2], clean[:2]) and bool((out[2:] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("Dh,whole", [(128, True), (64, False)])
+@pytest.mark.parametrize("value", [1e30, 2e7, float("inf")])
+def test_large_scores_leave_the_other_rows_bits_alone(value, Dh, whole, dtype):
+    """One component of a new token's key is large, so the rows that see it have large scores, of either sign: those that
+    do not see it keep their bits, though they share warps with them."""
+    lens = [(250, 30), (0, 20), (3000, 64)]
+    c = Paged(lens, 8, 2, Dh, 16, "tree", seed=9)
+    clean = run(c, dtype, None, whole)
+    new = [next(i for i in range(1, n) if 2 <= c.seen[b][:, i].sum() <= n // 2) for b, (_, n) in enumerate(lens)]
+    touched = torch.cat([torch.from_numpy(c.seen[b][:, i]).cuda() for b, i in enumerate(new)])
+    for b, (ctx, _) in enumerate(lens):
+        c.K[b][ctx + new[b], :, 3] = value
+    c.fill()
+    out = run(c, dtype, None, whole)
+    assert torch.equal(out[~touched], clean[~touched]) and not torch.equal(out[touched], clean[touched])

@@ -744,9 +744,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               if (__all_sync(0xffffffffu, fabsf(top) < 1.0e6f || row >= rows)) {
 #pragma unroll
                 for (int i = 0; i < WIDTH / 2; ++i) tree_fma2(x[2 * i], x[2 * i + 1], cs, -top);
-              } else {  // (the difference to the exact product, for scores that pass 2^24)
+              } else {
+                // scores that pass 2^24 take the rounded product, so that the largest one's difference
+                // is 0: a choice of the row, or its bits would depend on the other rows of its warp
+                const bool far = !(fabsf(top) < 1.0e6f);
+                const float by = far ? cs : 1.0f, rest = far ? 1.0f : cs;
 #pragma unroll
-                for (int i = 0; i < WIDTH; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], cs), -top);
+                for (int i = 0; i < WIDTH; ++i) x[i] = __fmaf_rn(__fmul_rn(x[i], by), rest, -top);
               }
               if (!inner) {
 #pragma unroll
