@@ -136,3 +136,14 @@ def test_large_scores_leave_the_other_rows_bits_alone(value, Dh, whole, dtype):
     c.fill()
     out = run(c, dtype, None, whole)
     assert torch.equal(out[~touched], clean[~touched]) and not torch.equal(out[touched], clean[touched])
+
+
+def test_a_mask_without_words_is_refused():
+    """No words hold no tokens' bits (and an empty tensor's address is NULL, which would mean a chain)."""
+    c = Paged([(20, 3)], 2, 1, 64, 16, "tree", seed=1)
+    out = torch.full((c.T, c.H, c.Dh), 3.0, device="cuda")
+    with pytest.raises((ValueError, wst.WstError)):
+        wst.wst_tree_attention_bf16(c.q, c.offsets, c.context, c.k_cache, c.v_cache, c.table, out, mask=c.mask[:, :0],
+                                    workspace=wst.workspace())
+    torch.cuda.synchronize()
+    assert bool((out == 3.0).all())

@@ -170,8 +170,8 @@ def wst_tree_attention_bf16(Q, q_offsets, context, k_cache, v_cache, page_table,
         if not (isinstance(mask, torch.Tensor) and mask.dtype is _I32 and mask.is_cuda and mask.dim() == 2 and mask.stride(1) == 1):
             _need(mask, "mask", _I32, (2,))
         rows, words = mask.shape
-        if rows != T:
-            raise ValueError("mask must be [T, words]")
+        if rows != T or (words < 1 and T > 0):  # (an empty tensor's address is NULL, which means a chain)
+            raise ValueError("mask must be [T, words], a word at least")
         ldm = mask.stride(0) if T > 1 else words
     if scale is None:
         scale = 1.0 / math.sqrt(Dh)
