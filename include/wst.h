@@ -779,6 +779,10 @@ wst_status wst_grouped_gemm_w4(int G, int M_total, int N, int K, const void* A, 
 /* Workspace bytes with which the 4-bit products cut their K loops. */
 size_t wst_gemm_w4_workspace_size(void);
 
+/* Rows of a tile (8, 16 or 32: a form of the kernel each) that a 4-bit product of these
+ * sizes takes on num_sms SMs; G 0: wst_gemm_w4.  0 for sizes out of range. */
+int wst_gemm_w4_tile_rows(int G, int M, int N, int K, int num_sms);
+
 /* Synchronize `stream`, then return and clear the first device-side error
  * latched in `workspace` (WST_OK if none). */
 wst_status wst_sync_status(void* workspace, void* stream);

@@ -61,6 +61,22 @@ int launch_w4_group(W4Problem& pr, const DeviceInfo& dev, cudaStream_t stream) {
   return launch_w4<NT, 4>(pr, dev, stream);
 }
 
+// Tiles of 8 nt rows, at most (G: groups of rows, 0 for the dense product).
+long long w4_tiles(int G, int M, int n_tiles, int nt) { return (((long long)M + 8 * nt - 1) / (8 * nt) + G) * n_tiles; }
+
+// Column tiles of 8 rows in a tile: as many as the rows need (twice the mean of a group's),
+// up to 4; fewer while that leaves a CTA at most 14 units, whose length then counts for
+// less than the sums that are merged.  (64 x 2,048 x 2,048 7.7, 9.1, 9.0 us with 1, 2, 4;
+// 64 x 4,096 x 4,096 22.6, 13.5, 14.2; 32 x 8,192 x 8,192 34.9, 22.3, 22.1.  Tiles of 64
+// rows, 8, took 48 us for 64 x 8,192 x 8,192 where 4 takes 38.)
+int w4_column_tiles(int G, int M, int N, int K, int num_sms) {
+  const int n_tiles = (N + kW4Feats - 1) / kW4Feats, k_units = (K + kW4K - 1) / kW4K;
+  const long long rows = G ? 2 * (((long long)M + G - 1) / G) : M;
+  int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  while (nt > 1 && w4_tiles(G, M, n_tiles, nt / 2) <= 14ll * num_sms / k_units) nt /= 2;
+  return nt;
+}
+
 int run_w4(const char* what, W4Problem& pr, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   W4Args& a = pr.a;
   if (a.N < 1 || a.K < 1 || a.M < 0 || a.G < 1)
@@ -101,16 +117,8 @@ int run_w4(const char* what, W4Problem& pr, void* workspace, size_t workspace_by
   a.ws = reinterpret_cast<WsHeader*>(ws);
   a.slots = reinterpret_cast<float*>(ws + kWsHeaderBytes);
   a.timeout_ns = wait_timeout_ns();
-  // Column tiles of 8 rows in a tile: as many as the rows need (twice the mean of a group's),
-  // up to 4; fewer while that leaves a CTA at most 14 units, whose length then counts for
-  // less than the sums that are merged.  (64 x 2,048 x 2,048 7.7, 9.1, 9.0 us with 1, 2, 4;
-  // 64 x 4,096 x 4,096 22.6, 13.5, 14.2; 32 x 8,192 x 8,192 34.9, 22.3, 22.1.  Tiles of 64
-  // rows, 8, took 48 us for 64 x 8,192 x 8,192 where 4 takes 38.)
-  const long long rows = a.offsets ? 2 * (((long long)a.M + a.G - 1) / a.G) : a.M;
-  int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-  auto tiles = [&](int n) { return (((long long)a.M + 8 * n - 1) / (8 * n) + (a.offsets ? a.G : 0)) * a.n_tiles; };
-  while (nt > 1 && tiles(nt / 2) <= 14ll * dev.num_sms / a.k_units) nt /= 2;
-  const long long units = tiles(nt);
+  const int nt = w4_column_tiles(a.offsets ? a.G : 0, a.M, a.N, a.K, dev.num_sms);
+  const long long units = w4_tiles(a.offsets ? a.G : 0, a.M, a.n_tiles, nt);
   if (units > 0x7fffffffll / a.k_units) return reject(ST_UNSUPPORTED, "%s: G=%d M=%d N=%d K=%d: too large", what, a.G, a.M, a.N, a.K);
   if (nt == 1) return launch_w4_group<1>(pr, dev, stream);
   if (nt == 2) return launch_w4_group<2>(pr, dev, stream);
@@ -125,6 +133,12 @@ using namespace wst;
 extern "C" {
 
 size_t wst_gemm_w4_workspace_size(void) { return kW4WorkspaceBytes; }
+
+int wst_gemm_w4_tile_rows(int G, int M, int N, int K, int num_sms) {
+  const int most = 0x7fffffff - 1024;
+  if (G < 0 || M < 0 || N < 1 || K < 1 || num_sms < 1 || G > most || M > most || N > most || K > most) return 0;
+  return 8 * w4_column_tiles(G, M, N, K, num_sms);
+}
 
 wst_status wst_gemm_w4(int M, int N, int K, const void* A, long lda, const void* W, long ldw, const void* scales,
                        long lds, int group, const void* bias, void* C, long ldc, wst_dtype c_type,

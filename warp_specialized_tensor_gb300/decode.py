@@ -19,7 +19,7 @@ from warp_specialized_tensor_gb300.moe import _dense, _need, _rows, _stream, _ty
 __all__ = [
     "ROPE_HALVES", "ROPE_PAIRS", "wst_cache_append_bf16",
     "wst_tree_attention_bf16", "wst_tree_attention_workspace_size", "tree_attention_workspace",
-    "wst_gemm_w4", "wst_grouped_gemm_w4", "wst_gemm_w4_workspace_size", "gemm_w4_workspace",
+    "wst_gemm_w4", "wst_grouped_gemm_w4", "wst_gemm_w4_workspace_size", "gemm_w4_workspace", "wst_gemm_w4_tile_rows",
 ]
 
 # enum of include/wst.h
@@ -37,7 +37,8 @@ def declare(lib) -> None:
             ("wst_tree_attention_workspace_size", Z, []),
             ("wst_gemm_w4", I, [I, I, I, P, L, P, L, P, L, I, P, P, L, I, I, P, Z, P]),
             ("wst_grouped_gemm_w4", I, [I, I, I, I, P, L, P, L, L, P, L, L, I, P, P, L, P, L, I, I, P, Z, P]),
-            ("wst_gemm_w4_workspace_size", Z, [])):
+            ("wst_gemm_w4_workspace_size", Z, []),
+            ("wst_gemm_w4_tile_rows", I, [I, I, I, I, I])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
 
@@ -197,6 +198,14 @@ def gemm_w4_workspace(device=None, stream=None) -> torch.Tensor:
     ws = torch.empty(wst_gemm_w4_workspace_size(), dtype=torch.uint8, device=device or "cuda")
     _w.wst_workspace_init(ws, stream)
     return ws
+
+
+def wst_gemm_w4_tile_rows(M: int, N: int, K: int, groups: int = 0, num_sms: int | None = None) -> int:
+    """Rows of a tile (8, 16 or 32: a form of the kernel each) that a product of these
+    sizes takes on num_sms SMs (the current device's if None); groups 0: wst_gemm_w4."""
+    if num_sms is None:
+        num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    return int(_lib().wst_gemm_w4_tile_rows(groups, M, N, K, num_sms))
 
 
 def _w4_operands(A, W, scales, C, group, dims):
