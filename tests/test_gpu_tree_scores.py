@@ -147,3 +147,19 @@ def test_a_mask_without_words_is_refused():
                                     workspace=wst.workspace())
     torch.cuda.synchronize()
     assert bool((out == 3.0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_last_page_behind_two_to_the_31_elements(dtype):
+    """A cache of more than 2^31 elements, the sequence on its last page and its first: the bounds of the other tests."""
+    pages, page, H, Hkv, Dh = 17000, 128, 8, 8, 128
+    c = Paged([(150, 3)], H, Hkv, Dh, page, "chain", seed=3)
+    k = torch.zeros(pages, page, Hkv, Dh, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    c.k_cache, c.v_cache = k, v
+    c.table[0, :2] = torch.tensor([pages - 1, 0], dtype=torch.int32, device="cuda")
+    c.fill()
+    k[0, 25:], v[0, 25:] = float("nan"), float("inf")
+    out = run(c, dtype, 1.0 / math.sqrt(Dh))
+    want, size, most = c.want(1.0 / math.sqrt(Dh))
+    assert bool(((out.double() - want).abs() <= c.tolerance(want, size, most, dtype)).all())
