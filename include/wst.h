@@ -715,7 +715,8 @@ wst_status wst_cache_append_bf16(int T, int H, int Hkv, int Dh, int rot, wst_rop
  *   O       o_type, element (t,h,d) at O + t*ldo + h*Dh + d; it must not overlap the
  *           inputs
  * The probabilities enter the product with V as bf16 (as three bf16, good to 2^-24,
- * where O is fp32); row maxima, sums and the output accumulate in fp32.
+ * where O is fp32); row maxima, sums and the output accumulate in fp32, where O is bf16 up
+ * to 65,536 keys at a time as the tensor core adds, which cuts off (up to 2^-11 of O).
  * After a tree is verified, two calls of wst_permute_rows move the accepted tokens'
  * rows of a cache together: into an array of their own and back behind the context
  * (a row's new place may be another's old one).

@@ -163,3 +163,77 @@ def test_last_page_behind_two_to_the_31_elements(dtype):
     out = run(c, dtype, 1.0 / math.sqrt(Dh))
     want, size, most = c.want(1.0 / math.sqrt(Dh))
     assert bool(((out.double() - want).abs() <= c.tolerance(want, size, most, dtype)).all())
+
+
+def long_sums(lens, H, Hkv, Dh, dtype, seed):
+    """Scores of whole numbers for bf16 output (P is a power of two, exact in bf16), in 64ths for fp32; V of one sign."""
+    c = Paged(lens, H, Hkv, Dh, 128, "chain", seed=seed)
+    c.q.zero_()
+    c.q[:, :, 0] = 1.0
+    c.q[:, :, 1] = 1.0
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    for b, (ctx, n) in enumerate(lens):
+        N = ctx + n
+        c.K[b].zero_()
+        if dtype is torch.bfloat16:
+            c.K[b][..., 0] = -torch.randint(0, 12, (N, Hkv), generator=g, device="cuda").bfloat16()
+        else:
+            c.K[b][..., 0] = (-torch.randint(0, 256, (N, Hkv), generator=g, device="cuda") / 64.0).bfloat16()
+        c.V[b] = (1.0 + torch.rand(N, Hkv, Dh, generator=g, device="cuda")).bfloat16()
+    c.fill()
+    return c
+
+
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("lens,H,Hkv,Dh", [([(2000, 1)], 4, 1, 128), ([(8000, 2), (3, 1), (129, 5)], 8, 2, 64), ([(70000, 1)], 8, 2, 128),
+                                           ([(70000, 40)], 8, 1, 64), ([(262143, 1)], 2, 1, 64)])
+def test_long_sums_fp32(lens, H, Hkv, Dh, whole):
+    """In units of 2^-24, everything of one sign: 42 for P and l of a block (the test above), a block's last 8 products
+    with V, each cut off by up to 2 (the two smaller parts' are 2^-8 of that): 17, and a rounding for every block in each
+    of the two sums.  (Cut off with every product over the whole length it is 40 for a block.)"""
+    c = long_sums(lens, H, Hkv, Dh, torch.float32, sum(lens[0]))
+    out = run(c, torch.float32, LN2, whole)
+    want, _, _ = c.want(LN2)
+    blocks = max(-(-(ctx + n) // 128) for ctx, n in lens)
+    bound = (42 + 17 + 2 * blocks) * 2.0 ** -24
+    err = ((out.double() - want) / want).abs()
+    assert float(err.max()) <= bound, float(err.max()) / bound
+    # where nothing adds up, these are a walk's steps: the mean, which cutting off would move with every block
+    assert abs(float(((out.double() - want) / want).mean())) <= (42 + 17 + 8) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("lens,H,Hkv,Dh", [([(8000, 1)], 8, 2, 128), ([(600000, 1)], 4, 1, 64), ([(300000, 3)], 4, 1, 128), ([(33000, 33)], 8, 2, 64),
+                                           ([(70000, 2), (100, 40), (131072, 1), (0, 5), (65535, 1)], 8, 2, 128)])
+def test_long_sums_bf16(lens, H, Hkv, Dh, whole):
+    """P and l are exact but for the scale (2^-22) and fp32's sums; what is left before the result's own rounding, half a
+    step of the bf16 at hand: the 8 products of up to 512 blocks, each cut off by up to 2^-23, 2^-11 in all, and the
+    roundings of the runs, of l and at the end, 2^-20.  (Cut off with every product, 300,000 keys are off by 2^-9.6.)"""
+    c = long_sums(lens, H, Hkv, Dh, torch.bfloat16, sum(lens[0]))
+    out = run(c, torch.bfloat16, LN2, whole)
+    want, _, _ = c.want(LN2)
+    half = torch.exp2(want.log2().floor()) * 2.0 ** -8
+    over = ((out.double() - want).abs() - half) / want
+    assert float(over.max()) <= 2.0 ** -11 + 2.0 ** -20, float(over.max()) * 2 ** 11
+
+
+def test_sharp_rows_over_several_runs():
+    """Maxima that grow in later runs, and rows that see nothing for a while: what was added up before is scaled."""
+    c = Paged([(140000, 3)], 4, 2, 128, 64, "any", seed=5, size=2.0)
+    n = c.lens[0][0]
+    c.K[0][:n] = (c.K[0][:n].float() * torch.linspace(0.05, 1.0, n, device="cuda")[:, None, None]).bfloat16()
+    c.q[:, :, 0] = 2.0
+    c.K[0][:66000, :, 0] = -3e38 * 4  # (rounds to -inf)
+    c.K[0][:1000, 1, 0] = 1.0
+    c.fill()
+    assert bool(c.K[0][:1000, 0, 0].isinf().all())
+    for dtype in (torch.bfloat16, torch.float32):
+        for whole in (True, False):
+            out = run(c, dtype, 0.05, whole)
+            K = c.K[0]
+            c.K[0] = torch.where(K.isinf(), -1e30, K)
+            want, size, _ = c.want(0.05)
+            c.K[0] = torch.where(K.isinf(), 0.0, K)
+            _, _, most = c.want(0.05)
+            c.K[0] = K
+            assert bool(((out.double() - want).abs() <= c.tolerance(want, size, most, dtype)).all())

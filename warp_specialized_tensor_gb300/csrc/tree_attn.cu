@@ -2,6 +2,7 @@
 // argument checks, tensor maps, the two launches.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "tree_attn.cuh"
 #include "wst.h"
@@ -11,7 +12,7 @@ namespace wst {
 
 namespace {
 
-template <int DH, bool OUT_F32>
+template <int DH, bool OUT_F32, bool LONG>
 int launch_tree(const TreeArgs& a, const void* Q, long long ldq, const void* K, const void* V, const DeviceInfo& dev,
                 cudaStream_t stream) {
   using Cfg = TreeCfg<DH, OUT_F32 ? 3 : 1>;
@@ -28,7 +29,7 @@ int launch_tree(const TreeArgs& a, const void* Q, long long ldq, const void* K, 
   const uint32_t box[4] = {64, (uint32_t)a.chunk, 1, 1};
   if ((st = encode_map(&tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, K, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))) return st;
   if ((st = encode_map(&tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, V, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))) return st;
-  auto kern = k_tree_attn<DH, OUT_F32>;
+  auto kern = k_tree_attn<DH, OUT_F32, LONG>;
   if ((st = ensure_smem_attr((const void*)kern, Cfg::kSmem))) return st;
   const int grid = std::min(dev.num_sms, kTreeMaxCtas);
   cudaError_t e = launch_early(kern, dim3((unsigned)grid), kTreeThreads, Cfg::kSmem, stream, tmQ, tmK, tmV, a);
@@ -134,11 +135,13 @@ wst_status wst_tree_attention_bf16(int B, int T, int H, int Hkv, int Dh, const v
   a.slots = reinterpret_cast<float*>(ws + kTreeSlotOffset);
   a.timeout_ns = wait_timeout_ns();
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (Dh == 128)
-    return (wst_status)(o_type == WST_F32 ? launch_tree<128, true>(a, Q, ldq, k_cache, v_cache, dev, s)
-                                          : launch_tree<128, false>(a, Q, ldq, k_cache, v_cache, dev, s));
-  return (wst_status)(o_type == WST_F32 ? launch_tree<64, true>(a, Q, ldq, k_cache, v_cache, dev, s)
-                                        : launch_tree<64, false>(a, Q, ldq, k_cache, v_cache, dev, s));
+  const bool is_long = (long long)max_pages * page_size > kTreeLong;
+  auto launch = [&](auto dh) {
+    constexpr int DH = decltype(dh)::value;
+    if (o_type == WST_F32) return launch_tree<DH, true, false>(a, Q, ldq, k_cache, v_cache, dev, s);
+    return is_long ? launch_tree<DH, false, true>(a, Q, ldq, k_cache, v_cache, dev, s) : launch_tree<DH, false, false>(a, Q, ldq, k_cache, v_cache, dev, s);
+  };
+  return (wst_status)(Dh == 128 ? launch(std::integral_constant<int, 128>()) : launch(std::integral_constant<int, 64>()));
 }
 
 }  // extern "C"

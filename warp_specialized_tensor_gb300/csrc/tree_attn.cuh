@@ -37,7 +37,9 @@
 //            (P <= 2^8; l sums the unrounded P).  One bf16 is off by up to 2^-8 of P, which
 //            a bf16 output's own rounding covers; for fp32 output P is three bf16, each what
 //            the ones before leave, off by 2^-24 together
-//   MMA      O += P . V         P from tensor memory, V from shared memory (for each part of P)
+//   MMA      O += P . V         P from tensor memory, V from shared memory (for each part of P;
+//            fp32 output, and bf16 output of long sequences, take O over into sums of their
+//            own, see kTreeRun)
 // From a score's product to the next in its buffer it is S, softmax, PV and three
 // handshakes, 5,000 clocks, of which the softmax is a third: three S/P buffers (two of the
 // wider ones of fp32 output) let S run ahead of PV.  (Two items at a time with one buffer
@@ -75,6 +77,19 @@ constexpr float kTreeGrowSum = 256.0f;  // 2^kTreeGrow
 
 constexpr int kTreeThreads = 256;
 constexpr int kTreeLead = 24;  // blocks, of one line before the other
+// A product into tensor memory cuts its sum off after 24 bits, always towards zero, with every
+// 16 keys of every part of P: 0.65 of 2^-23 on the average.  Left to add up, fp32 output was off
+// by 4e-5 on 8,000 keys in one CTA and by 2e-3 on 262,144.  So the softmax warps of fp32 output
+// take O over after every block, into fp32 sums in registers (2e-7 on 8,000 keys, 9e-7 on
+// 262,144; a plain fp32 form 1e-7.  One token each of 32 sequences of 4,096 115 -> 133 us, 16
+// trees of 64 224 -> 236, chunks of 500 140 -> 151; four warps of their own for the sums, handed
+// a block's O at a time, took 178, 332 and 188).  bf16 output, whose own rounding is off by up to
+// 2^-8, takes O over after kTreeRun blocks (8 cuts a block: 2^-11 at most), in a form of the
+// kernel apart, for tables that hold more than kTreeLong keys: the code for it makes the loop
+// slower where the softmax bounds it (trees 132 -> 141 us), but not one token on 262,144 keys
+// (158.5 -> 159.1).
+constexpr int kTreeRun = 512;
+constexpr int kTreeLong = kTreeRun * kTreeBN;
 
 // PARTS: bf16 numbers that hold one P, 1 for bf16 output, 3 for fp32.
 template <int DH, int PARTS>
@@ -85,6 +100,9 @@ struct TreeCfg {
   // S/P buffers and their columns of tensor memory: the first two parts of P lie over S,
   // the third behind it
   static constexpr int kSBufs = PARTS == 1 ? 3 : 2;
+  // keys of a step of the softmax (fp32 output keeps DH sums in registers: 32 at Dh 128, spilled,
+  // takes 157 us where 16 takes 133, 32 sequences of 4,096; at Dh 64 111 against 121)
+  static constexpr int kWidth = PARTS == 1 ? 64 : DH == 64 ? 32 : 16;
   static constexpr int kSCols = PARTS == 1 ? kTreeBN : kTreeBN + kTreeBN / 2;
   static constexpr int kBars = 2 * kKStages + 2 * kVStages + 2 + 3 * kSBufs + 1;
   static constexpr size_t kSmem = 1024 + (size_t)(2 + kKStages + kVStages) * kTile + 1024;
@@ -348,6 +366,15 @@ __device__ __forceinline__ void tree_tmem_load32(uint32_t taddr, float* v) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tree_tmem_load16(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+        "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
 // Waits for the thread's loads; v passes through, so that no use of it moves ahead.
 template <int N>
 __device__ __forceinline__ void tree_tmem_load_wait(float* v) {
@@ -361,6 +388,11 @@ __device__ __forceinline__ void tree_tmem_store16(uint32_t taddr, const uint32_t
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
       "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+__device__ __forceinline__ void tree_tmem_store8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Waits for a phase: tests for a while (a suspended wait takes longer to wake), then as
@@ -462,9 +494,35 @@ __device__ __forceinline__ void tree_load(const TreeArgs& p, const TreeWalker& w
   }
 }
 
+// A run's O, taken over: total = a total + O (a 0: total holds nothing yet), and those of the
+// runs before an item's last one, put back: O += a total.
+template <int DH>
+static __device__ __noinline__ void tree_take_run(uint32_t t_o, float* total, float a) {
+#pragma unroll 1
+  for (int c = 0; c < DH; c += 32) {
+    float v[32];
+    tmem_load32(t_o + c, v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) total[c + i] = a == 0.0f ? v[i] : fmaf(total[c + i], a, v[i]);
+  }
+}
+template <int DH>
+static __device__ __noinline__ void tree_add_runs(uint32_t t_o, const float* total, float a) {
+#pragma unroll 1
+  for (int c = 0; c < DH; c += 32) {
+    float v[32];
+    tmem_load32(t_o + c, v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = fmaf(total[c + i], a, v[i]);
+    tree_tmem_store32(t_o + c, v);
+  }
+  tree_tmem_store_wait();
+}
+
 // tmQ {Dh, H, T}, boxes of 64 x group x (tokens of a tile); tmK, tmV {Dh, page_size,
 // Hkv, pages}, boxes of 64 x chunk x 1 x 1; 128-byte swizzle.
-template <int DH, bool OUT_F32>
+// LONG: bf16 output, where a sequence may have more than kTreeLong keys.
+template <int DH, bool OUT_F32, bool LONG>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     k_tree_attn(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const TreeArgs p) {
@@ -624,18 +682,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           // 16 keys: 8 columns of P, 2 KB of V
           const uint64_t vd = sdesc_sw128(sV + vs * Cfg::kTile, kTreeBN * 128, 1024);
           const uint32_t a = tmem_base + (uint32_t)(COLS * b), d = tmem_base + Cfg::kTmemO;
+          if constexpr (PARTS == 3) {  // the smallest parts first: what is cut off goes by the sum so far
+#pragma unroll
+            for (int kk = 0; kk < kTreeBN / 16; ++kk)
+              tree_mma_ts(d, a + (uint32_t)(kTreeBN + kk * 8), vd + (uint32_t)(kk * 128), idesc, kk != 0 ? 1u : 0u);
+#pragma unroll
+            for (int kk = 0; kk < kTreeBN / 16; ++kk)
+              tree_mma_ts(d, a + (uint32_t)(kk * 16 + 8), vd + (uint32_t)(kk * 128), idesc, 1u);
+          }
 #pragma unroll
           for (int kk = 0; kk < kTreeBN / 16; ++kk)
-            tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc,
-                        (j > w.jb || kk != 0) ? 1u : 0u);
-          if constexpr (PARTS == 3) {
-#pragma unroll
-            for (int kk = 0; kk < kTreeBN / 16; ++kk)
-              tree_mma_ts(d, a + (uint32_t)((kk >> 1) * 32 + 16 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
-#pragma unroll
-            for (int kk = 0; kk < kTreeBN / 16; ++kk)
-              tree_mma_ts(d, a + (uint32_t)(kTreeBN + kk * 8), vd + (uint32_t)(kk * 128), idesc, 1u);
-          }
+            tree_mma_ts(d, a + (uint32_t)(PARTS == 3 ? kk * 16 : (kk >> 1) * 32 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc,
+                        (PARTS == 3 || (LONG ? (j - w.jb) % kTreeRun != 0 : j > w.jb) || kk != 0) ? 1u : 0u);
           umma_commit(pv_done + 8 * b);
           umma_commit(v_empty + 8 * vs);
           if (++vs == VS) {
@@ -684,7 +742,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const bool active = q * 32 < rows;  // (of the whole warp)
       const int ti = w.s.token(p, w.t) + my_tok;
       float m = -INFINITY, l = 0.0f;
-      for (int j = w.jb; j < w.je; ++j) {
+      // what has been taken from O so far, relative to the maximum m_total (fp32: in registers;
+      // runs: in local memory)
+      float total[PARTS == 3 || LONG ? DH : 1];
+      float m_total = -INFINITY;
+      if constexpr (PARTS == 3) {
+#pragma unroll
+        for (int i = 0; i < DH; ++i) total[i] = 0.0f;
+      }
+      int run = w.jb;
+    next_run:
+      for (int j = LONG ? run : w.jb; j < (LONG ? min(run + kTreeRun, w.je) : w.je); ++j) {
         const bool inner = (j + 1) * kTreeBN <= w.s.ctx;  // every row sees every key
         if (!__all_sync(0xffffffffu, tree_wait(guard, s_full + 8 * b, bph, (kRoleEpilogue << 16) | b))) {
           ok = false;
@@ -693,12 +761,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tc_fence_after_sync();
         const uint32_t t_s = t_lane + (uint32_t)(COLS * b);
         if (active) {
-          // 64 keys at a time (fp32 output: 32, for its parts' registers), in a loop: code
-          // that fits the instruction cache's first level (unrolled over the block, a warp
-          // waited for instructions a fourth of the time).  P of 32 keys goes over their
-          // scores: 16 columns of bf16 pairs, then (fp32 output) 16 of what those leave; what
-          // both leave goes behind the scores.
-          constexpr int WIDTH = PARTS == 1 ? 64 : 32;
+          // 64 keys at a time (fp32 output: fewer, for the registers of its parts and sums), in
+          // a loop: code that fits the instruction cache's first level (unrolled over the block,
+          // a warp waited for instructions a fourth of the time).  P goes over the scores: of
+          // 32 keys the first 16 columns are bf16 pairs; for fp32 output of 16 keys the first
+          // 8, then 8 of what those leave, and what both leave goes behind the scores.
+          constexpr int WIDTH = Cfg::kWidth;
           uint32_t vis[4] = {0u, 0u, 0u, 0u};
           if (!inner && row < rows) {
 #pragma unroll
@@ -709,9 +777,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int c = 0; c < kTreeBN / WIDTH; ++c) {
             const uint32_t t_c = t_s + WIDTH * c;
             uint32_t v0 = c == 0 ? vis[0] : vis[2], v1 = c == 0 ? vis[1] : vis[3];
-            if (PARTS == 3 && (c & 1)) v0 = c == 1 ? vis[1] : vis[3];
+            if constexpr (PARTS == 3) {
+              const int key = WIDTH * c;
+              v0 = (key < 64 ? key < 32 ? vis[0] : vis[1] : key < 96 ? vis[2] : vis[3]) >> (key & 31);
+            }
             float x[WIDTH];
             auto load = [&]() {
+              if constexpr (WIDTH == 16) tree_tmem_load16(t_c, x);
 #pragma unroll
               for (int d = 0; d < WIDTH / 32; ++d) tree_tmem_load32(t_c + 32 * d, x + 32 * d);
               tree_tmem_load_wait<WIDTH>(x);
@@ -736,7 +808,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               const float mx = maximum();
               if (m == -INFINITY) m = mx;
             }
-            uint32_t hi[WIDTH / 2], mid[PARTS == 3 ? 16 : 1], lo[PARTS == 3 ? 16 : 1];
+            uint32_t hi[PARTS == 3 ? WIDTH : WIDTH / 2], lo[WIDTH / 2];
             auto probabilities = [&]() -> float {
               // (no key seen yet, or none whose score is above -inf: P zero)
               const float top = m == -INFINITY ? 0.0f : m;
@@ -763,11 +835,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 x0 = tree_ex2(x0);
                 x1 = tree_ex2(x1);
                 tree_add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], x0, x1);
-                hi[i] = pack_bf16x2(x0, x1);
-                if constexpr (PARTS == 3) {  // (the differences are exact)
-                  const float r0 = x0 - __uint_as_float(hi[i] << 16), r1 = x1 - __uint_as_float(hi[i] & 0xffff0000u);
-                  mid[i] = pack_bf16x2(r0, r1);
-                  lo[i] = pack_bf16x2(r0 - __uint_as_float(mid[i] << 16), r1 - __uint_as_float(mid[i] & 0xffff0000u));
+                if constexpr (PARTS == 3) {  // (the differences are exact; of 16 keys eight first parts, then eight second ones)
+                  uint32_t &y = hi[i + (i & 8)], &z = hi[i + (i & 8) + 8];
+                  y = pack_bf16x2(x0, x1);
+                  const float r0 = x0 - __uint_as_float(y << 16), r1 = x1 - __uint_as_float(y & 0xffff0000u);
+                  z = pack_bf16x2(r0, r1);
+                  lo[i] = pack_bf16x2(r0 - __uint_as_float(z << 16), r1 - __uint_as_float(z & 0xffff0000u));
+                } else {
+                  hi[i] = pack_bf16x2(x0, x1);
                 }
               }
               return (rs[0] + rs[1]) + (rs[2] + rs[3]);
@@ -786,7 +861,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                   sum *= alpha;
                   m = mx;
                 }
-                if (j > w.jb) {  // (the first PV product overwrites O)
+                if (PARTS == 1 && j > (LONG ? run : w.jb)) {  // (a run's first PV product overwrites O)
                   if (!__all_sync(0xffffffffu, tree_wait(guard, pv_done + 8 * last_b, last_ph, (kRoleEpilogue << 16) | 0x100))) {
                     ok = false;
                     break;
@@ -801,41 +876,82 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     tree_tmem_store32(t_o + d * 32, v);
                   }
                 }
-                // the block's P so far, with the old maximum: WIDTH columns of every step (of
-                // which bf16 output uses half), and of the third parts half as many.  The steps
-                // before have stored it, and only this wait puts those stores before the loads.
+                // the block's P so far, with the old maximum: the columns of every step (of which
+                // bf16 output uses half), and of the third parts half as many.  The steps before
+                // have stored it, and only this wait puts those stores before the loads.
                 if (c > 0) tree_tmem_store_wait();
-                auto rescale = [&](uint32_t at) {
-                  float v[32];
-                  tmem_load32(at, v);
+                if constexpr (PARTS == 1) {
+                  auto rescale = [&](uint32_t at) {
+                    float v[32];
+                    tmem_load32(at, v);
 #pragma unroll
-                  for (int i = 0; i < (PARTS == 1 ? 16 : 32); ++i) {
-                    const uint32_t y = __float_as_uint(v[i]);
-                    v[i] = __uint_as_float(pack_bf16x2(__uint_as_float(y << 16) * alpha, __uint_as_float(y & 0xffff0000u) * alpha));
-                  }
-                  tree_tmem_store32(at, v);
-                };
+                    for (int i = 0; i < 16; ++i) {
+                      const uint32_t y = __float_as_uint(v[i]);
+                      v[i] = __uint_as_float(pack_bf16x2(__uint_as_float(y << 16) * alpha, __uint_as_float(y & 0xffff0000u) * alpha));
+                    }
+                    tree_tmem_store32(at, v);
+                  };
 #pragma unroll 1
-                for (int d = 0; d < c * (WIDTH / 32); ++d) rescale(t_s + 32 * d);
-                if (PARTS == 3 && c > 0) {  // (of this step too, which are written anew)
-                  rescale(t_s + kTreeBN);
-                  if (c > 1) rescale(t_s + kTreeBN + 32);
+                  for (int d = 0; d < c * (WIDTH / 32); ++d) rescale(t_s + 32 * d);
+                } else {
+                  auto rescale = [&](uint32_t at) {
+                    float v[16];
+                    tree_tmem_load16(at, v);
+                    tree_tmem_load_wait<16>(v);
+                    uint32_t y[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                      y[i] = pack_bf16x2(__uint_as_float(__float_as_uint(v[i]) << 16) * alpha, __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u) * alpha);
+                    tree_tmem_store16(at, y);
+                  };
+#pragma unroll 1
+                  for (int d = 0; d < c * (WIDTH / 16); ++d) rescale(t_s + 16 * d);
+#pragma unroll 1
+                  for (int d = 0; 2 * d < c * (WIDTH / 16); ++d) rescale(t_s + kTreeBN + 16 * d);  // (of this step too, which are written anew)
                 }
                 tree_tmem_store_wait();
               }
               part = probabilities();
             }
             sum += part;
-#pragma unroll
-            for (int d = 0; d < WIDTH / 32; ++d) tree_tmem_store16(t_c + 32 * d, hi + 16 * d);
             if constexpr (PARTS == 3) {
-              tree_tmem_store16(t_c + 16, mid);
-              tree_tmem_store16(t_s + kTreeBN + 16 * c, lo);
+#pragma unroll
+              for (int d = 0; d < WIDTH / 16; ++d) tree_tmem_store16(t_c + 16 * d, hi + 16 * d);
+              if constexpr (WIDTH == 16) tree_tmem_store8(t_s + kTreeBN + 8 * c, lo);
+              else tree_tmem_store16(t_s + kTreeBN + 16 * c, lo);
+            } else {
+#pragma unroll
+              for (int d = 0; d < WIDTH / 32; ++d) tree_tmem_store16(t_c + 32 * d, hi + 16 * d);
             }
           }
           if (!ok) break;
           l += sum;
           tree_tmem_store_wait();
+          if constexpr (PARTS == 3) {
+            // O of the block before this one, relative to m_total as what it is added to is; the
+            // next product, which overwrites it, waits for this warp
+            if (j > w.jb) {
+              if (!__all_sync(0xffffffffu, tree_wait(guard, pv_done + 8 * last_b, last_ph, (kRoleEpilogue << 16) | 0x700))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after_sync();
+#pragma unroll
+              for (int c = 0; c < DH / 32; ++c) {
+                float v[32];
+                tree_tmem_load32(t_o + c * 32, v);
+                tree_tmem_load_wait<32>(v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) tree_add2(total[c * 32 + 2 * i], total[c * 32 + 2 * i + 1], v[2 * i], v[2 * i + 1]);
+              }
+              if (__any_sync(0xffffffffu, m != m_total)) {
+                const float a = m == m_total ? 1.0f : tree_ex2(m_total - m);
+#pragma unroll
+                for (int i = 0; i < DH; ++i) total[i] *= a;
+              }
+            }
+            m_total = m;
+          }
         }
         if (!inner) {
           // V: clear the block's keys behind the sequence and what is not finite of the new
@@ -909,6 +1025,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         break;
       }
       tc_fence_after_sync();
+      if constexpr (LONG) {
+        if (run + kTreeRun < w.je) {
+          if (active) {
+            tree_take_run<DH>(t_o, total, run == w.jb ? 0.0f : m_total == m ? 1.0f : tree_ex2(m_total - m));
+            m_total = m;
+          }
+          run += kTreeRun;
+          goto next_run;
+        }
+        if (active && run > w.jb) tree_add_runs<DH>(t_o, total, m_total == m ? 1.0f : tree_ex2(m_total - m));
+      }
+      if (PARTS == 3 && active && w.je - w.jb > 1) {
+#pragma unroll
+        for (int c = 0; c < (PARTS == 3 ? DH / 32 : 0); ++c) {
+          float v[32];
+          tmem_load32(t_o + c * 32, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += total[c * 32 + i];
+          tree_tmem_store32(t_o + c * 32, v);
+        }
+        tree_tmem_store_wait();
+      }
       if (active) {
         const bool whole = w.jb == 0 && w.je == w.nb;
         const bool odd = odd_v[it & 3u] > it;  // (a later item's: looked into too)
