@@ -151,23 +151,6 @@ struct AttnArgs {
   float* slots;          // [kAttnMaxCtas][kAttnSlotFloats]
 };
 
-// 4-D TMA tile load (K and V: {Dh, H, Lkv, users}).
-__device__ __forceinline__ void attn_tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar,
-                                                 int x, int y, int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
-
-// 2^x on the special-function unit (ex2.approx.ftz: 2^-inf = +0).
-__device__ __forceinline__ float attn_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Three-input max / min (one instruction for two new scores).
 __device__ __forceinline__ float attn_max3(float a, float b, float c) {
   float d;
@@ -179,53 +162,6 @@ __device__ __forceinline__ float attn_min3(float a, float b, float c) {
   asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// Packed fp32 pairs: (x0, x1) = (x0 * a + c, x1 * a + c) and
-// (r0, r1) += (y0, y1), each lane rounded as its scalar form.
-__device__ __forceinline__ void attn_fma2(float& x0, float& x1, float a, float c) {
-  uint64_t x, av, cv;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(av) : "f"(a));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(cv) : "f"(c));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(x), "l"(av), "l"(cv));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
-}
-__device__ __forceinline__ void attn_add2(float& r0, float& r1, float y0, float y1) {
-  uint64_t r, y;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(r0), "f"(r1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(y0), "f"(y1));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(r), "l"(y));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
-}
-
-// Store 32 consecutive fp32 columns of this thread's TMEM lane (warp-wide).
-__device__ __forceinline__ void attn_tmem_store32(uint32_t taddr, const float (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
-      "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
-      "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
-      : "memory");
-}
-
-__device__ __forceinline__ void attn_tmem_store_wait() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// tcgen05.mma (cta_group::1, kind::f16) with the A operand in TMEM: lane r
-// holds row r, each 32-bit column two consecutive K elements (low half first).
-__device__ __forceinline__ void attn_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 struct AttnItem {
   int u, h;
   int row0;   // first query row of the tile
@@ -514,7 +450,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           mbar_arrive_expect_tx(kf_bar(ks), kAttnKBytes);
           for (int hf = 0; hf < 2; ++hf)
-            attn_tma_load_4d(smem_addr(sK + ks * kAttnKBytes + hf * (kAttnKBytes / 2)), &tmK, kf_bar(ks),
+            tma_load_4d(smem_addr(sK + ks * kAttnKBytes + hf * (kAttnKBytes / 2)), &tmK, kf_bar(ks),
                              hf * 64, x.h, j * kAttnBN, x.u);
           if (++ks == kAttnKStages) { ks = 0; kph ^= 1u; }
         }
@@ -539,7 +475,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         mbar_arrive_expect_tx(vf_bar(vs), kAttnKBytes);
         for (int hf = 0; hf < 2; ++hf)
-          attn_tma_load_4d(smem_addr(sV + vs * kAttnKBytes + hf * (kAttnKBytes / 2)), &tmV, vf_bar(vs),
+          tma_load_4d(smem_addr(sV + vs * kAttnKBytes + hf * (kAttnKBytes / 2)), &tmV, vf_bar(vs),
                            hf * 64, x.h, j * kAttnBN, x.u);
         if (++vs == kAttnVStages) { vs = 0; vph ^= 1u; }
       }
@@ -621,7 +557,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const uint32_t a_p = tmem_base + (uint32_t)(kAttnTmemS + kAttnBN * b);
 #pragma unroll
             for (int kk = 0; kk < kAttnBN / 16; ++kk)  // 16 keys: 8 TMEM columns of P, 2 KB of V
-              attn_mma_ts(d_o, a_p + (uint32_t)(kk * 8), vd0 + (uint32_t)(kk * 128), idesc_o,
+              umma_bf16_ts(d_o, a_p + (uint32_t)(kk * 8), vd0 + (uint32_t)(kk * 128), idesc_o,
                           (jj > 0 || kk != 0) ? 1u : 0u);
             umma_commit(pv_bar(b));
             umma_commit(ve_bar(vs));
@@ -725,10 +661,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int i = 0; i < kAttnBN / 2; ++i) {
             if (i == kAttnEarlyTestPair) s_ready = mbar_test_wait(sf_bar(b_next), ph_next);
-            attn_fma2(s[2 * i], s[2 * i + 1], cs, -m);
-            s[2 * i] = attn_ex2(s[2 * i]);
-            s[2 * i + 1] = attn_ex2(s[2 * i + 1]);
-            attn_add2(rs8[2 * (i & 3)], rs8[2 * (i & 3) + 1], s[2 * i], s[2 * i + 1]);
+            fma_f32x2(s[2 * i], s[2 * i + 1], cs, -m);
+            s[2 * i] = ex2_ftz(s[2 * i]);
+            s[2 * i + 1] = ex2_ftz(s[2 * i + 1]);
+            add_f32x2(rs8[2 * (i & 3)], rs8[2 * (i & 3) + 1], s[2 * i], s[2 * i + 1]);
           }
           const float rs = ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
           if (__any_sync(0xffffffffu, !(rs <= kAttnRescaleBound))) {
@@ -775,7 +711,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               if (!warp_wait_phase(guard, pv_bar(pbuf), pphase,
                                    (kRoleEpilogue << 16) | 0x100)) { ok = false; break; }
               tc_fence_after_sync();
-              const float alpha = grow ? attn_ex2(m - mx) : 1.0f;
+              const float alpha = grow ? ex2_ftz(m - mx) : 1.0f;
               if (grow) {
                 l *= alpha;
                 m = mx;
@@ -786,24 +722,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 tmem_load32(t_o + c * 32, v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] *= alpha;
-                attn_tmem_store32(t_o + c * 32, v);
+                tmem_store32(t_o + c * 32, v);
               }
-              attn_tmem_store_wait();
+              tmem_store_wait();
             }
           }
           if (kvalid >= kAttnBN) {
 #pragma unroll
             for (int i = 0; i < kAttnBN / 2; ++i) {
               if (i == kAttnEarlyTestPair) s_ready = mbar_test_wait(sf_bar(b_next), ph_next);
-              attn_fma2(s[2 * i], s[2 * i + 1], cs, -m);
-              s[2 * i] = attn_ex2(s[2 * i]);
-              s[2 * i + 1] = attn_ex2(s[2 * i + 1]);
-              attn_add2(rs8[2 * (i & 3)], rs8[2 * (i & 3) + 1], s[2 * i], s[2 * i + 1]);
+              fma_f32x2(s[2 * i], s[2 * i + 1], cs, -m);
+              s[2 * i] = ex2_ftz(s[2 * i]);
+              s[2 * i + 1] = ex2_ftz(s[2 * i + 1]);
+              add_f32x2(rs8[2 * (i & 3)], rs8[2 * (i & 3) + 1], s[2 * i], s[2 * i + 1]);
             }
           } else {
 #pragma unroll
             for (int i = 0; i < kAttnBN; ++i) {
-              s[i] = i < kvalid ? attn_ex2(fmaf(s[i], cs, -m)) : 0.0f;
+              s[i] = i < kvalid ? ex2_ftz(fmaf(s[i], cs, -m)) : 0.0f;
               rs8[i & 7] += s[i];
             }
           }
@@ -820,9 +756,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             pk[c] = __uint_as_float(pack_bf16x2(s[64 * h2 + 2 * c], s[64 * h2 + 2 * c + 1]));
-          attn_tmem_store32(t_lane + kAttnTmemS + kAttnBN * b + 32 * h2, pk);
+          tmem_store32(t_lane + kAttnTmemS + kAttnBN * b + 32 * h2, pk);
         }
-        attn_tmem_store_wait();
+        tmem_store_wait();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(pf_bar(b));
@@ -995,12 +931,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           float mn = m;
 #pragma unroll
           for (int k = 0; k < kAttnMergeBatch; ++k) mn = fmaxf(mn, mk[k]);
-          const float a_self = attn_ex2(m - mn);
+          const float a_self = ex2_ftz(m - mn);
           float ak[kAttnMergeBatch];
           l *= a_self;
 #pragma unroll
           for (int k = 0; k < kAttnMergeBatch; ++k) {
-            ak[k] = k < nb0 ? attn_ex2(mk[k] - mn) : 0.0f;
+            ak[k] = k < nb0 ? ex2_ftz(mk[k] - mn) : 0.0f;
             l = fmaf(lk[k], ak[k], l);
           }
           m = mn;
@@ -1029,12 +965,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
             }
             if (last) emit_chunk(c, v, inv);  // the merged, normalised rows
-            else attn_tmem_store32(t_o + c * 32, v);
+            else tmem_store32(t_o + c * 32, v);
           }
           if (last) {
             emitted = true;
           } else {
-            attn_tmem_store_wait();
+            tmem_store_wait();
             __syncwarp();  // the staging buffers are refilled by the next batch
           }
         }

@@ -152,56 +152,6 @@ struct TreeArgs {
   unsigned long long timeout_ns;
 };
 
-__device__ __forceinline__ void tree_tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
-// 2^x on the special-function unit (2^-inf = +0).
-__device__ __forceinline__ float tree_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Packed pairs: (x0, x1) = (x0 * a + c, x1 * a + c); (r0, r1) += (y0, y1).
-__device__ __forceinline__ void tree_fma2(float& x0, float& x1, float a, float c) {
-  uint64_t x, av, cv;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(av) : "f"(a));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(cv) : "f"(c));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(x), "l"(av), "l"(cv));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
-}
-__device__ __forceinline__ void tree_add2(float& r0, float& r1, float y0, float y1) {
-  uint64_t r, y;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(r0), "f"(r1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(y0), "f"(y1));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(r), "l"(y));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
-}
-__device__ __forceinline__ void tree_tmem_store32(uint32_t taddr, const float (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
-      "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]),
-      "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]),
-      "f"(v[31])
-      : "memory");
-}
-__device__ __forceinline__ void tree_tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// Product with the A operand in tensor memory.
-__device__ __forceinline__ void tree_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // sum over i < n of floor((a i + b) / 128), n < 2^23, a <= 256, b < 2^31: whole parts are
 // taken out, then the points under the line are counted along the other axis, until none
 // are left (a logarithm of 128 steps; the quotients fit 32 bits).
@@ -461,7 +411,7 @@ struct TreeLoads {
       if (page < 0 || page >= p.num_pages) latch_error(p.ws, 1u, (kRoleProducer << 16) | 0x20);
       const uint32_t to = dst + (uint32_t)((int)lane * p.chunk * 128);
       for (int hf = 0; hf < DH / 64; ++hf)
-        tree_tma_load_4d(to + hf * (kTreeBN * 128), tm, full, hf * 64, in_page * kTreeBN, w.h, page);
+        tma_load_4d(to + hf * (kTreeBN * 128), tm, full, hf * 64, in_page * kTreeBN, w.h, page);
     }
     if (++in_page >= p.page_size / kTreeBN) in_page = 0;
     if (j == min(w.jb + 1, w.je - 1)) {  // the next item, while copies of this one are in flight
@@ -514,9 +464,9 @@ static __device__ __noinline__ void tree_add_runs(uint32_t t_o, const float* tot
     tmem_load32(t_o + c, v);
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = fmaf(total[c + i], a, v[i]);
-    tree_tmem_store32(t_o + c, v);
+    tmem_store32(t_o + c, v);
   }
-  tree_tmem_store_wait();
+  tmem_store_wait();
 }
 
 // tmQ {Dh, H, T}, boxes of 64 x group x (tokens of a tile); tmK, tmV {Dh, page_size,
@@ -685,14 +635,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if constexpr (PARTS == 3) {  // the smallest parts first: what is cut off goes by the sum so far
 #pragma unroll
             for (int kk = 0; kk < kTreeBN / 16; ++kk)
-              tree_mma_ts(d, a + (uint32_t)(kTreeBN + kk * 8), vd + (uint32_t)(kk * 128), idesc, kk != 0 ? 1u : 0u);
+              umma_bf16_ts(d, a + (uint32_t)(kTreeBN + kk * 8), vd + (uint32_t)(kk * 128), idesc, kk != 0 ? 1u : 0u);
 #pragma unroll
             for (int kk = 0; kk < kTreeBN / 16; ++kk)
-              tree_mma_ts(d, a + (uint32_t)(kk * 16 + 8), vd + (uint32_t)(kk * 128), idesc, 1u);
+              umma_bf16_ts(d, a + (uint32_t)(kk * 16 + 8), vd + (uint32_t)(kk * 128), idesc, 1u);
           }
 #pragma unroll
           for (int kk = 0; kk < kTreeBN / 16; ++kk)
-            tree_mma_ts(d, a + (uint32_t)(PARTS == 3 ? kk * 16 : (kk >> 1) * 32 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc,
+            umma_bf16_ts(d, a + (uint32_t)(PARTS == 3 ? kk * 16 : (kk >> 1) * 32 + (kk & 1) * 8), vd + (uint32_t)(kk * 128), idesc,
                         (PARTS == 3 || (LONG ? (j - w.jb) % kTreeRun != 0 : j > w.jb) || kk != 0) ? 1u : 0u);
           umma_commit(pv_done + 8 * b);
           umma_commit(v_empty + 8 * vs);
@@ -815,7 +765,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               float rs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
               if (__all_sync(0xffffffffu, fabsf(top) < 1.0e6f || row >= rows)) {
 #pragma unroll
-                for (int i = 0; i < WIDTH / 2; ++i) tree_fma2(x[2 * i], x[2 * i + 1], cs, -top);
+                for (int i = 0; i < WIDTH / 2; ++i) fma_f32x2(x[2 * i], x[2 * i + 1], cs, -top);
               } else {
                 // scores that pass 2^24 take the rounded product, so that the largest one's difference
                 // is 0: a choice of the row, or its bits would depend on the other rows of its warp
@@ -832,9 +782,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               for (int i = 0; i < WIDTH / 2; ++i) {
                 float& x0 = x[2 * i];
                 float& x1 = x[2 * i + 1];
-                x0 = tree_ex2(x0);
-                x1 = tree_ex2(x1);
-                tree_add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], x0, x1);
+                x0 = ex2_ftz(x0);
+                x1 = ex2_ftz(x1);
+                add_f32x2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], x0, x1);
                 if constexpr (PARTS == 3) {  // (the differences are exact; of 16 keys eight first parts, then eight second ones)
                   uint32_t &y = hi[i + (i & 8)], &z = hi[i + (i & 8) + 8];
                   y = pack_bf16x2(x0, x1);
@@ -855,7 +805,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               const float mx = maximum();
               const bool grow = mx > m + kTreeGrow && row < rows;
               if (__any_sync(0xffffffffu, grow)) {
-                const float alpha = grow ? tree_ex2(m - mx) : 1.0f;
+                const float alpha = grow ? ex2_ftz(m - mx) : 1.0f;
                 if (grow) {
                   l *= alpha;
                   sum *= alpha;
@@ -873,13 +823,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     tmem_load32(t_o + d * 32, v);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] *= alpha;
-                    tree_tmem_store32(t_o + d * 32, v);
+                    tmem_store32(t_o + d * 32, v);
                   }
                 }
                 // the block's P so far, with the old maximum: the columns of every step (of which
                 // bf16 output uses half), and of the third parts half as many.  The steps before
                 // have stored it, and only this wait puts those stores before the loads.
-                if (c > 0) tree_tmem_store_wait();
+                if (c > 0) tmem_store_wait();
                 if constexpr (PARTS == 1) {
                   auto rescale = [&](uint32_t at) {
                     float v[32];
@@ -889,7 +839,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                       const uint32_t y = __float_as_uint(v[i]);
                       v[i] = __uint_as_float(pack_bf16x2(__uint_as_float(y << 16) * alpha, __uint_as_float(y & 0xffff0000u) * alpha));
                     }
-                    tree_tmem_store32(at, v);
+                    tmem_store32(at, v);
                   };
 #pragma unroll 1
                   for (int d = 0; d < c * (WIDTH / 32); ++d) rescale(t_s + 32 * d);
@@ -909,7 +859,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll 1
                   for (int d = 0; 2 * d < c * (WIDTH / 16); ++d) rescale(t_s + kTreeBN + 16 * d);  // (of this step too, which are written anew)
                 }
-                tree_tmem_store_wait();
+                tmem_store_wait();
               }
               part = probabilities();
             }
@@ -926,7 +876,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           if (!ok) break;
           l += sum;
-          tree_tmem_store_wait();
+          tmem_store_wait();
           if constexpr (PARTS == 3) {
             // O of the block before this one, relative to m_total as what it is added to is; the
             // next product, which overwrites it, waits for this warp
@@ -942,10 +892,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 tree_tmem_load32(t_o + c * 32, v);
                 tree_tmem_load_wait<32>(v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) tree_add2(total[c * 32 + 2 * i], total[c * 32 + 2 * i + 1], v[2 * i], v[2 * i + 1]);
+                for (int i = 0; i < 16; ++i) add_f32x2(total[c * 32 + 2 * i], total[c * 32 + 2 * i + 1], v[2 * i], v[2 * i + 1]);
               }
               if (__any_sync(0xffffffffu, m != m_total)) {
-                const float a = m == m_total ? 1.0f : tree_ex2(m_total - m);
+                const float a = m == m_total ? 1.0f : ex2_ftz(m_total - m);
 #pragma unroll
                 for (int i = 0; i < DH; ++i) total[i] *= a;
               }
@@ -1028,13 +978,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if constexpr (LONG) {
         if (run + kTreeRun < w.je) {
           if (active) {
-            tree_take_run<DH>(t_o, total, run == w.jb ? 0.0f : m_total == m ? 1.0f : tree_ex2(m_total - m));
+            tree_take_run<DH>(t_o, total, run == w.jb ? 0.0f : m_total == m ? 1.0f : ex2_ftz(m_total - m));
             m_total = m;
           }
           run += kTreeRun;
           goto next_run;
         }
-        if (active && run > w.jb) tree_add_runs<DH>(t_o, total, m_total == m ? 1.0f : tree_ex2(m_total - m));
+        if (active && run > w.jb) tree_add_runs<DH>(t_o, total, m_total == m ? 1.0f : ex2_ftz(m_total - m));
       }
       if (PARTS == 3 && active && w.je - w.jb > 1) {
 #pragma unroll
@@ -1043,9 +993,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           tmem_load32(t_o + c * 32, v);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] += total[c * 32 + i];
-          tree_tmem_store32(t_o + c * 32, v);
+          tmem_store32(t_o + c * 32, v);
         }
-        tree_tmem_store_wait();
+        tmem_store_wait();
       }
       if (active) {
         const bool whole = w.jb == 0 && w.je == w.nb;
@@ -1159,7 +1109,7 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
       }
       const float top = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), m);
       const float ms = top == -INFINITY ? 0.0f : top;
-      const float self = tree_ex2(m - ms);
+      const float self = ex2_ftz(m - ms);
       l *= self;
       o.x *= self;
       o.y *= self;
@@ -1167,7 +1117,7 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
       o.w *= self;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float a = tree_ex2(mk[k] - ms);
+        const float a = ex2_ftz(mk[k] - ms);
         l = fmaf(a, lk[k], l);
         o.x = fmaf(a, v[k].x, o.x);
         o.y = fmaf(a, v[k].y, o.y);
@@ -1182,7 +1132,7 @@ __global__ void __launch_bounds__(256) k_tree_merge(const TreeArgs p) {
     const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, o.x, d), __shfl_xor_sync(0xffffffffu, o.y, d),
                                  __shfl_xor_sync(0xffffffffu, o.z, d), __shfl_xor_sync(0xffffffffu, o.w, d));
     const float top = fmaxf(m, mo), ms = top == -INFINITY ? 0.0f : top;
-    const float a = tree_ex2(m - ms), c = tree_ex2(mo - ms);
+    const float a = ex2_ftz(m - ms), c = ex2_ftz(mo - ms);
     m = top;
     l = l * a + lo * c;
     o = make_float4(o.x * a + y.x * c, o.y * a + y.y * c, o.z * a + y.z * c, o.w * a + y.w * c);
