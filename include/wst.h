@@ -665,8 +665,10 @@ size_t wst_ikbo_attention_workspace_size(void);
  *   q_out[t][h] = R(q[t][h]),  slot of k_cache [h] = R(k[t][h]),
  *   slot of v_cache [h] = v[t][h]
  * R turns rot/2 pairs of the first rot components by positions[t]*inv_freq[j]
- * (radians; evaluated as if exactly, for any 32-bit position), pair j being
- * components (j, j + rot/2) (WST_ROPE_HALVES) or (2j, 2j + 1) (WST_ROPE_PAIRS):
+ * (radians, reduced by whole turns in 64-bit integers: off by at most
+ * |position * inv_freq| 2^-52 + 2^-30, 5e-7 at position 2^31 and inv_freq 1, and by
+ * fp32's rounding of what is left), pair j being components (j, j + rot/2)
+ * (WST_ROPE_HALVES) or (2j, 2j + 1) (WST_ROPE_PAIRS):
  *   (a, b) -> (a cos - b sin, b cos + a sin)
  * in fp32, rounded once to bf16; the other components are copied.
  *   q, k, v    x_type, element (t,h,d) at x + t*ldx + h*Dh + d; q may be NULL
@@ -719,7 +721,9 @@ wst_status wst_cache_append_bf16(int T, int H, int Hkv, int Dh, int rot, wst_rop
  * to 65,536 keys at a time as the tensor core adds, which cuts off (up to 2^-11 of O).
  * After a tree is verified, two calls of wst_permute_rows move the accepted tokens'
  * rows of a cache together: into an array of their own and back behind the context
- * (a row's new place may be another's old one).
+ * (a row's new place may be another's old one).  A row is a token's heads where they
+ * follow one another ([page][token][head]); in a cache of [page][head][token] every
+ * head of a token is a row of its own.
  * Supported: Dh 64 and 128, H / Hkv <= 128, page_size 8, 16, 32, 64 or a multiple of
  * 128, max_pages * page_size <= 2^30, T <= 2^30, B <= 2^29 (else
  * WST_ERR_UNSUPPORTED).

@@ -19,11 +19,13 @@
 // sequences, then the odd ones: the two tiles of a sequence are worked on by two CTAs at
 // nearly the same time, and the later one finds K and V in L2.  The cut between the lines is
 // shifted (Share's lead) so that the two are up to 24 blocks apart: at the same time both
-// miss L2 and read HBM.  (16 trees of 64 tokens on up to 8,192, 400 MB of K and V: 128 us;
-// with leads of 0, 4, 8, 16 141, 138, 136, 132, and 740 MB read at 0, 500 at 24; in the
-// sequences' order one CTA took a tile after the other, 138 us and 800 MB.)  Two tiles of a
-// sequence in one CTA read 400 MB but wait for each other's products, 129 us: tensor memory
-// holds one S/P buffer for each of two tiles, three for one.
+// miss L2 and read HBM.  (16 trees of 64 tokens on up to 8,192, 400 MB of K and V, four draws of
+// the lengths: 131, 124, 139, 138 us, without a lead 144, 119, 143, 143; 500 to 700 MB are read,
+// 740 without one.  It makes no difference to 32 trees on up to 2,048, nor to batches whose
+// sequences have no second tile, where it only makes shares unequal, by less than a block: 64
+// sequences of one token 135 us both ways.  In the sequences' order one CTA took a tile after
+// the other, 138 us and 800 MB.)  Two tiles of a sequence in one CTA read 400 MB but wait for
+// each other's products, 129 us, with one S/P buffer for each of the two.
 // A piece of a cut item leaves its un-normalised O, row maxima m and sums l in the
 // workspace, and a second kernel adds an item's pieces in a fixed order:
 //   m* = max m_i,  l* = sum l_i 2^(m_i - m*),  O = sum O_i 2^(m_i - m*) / l*
@@ -33,7 +35,8 @@
 // Inside a CTA, per block (online softmax in base 2, cs = scale * log2 e):
 //   MMA      S = Q . K^T        Q and K from shared memory, 128 x 128 x Dh
 //   softmax  P = 2^(cs S - m) as bf16 over S's tensor memory; m is a whole number that
-//            moves only when a score exceeds it by more than 8, which rescales O and l
+//            moves only when a score exceeds it by more than 8, which rescales O and l (fp32
+//            output: the sums that take O over)
 //            (P <= 2^8; l sums the unrounded P).  One bf16 is off by up to 2^-8 of P, which
 //            a bf16 output's own rounding covers; for fp32 output P is three bf16, each what
 //            the ones before leave, off by 2^-24 together
@@ -45,10 +48,11 @@
 // wider ones of fp32 output) let S run ahead of PV.  (Two items at a time with one buffer
 // each: 147 us for 32 sequences of 4,096 against 82.)  Two threads issue the products, so
 // that one's run under the other's wait.
-// Measured (32 heads on 8 of 128): one token on 262,144 keys 161 us, 1.07 GB at 6.7 TB/s;
-// one token each of 32 sequences of up to 4,096, 78 us, 403 MB, of which 14 are start, the
+// Measured (32 heads on 8 of 128): one token on 262,144 keys 159 us, 1.07 GB at 6.7 TB/s;
+// one token each of 32 sequences of up to 4,096, 77 us, 403 MB, of which 14 are start, the
 // items' ends and the second kernel; 4 chunks of 500 tokens behind up to 2,000 (28 heads on
-// 4) 103 us, 0.35 PFLOP/s: the softmax's chain, 3,300 clocks a block.
+// 4) 103 us, 0.35 PFLOP/s: the softmax's chain, 3,300 clocks a block.  fp32 output of these:
+// 269, 133, 151 us.
 //
 // A block that ends behind the context (a sequence's last one or two) takes another
 // path: each row's visible keys come as 128 bits, scores outside them do not count

@@ -29,10 +29,17 @@
 // barrier take the issuing thread about 200 clocks), one that adds the sets' sums of a
 // tile and stores it while they multiply the next, and one or two that order the rows (a
 // unit takes one 1,000 clocks at 8 rows, most of it latency).
-// Measured: 1 x 4,096 x 4,096 8.0 us (8.7 MB; a launch 2, the first loads and the merge of
-// four pieces the most of the rest), 16 x 8,192 x 8,192 with bias and SiLU 17.2 us (35 MB at
-// 2.0 TB/s), 64 rows of 64 experts, 1,536 x 4,096, 32 us (111 MB at 3.5 TB/s): a unit takes a
-// CTA 750 clocks at 8 rows and 1,000 at 16, of the integer pipe and the rows' order.
+// Measured (weights in L2, and out of it): 1 x 4,096 x 4,096 8.2 and 8.9 us, 16 x 8,192 x 8,192
+// with bias and SiLU 16.2 and 17.4 us, 64 rows of 64 experts, 1,536 x 4,096, 32 us.  Where the
+// time goes, in clocks of a CTA (2,070 a us) from the end of the kernel before:
+//                                  1 x 4,096^2   16 x 8,192^2   experts
+//   share found, roles start            2,250          1,960      5,750
+//   first unit there and ordered        2,650          3,300      4,200
+//   a set's units: wait + product   1 x 1,540      6 x 2,700  12 x 2,850
+//   sums handed over, tiles out         1,400          2,100      8,100
+//   last sums, merge (mean; last)  3,400; 5,500   4,900; 7,100  4,500; 7,100
+// A set needs 1,500 to 2,500 clocks for a unit alone, so its CTA one in 750 (four sets, 8 rows)
+// to 900 (three, 16 rows); the experts' sets also wait 850 of every 2,850 for their next one.
 #pragma once
 
 #include "work_split.cuh"
