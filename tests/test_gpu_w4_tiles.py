@@ -63,3 +63,16 @@ def test_grouped(sizes, behind, N, K, group, dtype, whole, tile):
         if o[e + 1] > o[e]:
             check(C[o[e]:o[e + 1]], *want(A[o[e]:o[e + 1]], W[e], S[e], K, group, bias[e], "bias"))
     assert bool((C[o[-1]:] == 3.0).all())
+
+
+@pytest.mark.parametrize("sizes,N,K,group", [([3, 0, 9, 1], 260, 515, 64), ([20, 33], 1500, 2000, 128)])
+def test_groups_that_share_weights(sizes, N, K, group):
+    """One matrix for all groups, a stride of 0."""
+    G, M = len(sizes), sum(sizes)
+    A, W, S, _ = inputs(M + N, M, N, K, group)
+    off = torch.tensor([0] + sizes, device="cuda").cumsum(0).to(torch.int32)
+    C = rows(torch.full((M, N), 3.0, device="cuda"))
+    ws = wst.gemm_w4_workspace()
+    wst.wst_grouped_gemm_w4(A, W[None].expand(G, *W.shape), S[None].expand(G, *S.shape), off, C, group=group, workspace=ws)
+    assert wst.wst_sync_status(ws) == 0
+    check(C, *want(A, W, S, K, group))
